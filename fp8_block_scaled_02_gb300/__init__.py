@@ -28,12 +28,23 @@ Functions (names follow the C entry points):
     kv_append(x, slots, scale, cache)    FP8 KV cache append (fp8kv_append), in place
     kv_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                         max_seq_len, sm_scale) -> o bf16 [B, Hq, 128]   (fp8kv_decode_attention)
+    kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size, num_blocks, num_tokens)
+                           -> KvPlan: the step's cache blocks and slot map from request lengths (fp8bs_kv_plan)
+    kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache)   4-bit KV cache append, in place (fp4kv_append)
+    kv4_gather(k_cache, v_cache, slots, k_scale, v_scale) -> k, v bf16 [T, Hkv, D]   (fp4kv_gather)
+    kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                         max_seq_len, sm_scale, workspace) -> o bf16 [T, Hq, D]   (fp4kv_decode_attention)
+        4-bit caches are uint8 of kv4_cache_shape(num_blocks, page_size, kv_heads, head_dim)
+    token_logprobs(logits, targets, top) -> TokenLogprobs: log probabilities of given tokens, entropy,
+                           top alternatives   (fp8bs_token_logprobs)
     check_device_error()   -> the kernels' error word (synchronises; reading clears it)
     select_path(m, n, k)   -> the kernel path an AUTO call takes (host only)
     debug_wait_expiry(), debug_encode_f32(first_bits, count)   test hooks (fp8bs_debug_*)
 """
 from __future__ import annotations
 
+import collections
+import contextlib
 import ctypes
 import os
 import threading
@@ -102,6 +113,14 @@ def lib() -> ctypes.CDLL:
         L.fp8kv_append.argtypes = [p, i64, i64, i64, p, p, p, i64, p]
         L.fp8kv_decode_attention.argtypes = [p, p, p, p, p, p, i64, p, i64, i64, i64, i64, i64, i64, i64,
                                              ctypes.c_float, p, p]
+        L.fp8bs_kv_plan.argtypes = [p, p, i64, p, i64, p, i64, p, i64, i64, i64, p, p, p, p, p, p, p]
+        L.fp4kv_append.argtypes = [p, i64, p, i64, i64, i64, i64, p, p, p, p, p, i64, i64, p]
+        L.fp4kv_gather.argtypes = [p, p, p, i64, i64, i64, i64, i64, p, p, p, p, p]
+        L.fp4kv_attention_ws_bytes.argtypes = [i64]
+        L.fp4kv_attention_ws_bytes.restype = i64
+        L.fp4kv_decode_attention.argtypes = [p, i64, p, i64, i64, p, p, p, p, p, i64, p, i64, i64, i64, i64, i64, i64,
+                                             i64, i64, ctypes.c_float, p, p, p, i64, p]
+        L.fp8bs_token_logprobs.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, p, p, p]
         L.w8a8_gemm.argtypes = [p, i64, p, p, p, i64, i64, p, p]
         L.w8a8_gemm_ex.argtypes = [p, i64, p, p, p, i64, i64, p, i32, p]
         L.fp8bs_select_path.argtypes = [i64, i64, i64, p, p, i32]
@@ -117,6 +136,7 @@ def lib() -> ctypes.CDLL:
                   "mxfp8_gemv_ex", "fp8row_quantize", "fp8tensor_quantize", "fp8row_gemv", "fp8row_gemv_ex",
                   "fp8tensor_gemv", "fp8tensor_gemv_ex", "fp8act_quantize", "w8a8_gemm", "w8a8_gemm_ex",
                   "fp8bs_moe_gemv", "fp8bs_moe_gemv_ws", "fp8kv_append", "fp8kv_decode_attention",
+                  "fp8bs_kv_plan", "fp4kv_append", "fp4kv_gather", "fp4kv_decode_attention", "fp8bs_token_logprobs",
                   "fp8bs_select_path", "fp8bs_check_device_error", "fp8bs_debug_wait_expiry",
                   "fp8bs_debug_encode_f32", "fp8bs_version"):
             getattr(L, f).restype = ctypes.c_int
@@ -155,13 +175,14 @@ class _Args:
     ``need(name, t, dtype, numel=..., shape=...)`` records a tensor; sizes
     are checked first (ValueError, for any device), then that every tensor
     sits on the device of the first one (ValueError), then CUDA, dtype and
-    contiguity (TypeError / ValueError).  ``ptr(name)`` gives the device
+    contiguity (TypeError / ValueError; with ``rows`` only the dimensions
+    after the first have to be contiguous).  ``ptr(name)`` gives the device
     address once ``check()`` has passed; ``device`` is where the call runs."""
 
     def __init__(self):
         self.items = []
 
-    def need(self, name, t, dtype, numel=None, shape=None):
+    def need(self, name, t, dtype, numel=None, shape=None, rows=False):
         import torch
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -169,23 +190,23 @@ class _Args:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if numel is not None and t.numel() != numel:
             raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-        self.items.append((name, t, dtype))
+        self.items.append((name, t, dtype, rows))
         return self
 
     def check(self):
         first = self.items[0][1].device
-        for name, t, _ in self.items:
+        for name, t, _, _ in self.items:
             if t.device != first:
                 raise ValueError(f"{name} is on {t.device}, the call's tensors on {first}")
-        for name, t, dtype in self.items:
+        for name, t, dtype, rows in self.items:
             if t.device.type != "cuda":
                 raise TypeError(f"{name} must be a CUDA tensor")
             if t.dtype != dtype:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+            if not (t.is_contiguous() or (rows and t.numel() and t[0].is_contiguous())):
+                raise ValueError(f"{name} must be contiguous" + (" in all but its first dimension" if rows else ""))
         self.device = first
-        self.ptrs = {name: ctypes.c_void_p(t.data_ptr()) for name, t, _ in self.items}
+        self.ptrs = {name: ctypes.c_void_p(t.data_ptr()) for name, t, _, _ in self.items}
         return self
 
     def ptr(self, name):
@@ -490,6 +511,195 @@ def kv_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
          a.ptr("v_cache"), a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("block_table"), max_blocks,
          a.ptr("seq_lens"), b, hq, hkv, d, page, nb, int(max_seq_len), float(sm_scale), a.ptr("out"), stream=stream)
     return out
+
+
+KvPlan = collections.namedtuple("KvPlan", "seq_lens cu_new slots positions requests free_head")
+TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs entropy top_ids top_logprobs")
+
+
+def _outputs_on(stream, like):
+    """Where a call makes its own outputs: in the memory pool of the stream
+    it runs on, so that their memory is not handed out again while it runs."""
+    import torch
+    if stream is None or like.device.type != "cuda":
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    return torch.cuda.stream(stream)
+
+
+def _row_stride(t):
+    """Elements from one row of the first dimension to the next."""
+    return t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else 0
+
+
+def kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size: int, num_blocks: int,
+            num_tokens: int, seq_lens=None, cu_new=None, slots=None, positions=None, requests=None,
+            free_head_out=None, stream=None):
+    """The paging plan of one step from request lengths (fp8bs_kv_plan): new
+    blocks of each request from the free list (written into block_table),
+    the slot, position and request of each of the step's num_tokens tokens
+    (-1 past the last and where a request is refused).  Returns a KvPlan;
+    seq_lens may be ctx_lens and free_head_out may be free_head."""
+    import torch
+    b = ctx_lens.numel()
+    rows, max_blocks = _shape2(block_table, "block_table")
+    if rows != b:
+        raise ValueError("block_table and ctx_lens disagree on the number of requests")
+    i32 = torch.int32
+    with _outputs_on(stream, ctx_lens):
+        seq_lens = _new(seq_lens, (b,), i32, ctx_lens)
+        cu_new = _new(cu_new, (b + 1,), i32, ctx_lens)
+        slots = _new(slots, (num_tokens,), i32, ctx_lens)
+        positions = _new(positions, (num_tokens,), i32, ctx_lens)
+        requests = _new(requests, (num_tokens,), i32, ctx_lens)
+        free_head_out = _new(free_head_out, (1,), i32, ctx_lens)
+    a = _Args().need("ctx_lens", ctx_lens, i32).need("new_lens", new_lens, i32, numel=b) \
+        .need("block_table", block_table, i32).need("free_blocks", free_blocks, i32) \
+        .need("free_head", free_head, i32, numel=1).need("seq_lens", seq_lens, i32, numel=b) \
+        .need("cu_new", cu_new, i32, numel=b + 1).need("slots", slots, i32, numel=num_tokens) \
+        .need("positions", positions, i32, numel=num_tokens).need("requests", requests, i32, numel=num_tokens) \
+        .need("free_head_out", free_head_out, i32, numel=1).check()
+    _run(a, "fp8bs_kv_plan", lib().fp8bs_kv_plan, a.ptr("ctx_lens"), a.ptr("new_lens"), b, a.ptr("block_table"),
+         max_blocks, a.ptr("free_blocks"), free_blocks.numel(), a.ptr("free_head"), int(page_size), int(num_blocks),
+         int(num_tokens), a.ptr("seq_lens"), a.ptr("cu_new"), a.ptr("slots"), a.ptr("positions"), a.ptr("requests"),
+         a.ptr("free_head_out"), stream=stream)
+    return KvPlan(seq_lens, cu_new, slots, positions, requests, free_head_out)
+
+
+def kv4_cache_shape(num_blocks: int, page_size: int, num_kv_heads: int, head_dim: int):
+    """Shape of one 4-bit cache (K or V), uint8: tiles of 16 tokens of one kv head."""
+    if page_size % 16 != 0:
+        raise ValueError("page_size must be a multiple of 16")
+    return num_blocks, num_kv_heads, page_size // 16, 9 * head_dim
+
+
+def _kv4_caches(a, k_cache, v_cache, hkv, d):
+    """Check a pair of 4-bit caches; returns (num_blocks, page_size)."""
+    import torch
+    if k_cache.dim() != 4 or tuple(k_cache.shape[1::2]) != (hkv, 9 * d):
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [num_blocks, {hkv}, page_size / 16, {9 * d}]")
+    a.need("k_cache", k_cache, torch.uint8).need("v_cache", v_cache, torch.uint8, shape=k_cache.shape)
+    return k_cache.shape[0], k_cache.shape[2] * 16
+
+
+def _kv4_scales(a, k_scale, v_scale):
+    import torch
+    return a.need("k_scale", k_scale, torch.float32, numel=1).need("v_scale", v_scale, torch.float32, numel=1)
+
+
+def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
+    """Quantize new keys and values [T, Hkv, D] bf16 into 4-bit caches at flat
+    token slots, in place (fp4kv_append).  k and v may be slices of a fused
+    projection: only the rows of one token have to be contiguous."""
+    import torch
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, D]")
+    t, hkv, d = k.shape
+    a = _Args().need("k", k, torch.bfloat16, rows=True).need("v", v, torch.bfloat16, shape=k.shape, rows=True) \
+        .need("slots", slots, torch.int32, numel=t)
+    nb, page = _kv4_caches(a, k_cache, v_cache, hkv, d)
+    _kv4_scales(a, k_scale, v_scale).check()
+    _run(a, "fp4kv_append", lib().fp4kv_append, a.ptr("k"), _row_stride(k), a.ptr("v"), _row_stride(v), t, hkv, d,
+         a.ptr("slots"), a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("k_cache"), a.ptr("v_cache"), page, nb,
+         stream=stream)
+    return k_cache, v_cache
+
+
+def kv4_gather(k_cache, v_cache, slots, k_scale, v_scale, k=None, v=None, stream=None):
+    """The cached tokens at flat slots in bf16 [T, Hkv, D] (fp4kv_gather)."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape[3] % 9 != 0:
+        raise ValueError("k_cache must be [num_blocks, Hkv, page_size / 16, 9 * D]")
+    t, hkv, d = slots.numel(), k_cache.shape[1], k_cache.shape[3] // 9
+    with _outputs_on(stream, k_cache):
+        k = _new(k, (t, hkv, d), torch.bfloat16, k_cache)
+        v = _new(v, (t, hkv, d), torch.bfloat16, k_cache)
+    a = _Args()
+    nb, page = _kv4_caches(a, k_cache, v_cache, hkv, d)
+    a.need("slots", slots, torch.int32).need("k", k, torch.bfloat16, numel=t * hkv * d) \
+        .need("v", v, torch.bfloat16, numel=t * hkv * d)
+    _kv4_scales(a, k_scale, v_scale).check()
+    _run(a, "fp4kv_gather", lib().fp4kv_gather, a.ptr("k_cache"), a.ptr("v_cache"), a.ptr("slots"), t, hkv, d, page,
+         nb, a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("k"), a.ptr("v"), stream=stream)
+    return k, v
+
+
+def kv4_workspace_bytes(head_dim: int) -> int:
+    """Bytes of device workspace kv4_decode_attention needs (fp4kv_attention_ws_bytes)."""
+    v = lib().fp4kv_attention_ws_bytes(head_dim)
+    if v < 0:
+        raise Fp8bsError(int(v), "fp4kv_attention_ws_bytes")
+    return int(v)
+
+
+def kv4_workspace(head_dim: int, device="cuda"):
+    """A workspace for kv4_decode_attention: one serves every shape of a head
+    size, but only one call at a time."""
+    import torch
+    return torch.empty(kv4_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
+
+
+def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_seq_len: int,
+                         sm_scale: float, workspace, cu_q=None, max_q: int = 1, window: int = 0, out=None, lse=None,
+                         return_lse: bool = False, stream=None):
+    """Attention of the newest tokens of each sequence over its 4-bit cache
+    (fp4kv_decode_attention): q [T, Hq, D] bf16 (a slice of a fused projection
+    will do), one token per sequence, or sequence b's tokens cu_q[b] ..
+    cu_q[b + 1] - 1, at most max_q.  Returns o [T, Hq, D], with return_lse
+    (o, lse [T, Hq] fp32)."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    t, hq, d = q.shape
+    b = seq_lens.numel()
+    bt_rows, max_blocks = _shape2(block_table, "block_table")
+    if bt_rows != b or (cu_q is None and t != b):
+        raise ValueError("q, block_table and seq_lens disagree on the number of sequences")
+    hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
+    with _outputs_on(stream, q):
+        out = _new(out, (t, hq, d), torch.bfloat16, q)
+        if return_lse:
+            lse = _new(lse, (t, hq), torch.float32, q)
+    a = _Args().need("q", q, torch.bfloat16, rows=True)
+    nb, page = _kv4_caches(a, k_cache, v_cache, hkv, d)
+    _kv4_scales(a, k_scale, v_scale).need("block_table", block_table, torch.int32) \
+        .need("seq_lens", seq_lens, torch.int32).need("out", out, torch.bfloat16, numel=t * hq * d) \
+        .need("workspace", workspace, torch.uint8)
+    if cu_q is not None:
+        a.need("cu_q", cu_q, torch.int32, numel=b + 1)
+    if lse is not None:
+        a.need("lse", lse, torch.float32, numel=t * hq)
+    a.check()
+    _run(a, "fp4kv_decode_attention", lib().fp4kv_decode_attention, a.ptr("q"), _row_stride(q),
+         a.ptr("cu_q") if cu_q is not None else None, t, int(max_q), a.ptr("k_cache"), a.ptr("v_cache"),
+         a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("block_table"), max_blocks, a.ptr("seq_lens"), b, hq, hkv, d,
+         page, nb, int(max_seq_len), int(window), float(sm_scale), a.ptr("out"),
+         a.ptr("lse") if lse is not None else None, a.ptr("workspace"), workspace.numel(), stream=stream)
+    return (out, lse) if return_lse else out
+
+
+def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
+                   stream=None):
+    """Log probabilities of the targets [M] under logits [M, V] (bf16 or fp32,
+    rows may be padded), each row's entropy and its `top` best tokens
+    (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
+    import torch
+    m, v = _shape2(logits, "logits")
+    with _outputs_on(stream, logits):
+        logprobs = _new(logprobs, (m,), torch.float32, logits)
+        entropy = _new(entropy, (m,), torch.float32, logits)
+        top_ids = _new(top_ids, (m, top), torch.int32, logits)
+        top_logprobs = _new(top_logprobs, (m, top), torch.float32, logits)
+    f32 = logits.dtype == torch.float32
+    a = _Args().need("logits", logits, torch.float32 if f32 else torch.bfloat16, rows=True) \
+        .need("targets", targets, torch.int32, numel=m).need("logprobs", logprobs, torch.float32, numel=m) \
+        .need("entropy", entropy, torch.float32, numel=m).need("top_ids", top_ids, torch.int32, numel=m * top) \
+        .need("top_logprobs", top_logprobs, torch.float32, numel=m * top).check()
+    _run(a, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs, a.ptr("logits"), int(f32),
+         max(_row_stride(logits), v), m, v, a.ptr("targets"), int(top), a.ptr("logprobs"), a.ptr("entropy"),
+         a.ptr("top_ids"), a.ptr("top_logprobs"), stream=stream)
+    return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
 
 
 def act_quantize(x, codes=None, scale=None, stream=None):

@@ -459,6 +459,143 @@ int w8a8_gemm(const uint8_t *x_codes, int64_t m, const float *x_scale, const uin
     return w8a8_gemm_ex(x_codes, m, x_scale, w_codes, w_scale, n, k, y_bf16, FP8BS_PATH_AUTO, stream);
 }
 
+int fp8bs_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t batch, int32_t *block_table,
+                  int64_t max_blocks_per_seq, const int32_t *free_blocks, int64_t num_free, const int32_t *free_head,
+                  int64_t page_size, int64_t num_blocks, int64_t num_tokens, int32_t *seq_lens, int32_t *cu_new,
+                  int32_t *slots, int32_t *positions, int32_t *requests, int32_t *free_head_out, void *stream) {
+    if (batch < 0 || batch > kPlanMaxBatch || max_blocks_per_seq <= 0 || max_blocks_per_seq >= kMaxDim ||
+        num_free < 0 || num_free >= kMaxDim || num_tokens < 0 || num_tokens >= kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (page_size < 1 || page_size > 65536 || num_blocks <= 0 || num_blocks >= kMaxDim ||
+        num_blocks * page_size >= kMaxDim || max_blocks_per_seq * page_size >= kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (!free_head || !cu_new || !free_head_out || (num_free > 0 && !free_blocks)) return FP8BS_ERR_NULL;
+    if (batch > 0 && (!ctx_lens || !new_lens || !block_table || !seq_lens)) return FP8BS_ERR_NULL;
+    if (num_tokens > 0 && (!slots || !positions || !requests)) return FP8BS_ERR_NULL;
+    const void *const ptrs[] = {ctx_lens, new_lens,  block_table, free_blocks, free_head,    seq_lens,
+                                cu_new,   slots,     positions,   requests,    free_head_out};
+    for (const void *p : ptrs)
+        if (!aligned(p, 4)) return FP8BS_ERR_ALIGN;
+    const KvPlanArgs a{ctx_lens, new_lens,  block_table,   free_blocks, free_head,          seq_lens,
+                       cu_new,   slots,     positions,     requests,    free_head_out,      batch,
+                       max_blocks_per_seq,  num_free,      page_size,   num_blocks,         num_tokens};
+    return cuda_status(launch_kv_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+int check_kv4_cache(int64_t kv_heads, int64_t head_dim, int64_t page_size, int64_t num_blocks) {
+    if (kv_heads <= 0 || kv_heads >= 4096 || (head_dim != 64 && head_dim != 128)) return FP8BS_ERR_SHAPE;
+    if (page_size < kKv4Tile || page_size % kKv4Tile != 0 || page_size > 4096) return FP8BS_ERR_SHAPE;
+    if (num_blocks <= 0 || num_blocks >= kMaxDim || num_blocks * page_size >= kMaxDim) return FP8BS_ERR_SHAPE;
+    return FP8BS_OK;
+}
+
+bool stride_ok(int64_t stride, int64_t row) { return stride >= 0 && stride < (int64_t{1} << 40) && row > 0; }
+
+}  // namespace
+
+int fp4kv_append(const void *k_bf16, int64_t k_stride, const void *v_bf16, int64_t v_stride, int64_t num_tokens,
+                 int64_t num_kv_heads, int64_t head_dim, const int32_t *slots, const float *k_scale,
+                 const float *v_scale, uint8_t *k_cache, uint8_t *v_cache, int64_t page_size, int64_t num_blocks,
+                 void *stream) {
+    if (num_tokens < 0 || num_tokens >= kMaxDim) return FP8BS_ERR_SHAPE;
+    const int st = check_kv4_cache(num_kv_heads, head_dim, page_size, num_blocks);
+    if (st != FP8BS_OK) return st;
+    const int64_t row = num_kv_heads * head_dim;
+    if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return FP8BS_ERR_SHAPE;
+    if (num_tokens == 0) return FP8BS_OK;
+    if (!k_bf16 || !v_bf16 || !slots || !k_scale || !v_scale || !k_cache || !v_cache) return FP8BS_ERR_NULL;
+    if (!aligned(k_bf16, 16) || !aligned(v_bf16, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(slots, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return FP8BS_ERR_ALIGN;
+    Kv4CopyArgs a = {};
+    a.k = k_bf16, a.v = v_bf16, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.slots = slots, a.k_scale = k_scale, a.v_scale = v_scale, a.k_cache = k_cache, a.v_cache = v_cache;
+    a.tokens = num_tokens, a.kv_heads = num_kv_heads, a.head_dim = head_dim, a.page_size = page_size;
+    a.num_slots = num_blocks * page_size;
+    return cuda_status(launch_kv4_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache, const int32_t *slots, int64_t num_tokens,
+                 int64_t num_kv_heads, int64_t head_dim, int64_t page_size, int64_t num_blocks, const float *k_scale,
+                 const float *v_scale, void *k_bf16, void *v_bf16, void *stream) {
+    if (num_tokens < 0 || num_tokens >= kMaxDim) return FP8BS_ERR_SHAPE;
+    const int st = check_kv4_cache(num_kv_heads, head_dim, page_size, num_blocks);
+    if (st != FP8BS_OK) return st;
+    if (num_tokens == 0) return FP8BS_OK;
+    if (!k_bf16 || !v_bf16 || !slots || !k_scale || !v_scale || !k_cache || !v_cache) return FP8BS_ERR_NULL;
+    if (!aligned(k_bf16, 16) || !aligned(v_bf16, 16) || !aligned(slots, 4) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return FP8BS_ERR_ALIGN;
+    Kv4CopyArgs a = {};
+    a.k_out = k_bf16, a.v_out = v_bf16;
+    a.slots = slots, a.k_scale = k_scale, a.v_scale = v_scale;
+    a.k_cache = const_cast<uint8_t *>(k_cache), a.v_cache = const_cast<uint8_t *>(v_cache);
+    a.tokens = num_tokens, a.kv_heads = num_kv_heads, a.head_dim = head_dim, a.page_size = page_size;
+    a.num_slots = num_blocks * page_size;
+    return cuda_status(launch_kv4_gather(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t fp4kv_attention_ws_bytes(int64_t head_dim) {
+    if (head_dim != 64 && head_dim != 128) return FP8BS_ERR_SHAPE;
+    return kv4_attention_ws_bytes(head_dim);
+}
+
+int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride, const int32_t *cu_q, int64_t num_q_tokens,
+                           int64_t max_q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale,
+                           const float *v_scale, const int32_t *block_table, int64_t max_blocks_per_seq,
+                           const int32_t *seq_lens, int64_t batch, int64_t num_q_heads, int64_t num_kv_heads,
+                           int64_t head_dim, int64_t page_size, int64_t num_blocks, int64_t max_seq_len,
+                           int64_t window, float sm_scale, void *out_bf16, float *lse, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+    const int st = check_kv4_cache(num_kv_heads, head_dim, page_size, num_blocks);
+    if (st != FP8BS_OK) return st;
+    if (batch < 0 || batch >= 65536 || num_q_tokens < 0 || num_q_tokens >= kMaxDim || max_q < 1 || max_q >= 65536)
+        return FP8BS_ERR_SHAPE;
+    if (num_q_heads <= 0 || num_q_heads >= 65536 || num_q_heads % num_kv_heads != 0) return FP8BS_ERR_SHAPE;
+    if (!cu_q && (num_q_tokens != batch || max_q != 1)) return FP8BS_ERR_SHAPE;
+    if (max_blocks_per_seq <= 0 || max_blocks_per_seq >= kMaxDim || max_blocks_per_seq * page_size >= kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (max_seq_len < 0 || max_seq_len > max_blocks_per_seq * page_size || window < 0 || window >= kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (!stride_ok(q_stride, num_q_heads * head_dim)) return FP8BS_ERR_SHAPE;
+    if (!(sm_scale == sm_scale) || sm_scale > 3.0e38f || sm_scale < -3.0e38f) return FP8BS_ERR_SHAPE;
+    if (batch == 0 || num_q_tokens == 0) return FP8BS_OK;
+    if (!q_bf16 || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out_bf16 ||
+        !workspace)
+        return FP8BS_ERR_NULL;
+    if (!aligned(q_bf16, 16) || q_stride % 8 != 0 || !aligned(cu_q, 4) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(out_bf16, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+        return FP8BS_ERR_ALIGN;
+    if (workspace_bytes < kv4_attention_ws_bytes(head_dim)) return FP8BS_ERR_SHAPE;
+    Kv4AttnArgs a = {};
+    a.q = q_bf16, a.cu_q = cu_q, a.k_cache = k_cache, a.v_cache = v_cache, a.k_scale = k_scale, a.v_scale = v_scale;
+    a.block_table = block_table, a.seq_lens = seq_lens, a.out = out_bf16, a.lse = lse, a.workspace = workspace;
+    a.q_stride = q_stride, a.tokens = num_q_tokens, a.max_q = max_q, a.batch = batch, a.q_heads = num_q_heads;
+    a.kv_heads = num_kv_heads, a.head_dim = head_dim, a.page_size = page_size, a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks_per_seq, a.max_seq_len = max_seq_len, a.window = window, a.sm_scale = sm_scale;
+    return cuda_status(launch_kv4_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_token_logprobs(const void *logits, int logits_f32, int64_t row_stride, int64_t rows, int64_t vocab,
+                         const int32_t *targets, int64_t top, float *logprobs, float *entropy, int32_t *top_ids,
+                         float *top_logprobs, void *stream) {
+    if (rows < 0 || rows >= kMaxDim || vocab <= 0 || vocab >= kMaxDim || row_stride < vocab ||
+        row_stride >= (int64_t{1} << 40) || top < 0 || top > kLogprobsMaxTop || top > vocab)
+        return FP8BS_ERR_SHAPE;
+    if (rows == 0) return FP8BS_OK;
+    if (!logits || !targets || !logprobs || !entropy || (top > 0 && (!top_ids || !top_logprobs)))
+        return FP8BS_ERR_NULL;
+    if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(targets, 4) || !aligned(logprobs, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+        return FP8BS_ERR_ALIGN;
+    const LogprobArgs a{logits, logits_f32 != 0, targets, logprobs, entropy, top_ids, top_logprobs,
+                        row_stride, rows, vocab, top};
+    return cuda_status(launch_token_logprobs(a, static_cast<cudaStream_t>(stream)));
+}
+
 int fp8bs_select_path(int64_t m, int64_t n, int64_t k, const void *x_bf16, const void *codes, int mx) {
     (void)n;
     if (m <= 0 || k <= 0) return FP8BS_ERR_SHAPE;
@@ -480,7 +617,7 @@ int fp8bs_debug_encode_f32(uint32_t first_bits, int64_t count, uint8_t *codes_u8
 int fp8bs_check_device_error(void *stream, uint32_t *word_out) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8BS_ERR_CUDA;
     const uint32_t w = take_decode_error() | take_prefill_error() | take_w8a8_error() | take_kv_error() |
-                       take_moe_error();
+                       take_moe_error() | take_plan_error() | take_kv4_error() | take_logprobs_error();
     if (word_out) *word_out = w;
     return w ? FP8BS_ERR_DEVICE : FP8BS_OK;
 }

@@ -176,6 +176,71 @@ cudaError_t launch_kv_append(const void *x, int64_t num_tokens, int64_t kv_heads
                              const float *scale, uint8_t *cache, int64_t num_slots, cudaStream_t stream);
 uint32_t take_kv_error();
 
+// kvplan.cu -- block tables and slot maps of one step from request lengths.
+constexpr int64_t kPlanMaxBatch = 16384;  // three int32 per request in shared memory
+struct KvPlanArgs {
+    const int32_t *ctx_lens, *new_lens;  // [batch]
+    int32_t *block_table;                // [batch, max_blocks]
+    const int32_t *free_blocks;          // [num_free]
+    const int32_t *free_head;            // [1]
+    int32_t *seq_lens;                   // [batch] (may be ctx_lens)
+    int32_t *cu_new;                     // [batch + 1]
+    int32_t *slots, *positions, *requests;  // [num_tokens]
+    int32_t *free_head_out;              // [1] (may be free_head)
+    int64_t batch, max_blocks, num_free, page_size, num_blocks, num_tokens;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t stream);
+uint32_t take_plan_error();
+
+// kv4.cu -- the 4-bit paged KV cache: append, gather, decode attention.
+// A cache is tiles of 16 tokens of one kv head, [num_blocks, kv_heads,
+// page_size / 16] of kv4_tile_bytes(head_dim) bytes: e2m1 codes
+// [16, head_dim / 2], then e4m3 scales [16, head_dim / 16].
+constexpr int kKv4Tile = 16;
+__host__ __device__ constexpr int64_t kv4_tile_bytes(int64_t head_dim) { return 9 * head_dim; }
+struct Kv4CopyArgs {
+    const void *k, *v;           // append: bf16 [tokens, kv_heads, head_dim], rows *_stride elements apart
+    void *k_out, *v_out;         // gather: bf16 [tokens, kv_heads, head_dim]
+    int64_t k_stride, v_stride;
+    const int32_t *slots;        // [tokens]
+    const float *k_scale, *v_scale;
+    uint8_t *k_cache, *v_cache;
+    int64_t tokens, kv_heads, head_dim, page_size, num_slots;
+};
+cudaError_t launch_kv4_append(const Kv4CopyArgs &a, cudaStream_t stream);
+cudaError_t launch_kv4_gather(const Kv4CopyArgs &a, cudaStream_t stream);
+struct Kv4AttnArgs {
+    const void *q;               // bf16 [tokens, q_heads, head_dim], rows q_stride elements apart
+    const int32_t *cu_q;         // [batch + 1], or nullptr: one query token per sequence
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table;  // [batch, max_blocks]
+    const int32_t *seq_lens;     // [batch]
+    void *out;                   // bf16 [tokens, q_heads, head_dim]
+    float *lse;                  // [tokens, q_heads] or nullptr
+    void *workspace;
+    int64_t q_stride, tokens, max_q, batch, q_heads, kv_heads, head_dim, page_size, num_blocks, max_blocks,
+        max_seq_len, window;
+    float sm_scale;
+};
+int64_t kv4_attention_ws_bytes(int64_t head_dim);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t stream);
+uint32_t take_kv4_error();
+
+// logprobs.cu -- log probabilities of given tokens, entropy, top alternatives.
+constexpr int64_t kLogprobsMaxTop = 32;
+struct LogprobArgs {
+    const void *logits;          // bf16 or fp32 [rows, vocab], rows row_stride elements apart
+    bool f32;
+    const int32_t *targets;      // [rows]
+    float *logprobs, *entropy;   // [rows]
+    int32_t *top_ids;            // [rows, top]
+    float *top_logprobs;         // [rows, top]
+    int64_t row_stride, rows, vocab, top;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream);
+uint32_t take_logprobs_error();
+
 // Multiprocessor count of the current device (cached per device).
 int device_sm_count();
 

@@ -2,9 +2,9 @@
  * fp8bs.h -- C ABI of libfp8bs: block-scaled FP8 (E4M3), MXFP8 and per-row /
  * per-tensor FP8 weight quantization, the W8A16 GEMV / skinny GEMM /
  * prefill GEMM that consumes it, the W8A8 route (dynamic per-tensor
- * activation quantization + e4m3 x e4m3 GEMM), the grouped MoE GEMV and an
- * FP8 E4M3 paged KV cache with split-KV decode attention, for NVIDIA GB300
- * (sm_103a).
+ * activation quantization + e4m3 x e4m3 GEMM), the grouped MoE GEMV, FP8
+ * E4M3 and 4-bit paged KV caches with split-KV decode attention, the step's
+ * paging plan and token log probabilities, for NVIDIA GB300 (sm_103a).
  *
  * Common conventions
  * ------------------
@@ -505,6 +505,205 @@ int w8a8_gemm_ex(const uint8_t *x_codes, int64_t m, const float *x_scale,
                  const uint8_t *w_codes, const float *w_scale, int64_t n,
                  int64_t k, void *y_bf16, int path, void *stream);
 
+/*
+ * fp8bs_kv_plan -- the paging plan of one serving step, built on the device
+ * from request lengths (no host synchronisation): which new cache blocks
+ * each request gets, and where each of the step's new tokens goes.  Serves
+ * the FP8 cache (fp8kv_append) and the 4-bit cache (fp4kv_append) alike.
+ *
+ * Defined by: no passage of the source pages has a counterpart (InfiniLM PR
+ * #586 takes the slot map and the block table as given).  With
+ * c = ctx_lens[b] cached and n = new_lens[b] new tokens of request b,
+ * P = page_size:
+ *   cu_new[b + 1] = cu_new[b] + n, cu_new[0] = 0   (the step's token axis)
+ *   have = ceil(c / P), need = ceil((c + n) / P) - have
+ *   the `need` new blocks are free_blocks[h], free_blocks[h + 1], ... with
+ *     h = *free_head + (the needs of the requests before b); they are stored
+ *     at block_table[b][have ...]
+ *   token cu_new[b] + i: requests = b, positions = c + i,
+ *     slots = block of (c + i) * P + (c + i) % P
+ *   seq_lens[b] = c + n;  *free_head_out = *free_head + (blocks handed out)
+ * Entries of the token arrays past cu_new[batch] are -1.
+ *
+ * A request is refused -- seq_lens[b] = c, its tokens keep their places on
+ * the token axis with positions and slots -1, it takes no block -- when the
+ * free list has run out for it (blocks are handed out in request order, so
+ * every later request that needs a block is refused too; sets
+ * bit 5 of the device error word), or when its lengths cannot be: c or n
+ * negative, c + n > max_blocks_per_seq * page_size, cu_new[b + 1] >
+ * num_tokens (sets bit 4; seq_lens[b] is c clamped to the table's range).  A
+ * block id outside [0, num_blocks) gives slots -1 (a free-list id also a
+ * table entry -1) and sets bit 4, as does a *free_head outside
+ * [0, num_free], for which every request that needs a block is refused.
+ *
+ *   ctx_lens, new_lens   device, [batch] int32 (n = 0: nothing new)
+ *   batch                0..16384 (0: only cu_new, the token arrays and the head)
+ *   block_table          device, [batch, max_blocks_per_seq] int32; entries
+ *                        below `have` are read, the new ones written
+ *   free_blocks          device, [num_free] int32 (may be NULL if num_free is 0)
+ *   free_head            device, 1 int32: blocks of the list already taken
+ *   page_size            1..65536, num_blocks * page_size < 2^31
+ *   num_tokens           size of the token arrays (>= the step's tokens)
+ *   seq_lens             device, [batch] int32, written; may be ctx_lens
+ *   cu_new               device, [batch + 1] int32, written
+ *   slots, positions, requests   device, [num_tokens] int32, written
+ *   free_head_out        device, 1 int32, written; may be free_head
+ * No other two arrays may overlap.
+ */
+int fp8bs_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens,
+                  int64_t batch, int32_t *block_table,
+                  int64_t max_blocks_per_seq, const int32_t *free_blocks,
+                  int64_t num_free, const int32_t *free_head,
+                  int64_t page_size, int64_t num_blocks, int64_t num_tokens,
+                  int32_t *seq_lens, int32_t *cu_new, int32_t *slots,
+                  int32_t *positions, int32_t *requests,
+                  int32_t *free_head_out, void *stream);
+
+/*
+ * 4-bit KV cache for paged attention: e2m1 codes with one e4m3 scale per 16
+ * elements and one fp32 scale per layer, 0.28 of the bytes of bf16.
+ *
+ * Defined by: no passage of the source pages has a counterpart; the paging,
+ * the per-layer fp32 k_scale / v_scale and the attention are those of
+ * InfiniLM PR #586's FP8 cache, the group format the element and block-scale
+ * formats of the 4-bit float type (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6).
+ *
+ * Cache layout, K and V each: uint8 [num_blocks, num_kv_heads,
+ * page_size / 16, 9 * head_dim]; a tile of 16 tokens of one kv head is its
+ * codes [16, head_dim / 2] (element 2j in the low nibble of byte j), then its
+ * scales [16, head_dim / 16].  The value of an element is code * scale * s.
+ * Token i of sequence b is in block block_table[b][i / page_size] at offset
+ * i % page_size.  head_dim is 64 or 128, page_size a multiple of 16 up to
+ * 4096, num_kv_heads < 4096, num_blocks * page_size < 2^31.
+ *
+ * fp4kv_append: for each token t and group of 16 elements x of k[t] (v[t]),
+ *   scale = e4m3(fl32(amax / fl32(6 s))), den = fl32(s * scale),
+ *   code = e2m1(fl32(x / den)), code = 0 where den = 0
+ * (nearest-even, saturating), stored at slot slots[t] = block * page_size +
+ * offset.  Slot -1 stores nothing (padding, refused requests); any other
+ * slot outside [0, num_blocks * page_size) stores nothing and sets the
+ * device error word (bit 4).  Two tokens of one call may not share a slot.
+ *
+ *   k_bf16, v_bf16     device, [num_tokens, num_kv_heads, head_dim] bf16,
+ *                      16-byte aligned, tokens k_stride (v_stride) elements
+ *                      apart, a multiple of 8 (e.g. rows of a fused
+ *                      projection)
+ *   slots              device, [num_tokens] int32
+ *   k_scale, v_scale   device, 1 positive float each (amax / 2688 of the
+ *                      layer's keys or values uses the whole range)
+ *   k_cache, v_cache   device, 16-byte aligned, written at the slots
+ */
+int fp4kv_append(const void *k_bf16, int64_t k_stride, const void *v_bf16,
+                 int64_t v_stride, int64_t num_tokens, int64_t num_kv_heads,
+                 int64_t head_dim, const int32_t *slots, const float *k_scale,
+                 const float *v_scale, uint8_t *k_cache, uint8_t *v_cache,
+                 int64_t page_size, int64_t num_blocks, void *stream);
+
+/*
+ * fp4kv_gather: the tokens at slots[t] of a 4-bit cache in bf16, e.g. a
+ * cached prefix for a dense prompt attention:
+ *   k_bf16[t] = bf16(fl32(code * scale * s))   (code * scale is exact)
+ * [num_tokens, num_kv_heads, head_dim], contiguous, 16-byte aligned.  Slot
+ * -1 gives zeros; any other slot out of range too, with bit 4 of the device
+ * error word.  Defined by: the cache above.
+ */
+int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
+                 const int32_t *slots, int64_t num_tokens,
+                 int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                 int64_t num_blocks, const float *k_scale,
+                 const float *v_scale, void *k_bf16, void *v_bf16,
+                 void *stream);
+
+/*
+ * fp4kv_decode_attention: attention of the newest tokens of each sequence
+ * over its 4-bit cache (one per sequence when decoding; several when drafted
+ * tokens are verified or a short prompt chunk is appended).  The keys of the
+ * query tokens themselves are already in the cache.  For query token i of
+ * the n_q of sequence b, at position p = seq_lens[b] - n_q + i:
+ *   o[i, h, :] = sum_l w_l * dec(V[l, g]),
+ *   w = softmax_l(sm_scale * q[i, h, :] . dec(K[l, g])),
+ *   lse[i, h] = log sum_l exp(sm_scale * q[i, h, :] . dec(K[l, g]))
+ * over keys l <= p (with window > 0: p - window < l <= p),
+ * g = h / (num_q_heads / num_kv_heads).  A row that sees no key gives o = 0,
+ * lse = -inf.  K and V decode exactly to f16 (code * scale); scores, the
+ * softmax and all sums are fp32 (the weights enter the V sum as f16, held
+ * against the running maximum so that 2^-39 of it is the smallest); one
+ * bf16 rounding at the end.
+ *
+ * Defined by: InfiniLM PR #586 (Benchmark: split-KV decode attention over
+ * the paged cache) for the decode form; several query tokens, the window and
+ * lse have no counterpart there.
+ *
+ *   q_bf16       device, [num_q_tokens, num_q_heads, head_dim] bf16, 16-byte
+ *                aligned, tokens q_stride elements apart, a multiple of 8
+ *   cu_q         device, [batch + 1] int32: sequence b's query tokens are
+ *                cu_q[b] .. cu_q[b + 1] - 1 (fp8bs_kv_plan's cu_new), at most
+ *                max_q of them; NULL: one per sequence, num_q_tokens = batch.
+ *                A range outside [0, num_q_tokens] or longer than max_q is
+ *                skipped (its rows are not written) and sets bit 4 of the
+ *                device error word.  Rows of no sequence are not written
+ *   k_scale, v_scale   device, 1 float each
+ *   block_table  device, [batch, max_blocks_per_seq] int32; the tokens of an
+ *                id outside [0, num_blocks) are left out and bit 4 is set
+ *   seq_lens     device, [batch] int32, 0..max_seq_len (clamped, bit 4)
+ *   max_seq_len  host upper bound of seq_lens, <= max_blocks_per_seq * page_size
+ *   max_q        host upper bound of the query tokens of a sequence, >= 1
+ *   out_bf16     device, [num_q_tokens, num_q_heads, head_dim] bf16,
+ *                16-byte aligned, written
+ *   lse          device, [num_q_tokens, num_q_heads] fp32, written, or NULL
+ *   workspace    device, 16-byte aligned, >= fp4kv_attention_ws_bytes(head_dim)
+ *                bytes: the partial results of sequences split over CTAs.
+ *                Its contents do not matter before or after; calls that
+ *                overlap on the GPU need one each
+ * The split of the work follows the lengths on the device: results are
+ * deterministic for given shapes and lengths.
+ */
+int64_t fp4kv_attention_ws_bytes(int64_t head_dim);
+int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride,
+                           const int32_t *cu_q, int64_t num_q_tokens,
+                           int64_t max_q, const uint8_t *k_cache,
+                           const uint8_t *v_cache, const float *k_scale,
+                           const float *v_scale, const int32_t *block_table,
+                           int64_t max_blocks_per_seq, const int32_t *seq_lens,
+                           int64_t batch, int64_t num_q_heads,
+                           int64_t num_kv_heads, int64_t head_dim,
+                           int64_t page_size, int64_t num_blocks,
+                           int64_t max_seq_len, int64_t window,
+                           float sm_scale, void *out_bf16, float *lse,
+                           void *workspace, int64_t workspace_bytes,
+                           void *stream);
+
+/*
+ * fp8bs_token_logprobs -- log probabilities of given tokens over rows of
+ * logits (e.g. fp8bs_gemv's lm_head output), with each row's entropy and top
+ * alternatives, reading the logits once:
+ *   lse = log sum_j exp(x_j),  logprobs[r] = x_target - lse,
+ *   entropy[r] = -sum_j p_j log p_j (nats),  p_j = exp(x_j - lse),
+ *   top_ids[r, :], top_logprobs[r, :] = the first `top` tokens of the row in
+ *   the order of value, highest first, then index, lowest first, and x - lse.
+ * All sums in fp32.  Logits may be -inf (masked tokens: p = 0, log
+ * probability -inf); a row of nothing but -inf gives logprob -inf, entropy 0
+ * and the tokens 0 .. top - 1 with -inf.  A row with NaN or +inf gives
+ * unspecified values (ids stay within [0, vocab) or are -1).
+ *
+ * Defined by: no passage of the source pages has a counterpart (FreeToken PR
+ * #636 serves the lm_head whose logits these are).
+ *
+ *   logits        device, [rows, vocab], rows row_stride elements apart
+ *                 (>= vocab); bf16, or fp32 if logits_f32 is non-zero;
+ *                 aligned to its element size
+ *   targets       device, [rows] int32; a negative target gives logprob 0,
+ *                 one >= vocab too, with bit 4 of the device error word
+ *   top           0..32, <= vocab (0: top_ids and top_logprobs may be NULL)
+ *   logprobs, entropy        device, [rows] fp32, written
+ *   top_ids, top_logprobs    device, [rows, top] int32 / fp32, written
+ */
+int fp8bs_token_logprobs(const void *logits, int logits_f32,
+                         int64_t row_stride, int64_t rows, int64_t vocab,
+                         const int32_t *targets, int64_t top, float *logprobs,
+                         float *entropy, int32_t *top_ids,
+                         float *top_logprobs, void *stream);
+
 /* Path FP8BS_PATH_AUTO would take for these shapes and pointers
  * (host-only, launches nothing).  `mx` selects the MXFP8 GEMV; the block,
  * per-row and per-tensor GEMVs share the same paths (mx = 0). */
@@ -525,7 +724,8 @@ const char *fp8bs_strerror(int status);
  * Defined by: no passage of the source pages (library infrastructure: the
  * bounded waits' failure report).  Beyond a status, the call hands back the
  * word itself (word_out) so that a caller can tell a wait expiry
- * (bits 0-3) from a bad index argument (bit 4).
+ * (bits 0-3) from a bad index argument (bit 4) and from a free list that
+ * ran out (bit 5).
  */
 int fp8bs_check_device_error(void *stream, uint32_t *word_out);
 
