@@ -44,7 +44,6 @@ Functions (names follow the C entry points):
 from __future__ import annotations
 
 import collections
-import contextlib
 import ctypes
 import os
 import threading
@@ -76,6 +75,8 @@ class Fp8bsError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libfp8bs.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -186,7 +187,7 @@ class _Args:
         import torch
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if numel is not None and t.numel() != numel:
             raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
@@ -195,6 +196,19 @@ class _Args:
 
     def check(self):
         first = self.items[0][1].device
+        good = first.type == "cuda"
+        for _, t, dtype, _ in self.items:
+            if t.device != first or t.dtype != dtype or not t.is_contiguous():
+                good = False
+                break
+        if not good:
+            self._refuse(first)
+        self.device = first
+        self.ptrs = {name: t.data_ptr() for name, t, _, _ in self.items}
+        return self
+
+    def _refuse(self, first):
+        """Raise for the first tensor that does not fit (none may: rows)."""
         for name, t, _, _ in self.items:
             if t.device != first:
                 raise ValueError(f"{name} is on {t.device}, the call's tensors on {first}")
@@ -205,20 +219,36 @@ class _Args:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             if not (t.is_contiguous() or (rows and t.numel() and t[0].is_contiguous())):
                 raise ValueError(f"{name} must be contiguous" + (" in all but its first dimension" if rows else ""))
-        self.device = first
-        self.ptrs = {name: ctypes.c_void_p(t.data_ptr()) for name, t, _, _ in self.items}
-        return self
 
     def ptr(self, name):
         return self.ptrs[name]
 
 
+def _raw_stream(stream, device):
+    """The cudaStream_t a call on `device` runs on."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on_device(device, what, fn, call_args, stream):
+    """fn(*call_args, stream) with `device` current."""
+    import torch
+    raw = _raw_stream(stream, device)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*call_args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*call_args, raw)
+    if status != 0:
+        _check(status, what)
+
+
 def _run(args: _Args, what: str, fn, *call_args, stream=None):
     """Call the library on the device of the call's tensors, on that
     device's current stream unless one is given."""
-    import torch
-    with torch.cuda.device(args.device):
-        _check(fn(*call_args, _stream(stream, args.device)), what)
+    _on_device(args.device, what, fn, call_args, stream)
 
 
 def _shape2(t, name):
@@ -322,7 +352,7 @@ def _batch_ops(ops, mx):
         elif a.device != device:
             raise ValueError(f"op {i} is on {a.device}, the batch on {device}")
         ys.append(y)
-        arr[i] = GemvOp(a.ptr("x").value, a.ptr("codes").value, a.ptr("scales").value, a.ptr("y").value, n, k)
+        arr[i] = GemvOp(a.ptr("x"), a.ptr("codes"), a.ptr("scales"), a.ptr("y"), n, k)
     return arr, m, ys, device
 
 
@@ -517,15 +547,16 @@ KvPlan = collections.namedtuple("KvPlan", "seq_lens cu_new slots positions reque
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs entropy top_ids top_logprobs")
 
 
-def _outputs_on(stream, like):
-    """Where a call makes its own outputs: in the memory pool of the stream
-    it runs on, so that their memory is not handed out again while it runs."""
+def _outputs(stream, device, make):
+    """make(), a call's own outputs: in the memory pool of the stream the call
+    runs on, so that their memory is not handed out again while it runs."""
     import torch
-    if stream is None or like.device.type != "cuda":
-        return contextlib.nullcontext()
+    if stream is None or device.type != "cuda":
+        return make()
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return make()
 
 
 def _row_stride(t):
@@ -546,24 +577,27 @@ def kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size: 
     rows, max_blocks = _shape2(block_table, "block_table")
     if rows != b:
         raise ValueError("block_table and ctx_lens disagree on the number of requests")
+    if num_tokens < 0:
+        raise ValueError("num_tokens must not be negative")
     i32 = torch.int32
-    with _outputs_on(stream, ctx_lens):
-        seq_lens = _new(seq_lens, (b,), i32, ctx_lens)
-        cu_new = _new(cu_new, (b + 1,), i32, ctx_lens)
-        slots = _new(slots, (num_tokens,), i32, ctx_lens)
-        positions = _new(positions, (num_tokens,), i32, ctx_lens)
-        requests = _new(requests, (num_tokens,), i32, ctx_lens)
-        free_head_out = _new(free_head_out, (1,), i32, ctx_lens)
     a = _Args().need("ctx_lens", ctx_lens, i32).need("new_lens", new_lens, i32, numel=b) \
         .need("block_table", block_table, i32).need("free_blocks", free_blocks, i32) \
-        .need("free_head", free_head, i32, numel=1).need("seq_lens", seq_lens, i32, numel=b) \
-        .need("cu_new", cu_new, i32, numel=b + 1).need("slots", slots, i32, numel=num_tokens) \
-        .need("positions", positions, i32, numel=num_tokens).need("requests", requests, i32, numel=num_tokens) \
-        .need("free_head_out", free_head_out, i32, numel=1).check()
+        .need("free_head", free_head, i32, numel=1)
+    outs = [slots, positions, requests, seq_lens, cu_new, free_head_out]
+    sizes = [num_tokens, num_tokens, num_tokens, b, b + 1, 1]
+    for name, t, n in zip(("slots", "positions", "requests", "seq_lens", "cu_new", "free_head_out"), outs, sizes):
+        if t is not None:
+            a.need(name, t, i32, numel=n)
+    a.check()
+    # one allocation holds every output the caller did not give
+    sizes = [n if t is None else 0 for t, n in zip(outs, sizes)]
+    own = _outputs(stream, a.device, lambda: torch.empty(sum(sizes), dtype=i32, device=a.device)).split(sizes)
+    outs = [o if t is None else t for t, o in zip(outs, own)]
+    p_slots, p_pos, p_req, p_seq, p_cu, p_head = [t.data_ptr() for t in outs]
     _run(a, "fp8bs_kv_plan", lib().fp8bs_kv_plan, a.ptr("ctx_lens"), a.ptr("new_lens"), b, a.ptr("block_table"),
          max_blocks, a.ptr("free_blocks"), free_blocks.numel(), a.ptr("free_head"), int(page_size), int(num_blocks),
-         int(num_tokens), a.ptr("seq_lens"), a.ptr("cu_new"), a.ptr("slots"), a.ptr("positions"), a.ptr("requests"),
-         a.ptr("free_head_out"), stream=stream)
+         int(num_tokens), p_seq, p_cu, p_slots, p_pos, p_req, p_head, stream=stream)
+    slots, positions, requests, seq_lens, cu_new, free_head_out = outs
     return KvPlan(seq_lens, cu_new, slots, positions, requests, free_head_out)
 
 
@@ -574,18 +608,15 @@ def kv4_cache_shape(num_blocks: int, page_size: int, num_kv_heads: int, head_dim
     return num_blocks, num_kv_heads, page_size // 16, 9 * head_dim
 
 
-def _kv4_caches(a, k_cache, v_cache, hkv, d):
-    """Check a pair of 4-bit caches; returns (num_blocks, page_size)."""
+def _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d):
+    """Records a pair of 4-bit caches and their scales; returns the _Args, num_blocks and page_size."""
     import torch
-    if k_cache.dim() != 4 or tuple(k_cache.shape[1::2]) != (hkv, 9 * d):
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [num_blocks, {hkv}, page_size / 16, {9 * d}]")
-    a.need("k_cache", k_cache, torch.uint8).need("v_cache", v_cache, torch.uint8, shape=k_cache.shape)
-    return k_cache.shape[0], k_cache.shape[2] * 16
-
-
-def _kv4_scales(a, k_scale, v_scale):
-    import torch
-    return a.need("k_scale", k_scale, torch.float32, numel=1).need("v_scale", v_scale, torch.float32, numel=1)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != hkv or shape[3] != 9 * d:
+        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [num_blocks, {hkv}, page_size / 16, {9 * d}]")
+    a = _Args().need("k_cache", k_cache, torch.uint8).need("v_cache", v_cache, torch.uint8, shape=shape) \
+        .need("k_scale", k_scale, torch.float32, numel=1).need("v_scale", v_scale, torch.float32, numel=1)
+    return a, shape[0], shape[2] * 16
 
 
 def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
@@ -596,10 +627,9 @@ def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
     if k.dim() != 3:
         raise ValueError("k must be [T, Hkv, D]")
     t, hkv, d = k.shape
-    a = _Args().need("k", k, torch.bfloat16, rows=True).need("v", v, torch.bfloat16, shape=k.shape, rows=True) \
-        .need("slots", slots, torch.int32, numel=t)
-    nb, page = _kv4_caches(a, k_cache, v_cache, hkv, d)
-    _kv4_scales(a, k_scale, v_scale).check()
+    a, nb, page = _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d)
+    a.need("k", k, torch.bfloat16, rows=True).need("v", v, torch.bfloat16, shape=k.shape, rows=True) \
+        .need("slots", slots, torch.int32, numel=t).check()
     _run(a, "fp4kv_append", lib().fp4kv_append, a.ptr("k"), _row_stride(k), a.ptr("v"), _row_stride(v), t, hkv, d,
          a.ptr("slots"), a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("k_cache"), a.ptr("v_cache"), page, nb,
          stream=stream)
@@ -612,16 +642,17 @@ def kv4_gather(k_cache, v_cache, slots, k_scale, v_scale, k=None, v=None, stream
     if k_cache.dim() != 4 or k_cache.shape[3] % 9 != 0:
         raise ValueError("k_cache must be [num_blocks, Hkv, page_size / 16, 9 * D]")
     t, hkv, d = slots.numel(), k_cache.shape[1], k_cache.shape[3] // 9
-    with _outputs_on(stream, k_cache):
-        k = _new(k, (t, hkv, d), torch.bfloat16, k_cache)
-        v = _new(v, (t, hkv, d), torch.bfloat16, k_cache)
-    a = _Args()
-    nb, page = _kv4_caches(a, k_cache, v_cache, hkv, d)
-    a.need("slots", slots, torch.int32).need("k", k, torch.bfloat16, numel=t * hkv * d) \
-        .need("v", v, torch.bfloat16, numel=t * hkv * d)
-    _kv4_scales(a, k_scale, v_scale).check()
+    a, nb, page = _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d)
+    a.need("slots", slots, torch.int32)
+    for name, x in (("k", k), ("v", v)):
+        if x is not None:
+            a.need(name, x, torch.bfloat16, numel=t * hkv * d)
+    a.check()
+    make = lambda: torch.empty((t, hkv, d), dtype=torch.bfloat16, device=a.device)
+    k = _outputs(stream, a.device, make) if k is None else k
+    v = _outputs(stream, a.device, make) if v is None else v
     _run(a, "fp4kv_gather", lib().fp4kv_gather, a.ptr("k_cache"), a.ptr("v_cache"), a.ptr("slots"), t, hkv, d, page,
-         nb, a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("k"), a.ptr("v"), stream=stream)
+         nb, a.ptr("k_scale"), a.ptr("v_scale"), k.data_ptr(), v.data_ptr(), stream=stream)
     return k, v
 
 
@@ -657,25 +688,25 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
     if bt_rows != b or (cu_q is None and t != b):
         raise ValueError("q, block_table and seq_lens disagree on the number of sequences")
     hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
-    with _outputs_on(stream, q):
-        out = _new(out, (t, hq, d), torch.bfloat16, q)
-        if return_lse:
-            lse = _new(lse, (t, hq), torch.float32, q)
-    a = _Args().need("q", q, torch.bfloat16, rows=True)
-    nb, page = _kv4_caches(a, k_cache, v_cache, hkv, d)
-    _kv4_scales(a, k_scale, v_scale).need("block_table", block_table, torch.int32) \
-        .need("seq_lens", seq_lens, torch.int32).need("out", out, torch.bfloat16, numel=t * hq * d) \
-        .need("workspace", workspace, torch.uint8)
+    a, nb, page = _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d)
+    a.need("q", q, torch.bfloat16, rows=True).need("block_table", block_table, torch.int32) \
+        .need("seq_lens", seq_lens, torch.int32).need("workspace", workspace, torch.uint8)
     if cu_q is not None:
         a.need("cu_q", cu_q, torch.int32, numel=b + 1)
+    if out is not None:
+        a.need("out", out, torch.bfloat16, numel=t * hq * d)
     if lse is not None:
         a.need("lse", lse, torch.float32, numel=t * hq)
     a.check()
+    if out is None:
+        out = _outputs(stream, a.device, lambda: torch.empty((t, hq, d), dtype=torch.bfloat16, device=a.device))
+    if lse is None and return_lse:
+        lse = _outputs(stream, a.device, lambda: torch.empty((t, hq), dtype=torch.float32, device=a.device))
     _run(a, "fp4kv_decode_attention", lib().fp4kv_decode_attention, a.ptr("q"), _row_stride(q),
          a.ptr("cu_q") if cu_q is not None else None, t, int(max_q), a.ptr("k_cache"), a.ptr("v_cache"),
          a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("block_table"), max_blocks, a.ptr("seq_lens"), b, hq, hkv, d,
-         page, nb, int(max_seq_len), int(window), float(sm_scale), a.ptr("out"),
-         a.ptr("lse") if lse is not None else None, a.ptr("workspace"), workspace.numel(), stream=stream)
+         page, nb, int(max_seq_len), int(window), float(sm_scale), out.data_ptr(),
+         lse.data_ptr() if lse is not None else None, a.ptr("workspace"), workspace.numel(), stream=stream)
     return (out, lse) if return_lse else out
 
 
@@ -686,19 +717,22 @@ def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, t
     (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
     import torch
     m, v = _shape2(logits, "logits")
-    with _outputs_on(stream, logits):
-        logprobs = _new(logprobs, (m,), torch.float32, logits)
-        entropy = _new(entropy, (m,), torch.float32, logits)
-        top_ids = _new(top_ids, (m, top), torch.int32, logits)
-        top_logprobs = _new(top_logprobs, (m, top), torch.float32, logits)
     f32 = logits.dtype == torch.float32
     a = _Args().need("logits", logits, torch.float32 if f32 else torch.bfloat16, rows=True) \
-        .need("targets", targets, torch.int32, numel=m).need("logprobs", logprobs, torch.float32, numel=m) \
-        .need("entropy", entropy, torch.float32, numel=m).need("top_ids", top_ids, torch.int32, numel=m * top) \
-        .need("top_logprobs", top_logprobs, torch.float32, numel=m * top).check()
+        .need("targets", targets, torch.int32, numel=m)
+    outs = [logprobs, entropy, top_logprobs, top_ids]
+    shapes = [(m,), (m,), (m, top), (m, top)]
+    dtypes = [torch.float32, torch.float32, torch.float32, torch.int32]
+    for name, t, shape, dtype in zip(("logprobs", "entropy", "top_logprobs", "top_ids"), outs, shapes, dtypes):
+        if t is not None:
+            a.need(name, t, dtype, numel=m if len(shape) == 1 else m * top)
+    a.check()
+    outs = [_outputs(stream, a.device, lambda: torch.empty(shape, dtype=dtype, device=a.device)) if t is None else t
+            for t, shape, dtype in zip(outs, shapes, dtypes)]
+    logprobs, entropy, top_logprobs, top_ids = outs
     _run(a, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs, a.ptr("logits"), int(f32),
-         max(_row_stride(logits), v), m, v, a.ptr("targets"), int(top), a.ptr("logprobs"), a.ptr("entropy"),
-         a.ptr("top_ids"), a.ptr("top_logprobs"), stream=stream)
+         max(_row_stride(logits), v), m, v, a.ptr("targets"), int(top), logprobs.data_ptr(), entropy.data_ptr(),
+         top_ids.data_ptr(), top_logprobs.data_ptr(), stream=stream)
     return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
 
 

@@ -555,9 +555,11 @@ int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride, const int32_t *
         return FP8BS_ERR_SHAPE;
     if (num_q_heads <= 0 || num_q_heads >= 65536 || num_q_heads % num_kv_heads != 0) return FP8BS_ERR_SHAPE;
     if (!cu_q && (num_q_tokens != batch || max_q != 1)) return FP8BS_ERR_SHAPE;
+    if (max_q * (num_q_heads / num_kv_heads) >= kMaxDim || num_q_tokens * num_q_heads >= (int64_t{1} << 40))
+        return FP8BS_ERR_SHAPE;
     if (max_blocks_per_seq <= 0 || max_blocks_per_seq >= kMaxDim || max_blocks_per_seq * page_size >= kMaxDim)
         return FP8BS_ERR_SHAPE;
-    if (max_seq_len < 0 || max_seq_len > max_blocks_per_seq * page_size || window < 0 || window >= kMaxDim)
+    if (max_seq_len < 0 || max_seq_len > max_blocks_per_seq * page_size || max_seq_len > kMaxDim - 64 || window < 0 || window >= kMaxDim)
         return FP8BS_ERR_SHAPE;
     if (!stride_ok(q_stride, num_q_heads * head_dim)) return FP8BS_ERR_SHAPE;
     if (!(sm_scale == sm_scale) || sm_scale > 3.0e38f || sm_scale < -3.0e38f) return FP8BS_ERR_SHAPE;

@@ -17,18 +17,14 @@
 #include "common.cuh"
 #include "internal.h"
 
+#include <mutex>
+
 namespace fp8bs {
 
 namespace {
 
 __device__ uint32_t g_kv4_err;
 
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 
 // The tile that holds slot `slot` of kv head `h`.
 __device__ __forceinline__ int64_t tile_index(int64_t slot, int h, int kv_heads, int page_size) {
@@ -128,82 +124,696 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a)
 }
 
 // --------------------------------------------------------------- attention
+// Query token i of the n_q tokens of a sequence of len keys stands at
+// position len - n_q + i and sees the keys up to its own (of those, the
+// newest `window`, if there is one).  With the log2-domain scores
+// s = sm_scale log2(e) q.k, a running maximum m and p = 2^(s - m + 14):
+//   l = sum p,  o = sum p v,  out = o / l,  lse = ln 2 (m - 14 + log2 l);
+// the 2^14 keeps weights down to 2^-39 of the largest out of f16's zero.
+//
+// Work: a segment is one (sequence, kv head, tile of R = 8 NT query rows); a
+// row is a (query token, head of the group) pair, so a K/V byte is read once
+// for R rows.  A unit is 32 keys of a segment.  The CTAs cut the line of all
+// units of all segments into equal shares (every CTA finds its own from a
+// prefix sum of the lengths), so a ragged batch fills the GPU evenly and a
+// single long sequence is spread over all of it.  A segment that crosses a
+// share's end leaves partial (m, l, o) records in the workspace, which
+// kv4_combine_kernel joins in the order of the CTAs.
+//
+// A CTA is one producer warp, which copies the units' tiles (one bulk copy of
+// 9 D bytes each) into a ring, and W consumer warps, which take units in turn:
+//   S^T[32 keys, R rows] = K q^T with f16 mma.sync m16n8k16.  The order of
+//   the contraction is free: lane t of a quad takes elements 32 t .. 32 t + 31
+//   of a key (D = 128), so its codes are one 16-byte load; codes convert to
+//   f16 exactly and are multiplied with their f16 scale exactly.
+//   O^T[D, R] += V^T P^T: row group g of the product is 16 consecutive
+//   elements, column pair t the keys kv4_row(t, j), so a lane's codes are 8
+//   bytes of each of four keys; two keys' values are interleaved by byte
+//   permutes.  P^T comes from the S^T fragments by movmatrix, because key m
+//   of S^T is key m of the product.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPShift = 14.0f;
+constexpr int kUnitTiles = 2;
+constexpr int kUnitKeys = kUnitTiles * kKv4Tile;
+constexpr int kMinUnits = 4;  // per CTA at least: one per warp or so
+constexpr int kMaxSms = 160;  // CTAs the workspace has records for: two per SM of 16 rows, or one of 32
 
-// One warp per (query token, query head): a key at a time, the head's D
-// elements over the lanes, an online softmax.  Query token i of the n_q
-// tokens of a sequence of len keys stands at position len - n_q + i and sees
-// the keys up to its own (of those, the newest `window`, if there is one).
-__global__ void __launch_bounds__(32) kv4_attn_kernel(Kv4AttnArgs a) {
-    const int lane = threadIdx.x;
-    const int b = blockIdx.z, h = blockIdx.y, i = blockIdx.x;
-    const int d = static_cast<int>(a.head_dim), per = d / 32;
-    const int hkv = static_cast<int>(a.kv_heads), kvh = h / static_cast<int>(a.q_heads / a.kv_heads);
-    pdl_wait();
-    int64_t first = b, n_q = 1;
+// W consumer warps and a ring of S units per CTA, RES CTAs per SM.
+template <int D, int NT>
+struct AttnCfg {
+    static constexpr int kRes = NT <= 2 ? 2 : 1;
+    static constexpr int W = NT == 2 ? 5 : 7;
+    static constexpr int S = NT == 2 ? 12 : 16;
+    static constexpr int kThreads = (W + 1) * 32;
+    static constexpr int R = 8 * NT;
+    static constexpr int kTileBytes = 9 * D;
+    static constexpr int kStageBytes = 2 * kUnitTiles * kTileBytes;
+    static constexpr int kRecFloats = R * (D + 2);  // m[R], l[R], o[R][D]
+    static constexpr int kSmemBytes = S * kStageBytes + W * kRecFloats * 4 + S * (8 + 8 + 4);
+    static_assert(kSmemBytes * kRes <= 226 * 1024, "shared memory per SM");
+};
+
+// One split segment, left by the CTA that holds its first part.
+struct SplitDesc {
+    int32_t last;     // last CTA of the segment; -1: none starts here
+    int32_t q0;       // first query token of the sequence
+    int32_t rows;     // rows of the tile
+    int32_t row0;     // first row of the tile
+    int32_t kvh;
+    int32_t pad[3];
+};
+
+// One sequence's share of the line of units.
+struct SeqWork {
+    int32_t len, q0, n_q;
+    int32_t tile0, tiles;  // first tile any row sees, end of the last
+    int32_t units, row_tiles;
+    uint32_t err;
+};
+
+template <int R>
+__device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int group) {
+    SeqWork w;
+    w.err = 0;
+    w.q0 = b;
+    w.n_q = 1;
     if (a.cu_q) {
-        first = a.cu_q[b];
-        n_q = static_cast<int64_t>(a.cu_q[b + 1]) - first;
+        const int64_t q0 = __ldg(a.cu_q + b), n = static_cast<int64_t>(__ldg(a.cu_q + b + 1)) - q0;
+        if (q0 < 0 || n < 0 || n > a.max_q || q0 + n > a.tokens) {
+            w.err = ERRBIT_INDEX;
+            w.n_q = 0;
+        } else {
+            w.n_q = static_cast<int32_t>(n);
+        }
+        w.q0 = static_cast<int32_t>(q0);
     }
-    if (n_q < 0 || n_q > a.max_q || first < 0 || first + n_q > a.tokens) {
-        if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_INDEX);
+    const int32_t len = __ldg(a.seq_lens + b), cap = static_cast<int32_t>(a.max_seq_len);
+    if (len < 0 || len > cap) w.err = ERRBIT_INDEX;
+    w.len = min(max(len, 0), cap);
+    const int64_t lo = a.window > 0 ? static_cast<int64_t>(w.len) - w.n_q - a.window + 1 : 0;
+    w.tiles = (w.len + kKv4Tile - 1) / kKv4Tile;
+    w.tile0 = lo > 0 ? static_cast<int32_t>(lo / kKv4Tile) : 0;
+    w.units = max(1, (w.tiles - w.tile0 + kUnitTiles - 1) / kUnitTiles);
+    w.row_tiles = (w.n_q * group + R - 1) / R;
+    return w;
+}
+
+// A CTA's walk along its share: pieces of segments, in order.
+template <int R>
+struct Walk {
+    SeqWork w;
+    int b;
+    int64_t p, left;  // next unit of sequence b, units left in the share
+    int kvh, row0;    // of the piece
+    int u0, u1;       // its units
+    __device__ __forceinline__ bool next(const Kv4AttnArgs &a, int hkv, int group) {
+        if (left <= 0) return false;
+        while (true) {
+            if (b >= a.batch) return false;
+            w = seq_work<R>(a, b, group);
+            const int64_t work = static_cast<int64_t>(w.units) * hkv * w.row_tiles;
+            if (p < work) break;
+            p -= work;  // the sequence is done, or has no rows
+            ++b;
+        }
+        const int64_t seg = p / w.units;
+        u0 = static_cast<int>(p - seg * w.units);
+        u1 = static_cast<int>(min(static_cast<int64_t>(w.units), u0 + left));
+        kvh = static_cast<int>(seg / w.row_tiles);
+        row0 = static_cast<int>(seg - static_cast<int64_t>(kvh) * w.row_tiles) * R;
+        p += u1 - u0;
+        left -= u1 - u0;
+        return true;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ void bar_consumers(int threads) {
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+
+// Key of a tile that is row m (and m + 8) of the score product, and column
+// pair t, half j of the value product: neighbouring m differ in parity, so
+// the 16-byte loads of eight lanes (two keys of 64 bytes) meet no bank twice.
+__device__ __forceinline__ int kv4_row(int m) { return (m & 1) ? 4 + ((m >> 1) ^ 1) : m >> 1; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes)
+    kv4_attn_kernel(const Kv4AttnArgs a, int min_units) {
+    using C = AttnCfg<D, NT>;
+    constexpr int W = C::W, S = C::S, R = C::R, T = C::kTileBytes;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *ring = smem;                                              // [S][K tiles | V tiles]
+    float *merge = reinterpret_cast<float *>(ring + S * C::kStageBytes);  // [W] records
+    uint64_t *full = reinterpret_cast<uint64_t *>(merge + W * C::kRecFloats);
+    uint64_t *empty = full + S;
+    int32_t *valid = reinterpret_cast<int32_t *>(empty + S);           // tiles a stage holds, one bit each
+    __shared__ int64_t s_sums[W + 1], s_p;
+    __shared__ int s_b;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hkv = static_cast<int>(a.kv_heads), group = static_cast<int>(a.q_heads / a.kv_heads);
+    const int batch = static_cast<int>(a.batch), cta = blockIdx.x;
+    SplitDesc *desc = reinterpret_cast<SplitDesc *>(a.workspace);
+    float *records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + 2 * kMaxSms * sizeof(SplitDesc));
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        fence_mbarrier_init();
+    }
+    pdl_launch_dependents();  // the combine kernel waits for the end of this grid
+    pdl_wait();               // q, the cache and the lengths may come from the previous kernel
+
+    // ---- this CTA's share
+    const int per = (batch + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(batch, tid * per), b1 = min(batch, b0 + per);
+    int64_t mine = 0;
+    uint32_t err = 0;
+    for (int b = b0; b < b1; ++b) {
+        const SeqWork w = seq_work<R>(a, b, group);
+        err |= w.err;
+        mine += static_cast<int64_t>(w.units) * hkv * w.row_tiles;
+    }
+    if (err && cta == 0) atomicOr(&g_kv4_err, err);
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sums[warp] = x;
+    __syncthreads();
+    int64_t total = 0, before = x - mine;
+#pragma unroll
+    for (int w = 0; w <= W; ++w) {
+        if (w < warp) before += s_sums[w];
+        total += s_sums[w];
+    }
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + min_units - 1) / min_units);
+    if (tid == 0) desc[cta].last = -1;
+    if (cta >= ctas) return;
+    const int64_t lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
+    if (lo >= before && lo < before + mine) {
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+            const SeqWork w = seq_work<R>(a, b, group);
+            const int64_t work = static_cast<int64_t>(w.units) * hkv * w.row_tiles;
+            if (lo < at + work) {
+                s_b = b;
+                s_p = lo - at;
+                break;
+            }
+            at += work;
+        }
+    }
+    __syncthreads();
+    Walk<R> walk;
+    walk.b = s_b;
+    walk.p = s_p;
+    walk.left = hi - lo;
+
+    if (warp == W) {
+        // ================================================== producer
+        const int tpp = static_cast<int>(a.page_size) / kKv4Tile;
+        int stage = 0;
+        uint32_t round = 0;  // how often the ring has wrapped
+        bool ok = true;
+        err = 0;
+        while (ok && walk.next(a, hkv, group)) {
+            const int32_t *trow = a.block_table + static_cast<int64_t>(walk.b) * a.max_blocks;
+            for (int ub = walk.u0; ok && ub < walk.u1; ub += 32 / kUnitTiles) {
+                // lane j: tile j of the next 16 units
+                const int n = min(32 / kUnitTiles, walk.u1 - ub);
+                const int tile = walk.w.tile0 + ub * kUnitTiles + lane;
+                const bool inside = lane < n * kUnitTiles && tile < walk.w.tiles;
+                const int pg = tile / tpp;
+                const int32_t blk = inside ? __ldg(trow + pg) : -1;
+                const bool have = inside && blk >= 0 && blk < a.num_blocks;
+                if (inside && !have) err = ERRBIT_INDEX;
+                const int64_t off =
+                    have ? ((static_cast<int64_t>(blk) * hkv + walk.kvh) * tpp + (tile - pg * tpp)) * T : 0;
+                const uint32_t haves = __ballot_sync(0xffffffffu, have);
+                for (int i = 0; i < n; ++i) {
+                    if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], (round - 1) & 1));
+                    if (!ok) break;
+                    const uint32_t mask = (haves >> (i * kUnitTiles)) & ((1u << kUnitTiles) - 1);
+                    if (lane == 0) {
+                        valid[stage] = static_cast<int32_t>(mask);
+                        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(__popc(mask) * 2 * T));
+                    }
+                    __syncwarp();
+                    if (lane / kUnitTiles == i && have) {
+                        uint8_t *dst = ring + stage * C::kStageBytes + (lane % kUnitTiles) * T;
+                        bulk_load_g2s(dst, a.k_cache + off, T, &full[stage]);
+                        bulk_load_g2s(dst + kUnitTiles * T, a.v_cache + off, T, &full[stage]);
+                    }
+                    if (++stage == S) stage = 0, ++round;
+                }
+            }
+        }
+        if (err) atomicOr(&g_kv4_err, err);
+        if (!ok) {  // a consumer gave up: never leave with copies in flight
+            if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_EMPTY_WAIT);
+            for (int i = 0; i < S; ++i) {
+                if (i < stage) (void)mbar_wait_bounded(&full[i], round & 1);
+                else (void)mbar_wait_bounded(&full[i], (round - 1) & 1);
+            }
+        }
         return;
     }
-    if (i >= n_q) return;
-    const int64_t cap = a.max_seq_len;
-    int64_t len = a.seq_lens[b];
-    if (len < 0 || len > cap) {
-        if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_INDEX);
-        len = len < 0 ? 0 : cap;
+
+    // ==================================================== consumers
+    const int g = lane >> 2, t = lane & 3;
+    const float base = a.sm_scale * __ldg(a.k_scale) * kLog2e;
+    const float v_scale = __ldg(a.v_scale);
+    constexpr int kLaneCodes = D / 4;   // codes of a key a lane holds for S^T
+    constexpr int kSteps = D / 16;
+    int turn = 0, stage = 0;            // whose unit is next, and where it is
+    uint32_t round = 0;
+    bool failed = false;
+
+    while (walk.next(a, hkv, group)) {
+        const int rows = walk.w.n_q * group - walk.row0;  // rows left of the sequence (some may be other tiles')
+        const int first_pos = walk.w.len - walk.w.n_q;    // position of query token 0
+
+        // ---- q as f16 B fragments, an exact power-of-two rescale per row
+        uint32_t bq[NT][kSteps][2];
+        float sc[NT][2];   // score scale of this lane's columns 2t, 2t + 1
+        int pos[NT][2];    // their positions
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = n * 8 + g;
+            const bool live = r < rows;
+            const int tok = live ? (walk.row0 + r) / group : 0, h = live ? walk.row0 + r - tok * group : 0;
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
+                                       static_cast<int64_t>(walk.w.q0 + tok) * a.q_stride +
+                                       (walk.kvh * group + h) * D + t * kLaneCodes;
+            uint4 v[kLaneCodes / 8];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < kLaneCodes / 8; ++i) {
+                v[i] = live ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+                mx = max_u16x2(max_u16x2(max_u16x2(mx, v[i].x & 0x7FFF7FFFu), v[i].y & 0x7FFF7FFFu),
+                               max_u16x2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+            }
+            uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
+            m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 1));
+            m16 = max(m16, __shfl_xor_sync(0xffffffffu, m16, 2));
+            const int e = f16_rescale_exp(m16);
+            const float up = pow2_int(e), down = pow2_int(-e);
+#pragma unroll
+            for (int i = 0; i < kLaneCodes / 8; ++i) {
+                bq[n][2 * i][0] = f32x2_to_f16x2(bf16lo_to_f32(v[i].x) * up, bf16hi_to_f32(v[i].x) * up);
+                bq[n][2 * i][1] = f32x2_to_f16x2(bf16lo_to_f32(v[i].y) * up, bf16hi_to_f32(v[i].y) * up);
+                bq[n][2 * i + 1][0] = f32x2_to_f16x2(bf16lo_to_f32(v[i].z) * up, bf16hi_to_f32(v[i].z) * up);
+                bq[n][2 * i + 1][1] = f32x2_to_f16x2(bf16lo_to_f32(v[i].w) * up, bf16hi_to_f32(v[i].w) * up);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sc[n][c] = base * __shfl_sync(0xffffffffu, down, 8 * t + 4 * c);
+                pos[n][c] = first_pos + __shfl_sync(0xffffffffu, tok, 8 * t + 4 * c);
+            }
+        }
+        // keys below `clear_hi` and from `clear_lo` on are seen by every row of the tile
+        const int last_tok = min(walk.row0 + R - 1, walk.w.n_q * group - 1) / group;
+        const int clear_hi = first_pos + walk.row0 / group + 1;
+        const int64_t clear_lo = a.window > 0 ? static_cast<int64_t>(first_pos) + last_tok - a.window + 1 : 0;
+
+        float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) m_run[n][c] = -INFINITY, l_run[n][c] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
+        }
+
+        for (int u = walk.u0; u < walk.u1; ++u) {
+            const bool my_turn = turn == warp;
+            if (++turn == W) turn = 0;
+            const int st = stage;
+            const uint32_t parity = round & 1;
+            if (++stage == S) stage = 0, ++round;
+            if (!my_turn || failed) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], parity))) {
+                if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_FULL_WAIT);
+                failed = true;
+                continue;
+            }
+            const uint32_t have = static_cast<uint32_t>(valid[st]);
+            const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + kUnitTiles * T;
+            const int key0 = (walk.w.tile0 + u * kUnitTiles) * kKv4Tile;
+
+            // ---- S^T: lane holds keys kv4_row(g), + 8 of each tile, rows 2t, 2t + 1 of each n
+            float s[kUnitTiles][NT][4];
+#pragma unroll
+            for (int h = 0; h < kUnitTiles; ++h) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[h][n][j] = 0.0f;
+                uint32_t f[2][kSteps * 2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int row = kv4_row(g) + 8 * q;
+                    const uint8_t *src = kt + h * T + row * (D / 2) + t * (kLaneCodes / 2);
+                    if constexpr (D == 128) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                        const uint32_t sb = *reinterpret_cast<const uint16_t *>(kt + h * T + 8 * D + row * 8 + 2 * t);
+                        const uint32_t s2 = e4m3x2_to_f16x2(sb);
+                        const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
+                        uint32_t c[4];
+                        e2m1x8_to_f16x2x4(w.x, c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[q][i] = mul_f16x2(c[i], sl);
+                        e2m1x8_to_f16x2x4(w.y, c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[q][4 + i] = mul_f16x2(c[i], sl);
+                        e2m1x8_to_f16x2x4(w.z, c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[q][8 + i] = mul_f16x2(c[i], sh);
+                        e2m1x8_to_f16x2x4(w.w, c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[q][12 + i] = mul_f16x2(c[i], sh);
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                        const uint32_t sb = kt[h * T + 8 * D + row * 4 + t];
+                        const uint32_t sl = e4m3x2_to_f16x2(sb | (sb << 8));
+                        uint32_t c[4];
+                        e2m1x8_to_f16x2x4(w.x, c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[q][i] = mul_f16x2(c[i], sl);
+                        e2m1x8_to_f16x2x4(w.y, c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[q][4 + i] = mul_f16x2(c[i], sl);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_f16_16816(s[h][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1],
+                                      bq[n][i][0], bq[n][i][1]);
+            }
+#pragma unroll
+            for (int h = 0; h < kUnitTiles; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[h][n][j] *= sc[n][j & 1];
+            if (have != (1u << kUnitTiles) - 1 || key0 + kUnitKeys > clear_hi || key0 < clear_lo) {
+#pragma unroll
+                for (int h = 0; h < kUnitTiles; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = key0 + h * kKv4Tile + kv4_row(g) + 8 * (j >> 1);
+                            const int p = pos[n][j & 1];
+                            const bool seen = ((have >> h) & 1) && key <= p && (a.window == 0 || key > p - a.window);
+                            if (!seen) s[h][n][j] = -INFINITY;
+                        }
+            }
+
+            // ---- online softmax per row over the unit's keys
+            float mt[NT][2];
+            bool grows = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = fmaxf(s[0][n][c], s[0][n][c + 2]);
+#pragma unroll
+                    for (int h = 1; h < kUnitTiles; ++h) v = fmaxf(v, fmaxf(s[h][n][c], s[h][n][c + 2]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                    mt[n][c] = v;
+                    grows |= v > m_run[n][c];
+                }
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float al[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float mn = fmaxf(m_run[n][c], mt[n][c]);
+                        al[c] = mn == -INFINITY ? 1.0f : ex2(m_run[n][c] - mn);
+                        m_run[n][c] = mn;
+                        l_run[n][c] *= al[c];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        o[n][i][0] *= al[0];
+                        o[n][i][1] *= al[1];
+                        o[n][i][2] *= al[0];
+                        o[n][i][3] *= al[1];
+                    }
+                }
+            }
+            uint32_t pb[kUnitTiles][NT][2];  // P^T as B fragments: keys 2t, 2t + 1 (+ 8) of the tile, row g
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float ref[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) ref[c] = m_run[n][c] == -INFINITY ? 0.0f : m_run[n][c] - kPShift;
+#pragma unroll
+                for (int h = 0; h < kUnitTiles; ++h) {
+                    float p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[j] = ex2(s[h][n][j] - ref[j & 1]);
+                    l_run[n][0] += p[0] + p[2];
+                    l_run[n][1] += p[1] + p[3];
+                    pb[h][n][0] = transpose8x8(f32x2_to_f16x2(p[0], p[1]));
+                    pb[h][n][1] = transpose8x8(f32x2_to_f16x2(p[2], p[3]));
+                }
+            }
+
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int h = 0; h < kUnitTiles; ++h) {
+                if (!((have >> h) & 1)) continue;  // never copied
+                uint32_t sb[4], w[4][D / 64];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = kv4_row(2 * t + (j & 1)) + 8 * (j >> 1);
+                    const uint8_t *src = vt + h * T + row * (D / 2) + g * (D / 16);
+                    if constexpr (D == 128) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                        w[j][0] = v.x;
+                        w[j][1] = v.y;
+                    } else {
+                        w[j][0] = *reinterpret_cast<const uint32_t *>(src);
+                    }
+                    sb[j] = vt[h * T + 8 * D + row * (D / 16) + g * D / 128];
+                    // keys past the end have weight 0, but old bytes there may be NaN
+                    if (key0 + h * kKv4Tile + row >= walk.w.len) sb[j] = 0;
+                }
+                const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    uint32_t f0[4], f1[4], f2[4], f3[4];
+                    e2m1x8_to_f16x2x4(w[0][q], f0);
+                    e2m1x8_to_f16x2x4(w[1][q], f1);
+                    e2m1x8_to_f16x2x4(w[2][q], f2);
+                    e2m1x8_to_f16x2x4(w[3][q], f3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = mul_f16x2(__byte_perm(f0[i], f1[i], 0x5410), s01);
+                        const uint32_t a1 = mul_f16x2(__byte_perm(f0[i], f1[i], 0x7632), s01);
+                        const uint32_t a2 = mul_f16x2(__byte_perm(f2[i], f3[i], 0x5410), s23);
+                        const uint32_t a3 = mul_f16x2(__byte_perm(f2[i], f3[i], 0x7632), s23);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16_16816(o[n][q * 4 + i], a0, a1, a2, a3, pb[h][n][0], pb[h][n][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+
+        // ---- the warps' parts of the piece: m[R], l[R], o[R][D] each
+        float *rec = merge + warp * C::kRecFloats;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[n][c];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                const int r = n * 8 + 2 * t + c;
+                if (g == 0) {
+                    rec[r] = m_run[n][c];
+                    rec[R + r] = l;
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+                    *reinterpret_cast<float2 *>(rec + 2 * R + r * D + g * (D / 8) + 2 * i) =
+                        make_float2(o[n][i][c], o[n][i][c + 2]);
+            }
+        bar_consumers(W * 32);
+        const bool starts = walk.u0 == 0, ends = walk.u1 == walk.w.units;
+        float *out_rec = records + static_cast<int64_t>(2 * cta + (starts ? 1 : 0)) * C::kRecFloats;
+        for (int e = tid; e < R * D / 4; e += W * 32) {
+            const int r = e / (D / 4), d4 = e - r * (D / 4);
+            if (r >= rows) break;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w) M = fmaxf(M, merge[w * C::kRecFloats + r]);
+            float L = 0.0f;
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float *src = merge + w * C::kRecFloats;
+                const float mw = src[r];
+                if (mw == -INFINITY) continue;
+                const float f = ex2(mw - M);
+                const float4 v = *reinterpret_cast<const float4 *>(src + 2 * R + r * D + d4 * 4);
+                L += f * src[R + r];
+                O.x += f * v.x, O.y += f * v.y, O.z += f * v.z, O.w += f * v.w;
+            }
+            if (starts && ends) {
+                const int tok = (walk.row0 + r) / group, h = walk.row0 + r - tok * group;
+                const int64_t row = static_cast<int64_t>(walk.w.q0 + tok) * a.q_heads + walk.kvh * group + h;
+                const float inv = L > 0.0f ? v_scale / L : 0.0f;
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d4 * 4) =
+                    make_uint2(f32x2_to_bf16x2(O.x * inv, O.y * inv), f32x2_to_bf16x2(O.z * inv, O.w * inv));
+                if (a.lse && d4 == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+            } else {
+                if (d4 == 0) {
+                    out_rec[r] = M;
+                    out_rec[R + r] = L;
+                }
+                *reinterpret_cast<float4 *>(out_rec + 2 * R + r * D + d4 * 4) = O;
+            }
+        }
+        if (starts && !ends && tid == 0) {  // the share's last piece: where the segment ends
+            const int64_t seg_end = hi + (walk.w.units - walk.u1);
+            SplitDesc *sd = desc + cta;
+            sd->q0 = walk.w.q0;
+            sd->rows = min(rows, R);
+            sd->row0 = walk.row0;
+            sd->kvh = walk.kvh;
+            sd->last = static_cast<int32_t>((seg_end * ctas + total - 1) / total - 1);
+        }
+        bar_consumers(W * 32);  // the records are free again
     }
-    const int64_t row = first + i;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + row * a.q_stride + static_cast<int64_t>(h) * d;
-    const float ks = *a.k_scale, vs = *a.v_scale;
-    float qv[4], o[4] = {};
-    for (int e = 0; e < per; ++e) qv[e] = __bfloat162float(q[lane * per + e]);
-    float m = -INFINITY, l = 0.0f;
-    const int64_t last = len - n_q + i;
-    const int64_t from = a.window > 0 && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
-    for (int64_t j = from; j <= last; ++j) {
-        const int32_t blk = a.block_table[b * a.max_blocks + j / a.page_size];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_INDEX);
-            continue;
-        }
-        const int64_t slot = static_cast<int64_t>(blk) * a.page_size + j % a.page_size;
-        const int64_t off = tile_index(slot, kvh, hkv, static_cast<int>(a.page_size)) * kv4_tile_bytes(d);
-        const int r = static_cast<int>(slot & (kKv4Tile - 1));
-        const uint8_t *kt = a.k_cache + off, *vt = a.v_cache + off;
-        const int cb = r * (d / 2) + lane * per / 2, sb = 8 * d + r * (d / 16) + lane * per / 16;
-        uint32_t kw = 0, vw = 0;
-        for (int e = 0; e < per / 2; ++e) {
-            kw |= static_cast<uint32_t>(kt[cb + e]) << (8 * e);
-            vw |= static_cast<uint32_t>(vt[cb + e]) << (8 * e);
-        }
-        uint32_t kh[4], vh[4];
-        e2m1x8_to_f16x2x4(kw, kh);
-        e2m1x8_to_f16x2x4(vw, vh);
-        const float ksc = f16x2_to_f32x2(e4m3x2_to_f16x2(kt[sb])).x * ks;
-        const float vsc = f16x2_to_f32x2(e4m3x2_to_f16x2(vt[sb])).x * vs;
-        float dot = 0.0f;
-        for (int e = 0; e < per; ++e) {
-            const float2 p = f16x2_to_f32x2(kh[e / 2]);
-            dot += qv[e] * ((e & 1 ? p.y : p.x) * ksc);
-        }
-        const float s = warp_sum(dot) * a.sm_scale * kLog2e;
-        const float mn = fmaxf(m, s);
-        const float al = exp2f(m - mn), p = exp2f(s - mn);
-        m = mn;
-        l = l * al + p;
-        for (int e = 0; e < per; ++e) {
-            const float2 v = f16x2_to_f32x2(vh[e / 2]);
-            o[e] = o[e] * al + p * ((e & 1 ? v.y : v.x) * vsc);
+}
+
+// Joins the parts of split segments: CTA (c, r) row r of the segment that
+// starts in share c and goes on in shares c + 1 .. last.
+constexpr int kCombineThreads = 128;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Kv4AttnArgs a) {
+    using C = AttnCfg<D, NT>;
+    constexpr int R = C::R, V = D / 32;  // V elements per lane
+    __shared__ float s_o[kCombineThreads / 32][D];
+    const int c = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const SplitDesc sd = reinterpret_cast<const SplitDesc *>(a.workspace)[c];
+    if (sd.last < 0 || r >= sd.rows) return;
+    const float *records =
+        reinterpret_cast<const float *>(static_cast<const uint8_t *>(a.workspace) + 2 * kMaxSms * sizeof(SplitDesc));
+    const int n = sd.last - c + 1;
+    auto part = [&](int j) { return records + static_cast<int64_t>(2 * (c + j) + (j == 0)) * C::kRecFloats; };
+    float M = -INFINITY;
+    for (int j = lane; j < n; j += 32) M = fmaxf(M, part(j)[r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.0f;
+    for (int j = lane; j < n; j += 32) {
+        const float m = part(j)[r];
+        if (m != -INFINITY) L += ex2(m - M) * part(j)[R + r];
+    }
+    L = [&] {
+        float v = L;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }();
+    float acc[V] = {};
+#pragma unroll 4
+    for (int j = warp; j < n; j += kCombineThreads / 32) {
+        const float *p = part(j);
+        const float m = p[r], f = m == -INFINITY ? 0.0f : ex2(m - M);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += f * p[2 * R + r * D + i * 32 + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_o[warp][i * 32 + lane] = acc[i];
+    __syncthreads();
+    const int group = static_cast<int>(a.q_heads / a.kv_heads);
+    const int tok = (sd.row0 + r) / group, h = sd.row0 + r - tok * group;
+    const int64_t row = static_cast<int64_t>(sd.q0 + tok) * a.q_heads + sd.kvh * group + h;
+    const float inv = L > 0.0f ? __ldg(a.v_scale) / L : 0.0f;
+    for (int d = threadIdx.x; d < D; d += kCombineThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kCombineThreads / 32; ++w) v += s_o[w][d];
+        static_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(v * inv);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D, int NT>
+cudaError_t launch_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
+    using C = AttnCfg<D, NT>;
+    auto kern = kv4_attn_kernel<D, NT>;
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+            if (e != cudaSuccess) return e;
+            done[dev] = true;
         }
     }
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (row * a.q_heads + h) * d;
-    for (int e = 0; e < per; ++e) out[lane * per + e] = __float2bfloat16_rn(l > 0.0f ? o[e] / l : 0.0f);
-    if (a.lse && lane == 0) a.lse[row * a.q_heads + h] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    const int sms = device_sm_count() < kMaxSms ? device_sm_count() : kMaxSms;
+    const unsigned ctas = static_cast<unsigned>(sms * C::kRes);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, kMinUnits);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(ctas, C::R, 1);
+    cfg.blockDim = dim3(kCombineThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, NT>, a);
+}
+
+template <int D>
+cudaError_t launch_attn_rows(const Kv4AttnArgs &a, cudaStream_t stream) {
+    const int64_t rows = a.max_q * (a.q_heads / a.kv_heads);
+    if (rows <= 8) return launch_attn<D, 1>(a, stream);
+    if (rows <= 16) return launch_attn<D, 2>(a, stream);
+    return launch_attn<D, 4>(a, stream);
 }
 
 int copy_blocks(const Kv4CopyArgs &a) {
@@ -237,15 +847,11 @@ cudaError_t launch_kv4_gather(const Kv4CopyArgs &a, cudaStream_t stream) {
 }
 
 int64_t kv4_attention_ws_bytes(int64_t head_dim) {
-    return 160 * 32 * 2 * (head_dim + 2) * 4 + 16384;
+    return 2 * kMaxSms * static_cast<int64_t>(sizeof(SplitDesc)) + int64_t{2} * kMaxSms * 32 * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t stream) {
-    if (a.tokens == 0) return cudaSuccess;
-    kv4_attn_kernel<<<dim3(static_cast<unsigned>(a.max_q), static_cast<unsigned>(a.q_heads),
-                           static_cast<unsigned>(a.batch)),
-                      32, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.head_dim == 128 ? launch_attn_rows<128>(a, stream) : launch_attn_rows<64>(a, stream);
 }
 
 uint32_t take_kv4_error() {
