@@ -140,8 +140,13 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a)
 // share's end leaves partial (m, l, o) records in the workspace, which
 // kv4_combine_kernel joins in the order of the CTAs.
 //
-// A CTA is one producer warp, which copies the units' tiles (one bulk copy of
-// 9 D bytes each) into a ring, and W consumer warps, which take units in turn:
+// A CTA is a producer warp and W consumer warps around a ring of S units.  The
+// producer walks the share and copies four units at a time, a lane per tile
+// (K and V of a unit are one run each where the page holds it); it is pieces
+// ahead of the consumers, so table lookups and copies cost no time between
+// them.  The consumers of a piece take its units in turn and join their
+// (m, l, o) in shared memory; a segment of one or two units is one warp's
+// alone, beside others.  Per unit:
 //   S^T[32 keys, R rows] = K q^T with f16 mma.sync m16n8k16.  The order of
 //   the contraction is free: lane t of a quad takes elements 32 t .. 32 t + 31
 //   of a key (D = 128), so its codes are one 16-byte load; codes convert to
@@ -154,21 +159,26 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.0f;
-constexpr int kUnitTiles = 2;
-constexpr int kUnitKeys = kUnitTiles * kKv4Tile;
-constexpr int kMinUnits = 4;  // per CTA at least: one per warp or so
 constexpr int kMaxSms = 160;  // CTAs the workspace has records for: two per SM of 16 rows, or one of 32
+// What a segment costs besides its units (its q, the merge of the warps, its
+// output), in units; shares are equal in units + kSegCost a segment.
+constexpr int kSegCost = 6;
+constexpr int kMinShare = 8;  // a CTA's share at least
+constexpr int kSolo = 2;      // segments of so few units are one warp's: the ring holds W of them
 
-// W consumer warps and a ring of S units per CTA, RES CTAs per SM.
+// A producer warp, W consumer warps and a ring of S units per CTA, kRes CTAs
+// per SM.
 template <int D, int NT>
 struct AttnCfg {
     static constexpr int kRes = NT <= 2 ? 2 : 1;
     static constexpr int W = NT == 2 ? 5 : 7;
+    static constexpr int UT = 2;                    // tiles per unit
+    static constexpr int kKeys = UT * kKv4Tile;     // keys per unit
     static constexpr int S = NT == 2 ? 12 : 16;
     static constexpr int kThreads = (W + 1) * 32;
     static constexpr int R = 8 * NT;
-    static constexpr int kTileBytes = 9 * D;
-    static constexpr int kStageBytes = 2 * kUnitTiles * kTileBytes;
+    static constexpr int T = 9 * D;                 // bytes of a tile
+    static constexpr int kStageBytes = 2 * UT * T;
     static constexpr int kRecFloats = R * (D + 2);  // m[R], l[R], o[R][D]
     static constexpr int kSmemBytes = S * kStageBytes + W * kRecFloats * 4 + S * (8 + 8 + 4);
     static_assert(kSmemBytes * kRes <= 226 * 1024, "shared memory per SM");
@@ -190,9 +200,12 @@ struct SeqWork {
     int32_t tile0, tiles;  // first tile any row sees, end of the last
     int32_t units, row_tiles;
     uint32_t err;
+    __device__ __forceinline__ int64_t cost(int hkv) const {
+        return (static_cast<int64_t>(units) + kSegCost) * hkv * row_tiles;
+    }
 };
 
-template <int R>
+template <int R, int UT>
 __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int group) {
     SeqWork w;
     w.err = 0;
@@ -214,37 +227,55 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int gro
     const int64_t lo = a.window > 0 ? static_cast<int64_t>(w.len) - w.n_q - a.window + 1 : 0;
     w.tiles = (w.len + kKv4Tile - 1) / kKv4Tile;
     w.tile0 = lo > 0 ? static_cast<int32_t>(lo / kKv4Tile) : 0;
-    w.units = max(1, (w.tiles - w.tile0 + kUnitTiles - 1) / kUnitTiles);
+    w.units = max(1, (w.tiles - w.tile0 + UT - 1) / UT);
     w.row_tiles = (w.n_q * group + R - 1) / R;
     return w;
 }
 
-// A CTA's walk along its share: pieces of segments, in order.
-template <int R>
+// A CTA's walk along its share: pieces of segments, in order.  On the line a
+// segment is kSegCost steps and then its units.
+template <int R, int UT>
 struct Walk {
     SeqWork w;
-    int b;
-    int64_t p, left;  // next unit of sequence b, units left in the share
-    int kvh, row0;    // of the piece
-    int u0, u1;       // its units
-    __device__ __forceinline__ bool next(const Kv4AttnArgs &a, int hkv, int group) {
-        if (left <= 0) return false;
-        while (true) {
-            if (b >= a.batch) return false;
-            w = seq_work<R>(a, b, group);
-            const int64_t work = static_cast<int64_t>(w.units) * hkv * w.row_tiles;
-            if (p < work) break;
-            p -= work;  // the sequence is done, or has no rows
-            ++b;
-        }
-        const int64_t seg = p / w.units;
-        u0 = static_cast<int>(p - seg * w.units);
-        u1 = static_cast<int>(min(static_cast<int64_t>(w.units), u0 + left));
+    int64_t left;  // steps left in the share
+    int b, at;     // next step of the segment
+    int kvh, row_tile;
+    int u0, u1;    // the piece's units
+
+    // Starts at step `p` of sequence `first`.
+    __device__ __forceinline__ void start(const Kv4AttnArgs &a, int first, int64_t p, int64_t steps, int group) {
+        b = first;
+        left = steps;
+        w = seq_work<R, UT>(a, b, group);
+        const int seg_cost = w.units + kSegCost;
+        const int64_t seg = p / seg_cost;
+        at = static_cast<int>(p - seg * seg_cost);
         kvh = static_cast<int>(seg / w.row_tiles);
-        row0 = static_cast<int>(seg - static_cast<int64_t>(kvh) * w.row_tiles) * R;
-        p += u1 - u0;
-        left -= u1 - u0;
-        return true;
+        row_tile = static_cast<int>(seg - static_cast<int64_t>(kvh) * w.row_tiles);
+    }
+    __device__ __forceinline__ bool next(const Kv4AttnArgs &a, int hkv, int group) {
+        while (left > 0) {
+            const int seg_cost = w.units + kSegCost;
+            if (at >= seg_cost) {
+                at = 0;
+                if (++row_tile < w.row_tiles) continue;
+                row_tile = 0;
+                if (++kvh < hkv) continue;
+                kvh = 0;
+                do {  // sequences without rows have no steps
+                    if (++b >= a.batch) return false;
+                    w = seq_work<R, UT>(a, b, group);
+                } while (w.row_tiles == 0);
+                continue;
+            }
+            const int end = static_cast<int>(min(static_cast<int64_t>(seg_cost), at + left));
+            u0 = max(0, at - kSegCost);
+            u1 = end - kSegCost;
+            left -= end - at;
+            at = end;
+            if (u1 > u0) return true;  // else the share ends before the segment's first unit
+        }
+        return false;
     }
 };
 
@@ -270,16 +301,15 @@ __device__ __forceinline__ void bar_consumers(int threads) {
 __device__ __forceinline__ int kv4_row(int m) { return (m & 1) ? 4 + ((m >> 1) ^ 1) : m >> 1; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes)
-    kv4_attn_kernel(const Kv4AttnArgs a, int min_units) {
+__global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes) kv4_attn_kernel(const Kv4AttnArgs a) {
     using C = AttnCfg<D, NT>;
-    constexpr int W = C::W, S = C::S, R = C::R, T = C::kTileBytes;
+    constexpr int W = C::W, R = C::R, T = C::T, UT = C::UT, S = C::S;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *ring = smem;                                              // [S][K tiles | V tiles]
+    uint8_t *ring = smem;                                                 // [S][K tiles | V tiles]
     float *merge = reinterpret_cast<float *>(ring + S * C::kStageBytes);  // [W] records
     uint64_t *full = reinterpret_cast<uint64_t *>(merge + W * C::kRecFloats);
     uint64_t *empty = full + S;
-    int32_t *valid = reinterpret_cast<int32_t *>(empty + S);           // tiles a stage holds, one bit each
+    int32_t *holds = reinterpret_cast<int32_t *>(empty + S);              // which tiles a stage holds, a bit each
     __shared__ int64_t s_sums[W + 1], s_p;
     __shared__ int s_b;
 
@@ -304,9 +334,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     int64_t mine = 0;
     uint32_t err = 0;
     for (int b = b0; b < b1; ++b) {
-        const SeqWork w = seq_work<R>(a, b, group);
+        const SeqWork w = seq_work<R, UT>(a, b, group);
         err |= w.err;
-        mine += static_cast<int64_t>(w.units) * hkv * w.row_tiles;
+        mine += w.cost(hkv);
     }
     if (err && cta == 0) atomicOr(&g_kv4_err, err);
     int64_t x = mine;
@@ -323,75 +353,101 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         if (w < warp) before += s_sums[w];
         total += s_sums[w];
     }
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + min_units - 1) / min_units);
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kMinShare - 1) / kMinShare);
     if (tid == 0) desc[cta].last = -1;
     if (cta >= ctas) return;
     const int64_t lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
     if (lo >= before && lo < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
-            const SeqWork w = seq_work<R>(a, b, group);
-            const int64_t work = static_cast<int64_t>(w.units) * hkv * w.row_tiles;
-            if (lo < at + work) {
+            const int64_t cost = seq_work<R, UT>(a, b, group).cost(hkv);
+            if (lo < at + cost) {
                 s_b = b;
                 s_p = lo - at;
                 break;
             }
-            at += work;
+            at += cost;
         }
     }
     __syncthreads();
-    Walk<R> walk;
-    walk.b = s_b;
-    walk.p = s_p;
-    walk.left = hi - lo;
+    Walk<R, UT> walk;
+    walk.start(a, s_b, s_p, hi - lo, group);
 
     if (warp == W) {
         // ================================================== producer
         const int tpp = static_cast<int>(a.page_size) / kKv4Tile;
-        int stage = 0;
-        uint32_t round = 0;  // how often the ring has wrapped
-        bool ok = true;
-        err = 0;
-        while (ok && walk.next(a, hkv, group)) {
-            const int32_t *trow = a.block_table + static_cast<int64_t>(walk.b) * a.max_blocks;
-            for (int ub = walk.u0; ok && ub < walk.u1; ub += 32 / kUnitTiles) {
-                // lane j: tile j of the next 16 units
-                const int n = min(32 / kUnitTiles, walk.u1 - ub);
-                const int tile = walk.w.tile0 + ub * kUnitTiles + lane;
-                const bool inside = lane < n * kUnitTiles && tile < walk.w.tiles;
+        constexpr uint32_t kNoTile = 0xffffffffu;
+        constexpr int kWindow = 32 / UT;  // units whose tiles the lanes look up together
+        constexpr int kBatch = 4;         // units copied together
+        uint32_t count = 0;               // units put into the ring
+        bool inside = walk.next(a, hkv, group);
+        int ub = walk.u0;
+        // the next window of units: how many, and lane j's place of its tile j
+        auto look_up = [&](uint32_t &place) -> int {
+            place = kNoTile;
+            if (!inside) return 0;
+            const int n = min(kWindow, walk.u1 - ub);
+            const int tile = walk.w.tile0 + ub * UT + lane;
+            if (lane < n * UT && tile < walk.w.tiles) {
                 const int pg = tile / tpp;
-                const int32_t blk = inside ? __ldg(trow + pg) : -1;
-                const bool have = inside && blk >= 0 && blk < a.num_blocks;
-                if (inside && !have) err = ERRBIT_INDEX;
-                const int64_t off =
-                    have ? ((static_cast<int64_t>(blk) * hkv + walk.kvh) * tpp + (tile - pg * tpp)) * T : 0;
-                const uint32_t haves = __ballot_sync(0xffffffffu, have);
-                for (int i = 0; i < n; ++i) {
-                    if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], (round - 1) & 1));
-                    if (!ok) break;
-                    const uint32_t mask = (haves >> (i * kUnitTiles)) & ((1u << kUnitTiles) - 1);
-                    if (lane == 0) {
-                        valid[stage] = static_cast<int32_t>(mask);
-                        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(__popc(mask) * 2 * T));
-                    }
-                    __syncwarp();
-                    if (lane / kUnitTiles == i && have) {
-                        uint8_t *dst = ring + stage * C::kStageBytes + (lane % kUnitTiles) * T;
-                        bulk_load_g2s(dst, a.k_cache + off, T, &full[stage]);
-                        bulk_load_g2s(dst + kUnitTiles * T, a.v_cache + off, T, &full[stage]);
-                    }
-                    if (++stage == S) stage = 0, ++round;
-                }
+                const int32_t blk = __ldg(a.block_table + static_cast<int64_t>(walk.b) * a.max_blocks + pg);
+                if (blk >= 0 && blk < a.num_blocks)
+                    place = static_cast<uint32_t>((static_cast<int64_t>(blk) * hkv + walk.kvh) * tpp + (tile - pg * tpp));
+                else
+                    atomicOr(&g_kv4_err, ERRBIT_INDEX);  // left out
             }
+            ub += n;
+            if (ub == walk.u1) {
+                inside = walk.next(a, hkv, group);
+                ub = walk.u0;
+            }
+            return n;
+        };
+        bool ok = true;
+        uint32_t place, place_next;
+        int n = look_up(place);
+        while (n > 0 && ok) {
+            const int n_next = look_up(place_next);
+            for (int first = 0; first < n; first += kBatch) {
+                // lane j < kBatch * UT: tile j % UT of unit first + j / UT
+                const uint32_t at = __shfl_sync(0xffffffffu, place, (first * UT + lane) & 31);
+                const bool live = lane < kBatch * UT && first + lane / UT < n;
+                const uint32_t idx = count + lane / UT, st = idx % S;
+                bool free_now = true;
+                if (live && idx >= S) free_now = mbar_wait_bounded(&empty[st], (idx / S - 1) & 1);
+                ok = __all_sync(0xffffffffu, free_now);
+                if (!ok) break;
+                const uint32_t have = __ballot_sync(0xffffffffu, live && at != kNoTile);
+                const uint32_t mask = (have >> (lane / UT * UT)) & ((1u << UT) - 1);
+                const uint32_t head = __shfl_sync(0xffffffffu, at, lane / UT * UT);
+                const uint32_t in_run = __ballot_sync(0xffffffffu, at == head + lane % UT);
+                const bool run =
+                    mask == (1u << UT) - 1 && ((in_run >> (lane / UT * UT)) & ((1u << UT) - 1)) == (1u << UT) - 1;
+                if (live && lane % UT == 0) {
+                    holds[st] = static_cast<int32_t>(mask);
+                    mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(mask) * 2 * T));
+                }
+                __syncwarp();
+                uint8_t *dst = ring + st * C::kStageBytes;
+                if (live && run) {  // one lane copies the unit's K, the next its V
+                    const int64_t off = static_cast<int64_t>(head) * T;
+                    if (lane % UT < 2)
+                        bulk_load_g2s(dst + lane % UT * (UT * T), (lane % UT ? a.v_cache : a.k_cache) + off, UT * T,
+                                      &full[st]);
+                } else if (live && at != kNoTile) {
+                    const int64_t off = static_cast<int64_t>(at) * T;
+                    bulk_load_g2s(dst + lane % UT * T, a.k_cache + off, T, &full[st]);
+                    bulk_load_g2s(dst + (UT + lane % UT) * T, a.v_cache + off, T, &full[st]);
+                }
+                count += min(kBatch, n - first);
+            }
+            n = n_next;
+            place = place_next;
         }
-        if (err) atomicOr(&g_kv4_err, err);
         if (!ok) {  // a consumer gave up: never leave with copies in flight
             if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_EMPTY_WAIT);
-            for (int i = 0; i < S; ++i) {
-                if (i < stage) (void)mbar_wait_bounded(&full[i], round & 1);
-                else (void)mbar_wait_bounded(&full[i], (round - 1) & 1);
-            }
+            for (uint32_t idx = count > S ? count - S : 0; idx < count; ++idx)
+                (void)mbar_wait_bounded(&full[idx % S], (idx / S) & 1);
         }
         return;
     }
@@ -400,15 +456,31 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     const int g = lane >> 2, t = lane & 3;
     const float base = a.sm_scale * __ldg(a.k_scale) * kLog2e;
     const float v_scale = __ldg(a.v_scale);
-    constexpr int kLaneCodes = D / 4;   // codes of a key a lane holds for S^T
+    constexpr int kLaneCodes = D / 4;  // codes of a key a lane holds for S^T
     constexpr int kSteps = D / 16;
-    int turn = 0, stage = 0;            // whose unit is next, and where it is
-    uint32_t round = 0;
+    const int64_t solo = min(static_cast<int64_t>(kSolo), (hi - lo) / W);  // where there is work for every warp
+    uint32_t count = 0;  // units of the pieces before this one
+    int turn = 0;        // the warp that takes the next piece's first unit
     bool failed = false;
 
     while (walk.next(a, hkv, group)) {
-        const int rows = walk.w.n_q * group - walk.row0;  // rows left of the sequence (some may be other tiles')
-        const int first_pos = walk.w.len - walk.w.n_q;    // position of query token 0
+        const int n_units = walk.u1 - walk.u0;
+        const bool starts = walk.u0 == 0, ends = walk.u1 == walk.w.units;
+        const bool alone = starts && ends && n_units <= solo;
+        int first = warp - turn;  // this warp's first unit of the piece; step W, or all of it alone
+        if (first < 0) first += W;
+        const int step = alone ? 1 : W;
+        const uint32_t piece = count;
+        count += static_cast<uint32_t>(n_units);
+        if (alone) {
+            if (++turn == W) turn = 0;
+            if (first != 0) continue;
+        } else {
+            turn = (turn + n_units) % W;
+        }
+        const int row0 = walk.row_tile * R;
+        const int rows = walk.w.n_q * group - row0;     // rows left of the sequence (some may be other tiles')
+        const int first_pos = walk.w.len - walk.w.n_q;  // position of query token 0
 
         // ---- q as f16 B fragments, an exact power-of-two rescale per row
         uint32_t bq[NT][kSteps][2];
@@ -418,7 +490,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         for (int n = 0; n < NT; ++n) {
             const int r = n * 8 + g;
             const bool live = r < rows;
-            const int tok = live ? (walk.row0 + r) / group : 0, h = live ? walk.row0 + r - tok * group : 0;
+            const int tok = live && walk.w.n_q > 1 ? (row0 + r) / group : 0, h = live ? row0 + r - tok * group : 0;
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
                                        static_cast<int64_t>(walk.w.q0 + tok) * a.q_stride +
                                        (walk.kvh * group + h) * D + t * kLaneCodes;
@@ -449,8 +521,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             }
         }
         // keys below `clear_hi` and from `clear_lo` on are seen by every row of the tile
-        const int last_tok = min(walk.row0 + R - 1, walk.w.n_q * group - 1) / group;
-        const int clear_hi = first_pos + walk.row0 / group + 1;
+        const int last_tok = walk.w.n_q > 1 ? min(row0 + R - 1, walk.w.n_q * group - 1) / group : 0;
+        const int clear_hi = first_pos + (walk.w.n_q > 1 ? row0 / group : 0) + 1;
         const int64_t clear_lo = a.window > 0 ? static_cast<int64_t>(first_pos) + last_tok - a.window + 1 : 0;
 
         float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4];
@@ -464,26 +536,21 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
         }
 
-        for (int u = walk.u0; u < walk.u1; ++u) {
-            const bool my_turn = turn == warp;
-            if (++turn == W) turn = 0;
-            const int st = stage;
-            const uint32_t parity = round & 1;
-            if (++stage == S) stage = 0, ++round;
-            if (!my_turn || failed) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], parity))) {
+        for (int u = first; u < n_units && !failed; u += step) {
+            const uint32_t idx = piece + static_cast<uint32_t>(u), st = idx % S;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (idx / S) & 1))) {
                 if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_FULL_WAIT);
                 failed = true;
-                continue;
+                break;
             }
-            const uint32_t have = static_cast<uint32_t>(valid[st]);
-            const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + kUnitTiles * T;
-            const int key0 = (walk.w.tile0 + u * kUnitTiles) * kKv4Tile;
+            const uint32_t have = static_cast<uint32_t>(holds[st]);
+            const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + UT * T;
+            const int key0 = (walk.w.tile0 + (walk.u0 + u) * UT) * kKv4Tile;
 
             // ---- S^T: lane holds keys kv4_row(g), + 8 of each tile, rows 2t, 2t + 1 of each n
-            float s[kUnitTiles][NT][4];
+            float s[UT][NT][4];
 #pragma unroll
-            for (int h = 0; h < kUnitTiles; ++h) {
+            for (int h = 0; h < UT; ++h) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -532,14 +599,14 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                                       bq[n][i][0], bq[n][i][1]);
             }
 #pragma unroll
-            for (int h = 0; h < kUnitTiles; ++h)
+            for (int h = 0; h < UT; ++h)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[h][n][j] *= sc[n][j & 1];
-            if (have != (1u << kUnitTiles) - 1 || key0 + kUnitKeys > clear_hi || key0 < clear_lo) {
+            if (have != (1u << UT) - 1 || key0 + C::kKeys > clear_hi || key0 < clear_lo) {
 #pragma unroll
-                for (int h = 0; h < kUnitTiles; ++h)
+                for (int h = 0; h < UT; ++h)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -560,7 +627,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int c = 0; c < 2; ++c) {
                     float v = fmaxf(s[0][n][c], s[0][n][c + 2]);
 #pragma unroll
-                    for (int h = 1; h < kUnitTiles; ++h) v = fmaxf(v, fmaxf(s[h][n][c], s[h][n][c + 2]));
+                    for (int h = 1; h < UT; ++h) v = fmaxf(v, fmaxf(s[h][n][c], s[h][n][c + 2]));
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
                     mt[n][c] = v;
@@ -586,14 +653,14 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     }
                 }
             }
-            uint32_t pb[kUnitTiles][NT][2];  // P^T as B fragments: keys 2t, 2t + 1 (+ 8) of the tile, row g
+            uint32_t pb[UT][NT][2];  // P^T as B fragments: keys 2t, 2t + 1 (+ 8) of the tile, row g
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float ref[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) ref[c] = m_run[n][c] == -INFINITY ? 0.0f : m_run[n][c] - kPShift;
 #pragma unroll
-                for (int h = 0; h < kUnitTiles; ++h) {
+                for (int h = 0; h < UT; ++h) {
                     float p[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) p[j] = ex2(s[h][n][j] - ref[j & 1]);
@@ -606,7 +673,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 
             // ---- O^T += V^T P^T
 #pragma unroll
-            for (int h = 0; h < kUnitTiles; ++h) {
+            for (int h = 0; h < UT; ++h) {
                 if (!((have >> h) & 1)) continue;  // never copied
                 uint32_t sb[4], w[4][D / 64];
 #pragma unroll
@@ -644,23 +711,50 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     }
                 }
             }
-            __syncwarp();
+            __syncwarp();  // the stage has been read
             if (lane == 0) mbar_arrive(&empty[st]);
         }
 
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], off);
+        const int q0 = walk.w.q0, head0 = walk.kvh * group;
+        if (alone) {  // lane: elements g D / 8 .. of rows 2t, 2t + 1 of each n
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int r = n * 8 + 2 * t + c;
+                    if (r >= rows) continue;
+                    const int tok = walk.w.n_q > 1 ? (row0 + r) / group : 0, h = row0 + r - tok * group;
+                    const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
+                    const float L = l_run[n][c], inv = L > 0.0f ? v_scale / L : 0.0f;
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + g * (D / 8));
+#pragma unroll
+                    for (int i = 0; i < kSteps; i += 4)
+                        dst[i / 4] = make_uint4(f32x2_to_bf16x2(o[n][i][c] * inv, o[n][i][c + 2] * inv),
+                                                f32x2_to_bf16x2(o[n][i + 1][c] * inv, o[n][i + 1][c + 2] * inv),
+                                                f32x2_to_bf16x2(o[n][i + 2][c] * inv, o[n][i + 2][c + 2] * inv),
+                                                f32x2_to_bf16x2(o[n][i + 3][c] * inv, o[n][i + 3][c + 2] * inv));
+                    if (a.lse && g == 0)
+                        a.lse[row] = L > 0.0f ? (m_run[n][c] - kPShift + log2f(L)) * kLn2 : -INFINITY;
+                }
+            continue;
+        }
         // ---- the warps' parts of the piece: m[R], l[R], o[R][D] each
         float *rec = merge + warp * C::kRecFloats;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float l = l_run[n][c];
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
                 const int r = n * 8 + 2 * t + c;
                 if (g == 0) {
                     rec[r] = m_run[n][c];
-                    rec[R + r] = l;
+                    rec[R + r] = l_run[n][c];
                 }
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
@@ -668,7 +762,6 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                         make_float2(o[n][i][c], o[n][i][c + 2]);
             }
         bar_consumers(W * 32);
-        const bool starts = walk.u0 == 0, ends = walk.u1 == walk.w.units;
         float *out_rec = records + static_cast<int64_t>(2 * cta + (starts ? 1 : 0)) * C::kRecFloats;
         for (int e = tid; e < R * D / 4; e += W * 32) {
             const int r = e / (D / 4), d4 = e - r * (D / 4);
@@ -689,8 +782,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 O.x += f * v.x, O.y += f * v.y, O.z += f * v.z, O.w += f * v.w;
             }
             if (starts && ends) {
-                const int tok = (walk.row0 + r) / group, h = walk.row0 + r - tok * group;
-                const int64_t row = static_cast<int64_t>(walk.w.q0 + tok) * a.q_heads + walk.kvh * group + h;
+                const int tok = (row0 + r) / group, h = row0 + r - tok * group;
+                const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
                 const float inv = L > 0.0f ? v_scale / L : 0.0f;
                 *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d4 * 4) =
                     make_uint2(f32x2_to_bf16x2(O.x * inv, O.y * inv), f32x2_to_bf16x2(O.z * inv, O.w * inv));
@@ -704,13 +797,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             }
         }
         if (starts && !ends && tid == 0) {  // the share's last piece: where the segment ends
-            const int64_t seg_end = hi + (walk.w.units - walk.u1);
             SplitDesc *sd = desc + cta;
-            sd->q0 = walk.w.q0;
+            sd->q0 = q0;
             sd->rows = min(rows, R);
-            sd->row0 = walk.row0;
-            sd->kvh = walk.kvh;
-            sd->last = static_cast<int32_t>((seg_end * ctas + total - 1) / total - 1);
+            sd->row0 = row0;
+            sd->kvh = head0 / group;
+            sd->last = static_cast<int32_t>(((hi + walk.w.units - walk.u1) * ctas + total - 1) / total - 1);
         }
         bar_consumers(W * 32);  // the records are free again
     }
@@ -800,7 +892,7 @@ cudaError_t launch_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, kMinUnits);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ctas, C::R, 1);
     cfg.blockDim = dim3(kCombineThreads, 1, 1);
