@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a)
 // (K and V of a unit are one run each where the page holds it); it is pieces
 // ahead of the consumers, so table lookups and copies cost no time between
 // them.  The consumers of a piece take its units in turn and join their
-// (m, l, o) in shared memory; a segment of one or two units is one warp's
-// alone, beside others.  Per unit:
+// (m, l, o) in shared memory; a segment of one unit is one warp's alone, beside
+// others.  Per unit:
 //   S^T[32 keys, R rows] = K q^T with f16 mma.sync m16n8k16.  The order of
 //   the contraction is free: lane t of a quad takes elements 32 t .. 32 t + 31
 //   of a key (D = 128), so its codes are one 16-byte load; codes convert to
@@ -164,7 +164,6 @@ constexpr int kMaxSms = 160;  // CTAs the workspace has records for: two per SM 
 // output), in units; shares are equal in units + kSegCost a segment.
 constexpr int kSegCost = 6;
 constexpr int kMinShare = 8;  // a CTA's share at least
-constexpr int kSolo = 2;      // segments of so few units are one warp's: the ring holds W of them
 
 // A producer warp, W consumer warps and a ring of S units per CTA, kRes CTAs
 // per SM.
@@ -174,7 +173,12 @@ struct AttnCfg {
     static constexpr int W = NT == 2 ? 5 : 7;
     static constexpr int UT = 2;                    // tiles per unit
     static constexpr int kKeys = UT * kKv4Tile;     // keys per unit
-    static constexpr int S = NT == 2 ? 12 : 16;
+    // A stage belongs to one consumer warp: unit i of a CTA is warp i % W's and
+    // in stage i % S, with W a divisor of S.  Copies land in any order, and a
+    // warp that waited for the next phase of a stage before the last one is
+    // complete would take the phase before that for it.
+    static constexpr int S = NT == 2 ? 15 : 14;
+    static_assert(S % W == 0, "a stage's units are one warp's");
     static constexpr int kThreads = (W + 1) * 32;
     static constexpr int R = 8 * NT;
     static constexpr int T = 9 * D;                 // bytes of a tile
@@ -458,26 +462,20 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     const float v_scale = __ldg(a.v_scale);
     constexpr int kLaneCodes = D / 4;  // codes of a key a lane holds for S^T
     constexpr int kSteps = D / 16;
-    const int64_t solo = min(static_cast<int64_t>(kSolo), (hi - lo) / W);  // where there is work for every warp
     uint32_t count = 0;  // units of the pieces before this one
-    int turn = 0;        // the warp that takes the next piece's first unit
+    int turn = 0;        // count % W
     bool failed = false;
 
     while (walk.next(a, hkv, group)) {
         const int n_units = walk.u1 - walk.u0;
         const bool starts = walk.u0 == 0, ends = walk.u1 == walk.w.units;
-        const bool alone = starts && ends && n_units <= solo;
-        int first = warp - turn;  // this warp's first unit of the piece; step W, or all of it alone
+        const bool alone = n_units == 1 && starts && ends;
+        int first = warp - turn;  // this warp's first unit of the piece
         if (first < 0) first += W;
-        const int step = alone ? 1 : W;
         const uint32_t piece = count;
         count += static_cast<uint32_t>(n_units);
-        if (alone) {
-            if (++turn == W) turn = 0;
-            if (first != 0) continue;
-        } else {
-            turn = (turn + n_units) % W;
-        }
+        turn = (turn + n_units) % W;
+        if (alone && first != 0) continue;
         const int row0 = walk.row_tile * R;
         const int rows = walk.w.n_q * group - row0;     // rows left of the sequence (some may be other tiles')
         const int first_pos = walk.w.len - walk.w.n_q;  // position of query token 0
@@ -536,7 +534,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
         }
 
-        for (int u = first; u < n_units && !failed; u += step) {
+        for (int u = first; u < n_units && !failed; u += W) {
             const uint32_t idx = piece + static_cast<uint32_t>(u), st = idx % S;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (idx / S) & 1))) {
                 if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_FULL_WAIT);
