@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         constexpr uint32_t kNoTile = 0xffffffffu;
         constexpr int kWindow = 32 / UT;  // units whose tiles the lanes look up together
         constexpr int kBatch = 4;         // units copied together
+        static_assert(UT == 2, "a lane for K and one for V");
         uint32_t count = 0;               // units put into the ring
         bool inside = walk.next(a, hkv, group);
         int ub = walk.u0;
@@ -412,39 +413,38 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         int n = look_up(place);
         while (n > 0 && ok) {
             const int n_next = look_up(place_next);
+            // lane j: tile j % UT of unit j / UT; its unit's first place, what it holds, whether it is one run
+            const uint32_t pair = ((1u << UT) - 1) << (lane / UT * UT);
+            const uint32_t head = __shfl_sync(0xffffffffu, place, lane / UT * UT);
+            const uint32_t mask = __ballot_sync(0xffffffffu, place != kNoTile) & pair;
+            const uint32_t follows = __ballot_sync(0xffffffffu, place == head + lane % UT) & pair;
+            const bool run = mask == pair && follows == pair;
+            const uint32_t idx = count + lane / UT, st = idx % S, parity = (idx / S - 1) & 1;
+            uint8_t *dst = ring + st * C::kStageBytes;
+            const uint8_t *src = a.k_cache + static_cast<int64_t>(run ? head : place) * T;
+            const uint8_t *src_v = a.v_cache + static_cast<int64_t>(run ? head : place) * T;
             for (int first = 0; first < n; first += kBatch) {
-                // lane j < kBatch * UT: tile j % UT of unit first + j / UT
-                const uint32_t at = __shfl_sync(0xffffffffu, place, (first * UT + lane) & 31);
-                const bool live = lane < kBatch * UT && first + lane / UT < n;
-                const uint32_t idx = count + lane / UT, st = idx % S;
+                const bool live = lane / (kBatch * UT) == first / kBatch && lane < n * UT;
                 bool free_now = true;
-                if (live && idx >= S) free_now = mbar_wait_bounded(&empty[st], (idx / S - 1) & 1);
+                if (live && idx >= S) free_now = mbar_wait_bounded(&empty[st], parity);
                 ok = __all_sync(0xffffffffu, free_now);
-                if (!ok) break;
-                const uint32_t have = __ballot_sync(0xffffffffu, live && at != kNoTile);
-                const uint32_t mask = (have >> (lane / UT * UT)) & ((1u << UT) - 1);
-                const uint32_t head = __shfl_sync(0xffffffffu, at, lane / UT * UT);
-                const uint32_t in_run = __ballot_sync(0xffffffffu, at == head + lane % UT);
-                const bool run =
-                    mask == (1u << UT) - 1 && ((in_run >> (lane / UT * UT)) & ((1u << UT) - 1)) == (1u << UT) - 1;
+                if (!ok) {
+                    count += static_cast<uint32_t>(first);
+                    break;
+                }
                 if (live && lane % UT == 0) {
-                    holds[st] = static_cast<int32_t>(mask);
+                    holds[st] = static_cast<int32_t>(mask >> lane);
                     mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(mask) * 2 * T));
                 }
                 __syncwarp();
-                uint8_t *dst = ring + st * C::kStageBytes;
                 if (live && run) {  // one lane copies the unit's K, the next its V
-                    const int64_t off = static_cast<int64_t>(head) * T;
-                    if (lane % UT < 2)
-                        bulk_load_g2s(dst + lane % UT * (UT * T), (lane % UT ? a.v_cache : a.k_cache) + off, UT * T,
-                                      &full[st]);
-                } else if (live && at != kNoTile) {
-                    const int64_t off = static_cast<int64_t>(at) * T;
-                    bulk_load_g2s(dst + lane % UT * T, a.k_cache + off, T, &full[st]);
-                    bulk_load_g2s(dst + (UT + lane % UT) * T, a.v_cache + off, T, &full[st]);
+                    bulk_load_g2s(dst + lane % UT * (UT * T), lane % UT ? src_v : src, UT * T, &full[st]);
+                } else if (live && place != kNoTile) {
+                    bulk_load_g2s(dst + lane % UT * T, src, T, &full[st]);
+                    bulk_load_g2s(dst + (UT + lane % UT) * T, src_v, T, &full[st]);
                 }
-                count += min(kBatch, n - first);
             }
+            if (ok) count += static_cast<uint32_t>(n);
             n = n_next;
             place = place_next;
         }
