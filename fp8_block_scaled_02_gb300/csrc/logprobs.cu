@@ -5,6 +5,16 @@
 //   lse = m + log l,  logprob(i) = x_i - lse,  entropy = log l - t / l.
 // The top alternatives are the first k of the row ordered by value, highest
 // first, and by index, lowest first, among equals.
+//
+// The row is read once, 16 bytes a load, by the CTAs of one cluster (one CTA
+// when there are many rows); every thread keeps a running (m, l, t) of its
+// elements.  The top comes out of the same maxima: the k-th largest of the
+// threads' maxima is a lower bound of the row part's k-th largest element,
+// and only threads whose maximum reaches it can hold one of the top k, about
+// k of the 512.  Their elements (1 / 512 of the part each) are read again,
+// from L2, and what reaches the bound is ranked in shared memory.  Rows of
+// equals, such as masked ones, whose equals at the bound do not fit there
+// take an ordered scan that stops when it has enough.
 #include "common.cuh"
 #include "internal.h"
 
@@ -14,93 +24,517 @@ namespace {
 
 __device__ uint32_t g_lp_err;
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpMaxSplit = 8;   // CTAs per row
+constexpr int kLpCandidates = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+// (x - m) below this has weight 0 in fp32; it keeps -inf out of t
+constexpr float kLowest = -200.0f;
 
-template <bool F32>
-__device__ __forceinline__ float logit(const void *row, int64_t i) {
-    return F32 ? static_cast<const float *>(row)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i]);
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// Two partial sums over parts of a row: the second is brought to the larger maximum.
-__device__ __forceinline__ void merge(float &m, float &l, float &t, float m2, float l2, float t2) {
-    const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
-    const float a = m == -INFINITY ? 0.0f : expf(m - mn), b = m2 == -INFINITY ? 0.0f : expf(m2 - mn);
-    const float da = fmaxf(m - mn, -200.0f), db = fmaxf(m2 - mn, -200.0f);  // their weights are 0 there
-    t = a * (t + da * l) + b * (t2 + db * l2);
-    l = a * l + b * l2;
-    m = mn;
+// Order of the values as unsigned integers: -0 is +0, NaN below everything.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return x != x ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(LogprobArgs a) {
-    __shared__ float sm[kLpThreads], sl[kLpThreads], st[kLpThreads];
-    __shared__ int32_t si[kLpThreads];
-    const int tid = threadIdx.x;
-    const int64_t r = blockIdx.x, v = a.vocab;
-    pdl_wait();
-    const void *row = static_cast<const char *>(a.logits) + r * a.row_stride * (F32 ? 4 : 2);
-    float m = -INFINITY, l = 0.0f, t = 0.0f;
-    for (int64_t i = tid; i < v; i += kLpThreads) {
-        const float x = logit<F32>(row, i);
-        if (x == -INFINITY) continue;
-        merge(m, l, t, x, 1.0f, 0.0f);
+struct Sums {
+    float m, l, t;
+};
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Over groups of `width` lanes: brought to the largest maximum once, then added.
+__device__ __forceinline__ Sums warp_merge(Sums s, int width = 32) {
+    float m = s.m;
+#pragma unroll
+    for (int o = width / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float d = s.m == -INFINITY ? kLowest : fmaxf(s.m - m, kLowest), c = ex2(d * kLog2e);
+    float l = c * s.l, t = c * (s.t + d * s.l);
+#pragma unroll
+    for (int o = width / 2; o > 0; o >>= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
     }
-    sm[tid] = m, sl[tid] = l, st[tid] = t;
-    __syncthreads();
-    for (int s = kLpThreads / 2; s > 0; s >>= 1) {
-        if (tid < s) {
-            merge(m, l, t, sm[tid + s], sl[tid + s], st[tid + s]);
-            sm[tid] = m, sl[tid] = l, st[tid] = t;
+    return Sums{m, l, t};
+}
+
+// One row as vectors of 16 aligned bytes; the first and the last may reach
+// beyond the row, where `pre` elements stand before it.
+template <bool F32>
+struct Row {
+    static constexpr int VE = F32 ? 4 : 8;
+    const char *base;  // of vector 0
+    int64_t vocab;
+    int pre, vecs;
+
+    __device__ __forceinline__ Row(const void *row, int64_t v) : vocab(v) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row);
+        pre = static_cast<int>(p & 15) / (F32 ? 4 : 2);
+        base = reinterpret_cast<const char *>(p & ~static_cast<uintptr_t>(15));
+        vecs = static_cast<int>((v + pre + VE - 1) / VE);
+    }
+    __device__ __forceinline__ int64_t element(int vec, int j) const { return static_cast<int64_t>(vec) * VE - pre + j; }
+    __device__ __forceinline__ bool whole(int vec) const {
+        return static_cast<int64_t>(vec) * VE >= pre && static_cast<int64_t>(vec + 1) * VE - pre <= vocab;
+    }
+    // The vector's values; -inf for what is not in the row.
+    __device__ __forceinline__ void load(int vec, float (&x)[VE]) const {
+        const char *p = base + static_cast<int64_t>(vec) * 16;
+        if (whole(vec)) {
+            unpack(ld_nc_v4(p), x);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            const int64_t e = element(vec, j);
+            x[j] = -INFINITY;
+            if (e >= 0 && e < vocab) {
+                if constexpr (F32) x[j] = reinterpret_cast<const float *>(p)[j];
+                else x[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[j]);
+            }
+        }
+    }
+    // The vector's values raised to FastSums' floor; returns the largest before that.
+    __device__ __forceinline__ float load_fast(int vec, float (&x)[VE]) const {
+        load(vec, x);
+        float vm = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            vm = fmaxf(vm, x[j]);
+            x[j] = fmaxf(x[j], -1e38f);
+        }
+        return vm;
+    }
+    // The values of a whole vector raised to FastSums' floor; returns the largest before that.
+    static __device__ __forceinline__ float unpack_fast(const uint4 v, float (&x)[VE]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (F32) {
+            unpack(v, x);
+            const float vm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+#pragma unroll
+            for (int j = 0; j < VE; ++j) x[j] = fmaxf(x[j], -1e38f);
+            return vm;
+        } else {
+            const uint32_t m2 = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u = max_bf16x2(w[j], 0xFE96FE96u);  // -1e38 in bf16
+                x[2 * j] = bf16lo_to_f32(u);
+                x[2 * j + 1] = bf16hi_to_f32(u);
+            }
+            return fmaxf(bf16lo_to_f32(m2), bf16hi_to_f32(m2));
+        }
+    }
+    static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[VE]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (F32) {
+                x[j] = __uint_as_float(w[j]);
+            } else {
+                x[2 * j] = bf16lo_to_f32(w[j]);
+                x[2 * j + 1] = bf16hi_to_f32(w[j]);
+            }
+        }
+    }
+};
+
+// Adds a vector to sums of any values.
+template <int VE>
+__device__ __forceinline__ void add_any(Sums &s, const float (&x)[VE]) {
+    float vm = x[0];
+#pragma unroll
+    for (int j = 1; j < VE; ++j) vm = fmaxf(vm, x[j]);
+    if (vm > s.m) {
+        const float d = fmaxf(s.m - vm, kLowest), c = ex2(d * kLog2e);
+        s.t = c * (s.t + d * s.l);
+        s.l *= c;
+        s.m = vm;
+    }
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+        const float d = fmaxf(x[j] - s.m, kLowest), e = ex2(d * kLog2e);
+        s.l += e;
+        s.t = fmaf(d, e, s.t);
+    }
+}
+
+// The same in four instructions an element for ordinary values, |m| < 2^19:
+// with L = fl(log2 e) and a reference r near m L, d = x L - r (one rounding),
+// l = sum 2^d, t = sum d 2^d.  The reference only has to keep 2^d in range: it
+// moves when a value passes it by 2^kSlack, so that the lanes of a warp hardly
+// ever do (with the maximum itself as the reference some lane of 32 does at
+// four of five vectors).  sums() brings it to m.  -inf counts as -1e38, whose
+// weight is 0.
+struct FastSums {
+    static constexpr float kSlack = 24.0f;
+    float m = -INFINITY, limit = -INFINITY, r = 0.0f, l = 0.0f, t = 0.0f;
+    static constexpr float kHuge = 524288.0f;
+
+    // x: values of at least kFloor (-inf raised to it); vm: the largest before that.
+    template <int VE>
+    __device__ __forceinline__ void add(const float (&x)[VE], float vm) {
+        if (vm > limit) {
+            const float rn = vm * kLog2e;
+            const float d = m == -INFINITY ? kLowest : fmaxf(r - rn, kLowest), c = ex2(d);
+            t = c * (t + d * l);
+            l *= c;
+            r = rn;
+            limit = vm + kSlack / kLog2e;
+        }
+        m = fmaxf(m, vm);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+            const float d = fmaf(x[j], kLog2e, -r), e = ex2(d);
+            l += e;
+            t = fmaf(d, e, t);
+        }
+    }
+    __device__ __forceinline__ bool ordinary() const { return m == -INFINITY || fabsf(m) < kHuge; }
+    __device__ __forceinline__ Sums sums() const {
+        if (m == -INFINITY) return Sums{m, 0.0f, 0.0f};
+        const float d0 = fmaf(m, kLog2e, -r), c = ex2(-d0);
+        return Sums{m, c * l, c * (t - d0 * l) * (1.0f / kLog2e)};
+    }
+};
+
+struct LpShared {
+    float vals[kLpCandidates + kLogprobsMaxTop];
+    int32_t ids[kLpCandidates + kLogprobsMaxTop];
+    int32_t flagged[kLpThreads];
+    Sums warp[kLpWarps];
+    int32_t counts[kLpWarps];
+    int32_t n_flagged, n;
+    // what the CTAs of the cluster hand to the first
+    Sums part[kLpMaxSplit];
+    float part_vals[kLpMaxSplit * kLogprobsMaxTop];
+    int32_t part_ids[kLpMaxSplit * kLogprobsMaxTop];
+};
+
+__device__ __forceinline__ bool better(float x, int32_t i, float y, int32_t j) { return x > y || (x == y && i < j); }
+
+// The first `top` of the n candidates (value, id >= 0) in order: emit(rank, i),
+// a warp per candidate; those below `least` are known not to be among them.
+template <class Emit>
+__device__ __forceinline__ void rank_candidates(const float *vals, const int32_t *ids, int n, int top, float least,
+                                                Emit emit) {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < n; i += kLpWarps) {
+        const float x = vals[i];
+        const int32_t id = ids[i];
+        if (id < 0 || x < least) continue;
+        int before = 0;
+        for (int j = lane; j < n; j += 32) before += ids[j] >= 0 && better(vals[j], ids[j], x, id) ? 1 : 0;
+        const int rank = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0 && rank < top) emit(rank, i);
+    }
+}
+
+// The candidates of vectors [v0, v1) for its first `top` elements, in sh.vals
+// and sh.ids; returns how many.  `m`: the maximum of this thread's vectors.
+template <bool F32>
+__device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, float m, LpShared &sh) {
+    constexpr int VE = Row<F32>::VE;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // ---- the top-th largest of the threads' maxima, by the upper half of its key (bf16 has no more)
+    const uint32_t key = order_key(m);
+    uint32_t bound = 0;
+    auto refine = [&](int from, int to) {
+        for (int bit = from; bit >= to; --bit) {
+            const uint32_t cand = bound | (1u << bit);
+            if (__syncthreads_count(key >= cand) >= top) bound = cand;
+        }
+    };
+    refine(31, 16);
+    const int per = (v1 - v0 + kLpThreads - 1) / kLpThreads;  // vectors of a thread
+    // ---- what the threads that reach it hold; strict: above it only
+    uint32_t unit = 0x10000u;  // what the bound resolves
+    for (int strict = 0; strict < 2; ++strict) {
+        if (tid == 0) sh.n_flagged = sh.n = 0;
+        __syncthreads();
+        const uint32_t least = strict ? bound + unit : bound;
+        if (key >= least) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = tid;
+        __syncthreads();
+        const int todo = sh.n_flagged * per;
+        for (int p = tid; p < todo; p += kLpThreads) {
+            const int f = p / per, v = v0 + sh.flagged[f] + (p - f * per) * kLpThreads;
+            if (v >= v1) continue;
+            float x[VE];
+            row.load(v, x);
+            float vm = x[0];
+#pragma unroll
+            for (int j = 1; j < VE; ++j) vm = fmaxf(vm, x[j]);
+            if (order_key(vm) < least) continue;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                const int64_t e = row.element(v, j);
+                if (order_key(x[j]) >= least && e >= 0 && e < row.vocab) {
+                    const int at = atomicAdd(&sh.n, 1);
+                    if (at < kLpCandidates) {
+                        sh.vals[at] = x[j];
+                        sh.ids[at] = static_cast<int32_t>(e);
+                    }
+                }
+            }
         }
         __syncthreads();
-    }
-    m = sm[0], l = sl[0], t = st[0];
-    const bool any = m != -INFINITY;
-    const float lz = any ? logf(l) : 0.0f;
-    if (tid == 0) {
-        const int64_t tgt = a.targets[r];
-        if (tgt >= v) atomicOr(&g_lp_err, ERRBIT_INDEX);
-        float lp = 0.0f;
-        if (tgt >= 0 && tgt < v) lp = any ? (logit<F32>(row, tgt) - m) - lz : -INFINITY;
-        a.logprobs[r] = lp;
-        a.entropy[r] = any ? lz - t / l : 0.0f;
-    }
-    // top alternatives: k times the best one after the last in the order
-    float px = INFINITY;
-    int32_t pi = -1;
-    for (int64_t n = 0; n < a.top; ++n) {
+        if (sh.n <= kLpCandidates) {
+            const int n = sh.n;
+            if (!strict || n >= top) return n;
+            // ---- and of the many equals at the bound the lowest indices
+            int have = n;
+            for (int v = v0; v < v1 && have < top; v += kLpThreads) {
+                float x[VE];
+                uint32_t eq = 0;
+                if (v + tid < v1) {
+                    row.load(v + tid, x);
+#pragma unroll
+                    for (int j = 0; j < VE; ++j) {
+                        const int64_t e = row.element(v + tid, j);
+                        // equal in what the bound resolves of the key
+                        const uint32_t k = order_key(x[j]);
+                        if (k - bound < unit && e >= 0 && e < row.vocab) eq |= 1u << j;
+                    }
+                }
+                const int mine = __popc(eq);
+                int upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                if (lane == 31) sh.counts[warp] = upto;
+                __syncthreads();
+                int at = have + upto - mine, all = 0;
+                for (int w = 0; w < kLpWarps; ++w) {
+                    if (w < warp) at += sh.counts[w];
+                    all += sh.counts[w];
+                }
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    if ((eq >> j) & 1) {
+                        if (at < top) {
+                            sh.vals[at] = x[j];
+                            sh.ids[at] = static_cast<int32_t>(row.element(v + tid, j));
+                        }
+                        ++at;
+                    }
+                have += all;
+                __syncthreads();
+            }
+            return min(have, top);
+        }
         __syncthreads();
+        if (F32 && !strict) {  // values of one upper half are not equals
+            refine(15, 0);
+            unit = 1;
+        }
+    }
+    // ---- more values above the bound than fit: take the best one after the last, `top` times
+    float last_x = INFINITY;
+    int32_t last_i = -1;
+    int n = 0;
+    for (; n < top; ++n) {
         float bx = -INFINITY;
         int32_t bi = 0x7fffffff;
-        for (int64_t i = tid; i < v; i += kLpThreads) {
-            const float x = logit<F32>(row, i);
-            const bool after = x < px || (x == px && i > pi);
-            if (after && (x > bx || (x == bx && i < bi))) bx = x, bi = static_cast<int32_t>(i);
-        }
-        sm[tid] = bx, si[tid] = bi;
-        __syncthreads();
-        for (int s = kLpThreads / 2; s > 0; s >>= 1) {
-            if (tid < s) {
-                if (sm[tid + s] > sm[tid] || (sm[tid + s] == sm[tid] && si[tid + s] < si[tid]))
-                    sm[tid] = sm[tid + s], si[tid] = si[tid + s];
+        for (int v = v0 + tid; v < v1; v += kLpThreads) {
+            float x[VE];
+            row.load(v, x);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                const int64_t e = row.element(v, j);
+                if (e < 0 || e >= row.vocab) continue;
+                const int32_t i = static_cast<int32_t>(e);
+                if (better(last_x, last_i, x[j], i) && better(x[j], i, bx, bi)) bx = x[j], bi = i;
             }
-            __syncthreads();
         }
-        px = sm[0], pi = si[0];
-        if (tid == 0) {
-            a.top_ids[r * a.top + n] = pi;
-            a.top_logprobs[r * a.top + n] = any ? (px - m) - lz : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float y = __shfl_xor_sync(0xffffffffu, bx, o);
+            const int32_t i = __shfl_xor_sync(0xffffffffu, bi, o);
+            if (better(y, i, bx, bi)) bx = y, bi = i;
+        }
+        __syncthreads();
+        if (lane == 0) sh.warp[warp].m = bx, sh.counts[warp] = bi;
+        __syncthreads();
+        for (int w = 0; w < kLpWarps; ++w)
+            if (better(sh.warp[w].m, sh.counts[w], bx, bi)) bx = sh.warp[w].m, bi = sh.counts[w];
+        if (bi == 0x7fffffff) break;  // none left (NaN among the values)
+        if (tid == 0) sh.vals[n] = bx, sh.ids[n] = bi;
+        last_x = bx, last_i = bi;
+    }
+    __syncthreads();
+    return n;
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobArgs a, int splits) {
+    constexpr int VE = Row<F32>::VE;
+    constexpr int kFlight = 4;  // 16-byte loads in flight per thread
+    __shared__ LpShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t r = blockIdx.x / splits;
+    const int part = static_cast<int>(blockIdx.x - r * splits);  // rank in the cluster
+    const int top = static_cast<int>(a.top);
+    if (splits > 1) cluster_arrive();  // the first CTA's shared memory is there once all have
+    pdl_wait();
+    const Row<F32> row(static_cast<const char *>(a.logits) + r * a.row_stride * (F32 ? 4 : 2), a.vocab);
+    const int v0 = static_cast<int>(static_cast<int64_t>(row.vecs) * part / splits);
+    const int v1 = static_cast<int>(static_cast<int64_t>(row.vecs) * (part + 1) / splits);
+
+    int64_t target = -1;
+    float x_target = 0.0f;
+    if (part == 0 && tid == 0) {
+        target = __ldg(a.targets + r);
+        if (target >= 0 && target < a.vocab) {
+            const char *p = static_cast<const char *>(a.logits) + (r * a.row_stride + target) * (F32 ? 4 : 2);
+            if constexpr (F32) x_target = *reinterpret_cast<const float *>(p);
+            else x_target = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p));
         }
     }
+    FastSums fast;
+    int v = v0 + tid;
+    if (v < v1 && !row.whole(v)) {  // the row's ragged start
+        float x[VE];
+        const float vm = row.load_fast(v, x);
+        fast.add<VE>(x, vm);
+        v += kLpThreads;
+    }
+    const int v_whole = v1 > v0 && !row.whole(v1 - 1) ? v1 - 1 : v1;
+    for (; v + (kFlight - 1) * kLpThreads < v_whole; v += kFlight * kLpThreads) {
+        uint4 w[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) w[i] = ld_nc_v4(row.base + static_cast<int64_t>(v + i * kLpThreads) * 16);
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            float x[VE];
+            const float vm = Row<F32>::unpack_fast(w[i], x);
+            fast.add<VE>(x, vm);
+        }
+    }
+    for (; v < v1; v += kLpThreads) {
+        float x[VE];
+        const float vm = row.load_fast(v, x);
+        fast.add<VE>(x, vm);
+    }
+    Sums s = fast.sums();
+    if (__syncthreads_or(!fast.ordinary())) {  // somewhere a maximum the fast sums cannot hold
+        s = Sums{-INFINITY, 0.0f, 0.0f};
+        for (v = v0 + tid; v < v1; v += kLpThreads) {
+            float x[VE];
+            row.load(v, x);
+            add_any<VE>(s, x);
+        }
+    }
+
+    const Sums w = warp_merge(s);
+    if (lane == 0) sh.warp[warp] = w;
+    __syncthreads();
+    Sums all = warp_merge(sh.warp[lane % kLpWarps], kLpWarps);
+    int n = 0;
+    if (top > 0) n = find_candidates<F32>(row, v0, v1, top, s.m, sh);
+
+    const float *vals = sh.vals;
+    const int32_t *ids = sh.ids;
+    float least = -INFINITY;
+    if (splits > 1) {
+        // the part's sums and first `top` go to the first CTA's shared memory
+        const uint32_t to = 0;
+        cluster_wait();
+        if (tid == 0) {
+            const uint32_t p = dsmem_map(smem_u32(&sh.part[part]), to);
+            dsmem_st_f32(p, all.m);
+            dsmem_st_f32(p + 4, all.l);
+            dsmem_st_f32(p + 8, all.t);
+        }
+        if (top > 0) {
+            const uint32_t pv = dsmem_map(smem_u32(&sh.part_vals[part * top]), to);
+            const uint32_t pi = dsmem_map(smem_u32(&sh.part_ids[part * top]), to);
+            for (int i = tid; i < top; i += kLpThreads)
+                if (i >= n) dsmem_st_f32(pi + 4 * i, __int_as_float(-1));
+            rank_candidates(sh.vals, sh.ids, n, top, least, [&](int rank, int i) {
+                dsmem_st_f32(pv + 4 * rank, sh.vals[i]);
+                dsmem_st_f32(pi + 4 * rank, __int_as_float(sh.ids[i]));
+            });
+        }
+        __syncwarp();
+        cluster_sync_all();
+        if (part != 0) return;
+        const Sums none{-INFINITY, 0.0f, 0.0f};
+        all = warp_merge(lane < splits ? sh.part[lane] : none);
+        vals = sh.part_vals;
+        ids = sh.part_ids;
+        n = splits * top;
+        // a part with `top` candidates has them all at or above its last
+        if (lane < splits && top > 0 && ids[lane * top + top - 1] >= 0) least = vals[lane * top + top - 1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) least = fmaxf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+
+    const bool any = all.m != -INFINITY;
+    const float lz = any ? logf(all.l) : 0.0f;
+    if (tid == 0) {
+        if (target >= a.vocab) atomicOr(&g_lp_err, ERRBIT_INDEX);
+        a.logprobs[r] = target < 0 || target >= a.vocab ? 0.0f : any ? (x_target - all.m) - lz : -INFINITY;
+        a.entropy[r] = any ? lz - all.t / all.l : 0.0f;
+    }
+    if (top > 0) {
+        int32_t *out_ids = a.top_ids + r * top;
+        float *out = a.top_logprobs + r * top;
+        int live = 0;  // candidates there are; fewer than top only where NaN took the others' places
+        for (int i = lane; i < n; i += 32) live += ids[i] >= 0 ? 1 : 0;
+        live = __reduce_add_sync(0xffffffffu, live);
+        for (int i = live + tid; i < top; i += kLpThreads) {
+            out_ids[i] = -1;
+            out[i] = -INFINITY;
+        }
+        rank_candidates(vals, ids, n, top, least, [&](int rank, int i) {
+            out_ids[rank] = ids[i];
+            out[rank] = any ? (vals[i] - all.m) - lz : -INFINITY;
+        });
+    }
+}
+
+// CTAs per row: as many as keep the GPU's two CTAs per SM busy in one wave,
+// while each still has a vector per thread.
+int pick_row_split(const LogprobArgs &a) {
+    const int64_t vecs = a.vocab / (a.f32 ? 4 : 8);
+    int s = 1;
+    while (s < kLpMaxSplit && 2 * s * a.rows <= 2 * static_cast<int64_t>(device_sm_count()) && vecs / (2 * s) >= kLpThreads)
+        s *= 2;
+    return s;
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
-    if (a.f32) logprobs_kernel<true><<<static_cast<unsigned>(a.rows), kLpThreads, 0, stream>>>(a);
-    else logprobs_kernel<false><<<static_cast<unsigned>(a.rows), kLpThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int splits = pick_row_split(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows * splits), 1, 1);
+    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return a.f32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a, splits)
+                 : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a, splits);
 }
 
 uint32_t take_logprobs_error() {
