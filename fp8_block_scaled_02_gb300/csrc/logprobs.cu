@@ -381,7 +381,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, flo
 template <bool F32>
 __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobArgs a, int splits) {
     constexpr int VE = Row<F32>::VE;
-    constexpr int kFlight = 4;  // 16-byte loads in flight per thread
+    constexpr int kFlight = 6;  // 16-byte loads in flight per thread: 132 us at 2048 x 152064 bf16, 138 with 4
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / splits;

@@ -74,6 +74,15 @@ def test_padded_and_unaligned_rows(pkg, pad, offset, dtype):
     check(pkg, x, [0, 3000, 1500, 7, 8], 20)
 
 
+@pytest.mark.parametrize("dtype,v", [(torch.bfloat16, 24576 + 8), (torch.bfloat16, 25003), (torch.float32, 12289),
+                                     (torch.float32, 20000)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_more_rows_than_a_wave_of_long_ones(pkg, dtype, v, pad):
+    """More CTAs than fit at once, rows of every alignment."""
+    x = logits(330, v, v, dtype, pad)
+    check(pkg, x, np.random.default_rng(v).integers(0, v, 330), 4)
+
+
 @pytest.mark.parametrize("v", [70, 5000, 152064])
 @pytest.mark.parametrize("low", [-np.inf, "lowest"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
