@@ -224,6 +224,23 @@ class _Args:
         return self.ptrs[name]
 
 
+def _checked(*specs):
+    """_Args' checks of (name, tensor, dtype, numel or None, rows) in one
+    quick pass; raises what _Args raises.  Returns the call's device."""
+    first = getattr(specs[0][1], "device", None)
+    for _, t, dtype, numel, _ in specs:
+        if (getattr(t, "device", None) != first or t.dtype != dtype or (numel is not None and t.numel() != numel)
+                or not t.is_contiguous()):
+            break
+    else:
+        if first.type == "cuda":
+            return first
+    a = _Args()
+    for name, t, dtype, numel, rows in specs:
+        a.need(name, t, dtype, numel=numel, rows=rows)
+    return a.check().device
+
+
 def _raw_stream(stream, device):
     """The cudaStream_t a call on `device` runs on."""
     import torch
@@ -232,7 +249,7 @@ def _raw_stream(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _on_device(device, what, fn, call_args, stream):
+def _call(device, what, fn, call_args, stream=None):
     """fn(*call_args, stream) with `device` current."""
     import torch
     raw = _raw_stream(stream, device)
@@ -248,7 +265,7 @@ def _on_device(device, what, fn, call_args, stream):
 def _run(args: _Args, what: str, fn, *call_args, stream=None):
     """Call the library on the device of the call's tensors, on that
     device's current stream unless one is given."""
-    _on_device(args.device, what, fn, call_args, stream)
+    _call(args.device, what, fn, call_args, stream)
 
 
 def _shape2(t, name):
@@ -547,16 +564,16 @@ KvPlan = collections.namedtuple("KvPlan", "seq_lens cu_new slots positions reque
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs entropy top_ids top_logprobs")
 
 
-def _outputs(stream, device, make):
-    """make(), a call's own outputs: in the memory pool of the stream the call
-    runs on, so that their memory is not handed out again while it runs."""
+def _empty(stream, device, shape, dtype):
+    """A call's own output: in the memory pool of the stream the call runs on,
+    so that its memory is not handed out again while it runs."""
     import torch
-    if stream is None or device.type != "cuda":
-        return make()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     with torch.cuda.stream(stream):
-        return make()
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _row_stride(t):
@@ -577,27 +594,30 @@ def kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size: 
     rows, max_blocks = _shape2(block_table, "block_table")
     if rows != b:
         raise ValueError("block_table and ctx_lens disagree on the number of requests")
+    num_tokens = int(num_tokens)
     if num_tokens < 0:
         raise ValueError("num_tokens must not be negative")
     i32 = torch.int32
-    a = _Args().need("ctx_lens", ctx_lens, i32).need("new_lens", new_lens, i32, numel=b) \
-        .need("block_table", block_table, i32).need("free_blocks", free_blocks, i32) \
-        .need("free_head", free_head, i32, numel=1)
-    outs = [slots, positions, requests, seq_lens, cu_new, free_head_out]
-    sizes = [num_tokens, num_tokens, num_tokens, b, b + 1, 1]
-    for name, t, n in zip(("slots", "positions", "requests", "seq_lens", "cu_new", "free_head_out"), outs, sizes):
-        if t is not None:
-            a.need(name, t, i32, numel=n)
-    a.check()
+    outs = (slots, positions, requests, seq_lens, cu_new, free_head_out)
+    sizes = (num_tokens, num_tokens, num_tokens, b, b + 1, 1)
+    given = [(name, t, i32, n, False) for name, t, n in
+             zip(("slots", "positions", "requests", "seq_lens", "cu_new", "free_head_out"), outs, sizes)
+             if t is not None]
+    device = _checked(("ctx_lens", ctx_lens, i32, None, False), ("new_lens", new_lens, i32, b, False),
+                      ("block_table", block_table, i32, None, False), ("free_blocks", free_blocks, i32, None, False),
+                      ("free_head", free_head, i32, 1, False), *given)
     # one allocation holds every output the caller did not give
-    sizes = [n if t is None else 0 for t, n in zip(outs, sizes)]
-    own = _outputs(stream, a.device, lambda: torch.empty(sum(sizes), dtype=i32, device=a.device)).split(sizes)
-    outs = [o if t is None else t for t, o in zip(outs, own)]
-    p_slots, p_pos, p_req, p_seq, p_cu, p_head = [t.data_ptr() for t in outs]
-    _run(a, "fp8bs_kv_plan", lib().fp8bs_kv_plan, a.ptr("ctx_lens"), a.ptr("new_lens"), b, a.ptr("block_table"),
-         max_blocks, a.ptr("free_blocks"), free_blocks.numel(), a.ptr("free_head"), int(page_size), int(num_blocks),
-         int(num_tokens), p_seq, p_cu, p_slots, p_pos, p_req, p_head, stream=stream)
-    slots, positions, requests, seq_lens, cu_new, free_head_out = outs
+    if given:
+        sizes = [n if t is None else 0 for t, n in zip(outs, sizes)]
+    own = torch.split_with_sizes(_empty(stream, device, (sum(sizes),), i32), sizes)
+    if given:
+        own = [o if t is None else t for t, o in zip(outs, own)]
+    slots, positions, requests, seq_lens, cu_new, free_head_out = own
+    _call(device, "fp8bs_kv_plan", lib().fp8bs_kv_plan,
+          (ctx_lens.data_ptr(), new_lens.data_ptr(), b, block_table.data_ptr(), max_blocks, free_blocks.data_ptr(),
+           free_blocks.numel(), free_head.data_ptr(), int(page_size), int(num_blocks), num_tokens, seq_lens.data_ptr(),
+           cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), requests.data_ptr(), free_head_out.data_ptr()),
+          stream)
     return KvPlan(seq_lens, cu_new, slots, positions, requests, free_head_out)
 
 
@@ -608,15 +628,17 @@ def kv4_cache_shape(num_blocks: int, page_size: int, num_kv_heads: int, head_dim
     return num_blocks, num_kv_heads, page_size // 16, 9 * head_dim
 
 
-def _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d):
-    """Records a pair of 4-bit caches and their scales; returns the _Args, num_blocks and page_size."""
+def _kv4_specs(k_cache, v_cache, k_scale, v_scale, hkv, d):
+    """What _checked has to see of a pair of 4-bit caches and their scales, num_blocks and page_size."""
     import torch
     shape = k_cache.shape
     if len(shape) != 4 or shape[1] != hkv or shape[3] != 9 * d:
         raise ValueError(f"k_cache has shape {tuple(shape)}, expected [num_blocks, {hkv}, page_size / 16, {9 * d}]")
-    a = _Args().need("k_cache", k_cache, torch.uint8).need("v_cache", v_cache, torch.uint8, shape=shape) \
-        .need("k_scale", k_scale, torch.float32, numel=1).need("v_scale", v_scale, torch.float32, numel=1)
-    return a, shape[0], shape[2] * 16
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(shape)}")
+    u8, f32 = torch.uint8, torch.float32
+    return (("k_cache", k_cache, u8, None, False), ("v_cache", v_cache, u8, None, False),
+            ("k_scale", k_scale, f32, 1, False), ("v_scale", v_scale, f32, 1, False)), shape[0], shape[2] * 16
 
 
 def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
@@ -624,15 +646,15 @@ def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
     token slots, in place (fp4kv_append).  k and v may be slices of a fused
     projection: only the rows of one token have to be contiguous."""
     import torch
-    if k.dim() != 3:
-        raise ValueError("k must be [T, Hkv, D]")
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, D]")
     t, hkv, d = k.shape
-    a, nb, page = _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d)
-    a.need("k", k, torch.bfloat16, rows=True).need("v", v, torch.bfloat16, shape=k.shape, rows=True) \
-        .need("slots", slots, torch.int32, numel=t).check()
-    _run(a, "fp4kv_append", lib().fp4kv_append, a.ptr("k"), _row_stride(k), a.ptr("v"), _row_stride(v), t, hkv, d,
-         a.ptr("slots"), a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("k_cache"), a.ptr("v_cache"), page, nb,
-         stream=stream)
+    specs, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, hkv, d)
+    device = _checked(*specs, ("slots", slots, torch.int32, t, False), ("k", k, torch.bfloat16, None, True),
+                      ("v", v, torch.bfloat16, None, True))
+    _call(device, "fp4kv_append", lib().fp4kv_append,
+          (k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), t, hkv, d, slots.data_ptr(),
+           k_scale.data_ptr(), v_scale.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page, nb), stream)
     return k_cache, v_cache
 
 
@@ -642,17 +664,14 @@ def kv4_gather(k_cache, v_cache, slots, k_scale, v_scale, k=None, v=None, stream
     if k_cache.dim() != 4 or k_cache.shape[3] % 9 != 0:
         raise ValueError("k_cache must be [num_blocks, Hkv, page_size / 16, 9 * D]")
     t, hkv, d = slots.numel(), k_cache.shape[1], k_cache.shape[3] // 9
-    a, nb, page = _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d)
-    a.need("slots", slots, torch.int32)
-    for name, x in (("k", k), ("v", v)):
-        if x is not None:
-            a.need(name, x, torch.bfloat16, numel=t * hkv * d)
-    a.check()
-    make = lambda: torch.empty((t, hkv, d), dtype=torch.bfloat16, device=a.device)
-    k = _outputs(stream, a.device, make) if k is None else k
-    v = _outputs(stream, a.device, make) if v is None else v
-    _run(a, "fp4kv_gather", lib().fp4kv_gather, a.ptr("k_cache"), a.ptr("v_cache"), a.ptr("slots"), t, hkv, d, page,
-         nb, a.ptr("k_scale"), a.ptr("v_scale"), k.data_ptr(), v.data_ptr(), stream=stream)
+    specs, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, hkv, d)
+    given = [(name, x, torch.bfloat16, t * hkv * d, False) for name, x in (("k", k), ("v", v)) if x is not None]
+    device = _checked(*specs, ("slots", slots, torch.int32, None, False), *given)
+    k = _empty(stream, device, (t, hkv, d), torch.bfloat16) if k is None else k
+    v = _empty(stream, device, (t, hkv, d), torch.bfloat16) if v is None else v
+    _call(device, "fp4kv_gather", lib().fp4kv_gather,
+          (k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), t, hkv, d, page, nb, k_scale.data_ptr(),
+           v_scale.data_ptr(), k.data_ptr(), v.data_ptr()), stream)
     return k, v
 
 
@@ -688,25 +707,21 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
     if bt_rows != b or (cu_q is None and t != b):
         raise ValueError("q, block_table and seq_lens disagree on the number of sequences")
     hkv = k_cache.shape[1] if k_cache.dim() == 4 else 0
-    a, nb, page = _kv4_args(k_cache, v_cache, k_scale, v_scale, hkv, d)
-    a.need("q", q, torch.bfloat16, rows=True).need("block_table", block_table, torch.int32) \
-        .need("seq_lens", seq_lens, torch.int32).need("workspace", workspace, torch.uint8)
-    if cu_q is not None:
-        a.need("cu_q", cu_q, torch.int32, numel=b + 1)
-    if out is not None:
-        a.need("out", out, torch.bfloat16, numel=t * hq * d)
-    if lse is not None:
-        a.need("lse", lse, torch.float32, numel=t * hq)
-    a.check()
+    specs, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, hkv, d)
+    given = [spec for spec in (("cu_q", cu_q, torch.int32, b + 1, False), ("out", out, torch.bfloat16, t * hq * d, False),
+                               ("lse", lse, torch.float32, t * hq, False)) if spec[1] is not None]
+    device = _checked(*specs, ("block_table", block_table, torch.int32, None, False),
+                      ("seq_lens", seq_lens, torch.int32, None, False), ("workspace", workspace, torch.uint8, None, False),
+                      *given, ("q", q, torch.bfloat16, None, True))
     if out is None:
-        out = _outputs(stream, a.device, lambda: torch.empty((t, hq, d), dtype=torch.bfloat16, device=a.device))
+        out = _empty(stream, device, (t, hq, d), torch.bfloat16)
     if lse is None and return_lse:
-        lse = _outputs(stream, a.device, lambda: torch.empty((t, hq), dtype=torch.float32, device=a.device))
-    _run(a, "fp4kv_decode_attention", lib().fp4kv_decode_attention, a.ptr("q"), _row_stride(q),
-         a.ptr("cu_q") if cu_q is not None else None, t, int(max_q), a.ptr("k_cache"), a.ptr("v_cache"),
-         a.ptr("k_scale"), a.ptr("v_scale"), a.ptr("block_table"), max_blocks, a.ptr("seq_lens"), b, hq, hkv, d,
-         page, nb, int(max_seq_len), int(window), float(sm_scale), out.data_ptr(),
-         lse.data_ptr() if lse is not None else None, a.ptr("workspace"), workspace.numel(), stream=stream)
+        lse = _empty(stream, device, (t, hq), torch.float32)
+    _call(device, "fp4kv_decode_attention", lib().fp4kv_decode_attention,
+          (q.data_ptr(), _row_stride(q), cu_q.data_ptr() if cu_q is not None else None, t, int(max_q), k_cache.data_ptr(),
+           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), max_blocks,
+           seq_lens.data_ptr(), b, hq, hkv, d, page, nb, int(max_seq_len), int(window), float(sm_scale), out.data_ptr(),
+           lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.numel()), stream)
     return (out, lse) if return_lse else out
 
 
@@ -717,22 +732,19 @@ def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, t
     (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
     import torch
     m, v = _shape2(logits, "logits")
+    top = int(top)
     f32 = logits.dtype == torch.float32
-    a = _Args().need("logits", logits, torch.float32 if f32 else torch.bfloat16, rows=True) \
-        .need("targets", targets, torch.int32, numel=m)
-    outs = [logprobs, entropy, top_logprobs, top_ids]
-    shapes = [(m,), (m,), (m, top), (m, top)]
-    dtypes = [torch.float32, torch.float32, torch.float32, torch.int32]
-    for name, t, shape, dtype in zip(("logprobs", "entropy", "top_logprobs", "top_ids"), outs, shapes, dtypes):
-        if t is not None:
-            a.need(name, t, dtype, numel=m if len(shape) == 1 else m * top)
-    a.check()
-    outs = [_outputs(stream, a.device, lambda: torch.empty(shape, dtype=dtype, device=a.device)) if t is None else t
-            for t, shape, dtype in zip(outs, shapes, dtypes)]
-    logprobs, entropy, top_logprobs, top_ids = outs
-    _run(a, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs, a.ptr("logits"), int(f32),
-         max(_row_stride(logits), v), m, v, a.ptr("targets"), int(top), logprobs.data_ptr(), entropy.data_ptr(),
-         top_ids.data_ptr(), top_logprobs.data_ptr(), stream=stream)
+    outs = (("logprobs", logprobs, torch.float32, (m,)), ("entropy", entropy, torch.float32, (m,)),
+            ("top_ids", top_ids, torch.int32, (m, top)), ("top_logprobs", top_logprobs, torch.float32, (m, top)))
+    given = [(name, t, dtype, m if len(shape) == 1 else m * top, False) for name, t, dtype, shape in outs
+             if t is not None]
+    device = _checked(("logits", logits, torch.float32 if f32 else torch.bfloat16, None, True),
+                      ("targets", targets, torch.int32, m, False), *given)
+    logprobs, entropy, top_ids, top_logprobs = [_empty(stream, device, shape, dtype) if t is None else t
+                                                for _, t, dtype, shape in outs]
+    _call(device, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs,
+          (logits.data_ptr(), int(f32), max(_row_stride(logits), v), m, v, targets.data_ptr(), top,
+           logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr()), stream)
     return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
 
 
