@@ -684,10 +684,10 @@ def kv4_workspace_bytes(head_dim: int) -> int:
 
 
 def kv4_workspace(head_dim: int, device="cuda"):
-    """A workspace for kv4_decode_attention: one serves every shape of a head
-    size, but only one call at a time."""
+    """A workspace for kv4_decode_attention (zeroed once, here): one serves
+    every shape of a head size, but only one call at a time."""
     import torch
-    return torch.empty(kv4_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
+    return torch.zeros(kv4_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
 
 
 def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_seq_len: int,

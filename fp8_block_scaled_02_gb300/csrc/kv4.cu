@@ -15,6 +15,7 @@
 // A tile is 16 tokens of one kv head: codes, then scales, contiguous, so a
 // whole tile is one aligned copy of 9 D bytes.
 #include "common.cuh"
+#include "fp8bs.h"
 #include "internal.h"
 
 #include <mutex>
@@ -137,8 +138,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a)
 // units of all segments into equal shares (every CTA finds its own from a
 // prefix sum of the lengths), so a ragged batch fills the GPU evenly and a
 // single long sequence is spread over all of it.  A segment that crosses a
-// share's end leaves partial (m, l, o) records in the workspace, which
-// kv4_combine_kernel joins in the order of the CTAs.
+// share's end leaves partial (m, l, o) records in the workspace; the CTA that
+// leaves the last one joins them, in the order of the CTAs.
 //
 // A CTA is a producer warp and W consumer warps around a ring of S units.  The
 // producer walks the share and copies four units at a time, a lane per tile
@@ -186,16 +187,6 @@ struct AttnCfg {
     static constexpr int kRecFloats = R * (D + 2);  // m[R], l[R], o[R][D]
     static constexpr int kSmemBytes = S * kStageBytes + W * kRecFloats * 4 + S * (8 + 8 + 4);
     static_assert(kSmemBytes * kRes <= 226 * 1024, "shared memory per SM");
-};
-
-// One split segment, left by the CTA that holds its first part.
-struct SplitDesc {
-    int32_t last;     // last CTA of the segment; -1: none starts here
-    int32_t q0;       // first query token of the sequence
-    int32_t rows;     // rows of the tile
-    int32_t row0;     // first row of the tile
-    int32_t kvh;
-    int32_t pad[3];
 };
 
 // One sequence's share of the line of units.
@@ -315,13 +306,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     uint64_t *empty = full + S;
     int32_t *holds = reinterpret_cast<int32_t *>(empty + S);              // which tiles a stage holds, a bit each
     __shared__ int64_t s_sums[W + 1], s_p;
-    __shared__ int s_b;
+    __shared__ int s_b, s_first, s_parts;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hkv = static_cast<int>(a.kv_heads), group = static_cast<int>(a.q_heads / a.kv_heads);
     const int batch = static_cast<int>(a.batch), cta = blockIdx.x;
-    SplitDesc *desc = reinterpret_cast<SplitDesc *>(a.workspace);
-    float *records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + 2 * kMaxSms * sizeof(SplitDesc));
+    uint32_t *arrived = static_cast<uint32_t *>(a.workspace);  // [2 kMaxSms], 0 between calls
+    float *records = reinterpret_cast<float *>(arrived + 2 * kMaxSms);
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
@@ -329,8 +320,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         }
         fence_mbarrier_init();
     }
-    pdl_launch_dependents();  // the combine kernel waits for the end of this grid
-    pdl_wait();               // q, the cache and the lengths may come from the previous kernel
+    pdl_wait();  // q, the cache and the lengths may come from the previous kernel
 
     // ---- this CTA's share
     const int per = (batch + C::kThreads - 1) / C::kThreads;
@@ -358,7 +348,6 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         total += s_sums[w];
     }
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kMinShare - 1) / kMinShare);
-    if (tid == 0) desc[cta].last = -1;
     if (cta >= ctas) return;
     const int64_t lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
     if (lo >= before && lo < before + mine) {
@@ -544,6 +533,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             const uint32_t have = static_cast<uint32_t>(holds[st]);
             const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + UT * T;
             const int key0 = (walk.w.tile0 + (walk.u0 + u) * UT) * kKv4Tile;
+            const bool ragged = have != (1u << UT) - 1 || key0 + C::kKeys > walk.w.len;
 
             // ---- S^T: lane holds keys kv4_row(g), + 8 of each tile, rows 2t, 2t + 1 of each n
             float s[UT][NT][4];
@@ -602,7 +592,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[h][n][j] *= sc[n][j & 1];
-            if (have != (1u << UT) - 1 || key0 + C::kKeys > clear_hi || key0 < clear_lo) {
+            if (ragged || key0 + C::kKeys > clear_hi || key0 < clear_lo) {
 #pragma unroll
                 for (int h = 0; h < UT; ++h)
 #pragma unroll
@@ -672,7 +662,6 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int h = 0; h < UT; ++h) {
-                if (!((have >> h) & 1)) continue;  // never copied
                 uint32_t sb[4], w[4][D / 64];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -686,8 +675,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                         w[j][0] = *reinterpret_cast<const uint32_t *>(src);
                     }
                     sb[j] = vt[h * T + 8 * D + row * (D / 16) + g * D / 128];
-                    // keys past the end have weight 0, but old bytes there may be NaN
-                    if (key0 + h * kKv4Tile + row >= walk.w.len) sb[j] = 0;
+                }
+                if (ragged) {  // keys past the end and tiles left out have weight 0, but old bytes there may be NaN
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = kv4_row(2 * t + (j & 1)) + 8 * (j >> 1);
+                        if (!((have >> h) & 1) || key0 + h * kKv4Tile + row >= walk.w.len) sb[j] = 0;
+                    }
                 }
                 const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
 #pragma unroll
@@ -794,72 +788,71 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 *reinterpret_cast<float4 *>(out_rec + 2 * R + r * D + d4 * 4) = O;
             }
         }
-        if (starts && !ends && tid == 0) {  // the share's last piece: where the segment ends
-            SplitDesc *sd = desc + cta;
-            sd->q0 = q0;
-            sd->rows = min(rows, R);
-            sd->row0 = row0;
-            sd->kvh = head0 / group;
-            sd->last = static_cast<int32_t>(((hi + walk.w.units - walk.u1) * ctas + total - 1) / total - 1);
+        if (starts && ends) {
+            bar_consumers(W * 32);  // the records are free again
+            continue;
         }
-        bar_consumers(W * 32);  // the records are free again
+        // ---- a part of a split segment: the last of its CTAs to come here joins them, in their order
+        __threadfence();
+        bar_consumers(W * 32);
+        if (tid == 0) {
+            // the line's step of the segment's first unit, and whose share a step is in
+            const int64_t at = starts ? hi - walk.u1 : lo - walk.u0;
+            auto owner = [&](int64_t step) { return static_cast<int>(((step + 1) * ctas + total - 1) / total - 1); };
+            const int c0 = owner(at), parts = owner(at + walk.w.units - 1) - c0 + 1;
+            const uint32_t before = atomicInc(arrived + c0, static_cast<uint32_t>(parts - 1));  // wraps to 0
+            s_first = c0;
+            s_parts = before == static_cast<uint32_t>(parts - 1) ? parts : 0;
+        }
+        bar_consumers(W * 32);
+        const int parts = s_parts;
+        if (parts == 0) continue;  // merge, s_first and s_parts are written after the next piece's barriers only
+        __threadfence();
+        auto part = [&](int j) { return records + static_cast<int64_t>(2 * (s_first + j) + (j == 0)) * C::kRecFloats; };
+        const int live = min(rows, R);
+        // weights of the parts, and v_scale / l, per row
+        static_assert(2 + kMaxSms * C::kRes <= W * (D + 2), "merge holds them");
+        for (int r = warp; r < live; r += W) {
+            float M = -INFINITY;
+            for (int j = lane; j < parts; j += 32) M = fmaxf(M, __ldcg(part(j) + r));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            float L = 0.0f;
+            for (int j = lane; j < parts; j += 32) {
+                const float m = __ldcg(part(j) + r), f = m == -INFINITY ? 0.0f : ex2(m - M);
+                L += f * __ldcg(part(j) + R + r);
+                merge[2 * R + j * R + r] = f;
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            if (lane == 0) {
+                merge[r] = L > 0.0f ? v_scale / L : 0.0f;
+                if (a.lse) {
+                    const int tok = (row0 + r) / group, h = row0 + r - tok * group;
+                    a.lse[static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h] =
+                        L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+        bar_consumers(W * 32);
+        for (int e = tid; e < live * D / 4; e += W * 32) {
+            const int r = e / (D / 4), d4 = e - r * (D / 4);
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int j = 0; j < parts; ++j) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(j) + 2 * R + r * D + d4 * 4));
+                const float f = merge[2 * R + j * R + r];
+                // a part without keys has no sum that is a number
+                if (f > 0.0f) O.x += f * v.x, O.y += f * v.y, O.z += f * v.z, O.w += f * v.w;
+            }
+            const int tok = (row0 + r) / group, h = row0 + r - tok * group;
+            const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
+            const float inv = merge[r];
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d4 * 4) =
+                make_uint2(f32x2_to_bf16x2(O.x * inv, O.y * inv), f32x2_to_bf16x2(O.z * inv, O.w * inv));
+        }
+        bar_consumers(W * 32);
     }
-}
-
-// Joins the parts of split segments: CTA (c, r) row r of the segment that
-// starts in share c and goes on in shares c + 1 .. last.
-constexpr int kCombineThreads = 128;
-
-template <int D, int NT>
-__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Kv4AttnArgs a) {
-    using C = AttnCfg<D, NT>;
-    constexpr int R = C::R, V = D / 32;  // V elements per lane
-    __shared__ float s_o[kCombineThreads / 32][D];
-    const int c = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
-    const SplitDesc sd = reinterpret_cast<const SplitDesc *>(a.workspace)[c];
-    if (sd.last < 0 || r >= sd.rows) return;
-    const float *records =
-        reinterpret_cast<const float *>(static_cast<const uint8_t *>(a.workspace) + 2 * kMaxSms * sizeof(SplitDesc));
-    const int n = sd.last - c + 1;
-    auto part = [&](int j) { return records + static_cast<int64_t>(2 * (c + j) + (j == 0)) * C::kRecFloats; };
-    float M = -INFINITY;
-    for (int j = lane; j < n; j += 32) M = fmaxf(M, part(j)[r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.0f;
-    for (int j = lane; j < n; j += 32) {
-        const float m = part(j)[r];
-        if (m != -INFINITY) L += ex2(m - M) * part(j)[R + r];
-    }
-    L = [&] {
-        float v = L;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    }();
-    float acc[V] = {};
-#pragma unroll 4
-    for (int j = warp; j < n; j += kCombineThreads / 32) {
-        const float *p = part(j);
-        const float m = p[r], f = m == -INFINITY ? 0.0f : ex2(m - M);
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += f * p[2 * R + r * D + i * 32 + lane];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) s_o[warp][i * 32 + lane] = acc[i];
-    __syncthreads();
-    const int group = static_cast<int>(a.q_heads / a.kv_heads);
-    const int tok = (sd.row0 + r) / group, h = sd.row0 + r - tok * group;
-    const int64_t row = static_cast<int64_t>(sd.q0 + tok) * a.q_heads + sd.kvh * group + h;
-    const float inv = L > 0.0f ? __ldg(a.v_scale) / L : 0.0f;
-    for (int d = threadIdx.x; d < D; d += kCombineThreads) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kCombineThreads / 32; ++w) v += s_o[w][d];
-        static_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(v * inv);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int D, int NT>
@@ -890,12 +883,7 @@ cudaError_t launch_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(ctas, C::R, 1);
-    cfg.blockDim = dim3(kCombineThreads, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, NT>, a);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int D>
@@ -937,7 +925,8 @@ cudaError_t launch_kv4_gather(const Kv4CopyArgs &a, cudaStream_t stream) {
 }
 
 int64_t kv4_attention_ws_bytes(int64_t head_dim) {
-    return 2 * kMaxSms * static_cast<int64_t>(sizeof(SplitDesc)) + int64_t{2} * kMaxSms * 32 * (head_dim + 2) * 4;
+    static_assert(2 * kMaxSms * 4 == FP4KV_WORKSPACE_COUNTER_BYTES, "the counters are first");
+    return 2 * kMaxSms * 4 + int64_t{2} * kMaxSms * 32 * (head_dim + 2) * 4;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t stream) {

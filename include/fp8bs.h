@@ -652,12 +652,15 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  *                16-byte aligned, written
  *   lse          device, [num_q_tokens, num_q_heads] fp32, written, or NULL
  *   workspace    device, 16-byte aligned, >= fp4kv_attention_ws_bytes(head_dim)
- *                bytes: the partial results of sequences split over CTAs.
- *                Its contents do not matter before or after; calls that
+ *                bytes: the partial results of sequences split over CTAs, and
+ *                counters of their arrival in its first
+ *                FP4KV_WORKSPACE_COUNTER_BYTES, which have to be zero before
+ *                its first use; every call leaves them zero.  Calls that
  *                overlap on the GPU need one each
  * The split of the work follows the lengths on the device: results are
  * deterministic for given shapes and lengths.
  */
+#define FP4KV_WORKSPACE_COUNTER_BYTES 1280
 int64_t fp4kv_attention_ws_bytes(int64_t head_dim);
 int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride,
                            const int32_t *cu_q, int64_t num_q_tokens,

@@ -20,6 +20,7 @@ from oracle.tolerance import bf16_bits_to_f64
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 KS, VS = np.float32(5.5 / 2688), np.float32(6.25 / 2688)
+COUNTERS = 1280                                                   # FP4KV_WORKSPACE_COUNTER_BYTES
 
 
 @pytest.fixture(scope="module")
@@ -158,11 +159,14 @@ def layer(lens, hkv, d, page, seed, extra=2):
 def attend(pkg, q, kc, vc, table, lens, sm, max_len=None, **kw):
     ks, vs = scales()
     t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
-    ws = pkg.kv4_workspace(kc.shape[3] // 9, DEV).fill_(0xA5)
+    ws = pkg.kv4_workspace(kc.shape[3] // 9, DEV)
+    ws[COUNTERS:] = 0xA5
     if kw.get("cu_q") is not None:
         kw["cu_q"] = t(np.asarray(kw["cu_q"], dtype=np.int32))
-    return pkg.kv4_decode_attention(q.to(DEV), t(kc), t(vc), ks, vs, t(table), t(np.asarray(lens, dtype=np.int32)),
-                                    max(max(lens), 1) if max_len is None else max_len, sm, ws, return_lse=True, **kw)
+    r = pkg.kv4_decode_attention(q.to(DEV), t(kc), t(vc), ks, vs, t(table), t(np.asarray(lens, dtype=np.int32)),
+                                 max(max(lens), 1) if max_len is None else max_len, sm, ws, return_lse=True, **kw)
+    assert int(ws[:COUNTERS].max()) == 0                          # as the next call needs them
+    return r
 
 
 def check(o, lse, q, cu, kc, vc, table, lens, sm, window=0, err=0, pkg=None):
