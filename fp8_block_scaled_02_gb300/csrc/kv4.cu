@@ -163,7 +163,7 @@ constexpr float kPShift = 14.0f;
 constexpr int kMaxSms = 160;  // CTAs the workspace has records for: two per SM of 16 rows, or one of 32
 // What a segment costs besides its units (its q, the merge of the warps, its
 // output), in units; shares are equal in units + kSegCost a segment.
-constexpr int kSegCost = 6;
+constexpr int kSegCost = 12;
 constexpr int kMinShare = 8;  // a CTA's share at least
 
 // A producer warp, W consumer warps and a ring of S units per CTA, kRes CTAs
