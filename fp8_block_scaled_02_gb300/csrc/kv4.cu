@@ -451,6 +451,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     const float v_scale = __ldg(a.v_scale);
     constexpr int kLaneCodes = D / 4;  // codes of a key a lane holds for S^T
     constexpr int kSteps = D / 16;
+    constexpr bool kQRegs = NT == 1;
+    static_assert(NT * kSteps * 32 * 8 <= C::kRecFloats * 4, "a record holds q");
     uint32_t count = 0;  // units of the pieces before this one
     int turn = 0;        // count % W
     bool failed = false;
@@ -470,7 +472,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         const int first_pos = walk.w.len - walk.w.n_q;  // position of query token 0
 
         // ---- q as f16 B fragments, an exact power-of-two rescale per row
-        uint32_t bq[NT][kSteps][2];
+        // (in registers for one n, else in the warp's record, which is free until the piece ends)
+        uint32_t bq[kQRegs ? NT : 1][kSteps][2];
+        uint2 *sq = reinterpret_cast<uint2 *>(merge + warp * C::kRecFloats) + lane;  // [NT][kSteps][32]
         float sc[NT][2];   // score scale of this lane's columns 2t, 2t + 1
         int pos[NT][2];    // their positions
 #pragma unroll
@@ -496,10 +500,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             const float up = pow2_int(e), down = pow2_int(-e);
 #pragma unroll
             for (int i = 0; i < kLaneCodes / 8; ++i) {
-                bq[n][2 * i][0] = f32x2_to_f16x2(bf16lo_to_f32(v[i].x) * up, bf16hi_to_f32(v[i].x) * up);
-                bq[n][2 * i][1] = f32x2_to_f16x2(bf16lo_to_f32(v[i].y) * up, bf16hi_to_f32(v[i].y) * up);
-                bq[n][2 * i + 1][0] = f32x2_to_f16x2(bf16lo_to_f32(v[i].z) * up, bf16hi_to_f32(v[i].z) * up);
-                bq[n][2 * i + 1][1] = f32x2_to_f16x2(bf16lo_to_f32(v[i].w) * up, bf16hi_to_f32(v[i].w) * up);
+                const uint2 b0 = make_uint2(f32x2_to_f16x2(bf16lo_to_f32(v[i].x) * up, bf16hi_to_f32(v[i].x) * up),
+                                            f32x2_to_f16x2(bf16lo_to_f32(v[i].y) * up, bf16hi_to_f32(v[i].y) * up));
+                const uint2 b1 = make_uint2(f32x2_to_f16x2(bf16lo_to_f32(v[i].z) * up, bf16hi_to_f32(v[i].z) * up),
+                                            f32x2_to_f16x2(bf16lo_to_f32(v[i].w) * up, bf16hi_to_f32(v[i].w) * up));
+                if constexpr (kQRegs) {
+                    bq[n][2 * i][0] = b0.x, bq[n][2 * i][1] = b0.y;
+                    bq[n][2 * i + 1][0] = b1.x, bq[n][2 * i + 1][1] = b1.y;
+                } else {
+                    sq[(n * kSteps + 2 * i) * 32] = b0;
+                    sq[(n * kSteps + 2 * i + 1) * 32] = b1;
+                }
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -582,9 +593,12 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16_16816(s[h][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1],
-                                      bq[n][i][0], bq[n][i][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        uint2 b;
+                        if constexpr (kQRegs) b = make_uint2(bq[n][i][0], bq[n][i][1]);
+                        else b = sq[(n * kSteps + i) * 32];
+                        mma_f16_16816(s[h][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1], b.x, b.y);
+                    }
             }
 #pragma unroll
             for (int h = 0; h < UT; ++h)
@@ -739,6 +753,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         }
         // ---- the warps' parts of the piece: m[R], l[R], o[R][D] each
         float *rec = merge + warp * C::kRecFloats;
+        __syncwarp();  // q has been read
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -891,6 +906,7 @@ cudaError_t launch_attn_rows(const Kv4AttnArgs &a, cudaStream_t stream) {
     const int64_t rows = a.max_q * (a.q_heads / a.kv_heads);
     if (rows <= 8) return launch_attn<D, 1>(a, stream);
     if (rows <= 16) return launch_attn<D, 2>(a, stream);
+    if (rows <= 24) return launch_attn<D, 3>(a, stream);
     return launch_attn<D, 4>(a, stream);
 }
 
