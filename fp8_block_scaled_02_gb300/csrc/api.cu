@@ -488,7 +488,7 @@ int check_kv4_cache(int64_t kv_heads, int64_t head_dim, int64_t page_size, int64
     if (kv_heads <= 0 || kv_heads >= 4096 || (head_dim != 64 && head_dim != 128)) return FP8BS_ERR_SHAPE;
     if (page_size < kKv4Tile || page_size % kKv4Tile != 0 || page_size > 4096) return FP8BS_ERR_SHAPE;
     if (num_blocks <= 0 || num_blocks >= kMaxDim || num_blocks * page_size >= kMaxDim) return FP8BS_ERR_SHAPE;
-    if (num_blocks * (page_size / kKv4Tile) * kv_heads >= 2 * kMaxDim - 2) return FP8BS_ERR_SHAPE;  // 32-bit tile numbers
+    if (num_blocks * (page_size / kKv4Tile) * kv_heads >= kMaxDim) return FP8BS_ERR_SHAPE;  // int32 tile numbers
     return FP8BS_OK;
 }
 

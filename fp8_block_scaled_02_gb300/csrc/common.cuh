@@ -120,6 +120,19 @@ __device__ __forceinline__ void tma_load_2d_hint(void *smem_dst, const CUtensorM
         : "memory");
 }
 
+// Four rows of a 2-D map whose box is one row, from column x: row[0 .. 3] one
+// after the other in shared memory (128-byte aligned).  A row out of range
+// reads zeros.
+__device__ __forceinline__ void tma_gather4_2d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t x,
+                                               const int32_t (&row)[4]) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]),
+        "r"(row[3])
+        : "memory");
+}
+
 // Untiled bulk copy of `bytes` (a multiple of 16; both addresses 16-byte
 // aligned) from global to this CTA's shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load_g2s(void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {

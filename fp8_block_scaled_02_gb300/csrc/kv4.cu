@@ -19,6 +19,7 @@
 #include "internal.h"
 
 #include <mutex>
+#include <utility>
 
 namespace fp8bs {
 
@@ -142,10 +143,12 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a)
 // leaves the last one joins them, in the order of the CTAs.
 //
 // A CTA is a producer warp and W consumer warps around a ring of S units.  The
-// producer walks the share and copies four units at a time, a lane per tile
-// (K and V of a unit are one run each where the page holds it); it is pieces
-// ahead of the consumers, so table lookups and copies cost no time between
-// them.  The consumers of a piece take its units in turn and join their
+// producer walks the share and copies units in pairs, by one gather of four
+// tiles for K and one for V wherever they lie (a tile is a row of the cache's
+// map); a warp issues a bulk copy in some 235 clocks, and copies of one or two
+// tiles, as pages of 16 allow, cost 143 us at 16 x 32768 keys of 8 heads, where this takes 134.
+// It is pieces ahead of the consumers, so table lookups and copies cost no
+// time between them.  The consumers of a piece take its units in turn and join their
 // (m, l, o) in shared memory; a segment of one unit is one warp's alone, beside
 // others.  Per unit:
 //   S^T[32 keys, R rows] = K q^T with f16 mma.sync m16n8k16.  The order of
@@ -177,15 +180,16 @@ struct AttnCfg {
     // A stage belongs to one consumer warp: unit i of a CTA is warp i % W's and
     // in stage i % S, with W a divisor of S.  Copies land in any order, and a
     // warp that waited for the next phase of a stage before the last one is
-    // complete would take the phase before that for it.
-    static constexpr int S = NT == 2 ? 15 : 14;
-    static_assert(S % W == 0, "a stage's units are one warp's");
+    // complete would take the phase before that for it.  Units are copied in
+    // pairs, so S is even.
+    static constexpr int S = NT == 2 ? 10 : 14;
+    static_assert(S % W == 0 && S % 2 == 0, "a stage's units are one warp's");
     static constexpr int kThreads = (W + 1) * 32;
     static constexpr int R = 8 * NT;
     static constexpr int T = 9 * D;                 // bytes of a tile
     static constexpr int kStageBytes = 2 * UT * T;
     static constexpr int kRecFloats = R * (D + 2);  // m[R], l[R], o[R][D]
-    static constexpr int kSmemBytes = S * kStageBytes + W * kRecFloats * 4 + S * (8 + 8 + 4);
+    static constexpr int kSmemBytes = S * kStageBytes + W * kRecFloats * 4 + S * (4 + 4 + 4);
     static_assert(kSmemBytes * kRes <= 226 * 1024, "shared memory per SM");
 };
 
@@ -274,6 +278,8 @@ struct Walk {
     }
 };
 
+constexpr uint32_t kNoTile = 0xffffffffu;  // a tile that is not there or left out: row -1 of the maps
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -296,15 +302,16 @@ __device__ __forceinline__ void bar_consumers(int threads) {
 __device__ __forceinline__ int kv4_row(int m) { return (m & 1) ? 4 + ((m >> 1) ^ 1) : m >> 1; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes) kv4_attn_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes) kv4_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Kv4AttnArgs a) {
     using C = AttnCfg<D, NT>;
     constexpr int W = C::W, R = C::R, T = C::T, UT = C::UT, S = C::S;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *ring = smem;                                                 // [S][K tiles | V tiles]
+    uint8_t *ring = smem;                                                 // [S / 2][K tiles | V tiles of two units]
     float *merge = reinterpret_cast<float *>(ring + S * C::kStageBytes);  // [W] records
     uint64_t *full = reinterpret_cast<uint64_t *>(merge + W * C::kRecFloats);
-    uint64_t *empty = full + S;
-    int32_t *holds = reinterpret_cast<int32_t *>(empty + S);              // which tiles a stage holds, a bit each
+    uint64_t *empty = full + S / 2;
+    int32_t *holds = reinterpret_cast<int32_t *>(empty + S / 2);              // which tiles a stage holds, a bit each
     __shared__ int64_t s_sums[W + 1], s_p;
     __shared__ int s_b, s_first, s_parts;
 
@@ -314,11 +321,15 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     uint32_t *arrived = static_cast<uint32_t *>(a.workspace);  // [2 kMaxSms], 0 between calls
     float *records = reinterpret_cast<float *>(arrived + 2 * kMaxSms);
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < S / 2; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
         }
         fence_mbarrier_init();
+    }
+    if (tid == 32) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
     }
     pdl_wait();  // q, the cache and the lengths may come from the previous kernel
 
@@ -369,31 +380,33 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     if (warp == W) {
         // ================================================== producer
         const int tpp = static_cast<int>(a.page_size) / kKv4Tile;
-        constexpr uint32_t kNoTile = 0xffffffffu;
-        constexpr int kWindow = 32 / UT;  // units whose tiles the lanes look up together
-        constexpr int kBatch = 4;         // units copied together
-        static_assert(UT == 2, "a lane for K and one for V");
-        uint32_t count = 0;               // units put into the ring
+        constexpr int kWindow = 32 / UT;  // units looked up together, a lane per tile
+        constexpr int kPairs = S / 2;     // pairs of units in the ring
+        uint32_t pairs = 0;               // pairs put into the ring before the window
         bool inside = walk.next(a, hkv, group);
         int ub = walk.u0;
-        // the next window of units: how many, and lane j's place of its tile j
+        // the next window of units, over piece ends: how many, and lane j's place of its tile j
         auto look_up = [&](uint32_t &place) -> int {
             place = kNoTile;
-            if (!inside) return 0;
-            const int n = min(kWindow, walk.u1 - ub);
-            const int tile = walk.w.tile0 + ub * UT + lane;
-            if (lane < n * UT && tile < walk.w.tiles) {
-                const int pg = tile / tpp;
-                const int32_t blk = __ldg(a.block_table + static_cast<int64_t>(walk.b) * a.max_blocks + pg);
-                if (blk >= 0 && blk < a.num_blocks)
-                    place = static_cast<uint32_t>((static_cast<int64_t>(blk) * hkv + walk.kvh) * tpp + (tile - pg * tpp));
-                else
-                    atomicOr(&g_kv4_err, ERRBIT_INDEX);  // left out
-            }
-            ub += n;
-            if (ub == walk.u1) {
-                inside = walk.next(a, hkv, group);
-                ub = walk.u0;
+            int n = 0;
+            while (inside && n < kWindow) {
+                const int take = min(kWindow - n, walk.u1 - ub);
+                const int tile = walk.w.tile0 + ub * UT + lane - n * UT;
+                if (lane >= n * UT && lane < (n + take) * UT && tile < walk.w.tiles) {
+                    const int pg = tile / tpp;
+                    const int32_t blk = __ldg(a.block_table + static_cast<int64_t>(walk.b) * a.max_blocks + pg);
+                    if (blk >= 0 && blk < a.num_blocks)
+                        place =
+                            static_cast<uint32_t>((static_cast<int64_t>(blk) * hkv + walk.kvh) * tpp + (tile - pg * tpp));
+                    else
+                        atomicOr(&g_kv4_err, ERRBIT_INDEX);  // left out
+                }
+                n += take;
+                ub += take;
+                if (ub == walk.u1) {
+                    inside = walk.next(a, hkv, group);
+                    ub = walk.u0;
+                }
             }
             return n;
         };
@@ -402,45 +415,41 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         int n = look_up(place);
         while (n > 0 && ok) {
             const int n_next = look_up(place_next);
-            // lane j: tile j % UT of unit j / UT; its unit's first place, what it holds, whether it is one run
-            const uint32_t pair = ((1u << UT) - 1) << (lane / UT * UT);
-            const uint32_t head = __shfl_sync(0xffffffffu, place, lane / UT * UT);
-            const uint32_t mask = __ballot_sync(0xffffffffu, place != kNoTile) & pair;
-            const uint32_t follows = __ballot_sync(0xffffffffu, place == head + lane % UT) & pair;
-            const bool run = mask == pair && follows == pair;
-            const uint32_t idx = count + lane / UT, st = idx % S, parity = (idx / S - 1) & 1;
-            uint8_t *dst = ring + st * C::kStageBytes;
-            const uint8_t *src = a.k_cache + static_cast<int64_t>(run ? head : place) * T;
-            const uint8_t *src_v = a.v_cache + static_cast<int64_t>(run ? head : place) * T;
-            for (int first = 0; first < n; first += kBatch) {
-                const bool live = lane / (kBatch * UT) == first / kBatch && lane < n * UT;
+            // lanes 2 j and 2 j + 1 copy K and V of pair j: four tiles each, rows of the caches' maps
+            int32_t row[2 * UT];
+#pragma unroll
+            for (int i = 0; i < 2 * UT; ++i)
+                row[i] = static_cast<int32_t>(__shfl_sync(0xffffffffu, place, ((lane / 2) * 2 * UT + i) & 31));
+            const uint32_t have = __ballot_sync(0xffffffffu, place != kNoTile);
+            const int window_pairs = (n + 1) / 2;
+            const uint32_t pair = pairs + lane / 2, st = pair % kPairs, parity = (pair / kPairs - 1) & 1;
+            uint8_t *dst = ring + st * (2 * C::kStageBytes) + lane % 2 * C::kStageBytes;
+            for (int first = 0; first < window_pairs; first += 2) {
+                const bool live = lane / 4 == first / 2 && lane / 2 < window_pairs;
                 bool free_now = true;
-                if (live && idx >= S) free_now = mbar_wait_bounded(&empty[st], parity);
+                if (live && pair >= kPairs) free_now = mbar_wait_bounded(&empty[st], parity);
                 ok = __all_sync(0xffffffffu, free_now);
                 if (!ok) {
-                    count += static_cast<uint32_t>(first);
+                    pairs += static_cast<uint32_t>(first);
                     break;
                 }
-                if (live && lane % UT == 0) {
-                    holds[st] = static_cast<int32_t>(mask >> lane);
-                    mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(mask) * 2 * T));
+                if (live) holds[2 * st + lane % 2] = static_cast<int32_t>((have >> (lane * UT)) & ((1u << UT) - 1));
+                __syncwarp();
+                if (live) {
+                    if (lane % 2 == 0) mbar_arrive_expect_tx(&full[st], 2 * C::kStageBytes);
+                    // a row out of range reads zeros
+                    tma_gather4_2d(dst, lane % 2 ? &tm_v : &tm_k, &full[st], 0, row);
                 }
                 __syncwarp();
-                if (live && run) {  // one lane copies the unit's K, the next its V
-                    bulk_load_g2s(dst + lane % UT * (UT * T), lane % UT ? src_v : src, UT * T, &full[st]);
-                } else if (live && place != kNoTile) {
-                    bulk_load_g2s(dst + lane % UT * T, src, T, &full[st]);
-                    bulk_load_g2s(dst + (UT + lane % UT) * T, src_v, T, &full[st]);
-                }
             }
-            if (ok) count += static_cast<uint32_t>(n);
+            if (ok) pairs += static_cast<uint32_t>(window_pairs);
             n = n_next;
             place = place_next;
         }
         if (!ok) {  // a consumer gave up: never leave with copies in flight
             if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_EMPTY_WAIT);
-            for (uint32_t idx = count > S ? count - S : 0; idx < count; ++idx)
-                (void)mbar_wait_bounded(&full[idx % S], (idx / S) & 1);
+            for (uint32_t i = pairs > kPairs ? pairs - kPairs : 0; i < pairs; ++i)
+                (void)mbar_wait_bounded(&full[i % kPairs], (i / kPairs) & 1);
         }
         return;
     }
@@ -536,13 +545,13 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 
         for (int u = first; u < n_units && !failed; u += W) {
             const uint32_t idx = piece + static_cast<uint32_t>(u), st = idx % S;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (idx / S) & 1))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[st / 2], (idx / S) & 1))) {
                 if (lane == 0) atomicOr(&g_kv4_err, ERRBIT_FULL_WAIT);
                 failed = true;
                 break;
             }
             const uint32_t have = static_cast<uint32_t>(holds[st]);
-            const uint8_t *kt = ring + st * C::kStageBytes, *vt = kt + UT * T;
+            const uint8_t *kt = ring + st / 2 * (2 * C::kStageBytes) + st % 2 * (UT * T), *vt = kt + C::kStageBytes;
             const int key0 = (walk.w.tile0 + (walk.u0 + u) * UT) * kKv4Tile;
             const bool ragged = have != (1u << UT) - 1 || key0 + C::kKeys > walk.w.len;
 
@@ -718,7 +727,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 }
             }
             __syncwarp();  // the stage has been read
-            if (lane == 0) mbar_arrive(&empty[st]);
+            if (lane == 0) mbar_arrive(&empty[st / 2]);
         }
 
 #pragma unroll
@@ -898,7 +907,13 @@ cudaError_t launch_attn(const Kv4AttnArgs &a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    CUtensorMap tm_k, tm_v;
+    const uint64_t tiles = static_cast<uint64_t>(a.num_blocks * (a.page_size / kKv4Tile) * a.kv_heads);
+    for (const auto &m : {std::make_pair(&tm_k, a.k_cache), std::make_pair(&tm_v, a.v_cache)})
+        if (!encode_tensor_map_2d(m.first, CU_TENSOR_MAP_DATA_TYPE_INT64, m.second, C::T / 8, tiles, C::T, C::T / 8, 1,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, a);
 }
 
 template <int D>
