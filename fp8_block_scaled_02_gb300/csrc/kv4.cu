@@ -30,100 +30,155 @@ namespace {
 __device__ uint32_t g_kv4_err;
 
 
-// The tile that holds slot `slot` of kv head `h`.
-__device__ __forceinline__ int64_t tile_index(int64_t slot, int h, int kv_heads, int page_size) {
-    const int64_t blk = slot / page_size;
-    const int off = static_cast<int>(slot - blk * page_size);
-    return (blk * kv_heads + h) * (page_size / kKv4Tile) + off / kKv4Tile;
-}
-
 // ------------------------------------------------------- append and gather
+// A thread has 32 consecutive elements of a head vector (two groups): 64 bytes
+// of bf16, 16 of codes and 2 of scales; a warp's accesses are contiguous.  Both
+// are bound by HBM (read 2 B, write 9/16 B an element, or the reverse).
 constexpr int kCopyThreads = 256;
 
-// One thread per group of 16 elements; blockIdx.y selects K or V.
-__global__ void __launch_bounds__(kCopyThreads) kv4_append_kernel(Kv4CopyArgs a) {
+__device__ __forceinline__ void ld_nc_v8(const void *p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+
+__device__ __forceinline__ void st_v8(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// The thread's pair of groups: token, and pair within the token's row.
+struct CopyItem {
+    int64_t token;
+    uint32_t pair;
+};
+
+// The thread's item: a block's items are contiguous.  `inverse` = ceil(2^64 / per_row)
+// divides every item number below 2^47 exactly by a multiplication.
+__device__ __forceinline__ CopyItem copy_item(uint64_t inverse, uint32_t per_row) {
+    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, t = __umul64hi(i, inverse);
+    return CopyItem{static_cast<int64_t>(t), static_cast<uint32_t>(i - t * per_row)};
+}
+
+// Where the codes and the scales of a pair of groups of a slot are.
+template <int D>
+__device__ __forceinline__ uint8_t *slot_codes(uint8_t *cache, uint32_t slot, uint32_t h, uint32_t pair, uint32_t kv_heads,
+                                               uint32_t tiles_per_page, uint8_t **scales) {
+    const uint32_t tile = slot / kKv4Tile, row = slot % kKv4Tile, blk = tile / tiles_per_page;
+    uint8_t *t = cache + ((static_cast<int64_t>(blk) * kv_heads + h) * tiles_per_page + (tile - blk * tiles_per_page)) *
+                             kv4_tile_bytes(D);
+    *scales = t + 8 * D + row * (D / 16) + 2 * pair;
+    return t + row * (D / 2) + 16 * pair;
+}
+
+// 16 bf16 values (8 words) -> their group's scale code and e2m1 codes.
+__device__ __forceinline__ uint32_t encode_group(const uint32_t *u, float s, float six_s, uint2 &codes) {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx = max_u16x2(mx, u[j] & 0x7FFF7FFFu);
+    const float amax = __uint_as_float(max(mx & 0xFFFFu, mx >> 16) << 16);
+    const uint32_t sc = f32x2_to_e4m3x2(amax / six_s, 0.0f) & 0xFFu;
+    const float den = f16x2_to_f32x2(e4m3x2_to_f16x2(sc)).x * s;
+    codes = make_uint2(0, 0);
+    if (den > 0.0f) {
+        float q[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            q[j >> 2][2 * (j & 3)] = bf16lo_to_f32(u[j]) / den;
+            q[j >> 2][2 * (j & 3) + 1] = bf16hi_to_f32(u[j]) / den;
+        }
+        codes = make_uint2(f32x8_to_e2m1x8(q[0]), f32x8_to_e2m1x8(q[1]));
+    }
+    return sc;
+}
+
+// blockIdx.y selects K or V; 64-byte pieces of x are 32-byte aligned if `wide`.
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads) kv4_append_kernel(Kv4CopyArgs a, uint64_t inverse, bool wide) {
     const bool is_v = blockIdx.y != 0;
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(is_v ? a.v : a.k);
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     uint8_t *cache = is_v ? a.v_cache : a.k_cache;
-    const int d = static_cast<int>(a.head_dim), groups = d / 16;
-    const int per_row = static_cast<int>(a.kv_heads) * groups;
+    const uint32_t kv_heads = static_cast<uint32_t>(a.kv_heads), per_row = kv_heads * (D / 32);
+    const uint32_t tpp = static_cast<uint32_t>(a.page_size / kKv4Tile);
+    const CopyItem it = copy_item(inverse, per_row);
+    pdl_launch_dependents();
     pdl_wait();
-    const float s = __ldg(is_v ? a.v_scale : a.k_scale);
-    const float six_s = 6.0f * s;
-    const int64_t total = a.tokens * per_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
-        const int64_t t = i / per_row;
-        const int e = static_cast<int>(i - t * per_row), h = e / groups, g = e - h * groups;
-        const int64_t slot = __ldg(a.slots + t);
-        if (slot < 0 || slot >= a.num_slots) {
-            if (slot != -1 && e == 0 && !is_v) atomicOr(&g_kv4_err, ERRBIT_INDEX);
-            continue;
-        }
-        const __nv_bfloat16 *src = x + t * stride + static_cast<int64_t>(e) * 16;
-        const uint4 w[2] = {ld_nc_v4(src), ld_nc_v4(src + 8)};
-        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-        uint32_t mx = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mx = max_u16x2(mx, u[j] & 0x7FFF7FFFu);
-        const float amax = __uint_as_float(max(mx & 0xFFFFu, mx >> 16) << 16);
-        const uint32_t sc = f32x2_to_e4m3x2(amax / six_s, 0.0f) & 0xFFu;
-        const float den = f16x2_to_f32x2(e4m3x2_to_f16x2(sc)).x * s;
-        uint2 codes = make_uint2(0, 0);
-        if (den > 0.0f) {
-            float q[2][8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                q[j >> 2][2 * (j & 3)] = bf16lo_to_f32(u[j]) / den;
-                q[j >> 2][2 * (j & 3) + 1] = bf16hi_to_f32(u[j]) / den;
-            }
-            codes = make_uint2(f32x8_to_e2m1x8(q[0]), f32x8_to_e2m1x8(q[1]));
-        }
-        uint8_t *tile = cache + tile_index(slot, h, static_cast<int>(a.kv_heads), static_cast<int>(a.page_size)) *
-                                    kv4_tile_bytes(d);
-        const int row = static_cast<int>(slot & (kKv4Tile - 1));
-        *reinterpret_cast<uint2 *>(tile + row * (d / 2) + g * 8) = codes;
-        tile[8 * d + row * groups + g] = static_cast<uint8_t>(sc);
+    if (it.token >= a.tokens) return;
+    const int64_t slot = __ldg(a.slots + it.token);
+    if (slot < 0 || slot >= a.num_slots) {
+        if (slot != -1 && it.pair == 0 && !is_v) atomicOr(&g_kv4_err, ERRBIT_INDEX);
+        return;
     }
+    const __nv_bfloat16 *src = x + it.token * stride + it.pair * 32;
+    uint32_t u[2][8];
+    if (wide) {
+        ld_nc_v8(src, u[0]);
+        ld_nc_v8(src + 16, u[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 w = ld_nc_v4(src + 8 * i);
+            uint32_t *d = u[i / 2] + 4 * (i & 1);
+            d[0] = w.x, d[1] = w.y, d[2] = w.z, d[3] = w.w;
+        }
+    }
+    const float s = __ldg(is_v ? a.v_scale : a.k_scale), six_s = 6.0f * s;
+    uint2 c0, c1;
+    const uint32_t s0 = encode_group(u[0], s, six_s, c0), s1 = encode_group(u[1], s, six_s, c1);
+    uint8_t *scales;
+    uint8_t *codes = slot_codes<D>(cache, static_cast<uint32_t>(slot), it.pair / (D / 32), it.pair % (D / 32), kv_heads,
+                                   tpp, &scales);
+    *reinterpret_cast<uint4 *>(codes) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+    *reinterpret_cast<uint16_t *>(scales) = static_cast<uint16_t>(s0 | (s1 << 8));
 }
 
-__global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a, uint64_t inverse, bool wide) {
     const bool is_v = blockIdx.y != 0;
-    const uint8_t *cache = is_v ? a.v_cache : a.k_cache;
-    uint4 *out = static_cast<uint4 *>(is_v ? a.v_out : a.k_out);
-    const int d = static_cast<int>(a.head_dim), groups = d / 16;
-    const int per_row = static_cast<int>(a.kv_heads) * groups;
+    uint8_t *cache = is_v ? a.v_cache : a.k_cache;
+    const uint32_t kv_heads = static_cast<uint32_t>(a.kv_heads), per_row = kv_heads * (D / 32);
+    const uint32_t tpp = static_cast<uint32_t>(a.page_size / kKv4Tile);
+    const CopyItem it = copy_item(inverse, per_row);
+    pdl_launch_dependents();
     pdl_wait();
-    const float s = __ldg(is_v ? a.v_scale : a.k_scale);
-    const int64_t total = a.tokens * per_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
-        const int64_t t = i / per_row;
-        const int e = static_cast<int>(i - t * per_row), h = e / groups, g = e - h * groups;
-        const int64_t slot = __ldg(a.slots + t);
-        uint32_t r[8] = {};
-        if (slot < 0 || slot >= a.num_slots) {
-            if (slot != -1 && e == 0 && !is_v) atomicOr(&g_kv4_err, ERRBIT_INDEX);
-        } else {
-            const uint8_t *tile = cache + tile_index(slot, h, static_cast<int>(a.kv_heads),
-                                                     static_cast<int>(a.page_size)) * kv4_tile_bytes(d);
-            const int row = static_cast<int>(slot & (kKv4Tile - 1));
-            const uint2 codes = *reinterpret_cast<const uint2 *>(tile + row * (d / 2) + g * 8);
-            const uint32_t sc = tile[8 * d + row * groups + g];
-            const uint32_t sc2 = e4m3x2_to_f16x2(sc | (sc << 8));
-            uint32_t h0[4], h1[4];
-            e2m1x8_to_f16x2x4(codes.x, h0);
-            e2m1x8_to_f16x2x4(codes.y, h1);
+    if (it.token >= a.tokens) return;
+    const int64_t slot = __ldg(a.slots + it.token);
+    uint32_t r[2][8] = {};
+    if (slot < 0 || slot >= a.num_slots) {
+        if (slot != -1 && it.pair == 0 && !is_v) atomicOr(&g_kv4_err, ERRBIT_INDEX);
+    } else {
+        uint8_t *scales;
+        const uint8_t *codes = slot_codes<D>(cache, static_cast<uint32_t>(slot), it.pair / (D / 32), it.pair % (D / 32),
+                                             kv_heads, tpp, &scales);
+        const uint4 c = ld_nc_v4(codes);
+        const uint32_t sc = *reinterpret_cast<const uint16_t *>(scales);
+        const float s = __ldg(is_v ? a.v_scale : a.k_scale);
+        const uint32_t s2 = e4m3x2_to_f16x2(sc), w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+            e2m1x8_to_f16x2x4(w[i], h);
+            const uint32_t scale2 = __byte_perm(s2, s2, i < 2 ? 0x1010 : 0x3232);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 lo = f16x2_to_f32x2(mul_f16x2(h0[j], sc2)), hi = f16x2_to_f32x2(mul_f16x2(h1[j], sc2));
-                r[j] = f32x2_to_bf16x2(lo.x * s, lo.y * s);
-                r[4 + j] = f32x2_to_bf16x2(hi.x * s, hi.y * s);
+                const float2 v = f16x2_to_f32x2(mul_f16x2(h[j], scale2));
+                r[i / 2][4 * (i & 1) + j] = f32x2_to_bf16x2(v.x * s, v.y * s);
             }
         }
-        out[2 * i] = make_uint4(r[0], r[1], r[2], r[3]);
-        out[2 * i + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(is_v ? a.v_out : a.k_out) +
+                         (it.token * per_row + it.pair) * 32;
+    if (wide) {
+        st_v8(out, r[0]);
+        st_v8(out + 16, r[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t *d = r[i / 2] + 4 * (i & 1);
+            *reinterpret_cast<uint4 *>(out + 8 * i) = make_uint4(d[0], d[1], d[2], d[3]);
+        }
     }
 }
 
@@ -176,7 +231,7 @@ constexpr int kMinShare = 8;  // a CTA's share at least
 template <int D, int NT>
 struct AttnCfg {
     static constexpr int kRes = NT <= 2 ? 2 : 1;
-    static constexpr int W = NT == 2 ? 5 : 7;
+    static constexpr int W = NT == 1 ? 8 : NT == 2 ? 5 : 7;
     static constexpr int UT = 2;                    // tiles per unit
     static constexpr int kKeys = UT * kKv4Tile;     // keys per unit
     // A stage belongs to one consumer warp: unit i of a CTA is warp i % W's and
@@ -184,7 +239,7 @@ struct AttnCfg {
     // warp that waited for the next phase of a stage before the last one is
     // complete would take the phase before that for it.  Units are copied in
     // pairs, so S is even.
-    static constexpr int S = NT == 2 ? 10 : 14;
+    static constexpr int S = 2 * W;
     static_assert(S % W == 0 && S % 2 == 0, "a stage's units are one warp's");
     static constexpr int kThreads = (W + 1) * 32;
     static constexpr int R = 8 * NT;
@@ -327,6 +382,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     int32_t *holds = reinterpret_cast<int32_t *>(empty + S / 2);              // which tiles a stage holds, a bit each
     __shared__ int64_t s_sums[W + 1], s_p;
     __shared__ int s_b, s_first, s_parts;
+    __shared__ Walk<R, UT> s_walk[W];
+    __shared__ struct {
+        int64_t total, ctas, lo, hi;  // of the line: its steps, the shares, this one
+    } s_line;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hkv = static_cast<int>(a.kv_heads), group = static_cast<int>(a.q_heads / a.kv_heads);
@@ -374,6 +433,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kMinShare - 1) / kMinShare);
     if (cta >= ctas) return;
     const int64_t lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
+    if (tid == 0) s_line.total = total, s_line.ctas = ctas, s_line.lo = lo, s_line.hi = hi;
     if (lo >= before && lo < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
@@ -473,37 +533,46 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     const float v_scale = __ldg(a.v_scale);
     constexpr int kLaneCodes = D / 4;  // codes of a key a lane holds for S^T
     constexpr int kSteps = D / 16;
-    constexpr bool kQRegs = NT == 1;
     static_assert(NT * kSteps * 32 * 8 <= C::kRecFloats * 4, "a record holds q");
     uint32_t count = 0;  // units of the pieces before this one
     int turn = 0;        // count % W
     bool failed = false;
 
-    while (walk.next(a, hkv, group)) {
+    // The walk stays in shared memory: what the unit loop does not need would
+    // cost it a dozen registers.
+    Walk<R, UT> &kept = s_walk[warp];
+    if (lane == 0) kept = walk;
+    __syncwarp();
+    while (true) {
+        Walk<R, UT> walk = kept;
+        __syncwarp();
+        const bool more = walk.next(a, hkv, group);
+        if (lane == 0) kept = walk;
+        __syncwarp();
+        if (!more) break;
         const int n_units = walk.u1 - walk.u0;
-        const bool starts = walk.u0 == 0, ends = walk.u1 == walk.w.units;
-        const bool alone = n_units == 1 && starts && ends;
+        const bool alone = n_units == 1 && walk.w.units == 1;
         int first = warp - turn;  // this warp's first unit of the piece
         if (first < 0) first += W;
         const uint32_t piece = count;
         count += static_cast<uint32_t>(n_units);
         turn = (turn + n_units) % W;
         if (alone && first != 0) continue;
-        const int row0 = walk.row_tile * R;
-        const int rows = walk.w.n_q * group - row0;     // rows left of the sequence (some may be other tiles')
+        const int tile_row0 = walk.row_tile * R;
+        const int tile_rows = walk.w.n_q * group - tile_row0;  // rows left of the sequence (some may be other tiles')
         const int first_pos = walk.w.len - walk.w.n_q;  // position of query token 0
 
         // ---- q as f16 B fragments, an exact power-of-two rescale per row
-        // (in registers for one n, else in the warp's record, which is free until the piece ends)
-        uint32_t bq[kQRegs ? NT : 1][kSteps][2];
+        // in the warp's record, which is free until the piece ends: with them in registers a thread would need
+        // more than the 96 that let a ninth warp run beside eight (129 us instead of 123 at 16 x 32768 keys)
         uint2 *sq = reinterpret_cast<uint2 *>(merge + warp * C::kRecFloats) + lane;  // [NT][kSteps][32]
         float sc[NT][2];   // score scale of this lane's columns 2t, 2t + 1
         int pos[NT][2];    // their positions
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = n * 8 + g;
-            const bool live = r < rows;
-            const int tok = live && walk.w.n_q > 1 ? (row0 + r) / group : 0, h = live ? row0 + r - tok * group : 0;
+            const bool live = r < tile_rows;
+            const int tok = live && walk.w.n_q > 1 ? (tile_row0 + r) / group : 0, h = live ? tile_row0 + r - tok * group : 0;
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
                                        static_cast<int64_t>(walk.w.q0 + tok) * a.q_stride +
                                        (walk.kvh * group + h) * D + t * kLaneCodes;
@@ -526,13 +595,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                                             f32x2_to_f16x2(bf16lo_to_f32(v[i].y) * up, bf16hi_to_f32(v[i].y) * up));
                 const uint2 b1 = make_uint2(f32x2_to_f16x2(bf16lo_to_f32(v[i].z) * up, bf16hi_to_f32(v[i].z) * up),
                                             f32x2_to_f16x2(bf16lo_to_f32(v[i].w) * up, bf16hi_to_f32(v[i].w) * up));
-                if constexpr (kQRegs) {
-                    bq[n][2 * i][0] = b0.x, bq[n][2 * i][1] = b0.y;
-                    bq[n][2 * i + 1][0] = b1.x, bq[n][2 * i + 1][1] = b1.y;
-                } else {
-                    sq[(n * kSteps + 2 * i) * 32] = b0;
-                    sq[(n * kSteps + 2 * i + 1) * 32] = b1;
-                }
+                sq[(n * kSteps + 2 * i) * 32] = b0;
+                sq[(n * kSteps + 2 * i + 1) * 32] = b1;
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -541,9 +605,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             }
         }
         // keys below `clear_hi` and from `clear_lo` on are seen by every row of the tile
-        const int last_tok = walk.w.n_q > 1 ? min(row0 + R - 1, walk.w.n_q * group - 1) / group : 0;
-        const int clear_hi = first_pos + (walk.w.n_q > 1 ? row0 / group : 0) + 1;
-        const int64_t clear_lo = a.window > 0 ? static_cast<int64_t>(first_pos) + last_tok - a.window + 1 : 0;
+        const int last_tok = walk.w.n_q > 1 ? min(tile_row0 + R - 1, walk.w.n_q * group - 1) / group : 0;
+        const int clear_hi = first_pos + (walk.w.n_q > 1 ? tile_row0 / group : 0) + 1;
+        const int clear_lo =
+            a.window > 0 ? static_cast<int>(max(int64_t{0}, static_cast<int64_t>(first_pos) + last_tok - a.window + 1)) : 0;
+        const int len = walk.w.len, piece_key = (walk.w.tile0 + walk.u0 * UT) * kKv4Tile;
 
         float m_run[NT][2], l_run[NT][2], o[NT][kSteps][4];
 #pragma unroll
@@ -565,8 +631,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             }
             const uint32_t have = static_cast<uint32_t>(holds[st]);
             const uint8_t *kt = ring + st / 2 * (2 * C::kStageBytes) + st % 2 * (UT * T), *vt = kt + C::kStageBytes;
-            const int key0 = (walk.w.tile0 + (walk.u0 + u) * UT) * kKv4Tile;
-            const bool ragged = have != (1u << UT) - 1 || key0 + C::kKeys > walk.w.len;
+            const int key0 = piece_key + u * C::kKeys;
+            const bool ragged = have != (1u << UT) - 1 || key0 + C::kKeys > len;
 
             // ---- S^T: lane holds keys kv4_row(g), + 8 of each tile, rows 2t, 2t + 1 of each n
             float s[UT][NT][4];
@@ -616,9 +682,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int i = 0; i < kSteps; ++i)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        uint2 b;
-                        if constexpr (kQRegs) b = make_uint2(bq[n][i][0], bq[n][i][1]);
-                        else b = sq[(n * kSteps + i) * 32];
+                        const uint2 b = sq[(n * kSteps + i) * 32];
                         mma_f16_16816(s[h][n], f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1], b.x, b.y);
                     }
             }
@@ -716,7 +780,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int row = kv4_row(2 * t + (j & 1)) + 8 * (j >> 1);
-                        if (!((have >> h) & 1) || key0 + h * kKv4Tile + row >= walk.w.len) sb[j] = 0;
+                        if (!((have >> h) & 1) || key0 + h * kKv4Tile + row >= len) sb[j] = 0;
                     }
                 }
                 const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
@@ -751,7 +815,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], off);
-        const int q0 = walk.w.q0, head0 = walk.kvh * group;
+        const int q0 = kept.w.q0, n_q = kept.w.n_q, head0 = kept.kvh * group, row0 = kept.row_tile * R;
+        const int rows = n_q * group - row0;
+        const bool starts = kept.u0 == 0, ends = kept.u1 == kept.w.units;
         if (alone) {  // lane: elements g D / 8 .. of rows 2t, 2t + 1 of each n
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -759,7 +825,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int c = 0; c < 2; ++c) {
                     const int r = n * 8 + 2 * t + c;
                     if (r >= rows) continue;
-                    const int tok = walk.w.n_q > 1 ? (row0 + r) / group : 0, h = row0 + r - tok * group;
+                    const int tok = n_q > 1 ? (row0 + r) / group : 0, h = row0 + r - tok * group;
                     const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
                     const float L = l_run[n][c], inv = L > 0.0f ? v_scale / L : 0.0f;
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + g * (D / 8));
@@ -835,9 +901,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         bar_consumers(W * 32);
         if (tid == 0) {
             // the line's step of the segment's first unit, and whose share a step is in
-            const int64_t at = starts ? hi - walk.u1 : lo - walk.u0;
-            auto owner = [&](int64_t step) { return static_cast<int>(((step + 1) * ctas + total - 1) / total - 1); };
-            const int c0 = owner(at), parts = owner(at + walk.w.units - 1) - c0 + 1;
+            const int64_t at = starts ? s_line.hi - kept.u1 : s_line.lo - kept.u0;
+            auto owner = [&](int64_t step) { return static_cast<int>(((step + 1) * s_line.ctas + s_line.total - 1) / s_line.total - 1); };
+            const int c0 = owner(at), parts = owner(at + kept.w.units - 1) - c0 + 1;
             const uint32_t before = atomicInc(arrived + c0, static_cast<uint32_t>(parts - 1));  // wraps to 0
             s_first = c0;
             s_parts = before == static_cast<uint32_t>(parts - 1) ? parts : 0;
@@ -939,16 +1005,14 @@ cudaError_t launch_attn_rows(const Kv4AttnArgs &a, cudaStream_t stream) {
     return launch_attn<D, 4>(a, stream);
 }
 
-int copy_blocks(const Kv4CopyArgs &a) {
-    const int64_t total = a.tokens * a.kv_heads * (a.head_dim / 16);
-    int64_t blocks = (total + kCopyThreads - 1) / kCopyThreads;
-    const int64_t cap = static_cast<int64_t>(device_sm_count()) * 8;
-    return static_cast<int>(blocks > cap ? cap : blocks);
-}
-
-cudaError_t launch_pdl(void (*kern)(Kv4CopyArgs), dim3 grid, const Kv4CopyArgs &a, cudaStream_t stream) {
+cudaError_t launch_copy(void (*kern)(Kv4CopyArgs, uint64_t, bool), const Kv4CopyArgs &a, bool wide, cudaStream_t stream) {
+    const uint64_t per_row = static_cast<uint64_t>(a.kv_heads * (a.head_dim / 32));  // >= 2
+    const uint64_t inverse = ~uint64_t{0} / per_row + 1;
+    const int64_t items = a.tokens * static_cast<int64_t>(per_row);
+    const int64_t blocks = (items + kCopyThreads - 1) / kCopyThreads;
+    if (blocks >= int64_t{1} << 31) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 2, 1);
     cfg.blockDim = dim3(kCopyThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -956,17 +1020,21 @@ cudaError_t launch_pdl(void (*kern)(Kv4CopyArgs), dim3 grid, const Kv4CopyArgs &
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, a, inverse, wide);
 }
+
+bool aligned32(const void *p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4CopyArgs &a, cudaStream_t stream) {
-    return launch_pdl(kv4_append_kernel, dim3(copy_blocks(a), 2, 1), a, stream);
+    const bool wide = aligned32(a.k) && aligned32(a.v) && a.k_stride % 16 == 0 && a.v_stride % 16 == 0;
+    return launch_copy(a.head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, a, wide, stream);
 }
 
 cudaError_t launch_kv4_gather(const Kv4CopyArgs &a, cudaStream_t stream) {
-    return launch_pdl(kv4_gather_kernel, dim3(copy_blocks(a), 2, 1), a, stream);
+    const bool wide = aligned32(a.k_out) && aligned32(a.v_out);
+    return launch_copy(a.head_dim == 128 ? kv4_gather_kernel<128> : kv4_gather_kernel<64>, a, wide, stream);
 }
 
 int64_t kv4_attention_ws_bytes(int64_t head_dim) {
