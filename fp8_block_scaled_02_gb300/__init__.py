@@ -48,6 +48,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 PATH_AUTO, PATH_DECODE, PATH_PREFILL, PATH_GENERIC = 0, 1, 2, 3
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DECODE: "decode", PATH_PREFILL: "prefill", PATH_GENERIC: "generic"}
 
@@ -158,7 +160,6 @@ def _check(status: int, what: str):
 
 
 def _stream(stream, device=None):
-    import torch
     if stream is None:
         return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, int):
@@ -184,7 +185,6 @@ class _Args:
         self.items = []
 
     def need(self, name, t, dtype, numel=None, shape=None, rows=False):
-        import torch
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if shape is not None and t.shape != tuple(shape):
@@ -224,13 +224,23 @@ class _Args:
         return self.ptrs[name]
 
 
+def _rows_contiguous(t):
+    """Whether every t[i] is contiguous."""
+    n = 1
+    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+        if size != 1 and stride != n:
+            return False
+        n *= size
+    return True
+
+
 def _checked(*specs):
     """_Args' checks of (name, tensor, dtype, numel or None, rows) in one
     quick pass; raises what _Args raises.  Returns the call's device."""
     first = getattr(specs[0][1], "device", None)
-    for _, t, dtype, numel, _ in specs:
+    for _, t, dtype, numel, rows in specs:
         if (getattr(t, "device", None) != first or t.dtype != dtype or (numel is not None and t.numel() != numel)
-                or not t.is_contiguous()):
+                or not (t.is_contiguous() or (rows and _rows_contiguous(t)))):
             break
     else:
         if first.type == "cuda":
@@ -243,7 +253,6 @@ def _checked(*specs):
 
 def _raw_stream(stream, device):
     """The cudaStream_t a call on `device` runs on."""
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
@@ -251,7 +260,6 @@ def _raw_stream(stream, device):
 
 def _call(device, what, fn, call_args, stream=None):
     """fn(*call_args, stream) with `device` current."""
-    import torch
     raw = _raw_stream(stream, device)
     if torch.cuda.current_device() == device.index:
         status = fn(*call_args, raw)
@@ -275,13 +283,11 @@ def _shape2(t, name):
 
 
 def _new(t, shape, dtype, like):
-    import torch
     return torch.empty(shape, dtype=dtype, device=like.device) if t is None else t
 
 
 def quantize(w, block: int = 128, codes=None, scales=None, stream=None):
     """Block-FP8 load-time quantization of a bf16 [N, K] CUDA tensor."""
-    import torch
     n, k = _shape2(w, "w")
     codes = _new(codes, (n, k), torch.uint8, w)
     scales = _new(scales, (cdiv(n, 128), cdiv(k, 128)), torch.float32, w)
@@ -293,7 +299,6 @@ def quantize(w, block: int = 128, codes=None, scales=None, stream=None):
 
 
 def _gemv_args(x, codes, y, scales, sdtype, snumel, check=True):
-    import torch
     m, k = _shape2(x, "x")
     n, k2 = _shape2(codes, "codes")
     if k2 != k:
@@ -310,7 +315,6 @@ def _block_numel(n, k):
 
 def gemv(x, codes, scales, y=None, path: int = PATH_AUTO, stream=None):
     """y[M, N] = x[M, K] . dequant(codes, scales)^T (bf16 out, fp32 accumulate)."""
-    import torch
     a, m, n, k, y = _gemv_args(x, codes, y, scales, torch.float32, _block_numel)
     _run(a, "fp8bs_gemv", lib().fp8bs_gemv_ex, a.ptr("x"), m, a.ptr("codes"), a.ptr("scales"), n, k, a.ptr("y"),
          int(path), stream=stream)
@@ -329,7 +333,6 @@ def gemv_ws(x, codes, scales, workspace, y=None, stream=None):
     """gemv with caller-provided device scratch (fp8bs_gemv_ws): x is
     converted once per call to f16 in `workspace` (a uint8 CUDA tensor of at
     least gemv_ws_bytes(M, K) bytes) and the decode kernel reads that copy."""
-    import torch
     a, m, n, k, y = _gemv_args(x, codes, y, scales, torch.float32, _block_numel, check=False)
     a.need("workspace", workspace, torch.uint8).check()
     _run(a, "fp8bs_gemv_ws", lib().fp8bs_gemv_ws, a.ptr("x"), m, a.ptr("codes"), a.ptr("scales"), n, k, a.ptr("y"),
@@ -338,7 +341,6 @@ def gemv_ws(x, codes, scales, workspace, y=None, stream=None):
 
 
 def _batch_ops(ops, mx):
-    import torch
     arr = (GemvOp * max(1, len(ops)))()
     if not ops:
         return arr, 0, [], None
@@ -374,7 +376,6 @@ def _batch_ops(ops, mx):
 
 
 def _run_batch(fn, what, ops, mx, path, stream):
-    import torch
     arr, m, ys, device = _batch_ops(ops, mx)
     if not ops:
         return ys
@@ -402,7 +403,6 @@ class GemvBatch:
         self.ops = ops  # keeps the tensors alive
 
     def __call__(self, stream=None):
-        import torch
         if not self.count:
             return self.ys
         with torch.cuda.device(self.device):
@@ -419,7 +419,6 @@ def mx_gemv_batch(ops, path: int = PATH_AUTO, stream=None):
 
 def mx_quantize(w, codes=None, e8m0=None, stream=None):
     """MXFP8 load-time quantization of a bf16 [N, K] CUDA tensor."""
-    import torch
     n, k = _shape2(w, "w")
     codes = _new(codes, (n, k), torch.uint8, w)
     e8m0 = _new(e8m0, (n, cdiv(k, 32)), torch.uint8, w)
@@ -431,7 +430,6 @@ def mx_quantize(w, codes=None, e8m0=None, stream=None):
 
 def mx_gemv(x, codes, e8m0, y=None, path: int = PATH_AUTO, stream=None):
     """y[M, N] = x[M, K] . dequant_mx(codes, e8m0)^T."""
-    import torch
     a, m, n, k, y = _gemv_args(x, codes, y, e8m0, torch.uint8, lambda n, k: n * cdiv(k, 32))
     _run(a, "mxfp8_gemv", lib().mxfp8_gemv_ex, a.ptr("x"), m, a.ptr("codes"), a.ptr("scales"), n, k, a.ptr("y"),
          int(path), stream=stream)
@@ -439,7 +437,6 @@ def mx_gemv(x, codes, e8m0, y=None, path: int = PATH_AUTO, stream=None):
 
 
 def _rowwise_quantize(fn, what, w, codes, scales, count, stream):
-    import torch
     n, k = _shape2(w, "w")
     codes = _new(codes, (n, k), torch.uint8, w)
     scales = _new(scales, (count(n),), torch.float32, w)
@@ -462,7 +459,6 @@ def tensor_quantize(w, codes=None, scale=None, stream=None):
 def row_gemv(x, codes, scales, y=None, path: int = PATH_AUTO, stream=None):
     """y[M, N] = x[M, K] . (dec(codes) * s_row)^T.  ``scales`` of shape [N]
     calls fp8row_gemv, of shape [1] fp8tensor_gemv."""
-    import torch
     n = _shape2(codes, "codes")[0]
     per_row = tuple(scales.shape) == (n,) and n > 1
     if not per_row and tuple(scales.shape) not in ((1,), ()):
@@ -475,7 +471,6 @@ def row_gemv(x, codes, scales, y=None, path: int = PATH_AUTO, stream=None):
 
 
 def _moe_args(x, ids, codes, scales, y):
-    import torch
     m, k = _shape2(x, "x")
     if codes.dim() != 3:
         raise ValueError("codes must be [E, N, K]")
@@ -513,7 +508,6 @@ def moe_gemv_ws(x, ids, codes, scales, workspace, y=None, stream=None):
     than 32 tokens run as one grouped tensor-core GEMM over the routed
     experts; `workspace` is a uint8 CUDA tensor of at least
     moe_gemv_ws_bytes(M, topk, E, K) bytes."""
-    import torch
     a, m, topk, e, n, k, y = _moe_args(x, ids, codes, scales, y)
     a.need("workspace", workspace, torch.uint8).check()
     _run(a, "fp8bs_moe_gemv_ws", lib().fp8bs_moe_gemv_ws, a.ptr("x"), m, a.ptr("ids"), topk, a.ptr("codes"),
@@ -524,7 +518,6 @@ def moe_gemv_ws(x, ids, codes, scales, workspace, y=None, stream=None):
 def kv_append(x, slots, scale, cache, stream=None):
     """Quantize new keys or values x [T, Hkv, 128] bf16 into the e4m3 cache
     [num_blocks, page_size, Hkv, 128] at flat token slots (in place)."""
-    import torch
     if x.dim() != 3 or cache.dim() != 4:
         raise ValueError("x must be [T, Hkv, 128] and cache [num_blocks, page_size, Hkv, 128]")
     t, hkv, d = x.shape
@@ -541,7 +534,6 @@ def kv_append(x, slots, scale, cache, stream=None):
 def kv_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_seq_len: int,
                         sm_scale: float, out=None, stream=None):
     """Paged decode attention over the FP8 KV cache: q [B, Hq, 128] bf16."""
-    import torch
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [B, Hq, 128] and the caches [num_blocks, page_size, Hkv, 128]")
     b, hq, d = q.shape
@@ -567,7 +559,6 @@ TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs entropy top_id
 def _empty(stream, device, shape, dtype):
     """A call's own output: in the memory pool of the stream the call runs on,
     so that its memory is not handed out again while it runs."""
-    import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
@@ -589,7 +580,6 @@ def kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size: 
     the slot, position and request of each of the step's num_tokens tokens
     (-1 past the last and where a request is refused).  Returns a KvPlan;
     seq_lens may be ctx_lens and free_head_out may be free_head."""
-    import torch
     b = ctx_lens.numel()
     rows, max_blocks = _shape2(block_table, "block_table")
     if rows != b:
@@ -600,9 +590,11 @@ def kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size: 
     i32 = torch.int32
     outs = (slots, positions, requests, seq_lens, cu_new, free_head_out)
     sizes = (num_tokens, num_tokens, num_tokens, b, b + 1, 1)
-    given = [(name, t, i32, n, False) for name, t, n in
-             zip(("slots", "positions", "requests", "seq_lens", "cu_new", "free_head_out"), outs, sizes)
-             if t is not None]
+    given = ()
+    if any(t is not None for t in outs):
+        given = [(name, t, i32, n, False) for name, t, n in
+                 zip(("slots", "positions", "requests", "seq_lens", "cu_new", "free_head_out"), outs, sizes)
+                 if t is not None]
     device = _checked(("ctx_lens", ctx_lens, i32, None, False), ("new_lens", new_lens, i32, b, False),
                       ("block_table", block_table, i32, None, False), ("free_blocks", free_blocks, i32, None, False),
                       ("free_head", free_head, i32, 1, False), *given)
@@ -630,7 +622,6 @@ def kv4_cache_shape(num_blocks: int, page_size: int, num_kv_heads: int, head_dim
 
 def _kv4_specs(k_cache, v_cache, k_scale, v_scale, hkv, d):
     """What _checked has to see of a pair of 4-bit caches and their scales, num_blocks and page_size."""
-    import torch
     shape = k_cache.shape
     if len(shape) != 4 or shape[1] != hkv or shape[3] != 9 * d:
         raise ValueError(f"k_cache has shape {tuple(shape)}, expected [num_blocks, {hkv}, page_size / 16, {9 * d}]")
@@ -645,7 +636,6 @@ def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
     """Quantize new keys and values [T, Hkv, D] bf16 into 4-bit caches at flat
     token slots, in place (fp4kv_append).  k and v may be slices of a fused
     projection: only the rows of one token have to be contiguous."""
-    import torch
     if k.dim() != 3 or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hkv, D]")
     t, hkv, d = k.shape
@@ -660,7 +650,6 @@ def kv4_append(k, v, slots, k_scale, v_scale, k_cache, v_cache, stream=None):
 
 def kv4_gather(k_cache, v_cache, slots, k_scale, v_scale, k=None, v=None, stream=None):
     """The cached tokens at flat slots in bf16 [T, Hkv, D] (fp4kv_gather)."""
-    import torch
     if k_cache.dim() != 4 or k_cache.shape[3] % 9 != 0:
         raise ValueError("k_cache must be [num_blocks, Hkv, page_size / 16, 9 * D]")
     t, hkv, d = slots.numel(), k_cache.shape[1], k_cache.shape[3] // 9
@@ -686,7 +675,6 @@ def kv4_workspace_bytes(head_dim: int) -> int:
 def kv4_workspace(head_dim: int, device="cuda"):
     """A workspace for kv4_decode_attention (zeroed once, here): one serves
     every shape of a head size, but only one call at a time."""
-    import torch
     return torch.zeros(kv4_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
 
 
@@ -698,7 +686,6 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
     will do), one token per sequence, or sequence b's tokens cu_q[b] ..
     cu_q[b + 1] - 1, at most max_q.  Returns o [T, Hq, D], with return_lse
     (o, lse [T, Hq] fp32)."""
-    import torch
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     t, hq, d = q.shape
@@ -730,18 +717,22 @@ def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, t
     """Log probabilities of the targets [M] under logits [M, V] (bf16 or fp32,
     rows may be padded), each row's entropy and its `top` best tokens
     (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
-    import torch
     m, v = _shape2(logits, "logits")
     top = int(top)
     f32 = logits.dtype == torch.float32
-    outs = (("logprobs", logprobs, torch.float32, (m,)), ("entropy", entropy, torch.float32, (m,)),
-            ("top_ids", top_ids, torch.int32, (m, top)), ("top_logprobs", top_logprobs, torch.float32, (m, top)))
-    given = [(name, t, dtype, m if len(shape) == 1 else m * top, False) for name, t, dtype, shape in outs
-             if t is not None]
+    given = [spec for spec in (("logprobs", logprobs, torch.float32, m, False), ("entropy", entropy, torch.float32, m, False),
+                               ("top_ids", top_ids, torch.int32, m * top, False),
+                               ("top_logprobs", top_logprobs, torch.float32, m * top, False)) if spec[1] is not None]
     device = _checked(("logits", logits, torch.float32 if f32 else torch.bfloat16, None, True),
                       ("targets", targets, torch.int32, m, False), *given)
-    logprobs, entropy, top_ids, top_logprobs = [_empty(stream, device, shape, dtype) if t is None else t
-                                                for _, t, dtype, shape in outs]
+    if logprobs is None:
+        logprobs = _empty(stream, device, (m,), torch.float32)
+    if entropy is None:
+        entropy = _empty(stream, device, (m,), torch.float32)
+    if top_ids is None:
+        top_ids = _empty(stream, device, (m, top), torch.int32)
+    if top_logprobs is None:
+        top_logprobs = _empty(stream, device, (m, top), torch.float32)
     _call(device, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs,
           (logits.data_ptr(), int(f32), max(_row_stride(logits), v), m, v, targets.data_ptr(), top,
            logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr()), stream)
@@ -750,7 +741,6 @@ def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, t
 
 def act_quantize(x, codes=None, scale=None, stream=None):
     """Dynamic per-tensor e4m3 quantization of bf16 activations [M, K]."""
-    import torch
     m, k = _shape2(x, "x")
     codes = _new(codes, (m, k), torch.uint8, x)
     scale = _new(scale, (1,), torch.float32, x)
@@ -763,7 +753,6 @@ def act_quantize(x, codes=None, scale=None, stream=None):
 
 def w8a8_gemm(xq, sx, wq, sw, y=None, path: int = PATH_AUTO, stream=None):
     """y[M, N] = sx * sw * dec(xq) . dec(wq)^T (e4m3 x e4m3, fp32 accumulate, bf16 out)."""
-    import torch
     m, k = _shape2(xq, "xq")
     n, k2 = _shape2(wq, "wq")
     if k2 != k:
@@ -797,7 +786,6 @@ def debug_encode_f32(first_bits: int, count: int, out=None, stream=None):
     """The quantizers' e4m3 encode step on the binary32 bit patterns
     first_bits .. first_bits + count - 1 (fp8bs_debug_encode_f32); returns
     uint8 codes on the device."""
-    import torch
     if out is None:
         out = torch.empty(count, dtype=torch.uint8, device="cuda")
     if out.numel() < count:
