@@ -178,7 +178,7 @@ __device__ __forceinline__ void add_any(Sums &s, const float (&x)[VE]) {
 // four of five vectors).  sums() brings it to m.  -inf counts as -1e38, whose
 // weight is 0.
 struct FastSums {
-    static constexpr float kSlack = 24.0f;
+    static constexpr float kSlack = 5.0f;
     float m = -INFINITY, limit = -INFINITY, r = 0.0f, l = 0.0f, t = 0.0f;
     static constexpr float kHuge = 524288.0f;
 
