@@ -28,6 +28,8 @@ constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpMaxSplit = 8;   // CTAs per row
 constexpr int kLpCandidates = 1024;
+constexpr int kLpBest = 4;       // of a warp's maxima, for the bound
+static_assert(kLpWarps * kLpBest >= kLogprobsMaxTop && kLpWarps * kLpBest % 32 == 0, "as many as the top can have");
 constexpr float kLog2e = 1.4426950408889634f;
 // (x - m) below this has weight 0 in fp32; it keeps -inf out of t
 constexpr float kLowest = -200.0f;
@@ -36,6 +38,11 @@ __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ const void *row_start(const LogprobArgs &a, int64_t r) {
+    return static_cast<const char *>(a.logits) + r * a.row_stride * (F32 ? 4 : 2);
 }
 
 // Order of the values as unsigned integers: -0 is +0, NaN below everything.
@@ -88,6 +95,10 @@ struct Row {
     __device__ __forceinline__ bool whole(int vec) const {
         return static_cast<int64_t>(vec) * VE >= pre && static_cast<int64_t>(vec + 1) * VE - pre <= vocab;
     }
+    __device__ __forceinline__ float at(int64_t e) const {
+        if constexpr (F32) return reinterpret_cast<const float *>(base)[pre + e];
+        else return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[pre + e]);
+    }
     // The vector's values; -inf for what is not in the row.
     __device__ __forceinline__ void load(int vec, float (&x)[VE]) const {
         const char *p = base + static_cast<int64_t>(vec) * 16;
@@ -116,25 +127,31 @@ struct Row {
         }
         return vm;
     }
+    // The largest value of a whole vector.
+    static __device__ __forceinline__ float most(const uint4 v) {
+        if constexpr (F32) {
+            return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+        } else {
+            const uint32_t m2 = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
+            return fmaxf(bf16lo_to_f32(m2), bf16hi_to_f32(m2));
+        }
+    }
     // The values of a whole vector raised to FastSums' floor; returns the largest before that.
     static __device__ __forceinline__ float unpack_fast(const uint4 v, float (&x)[VE]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if constexpr (F32) {
             unpack(v, x);
-            const float vm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 #pragma unroll
             for (int j = 0; j < VE; ++j) x[j] = fmaxf(x[j], -1e38f);
-            return vm;
         } else {
-            const uint32_t m2 = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t u = max_bf16x2(w[j], 0xFE96FE96u);  // -1e38 in bf16
                 x[2 * j] = bf16lo_to_f32(u);
                 x[2 * j + 1] = bf16hi_to_f32(u);
             }
-            return fmaxf(bf16lo_to_f32(m2), bf16hi_to_f32(m2));
         }
+        return most(v);
     }
     static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[VE]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -175,19 +192,20 @@ __device__ __forceinline__ void add_any(Sums &s, const float (&x)[VE]) {
 // l = sum 2^d, t = sum d 2^d.  The reference only has to keep 2^d in range: it
 // moves when a value passes it by 2^kSlack, so that the lanes of a warp hardly
 // ever do (with the maximum itself as the reference some lane of 32 does at
-// four of five vectors).  sums() brings it to m.  -inf counts as -1e38, whose
-// weight is 0.
+// four of five vectors).  sums() brings it to m.  -inf counts as -1e38, and
+// neither it nor any masked value below -2^19 becomes the reference; their
+// weights are 0 unless the row has nothing else, which add_any then sums.
 struct FastSums {
     static constexpr float kSlack = 5.0f;
-    float m = -INFINITY, limit = -INFINITY, r = 0.0f, l = 0.0f, t = 0.0f;
     static constexpr float kHuge = 524288.0f;
+    float m = -INFINITY, limit = -kHuge, r = 0.0f, l = 0.0f, t = 0.0f;  // below -kHuge nothing is a reference
 
     // x: values of at least kFloor (-inf raised to it); vm: the largest before that.
     template <int VE>
     __device__ __forceinline__ void add(const float (&x)[VE], float vm) {
         if (vm > limit) {
             const float rn = vm * kLog2e;
-            const float d = m == -INFINITY ? kLowest : fmaxf(r - rn, kLowest), c = ex2(d);
+            const float d = limit == -kHuge ? kLowest : fmaxf(r - rn, kLowest), c = ex2(d);
             t = c * (t + d * l);
             l *= c;
             r = rn;
@@ -214,6 +232,8 @@ struct LpShared {
     int32_t ids[kLpCandidates + kLogprobsMaxTop];
     int32_t flagged[kLpThreads];
     Sums warp[kLpWarps];
+    uint32_t best_keys[kLpWarps * kLpBest];
+    float best[kLpWarps];
     int32_t counts[kLpWarps];
     int32_t n_flagged, n;
     // what the CTAs of the cluster hand to the first
@@ -224,13 +244,13 @@ struct LpShared {
 
 __device__ __forceinline__ bool better(float x, int32_t i, float y, int32_t j) { return x > y || (x == y && i < j); }
 
-// The first `top` of the n candidates (value, id >= 0) in order: emit(rank, i),
-// a warp per candidate; those below `least` are known not to be among them.
+// The first `top` of the n candidates (value, id >= 0) in order: emit(rank, i);
+// those below `least` are known not to be among them.
 template <class Emit>
 __device__ __forceinline__ void rank_candidates(const float *vals, const int32_t *ids, int n, int top, float least,
                                                 Emit emit) {
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < n; i += kLpWarps) {
+    for (int i = threadIdx.x >> 5; i < n; i += kLpWarps) {  // a warp per candidate
         const float x = vals[i];
         const int32_t id = ids[i];
         if (id < 0 || x < least) continue;
@@ -242,18 +262,37 @@ __device__ __forceinline__ void rank_candidates(const float *vals, const int32_t
 }
 
 // The candidates of vectors [v0, v1) for its first `top` elements, in sh.vals
-// and sh.ids; returns how many.  `m`: the maximum of this thread's vectors.
+// and sh.ids; returns how many.  key: of the maximum of this thread's vectors.
 template <bool F32>
-__device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, float m, LpShared &sh) {
+__device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uint32_t key, LpShared &sh) {
     constexpr int VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // ---- the top-th largest of the threads' maxima, by the upper half of its key (bf16 has no more)
-    const uint32_t key = order_key(m);
+    // ---- a bound at or below the top-th largest of the threads' maxima, by the upper half of its key (bf16 has no
+    // more): the top-th largest of the kLpBest largest of each warp, which every warp finds for itself.  (Sixteen
+    // rounds of counting over the CTA's barrier took 1600 clocks, this 700.)
+    uint32_t left = key;
+#pragma unroll
+    for (int i = 0; i < kLpBest; ++i) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, left);
+        const uint32_t holders = __ballot_sync(0xffffffffu, left == best);
+        if (lane == __ffs(holders) - 1) {
+            sh.best_keys[warp * kLpBest + i] = best;
+            left = 0;
+        }
+    }
+    __syncthreads();
     uint32_t bound = 0;
     auto refine = [&](int from, int to) {
+        uint32_t k[kLpWarps * kLpBest / 32];
+#pragma unroll
+        for (int i = 0; i < kLpWarps * kLpBest / 32; ++i) k[i] = sh.best_keys[lane + i * 32];
+#pragma unroll 1
         for (int bit = from; bit >= to; --bit) {
             const uint32_t cand = bound | (1u << bit);
-            if (__syncthreads_count(key >= cand) >= top) bound = cand;
+            int reach = 0;
+#pragma unroll
+            for (int i = 0; i < kLpWarps * kLpBest / 32; ++i) reach += __popc(__ballot_sync(0xffffffffu, k[i] >= cand));
+            if (reach >= top) bound = cand;
         }
     };
     refine(31, 16);
@@ -268,7 +307,8 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, flo
         __syncthreads();
         const int todo = sh.n_flagged * per;
         for (int p = tid; p < todo; p += kLpThreads) {
-            const int f = p / per, v = v0 + sh.flagged[f] + (p - f * per) * kLpThreads;
+            const uint32_t f = p / static_cast<uint32_t>(per);
+            const int v = v0 + sh.flagged[f] + static_cast<int>(p - f * per) * kLpThreads;
             if (v >= v1) continue;
             float x[VE];
             row.load(v, x);
@@ -303,8 +343,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, flo
                     for (int j = 0; j < VE; ++j) {
                         const int64_t e = row.element(v + tid, j);
                         // equal in what the bound resolves of the key
-                        const uint32_t k = order_key(x[j]);
-                        if (k - bound < unit && e >= 0 && e < row.vocab) eq |= 1u << j;
+                        if (order_key(x[j]) - bound < unit && e >= 0 && e < row.vocab) eq |= 1u << j;
                     }
                 }
                 const int mine = __popc(eq);
@@ -366,10 +405,10 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, flo
             if (better(y, i, bx, bi)) bx = y, bi = i;
         }
         __syncthreads();
-        if (lane == 0) sh.warp[warp].m = bx, sh.counts[warp] = bi;
+        if (lane == 0) sh.best[warp] = bx, sh.counts[warp] = bi;
         __syncthreads();
         for (int w = 0; w < kLpWarps; ++w)
-            if (better(sh.warp[w].m, sh.counts[w], bx, bi)) bx = sh.warp[w].m, bi = sh.counts[w];
+            if (better(sh.best[w], sh.counts[w], bx, bi)) bx = sh.best[w], bi = sh.counts[w];
         if (bi == 0x7fffffff) break;  // none left (NaN among the values)
         if (tid == 0) sh.vals[n] = bx, sh.ids[n] = bi;
         last_x = bx, last_i = bi;
@@ -378,31 +417,10 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, flo
     return n;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobArgs a, int splits) {
+// The sums of this thread's vectors v0 + tid, + kLpThreads, ... below v1.
+template <bool F32, int kFlight>
+__device__ __forceinline__ Sums read_row(const Row<F32> &row, int v0, int v1, int tid) {
     constexpr int VE = Row<F32>::VE;
-    constexpr int kFlight = 6;  // 16-byte loads in flight per thread: 132 us at 2048 x 152064 bf16, 138 with 4
-    __shared__ LpShared sh;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t r = blockIdx.x / splits;
-    const int part = static_cast<int>(blockIdx.x - r * splits);  // rank in the cluster
-    const int top = static_cast<int>(a.top);
-    if (splits > 1) cluster_arrive();  // the first CTA's shared memory is there once all have
-    pdl_wait();
-    const Row<F32> row(static_cast<const char *>(a.logits) + r * a.row_stride * (F32 ? 4 : 2), a.vocab);
-    const int v0 = static_cast<int>(static_cast<int64_t>(row.vecs) * part / splits);
-    const int v1 = static_cast<int>(static_cast<int64_t>(row.vecs) * (part + 1) / splits);
-
-    int64_t target = -1;
-    float x_target = 0.0f;
-    if (part == 0 && tid == 0) {
-        target = __ldg(a.targets + r);
-        if (target >= 0 && target < a.vocab) {
-            const char *p = static_cast<const char *>(a.logits) + (r * a.row_stride + target) * (F32 ? 4 : 2);
-            if constexpr (F32) x_target = *reinterpret_cast<const float *>(p);
-            else x_target = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p));
-        }
-    }
     FastSums fast;
     int v = v0 + tid;
     if (v < v1 && !row.whole(v)) {  // the row's ragged start
@@ -428,22 +446,53 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobAr
         const float vm = row.load_fast(v, x);
         fast.add<VE>(x, vm);
     }
-    Sums s = fast.sums();
-    if (__syncthreads_or(!fast.ordinary())) {  // somewhere a maximum the fast sums cannot hold
-        s = Sums{-INFINITY, 0.0f, 0.0f};
-        for (v = v0 + tid; v < v1; v += kLpThreads) {
-            float x[VE];
-            row.load(v, x);
-            add_any<VE>(s, x);
-        }
+    if (fast.ordinary()) return fast.sums();
+    Sums s{-INFINITY, 0.0f, 0.0f};  // a maximum that the fast sums cannot hold
+    for (v = v0 + tid; v < v1; v += kLpThreads) {
+        float x[VE];
+        row.load(v, x);
+        add_any<VE>(s, x);
     }
+    return s;
+}
 
+// What a row gives besides its top.  `x`: the target's logit.
+__device__ __forceinline__ void store_row(const LogprobArgs &a, int64_t r, const Sums &all, int64_t target, float x) {
+    const bool any = all.m != -INFINITY;
+    const float lz = any ? logf(all.l) : 0.0f;
+    if (target >= a.vocab) atomicOr(&g_lp_err, ERRBIT_INDEX);
+    a.logprobs[r] = target < 0 || target >= a.vocab ? 0.0f : any ? (x - all.m) - lz : -INFINITY;
+    a.entropy[r] = any ? lz - all.t / all.l : 0.0f;
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobArgs a, int splits) {
+    __shared__ LpShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t r = blockIdx.x / splits;
+    const int part = static_cast<int>(blockIdx.x - r * splits);  // rank in the cluster
+    const int top = static_cast<int>(a.top);
+    if (splits > 1) cluster_arrive();  // the first CTA's shared memory is there once all have
+    pdl_wait();
+    const Row<F32> row(row_start<F32>(a, r), a.vocab);
+    const int v0 = static_cast<int>(static_cast<int64_t>(row.vecs) * part / splits);
+    const int v1 = static_cast<int>(static_cast<int64_t>(row.vecs) * (part + 1) / splits);
+
+    int64_t target = -1;
+    float x_target = 0.0f;
+    if (part == 0 && tid == 0) {
+        target = __ldg(a.targets + r);
+        if (target >= 0 && target < a.vocab) x_target = row.at(target);
+    }
+    const Sums s = read_row<F32, 6>(row, v0, v1, tid);  // six loads in flight: 132 us at 2048 x 152064 bf16, 138 with four
     const Sums w = warp_merge(s);
     if (lane == 0) sh.warp[warp] = w;
     __syncthreads();
     Sums all = warp_merge(sh.warp[lane % kLpWarps], kLpWarps);
     int n = 0;
-    if (top > 0) n = find_candidates<F32>(row, v0, v1, top, s.m, sh);
+    if (top > 0) {
+        n = find_candidates<F32>(row, v0, v1, top, order_key(s.m), sh);
+    }
 
     const float *vals = sh.vals;
     const int32_t *ids = sh.ids;
@@ -484,11 +533,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobAr
 
     const bool any = all.m != -INFINITY;
     const float lz = any ? logf(all.l) : 0.0f;
-    if (tid == 0) {
-        if (target >= a.vocab) atomicOr(&g_lp_err, ERRBIT_INDEX);
-        a.logprobs[r] = target < 0 || target >= a.vocab ? 0.0f : any ? (x_target - all.m) - lz : -INFINITY;
-        a.entropy[r] = any ? lz - all.t / all.l : 0.0f;
-    }
+    if (tid == 0) store_row(a, r, all, target, x_target);
     if (top > 0) {
         int32_t *out_ids = a.top_ids + r * top;
         float *out = a.top_logprobs + r * top;

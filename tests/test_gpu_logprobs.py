@@ -83,6 +83,23 @@ def test_more_rows_than_a_wave_of_long_ones(pkg, dtype, v, pad):
     check(pkg, x, np.random.default_rng(v).integers(0, v, 330), 4)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,v,top", [(609, 3001, 20), (700, 1, 1), (1301, 500, 0), (650, 9001, 32)])
+def test_many_rows(pkg, m, v, top, dtype):
+    """More rows than CTAs at once; among them masked ones, of equals, of large values a fixed distance apart, far
+    from zero."""
+    x = logits(m, v, m, dtype, pad=5).clone()
+    if v > 100:
+        x[3::50] = torch.finfo(dtype).min
+        x[3::50, 7:13] = 1.0
+        x[4::50] = -np.inf
+        x[5::50] = 0.25
+        x[6::50, ::512] += 100
+        x[7::50] -= 1e6
+        x[8::50, v // 2:] = -np.inf
+    check(pkg, x, np.random.default_rng(m).integers(0, v, m), top)
+
+
 @pytest.mark.parametrize("v", [70, 5000, 152064])
 @pytest.mark.parametrize("low", [-np.inf, "lowest"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -99,6 +116,17 @@ def test_masked_rows(pkg, v, low, dtype):
         x[r] = row
         t.append(int(idx[0]) if keep else 5)
     check(pkg, x, t, 20)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_masked_values_before_ordinary_ones(pkg, dtype):
+    """What a thread reads first is the type's lowest value (or far below the rest), what it reads later is not."""
+    x = logits(4, 20000, 14, dtype).clone()
+    x[0, :8192] = torch.finfo(dtype).min
+    x[1, :8192] = -1e6
+    x[2, ::2] = torch.finfo(dtype).min
+    x[3, 3000:] = torch.finfo(dtype).min
+    check(pkg, x, [9000, 9000, 1, 7], 20)
 
 
 def test_a_masked_target(pkg):
