@@ -11,8 +11,9 @@
 // elements.  The top comes out of the same maxima: the k-th largest of the
 // threads' maxima is a lower bound of the row part's k-th largest element,
 // and only threads whose maximum reaches it can hold one of the top k, about
-// k of the 512.  Their elements (1 / 512 of the part each) are read again,
-// from L2, and what reaches the bound is ranked in shared memory.  Rows of
+// k of the 512.  Of their elements those in pieces (an eighth or so) whose
+// maximum reaches the bound are read again, from L2, and what reaches the
+// bound is ranked in shared memory.  Rows of
 // equals, such as masked ones, whose equals at the bound do not fit there
 // take an ordered scan that stops when it has enough.
 #include "common.cuh"
@@ -24,12 +25,11 @@ namespace {
 
 __device__ uint32_t g_lp_err;
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpMaxSplit = 8;   // CTAs per row
 constexpr int kLpCandidates = 1024;
-constexpr int kLpBest = 4;       // of a warp's maxima, for the bound
-static_assert(kLpWarps * kLpBest >= kLogprobsMaxTop && kLpWarps * kLpBest % 32 == 0, "as many as the top can have");
+static_assert(kLogprobsMaxTop <= 32, "the bound comes from 32 maxima");
+constexpr int kLpPieces = 8;     // of a thread's vectors
+constexpr int kFlight = 6;       // 16-byte loads in flight per thread: 132 us at 2048 x 152064 bf16, 138 with four
 constexpr float kLog2e = 1.4426950408889634f;
 // (x - m) below this has weight 0 in fp32; it keeps -inf out of t
 constexpr float kLowest = -200.0f;
@@ -126,6 +126,15 @@ struct Row {
             x[j] = fmaxf(x[j], -1e38f);
         }
         return vm;
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[VE]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (F32) w[j] = __float_as_uint(x[j]);
+            else w[j] = f32x2_to_bf16x2(x[2 * j], x[2 * j + 1]);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     // The largest value of a whole vector.
     static __device__ __forceinline__ float most(const uint4 v) {
@@ -227,14 +236,17 @@ struct FastSums {
     }
 };
 
+template <int TH>
 struct LpShared {
+    static constexpr int kWarps = TH / 32;
     float vals[kLpCandidates + kLogprobsMaxTop];
     int32_t ids[kLpCandidates + kLogprobsMaxTop];
-    int32_t flagged[kLpThreads];
-    Sums warp[kLpWarps];
-    uint32_t best_keys[kLpWarps * kLpBest];
-    float best[kLpWarps];
-    int32_t counts[kLpWarps];
+    float piece_max[kLpPieces][TH];
+    int32_t flagged[kLpPieces * TH];  // piece << 16 | thread
+    Sums warp[kWarps];
+    uint32_t best_keys[32];
+    float best[kWarps];
+    int32_t counts[kWarps];
     int32_t n_flagged, n;
     // what the CTAs of the cluster hand to the first
     Sums part[kLpMaxSplit];
@@ -246,11 +258,11 @@ __device__ __forceinline__ bool better(float x, int32_t i, float y, int32_t j) {
 
 // The first `top` of the n candidates (value, id >= 0) in order: emit(rank, i);
 // those below `least` are known not to be among them.
-template <class Emit>
+template <int TH, class Emit>
 __device__ __forceinline__ void rank_candidates(const float *vals, const int32_t *ids, int n, int top, float least,
                                                 Emit emit) {
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < n; i += kLpWarps) {  // a warp per candidate
+    for (int i = threadIdx.x >> 5; i < n; i += TH / 32) {  // a warp per candidate
         const float x = vals[i];
         const int32_t id = ids[i];
         if (id < 0 || x < least) continue;
@@ -261,55 +273,66 @@ __device__ __forceinline__ void rank_candidates(const float *vals, const int32_t
     }
 }
 
+// A thread's vectors in pieces, whose maxima are kept: `per` of them, the
+// first `size` in piece 0, and so on.
+template <int TH>
+struct Pieces {
+    int per, size;
+    __device__ __forceinline__ explicit Pieces(int vecs) {
+        per = (vecs + TH - 1) / TH;
+        size = max(1, ((per + kLpPieces - 1) / kLpPieces + kFlight - 1) / kFlight * kFlight);  // whole rounds of loads
+    }
+};
+
 // The candidates of vectors [v0, v1) for its first `top` elements, in sh.vals
-// and sh.ids; returns how many.  key: of the maximum of this thread's vectors.
-template <bool F32>
-__device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uint32_t key, LpShared &sh) {
+// and sh.ids; returns how many.  m: the maximum of this thread's vectors;
+// sh.piece_max has its pieces'.
+template <bool F32, int TH>
+__device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, float m, LpShared<TH> &sh) {
+    constexpr int kBest = 1024 / TH;  // of each warp's maxima: 32 in all
     constexpr int VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // ---- a bound at or below the top-th largest of the threads' maxima, by the upper half of its key (bf16 has no
-    // more): the top-th largest of the kLpBest largest of each warp, which every warp finds for itself.  (Sixteen
-    // rounds of counting over the CTA's barrier took 1600 clocks, this 700.)
-    uint32_t left = key;
+    // more): the top-th largest of the two largest of each warp, which every warp finds for itself
+    uint32_t left = order_key(m);
 #pragma unroll
-    for (int i = 0; i < kLpBest; ++i) {
+    for (int i = 0; i < kBest; ++i) {
         const uint32_t best = __reduce_max_sync(0xffffffffu, left);
         const uint32_t holders = __ballot_sync(0xffffffffu, left == best);
         if (lane == __ffs(holders) - 1) {
-            sh.best_keys[warp * kLpBest + i] = best;
+            sh.best_keys[warp * kBest + i] = best;
             left = 0;
         }
     }
     __syncthreads();
-    uint32_t bound = 0;
-    auto refine = [&](int from, int to) {
-        uint32_t k[kLpWarps * kLpBest / 32];
+    uint32_t bound;
+    {
+        const uint32_t mine = sh.best_keys[lane];
+        int above = 0;
 #pragma unroll
-        for (int i = 0; i < kLpWarps * kLpBest / 32; ++i) k[i] = sh.best_keys[lane + i * 32];
-#pragma unroll 1
-        for (int bit = from; bit >= to; --bit) {
-            const uint32_t cand = bound | (1u << bit);
-            int reach = 0;
-#pragma unroll
-            for (int i = 0; i < kLpWarps * kLpBest / 32; ++i) reach += __popc(__ballot_sync(0xffffffffu, k[i] >= cand));
-            if (reach >= top) bound = cand;
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t other = __shfl_sync(0xffffffffu, mine, i);
+            above += other > mine || (other == mine && i < lane) ? 1 : 0;
         }
-    };
-    refine(31, 16);
-    const int per = (v1 - v0 + kLpThreads - 1) / kLpThreads;  // vectors of a thread
-    // ---- what the threads that reach it hold; strict: above it only
+        bound = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == top - 1)) - 1) & 0xFFFF0000u;
+    }
+    const Pieces<TH> pieces(v1 - v0);
+    // ---- what the pieces that reach it hold; strict: above it only
     uint32_t unit = 0x10000u;  // what the bound resolves
     for (int strict = 0; strict < 2; ++strict) {
         if (tid == 0) sh.n_flagged = sh.n = 0;
         __syncthreads();
         const uint32_t least = strict ? bound + unit : bound;
-        if (key >= least) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = tid;
+        if (order_key(m) >= least)
+            for (int i = 0; i * pieces.size < pieces.per; ++i)
+                if (order_key(sh.piece_max[i][tid]) >= least) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = tid | i << 16;
         __syncthreads();
-        const int todo = sh.n_flagged * per;
-        for (int p = tid; p < todo; p += kLpThreads) {
-            const uint32_t f = p / static_cast<uint32_t>(per);
-            const int v = v0 + sh.flagged[f] + static_cast<int>(p - f * per) * kLpThreads;
-            if (v >= v1) continue;
+        const int todo = sh.n_flagged * pieces.size;
+        for (int p = tid; p < todo; p += TH) {
+            const uint32_t f = p / static_cast<uint32_t>(pieces.size), at = p - f * pieces.size;
+            const int owner = sh.flagged[f] & 0xFFFF, i = (sh.flagged[f] >> 16) * pieces.size + static_cast<int>(at);
+            const int v = v0 + owner + i * TH;
+            if (i >= pieces.per || v >= v1) continue;
             float x[VE];
             row.load(v, x);
             float vm = x[0];
@@ -320,10 +343,10 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
             for (int j = 0; j < VE; ++j) {
                 const int64_t e = row.element(v, j);
                 if (order_key(x[j]) >= least && e >= 0 && e < row.vocab) {
-                    const int at = atomicAdd(&sh.n, 1);
-                    if (at < kLpCandidates) {
-                        sh.vals[at] = x[j];
-                        sh.ids[at] = static_cast<int32_t>(e);
+                    const int n = atomicAdd(&sh.n, 1);
+                    if (n < kLpCandidates) {
+                        sh.vals[n] = x[j];
+                        sh.ids[n] = static_cast<int32_t>(e);
                     }
                 }
             }
@@ -334,7 +357,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
             if (!strict || n >= top) return n;
             // ---- and of the many equals at the bound the lowest indices
             int have = n;
-            for (int v = v0; v < v1 && have < top; v += kLpThreads) {
+            for (int v = v0; v < v1 && have < top; v += TH) {
                 float x[VE];
                 uint32_t eq = 0;
                 if (v + tid < v1) {
@@ -356,7 +379,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
                 if (lane == 31) sh.counts[warp] = upto;
                 __syncthreads();
                 int at = have + upto - mine, all = 0;
-                for (int w = 0; w < kLpWarps; ++w) {
+                for (int w = 0; w < TH / 32; ++w) {
                     if (w < warp) at += sh.counts[w];
                     all += sh.counts[w];
                 }
@@ -375,8 +398,12 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
             return min(have, top);
         }
         __syncthreads();
-        if (F32 && !strict) {  // values of one upper half are not equals
-            refine(15, 0);
+        if (F32 && !strict) {  // values of one upper half are not equals: the rest of the bound, by counting
+            const uint32_t key = order_key(m);
+            for (int bit = 15; bit >= 0; --bit) {
+                const uint32_t cand = bound | (1u << bit);
+                if (__syncthreads_count(key >= cand) >= top) bound = cand;
+            }
             unit = 1;
         }
     }
@@ -387,7 +414,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
     for (; n < top; ++n) {
         float bx = -INFINITY;
         int32_t bi = 0x7fffffff;
-        for (int v = v0 + tid; v < v1; v += kLpThreads) {
+        for (int v = v0 + tid; v < v1; v += TH) {
             float x[VE];
             row.load(v, x);
 #pragma unroll
@@ -407,7 +434,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
         __syncthreads();
         if (lane == 0) sh.best[warp] = bx, sh.counts[warp] = bi;
         __syncthreads();
-        for (int w = 0; w < kLpWarps; ++w)
+        for (int w = 0; w < TH / 32; ++w)
             if (better(sh.best[w], sh.counts[w], bx, bi)) bx = sh.best[w], bi = sh.counts[w];
         if (bi == 0x7fffffff) break;  // none left (NaN among the values)
         if (tid == 0) sh.vals[n] = bx, sh.ids[n] = bi;
@@ -417,38 +444,57 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, uin
     return n;
 }
 
-// The sums of this thread's vectors v0 + tid, + kLpThreads, ... below v1.
-template <bool F32, int kFlight>
-__device__ __forceinline__ Sums read_row(const Row<F32> &row, int v0, int v1, int tid) {
+// The sums of this thread's vectors v0 + tid, + TH, ... below v1, and
+// with `pieces` the maxima of its pieces.
+template <bool F32, int TH>
+__device__ __forceinline__ Sums read_row(const Row<F32> &row, int v0, int v1, int tid, const Pieces<TH> &pieces,
+                                         bool keep, LpShared<TH> &sh) {
     constexpr int VE = Row<F32>::VE;
     FastSums fast;
-    int v = v0 + tid;
-    if (v < v1 && !row.whole(v)) {  // the row's ragged start
-        float x[VE];
-        const float vm = row.load_fast(v, x);
-        fast.add<VE>(x, vm);
-        v += kLpThreads;
-    }
+    float max_all = -INFINITY;
+    int piece = 0, end = pieces.size;  // of the piece, in vectors of this thread
+    auto close = [&]() {
+        if (keep) sh.piece_max[piece][tid] = fast.m;
+        ++piece;
+        end += pieces.size;
+        max_all = fmaxf(max_all, fast.m);
+        fast.m = -INFINITY;
+    };
+    int v = v0 + tid, i = 0;
     const int v_whole = v1 > v0 && !row.whole(v1 - 1) ? v1 - 1 : v1;
-    for (; v + (kFlight - 1) * kLpThreads < v_whole; v += kFlight * kLpThreads) {
+    // whole rounds of loads, but for a ragged start
+    for (; v + (kFlight - 1) * TH < v_whole; v += kFlight * TH, i += kFlight) {
+        if (i == end) close();
         uint4 w[kFlight];
+        const bool ragged = !row.whole(v);
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) w[i] = ld_nc_v4(row.base + static_cast<int64_t>(v + i * kLpThreads) * 16);
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
+        for (int j = 0; j < kFlight; ++j)
+            if (j > 0 || !ragged) w[j] = ld_nc_v4(row.base + static_cast<int64_t>(v + j * TH) * 16);
+        if (ragged) {
             float x[VE];
-            const float vm = Row<F32>::unpack_fast(w[i], x);
+            row.load(v, x);
+            w[0] = Row<F32>::pack(x);
+        }
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+            float x[VE];
+            const float vm = Row<F32>::unpack_fast(w[j], x);
             fast.add<VE>(x, vm);
         }
     }
-    for (; v < v1; v += kLpThreads) {
+    for (; v < v1; v += TH, ++i) {
+        if (i == end) close();
         float x[VE];
         const float vm = row.load_fast(v, x);
         fast.add<VE>(x, vm);
     }
+    close();
+    if (keep)  // pieces this thread has nothing of
+        for (; piece * pieces.size < pieces.per; ++piece) sh.piece_max[piece][tid] = -INFINITY;
+    fast.m = max_all;
     if (fast.ordinary()) return fast.sums();
     Sums s{-INFINITY, 0.0f, 0.0f};  // a maximum that the fast sums cannot hold
-    for (v = v0 + tid; v < v1; v += kLpThreads) {
+    for (v = v0 + tid; v < v1; v += TH) {
         float x[VE];
         row.load(v, x);
         add_any<VE>(s, x);
@@ -465,9 +511,9 @@ __device__ __forceinline__ void store_row(const LogprobArgs &a, int64_t r, const
     a.entropy[r] = any ? lz - all.t / all.l : 0.0f;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobArgs a, int splits) {
-    __shared__ LpShared sh;
+template <bool F32, int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH) logprobs_kernel(const LogprobArgs a, int splits) {
+    __shared__ LpShared<TH> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / splits;
     const int part = static_cast<int>(blockIdx.x - r * splits);  // rank in the cluster
@@ -484,15 +530,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobAr
         target = __ldg(a.targets + r);
         if (target >= 0 && target < a.vocab) x_target = row.at(target);
     }
-    const Sums s = read_row<F32, 6>(row, v0, v1, tid);  // six loads in flight: 132 us at 2048 x 152064 bf16, 138 with four
+    const Sums s = read_row<F32, TH>(row, v0, v1, tid, Pieces<TH>(v1 - v0), top > 0, sh);
     const Sums w = warp_merge(s);
     if (lane == 0) sh.warp[warp] = w;
-    __syncthreads();
-    Sums all = warp_merge(sh.warp[lane % kLpWarps], kLpWarps);
     int n = 0;
-    if (top > 0) {
-        n = find_candidates<F32>(row, v0, v1, top, order_key(s.m), sh);
-    }
+    if (top > 0) n = find_candidates<F32, TH>(row, v0, v1, top, s.m, sh);
+    else __syncthreads();
+    Sums all = warp_merge(sh.warp[lane % (TH / 32)], TH / 32);
 
     const float *vals = sh.vals;
     const int32_t *ids = sh.ids;
@@ -510,9 +554,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobAr
         if (top > 0) {
             const uint32_t pv = dsmem_map(smem_u32(&sh.part_vals[part * top]), to);
             const uint32_t pi = dsmem_map(smem_u32(&sh.part_ids[part * top]), to);
-            for (int i = tid; i < top; i += kLpThreads)
+            for (int i = tid; i < top; i += TH)
                 if (i >= n) dsmem_st_f32(pi + 4 * i, __int_as_float(-1));
-            rank_candidates(sh.vals, sh.ids, n, top, least, [&](int rank, int i) {
+            rank_candidates<TH>(sh.vals, sh.ids, n, top, least, [&](int rank, int i) {
                 dsmem_st_f32(pv + 4 * rank, sh.vals[i]);
                 dsmem_st_f32(pi + 4 * rank, __int_as_float(sh.ids[i]));
             });
@@ -540,34 +584,32 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LogprobAr
         int live = 0;  // candidates there are; fewer than top only where NaN took the others' places
         for (int i = lane; i < n; i += 32) live += ids[i] >= 0 ? 1 : 0;
         live = __reduce_add_sync(0xffffffffu, live);
-        for (int i = live + tid; i < top; i += kLpThreads) {
+        for (int i = live + tid; i < top; i += TH) {
             out_ids[i] = -1;
             out[i] = -INFINITY;
         }
-        rank_candidates(vals, ids, n, top, least, [&](int rank, int i) {
+        rank_candidates<TH>(vals, ids, n, top, least, [&](int rank, int i) {
             out_ids[rank] = ids[i];
             out[rank] = any ? (vals[i] - all.m) - lz : -INFINITY;
         });
     }
 }
 
-// CTAs per row: as many as keep the GPU's two CTAs per SM busy in one wave,
-// while each still has a vector per thread.
+// CTAs per row: as many as keep the GPU's two CTAs of 512 threads per SM busy
+// in one wave, while each still has a vector per thread.
 int pick_row_split(const LogprobArgs &a) {
     const int64_t vecs = a.vocab / (a.f32 ? 4 : 8);
     int s = 1;
-    while (s < kLpMaxSplit && 2 * s * a.rows <= 2 * static_cast<int64_t>(device_sm_count()) && vecs / (2 * s) >= kLpThreads)
+    while (s < kLpMaxSplit && 2 * s * a.rows <= 2 * static_cast<int64_t>(device_sm_count()) && vecs / (2 * s) >= 512)
         s *= 2;
     return s;
 }
 
-}  // namespace
-
-cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
-    const int splits = pick_row_split(a);
+template <bool F32, int TH>
+cudaError_t launch_rows(const LogprobArgs &a, int splits, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * splits), 1, 1);
-    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.blockDim = dim3(TH, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -578,8 +620,17 @@ cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
     attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return a.f32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a, splits)
-                 : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a, splits);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<F32, TH>, a, splits);
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
+    const int splits = pick_row_split(a);
+    // Few rows: 512 threads a CTA, more of a row in flight (one row of 152064 bf16, top 20: 11.2 us, 13.8 with 256).
+    // Many: 256, so that four CTAs of an SM read while one looks for its top (2048 rows: 123 us, 136 with 512).
+    if (splits > 1) return a.f32 ? launch_rows<true, 512>(a, splits, stream) : launch_rows<false, 512>(a, splits, stream);
+    return a.f32 ? launch_rows<true, 256>(a, 1, stream) : launch_rows<false, 256>(a, 1, stream);
 }
 
 uint32_t take_logprobs_error() {
