@@ -72,6 +72,25 @@ __device__ __forceinline__ uint8_t *slot_codes(uint8_t *cache, uint32_t slot, ui
     return t + row * (D / 2) + 16 * pair;
 }
 
+// (lo / d, hi / d) by Markstein's correction (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
+// Dev. 34(1), 1990): q0 = RN(x y), r = x - d q0 exactly, q = RN(q0 + r y) with
+// y = RN(1/d), two values a packed fma; the sign is x's also where q is 0.
+// With d in [2^-92, 2^92] and |x| y < 1e30 no step leaves the normal range
+// where it matters, and the e2m1 code of q is that of the IEEE quotient for
+// every divisor mantissa (tests/csrc/quotient_e2m1.c).
+__device__ __forceinline__ void quotient2(float lo, float hi, uint64_t nd2, uint64_t y2, float &qlo, float &qhi) {
+    const uint64_t negzero2 = 0x8000000080000000ull;
+    uint64_t x2, q0, r, q;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x2) : "f"(lo), "f"(hi));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q0) : "l"(x2), "l"(y2), "l"(negzero2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(nd2), "l"(q0), "l"(x2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(y2), "l"(q0));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(qlo), "=f"(qhi) : "l"(q));
+    qlo = copysignf(qlo, lo);
+    qhi = copysignf(qhi, hi);
+}
+
 // 16 bf16 values (8 words) -> their group's scale code and e2m1 codes.
 __device__ __forceinline__ uint32_t encode_group(const uint32_t *u, float s, float six_s, uint2 &codes) {
     uint32_t mx = 0;
@@ -81,15 +100,25 @@ __device__ __forceinline__ uint32_t encode_group(const uint32_t *u, float s, flo
     const uint32_t sc = f32x2_to_e4m3x2(amax / six_s, 0.0f) & 0xFFu;
     const float den = f16x2_to_f32x2(e4m3x2_to_f16x2(sc)).x * s;
     codes = make_uint2(0, 0);
-    if (den > 0.0f) {
-        float q[2][8];
+    float q[2][8];
+    if (den >= 0x1p-92f && den <= 0x1p92f && amax < 1e30f * den) {
+        const float y = __frcp_rn(den);
+        uint64_t nd2, y2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(nd2) : "f"(-den));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(y2) : "f"(y));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            quotient2(bf16lo_to_f32(u[j]), bf16hi_to_f32(u[j]), nd2, y2, q[j >> 2][2 * (j & 3)], q[j >> 2][2 * (j & 3) + 1]);
+    } else if (den > 0.0f) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             q[j >> 2][2 * (j & 3)] = bf16lo_to_f32(u[j]) / den;
             q[j >> 2][2 * (j & 3) + 1] = bf16hi_to_f32(u[j]) / den;
         }
-        codes = make_uint2(f32x8_to_e2m1x8(q[0]), f32x8_to_e2m1x8(q[1]));
+    } else {
+        return sc;
     }
+    codes = make_uint2(f32x8_to_e2m1x8(q[0]), f32x8_to_e2m1x8(q[1]));
     return sc;
 }
 
@@ -221,10 +250,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.0f;
 constexpr int kMaxSms = 160;  // CTAs the workspace has records for: two per SM of 16 rows, or one of 32
-// What a segment costs besides its units (its q, the merge of the warps, its
-// output), in units; shares are equal in units + kSegCost a segment.
-constexpr int kSegCost = 12;
-constexpr int kMinShare = 8;  // a CTA's share at least
+constexpr int kMinShare = 8;  // a CTA's share at least, in steps of the line
 
 // A producer warp, W consumer warps and a ring of S units per CTA, kRes CTAs
 // per SM.
@@ -245,6 +271,10 @@ struct AttnCfg {
     static constexpr int R = 8 * NT;
     static constexpr int T = 9 * D;                 // bytes of a tile
     static constexpr int kStageBytes = 2 * UT * T;
+    // What a segment costs besides its units (its q, the merge of the warps, its
+    // output), in units, which cost more with more rows; shares are equal in
+    // units + kSegCost a segment (48 ragged sequences: 83 us with 6, 72 with 12, 70 with 20).
+    static constexpr int kSegCost = NT == 1 ? 20 : 12;
     static constexpr int kRecFloats = R * (D + 2);  // m[R], l[R], o[R][D]
     static constexpr int kSmemBytes = S * kStageBytes + W * kRecFloats * 4 + S * (4 + 4 + 4);
     static_assert(kSmemBytes * kRes <= 226 * 1024, "shared memory per SM");
@@ -256,8 +286,8 @@ struct SeqWork {
     int32_t tile0, tiles;  // first tile any row sees, end of the last
     int32_t units, row_tiles;
     uint32_t err;
-    __device__ __forceinline__ int64_t cost(int hkv) const {
-        return (static_cast<int64_t>(units) + kSegCost) * hkv * row_tiles;
+    __device__ __forceinline__ int64_t cost(int seg_cost, int hkv) const {
+        return (static_cast<int64_t>(units) + seg_cost) * hkv * row_tiles;
     }
 };
 
@@ -290,7 +320,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int gro
 
 // A CTA's walk along its share: pieces of segments, in order.  On the line a
 // segment is kSegCost steps and then its units.
-template <int R, int UT>
+template <int R, int UT, int kSegCost>
 struct Walk {
     SeqWork w;
     int64_t left;  // steps left in the share
@@ -382,7 +412,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     int32_t *holds = reinterpret_cast<int32_t *>(empty + S / 2);              // which tiles a stage holds, a bit each
     __shared__ int64_t s_sums[W + 1], s_p;
     __shared__ int s_b, s_first, s_parts;
-    __shared__ Walk<R, UT> s_walk[W];
+    __shared__ Walk<R, UT, C::kSegCost> s_walk[W];
     __shared__ struct {
         int64_t total, ctas, lo, hi;  // of the line: its steps, the shares, this one
     } s_line;
@@ -413,7 +443,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     for (int b = b0; b < b1; ++b) {
         const SeqWork w = seq_work<R, UT>(a, b, group);
         err |= w.err;
-        mine += w.cost(hkv);
+        mine += w.cost(C::kSegCost, hkv);
     }
     if (err && cta == 0) atomicOr(&g_kv4_err, err);
     int64_t x = mine;
@@ -437,7 +467,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     if (lo >= before && lo < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
-            const int64_t cost = seq_work<R, UT>(a, b, group).cost(hkv);
+            const int64_t cost = seq_work<R, UT>(a, b, group).cost(C::kSegCost, hkv);
             if (lo < at + cost) {
                 s_b = b;
                 s_p = lo - at;
@@ -447,7 +477,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         }
     }
     __syncthreads();
-    Walk<R, UT> walk;
+    Walk<R, UT, C::kSegCost> walk;
     walk.start(a, s_b, s_p, hi - lo, group);
 
     if (warp == W) {
@@ -540,11 +570,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 
     // The walk stays in shared memory: what the unit loop does not need would
     // cost it a dozen registers.
-    Walk<R, UT> &kept = s_walk[warp];
+    Walk<R, UT, C::kSegCost> &kept = s_walk[warp];
     if (lane == 0) kept = walk;
     __syncwarp();
     while (true) {
-        Walk<R, UT> walk = kept;
+        Walk<R, UT, C::kSegCost> walk = kept;
         __syncwarp();
         const bool more = walk.next(a, hkv, group);
         if (lane == 0) kept = walk;

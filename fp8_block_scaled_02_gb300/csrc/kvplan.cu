@@ -194,7 +194,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t stream) {
     attrs[1].val.clusterDim.y = 1;
     attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kv_plan_kernel, a);
 }
 
