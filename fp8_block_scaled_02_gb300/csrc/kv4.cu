@@ -231,8 +231,9 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
 // A CTA is a producer warp and W consumer warps around a ring of S units.  The
 // producer walks the share and copies units in pairs, by one gather of four
 // tiles for K and one for V wherever they lie (a tile is a row of the cache's
-// map); a warp issues a bulk copy in some 235 clocks, and copies of one or two
-// tiles, as pages of 16 allow, cost 143 us at 16 x 32768 keys of 8 heads, where this takes 134.
+// map); a warp issues a bulk copy in some 235 clocks, and with copies of one or
+// two tiles, as pages of 16 allow, it did not keep up (16 x 32768 keys of 8
+// heads: 143 us, 134 with the gather; 123 with the steps after it).
 // It is pieces ahead of the consumers, so table lookups and copies cost no
 // time between them.  The consumers of a piece take its units in turn and join their
 // (m, l, o) in shared memory; a segment of one unit is one warp's alone, beside
@@ -385,7 +386,7 @@ __device__ __forceinline__ void bar_consumers(int threads) {
 
 // (a.h sa, b.h sb) for half h of a and b, from (sa, 0) and (0, sb): two
 // instructions of the FMA pipe instead of a byte permute and one; the ALU pipe
-// has the conversions already (2 us of 130 at 16 x 32768 keys of 8 heads).
+// has the conversions already (128 us instead of 130 at 16 x 32768 keys of 8 heads when it came).
 __device__ __forceinline__ uint32_t pair_f16(uint32_t a, uint32_t b, uint32_t sa, uint32_t sb, int h) {
     const __half2 va = *reinterpret_cast<const __half2 *>(&a), vb = *reinterpret_cast<const __half2 *>(&b);
     const __half2 x = h ? __high2half2(va) : __low2half2(va), y = h ? __high2half2(vb) : __low2half2(vb);
@@ -593,8 +594,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         const int first_pos = walk.w.len - walk.w.n_q;  // position of query token 0
 
         // ---- q as f16 B fragments, an exact power-of-two rescale per row
-        // in the warp's record, which is free until the piece ends: with them in registers a thread would need
-        // more than the 96 that let a ninth warp run beside eight (129 us instead of 123 at 16 x 32768 keys)
+        // in the warp's record, which is free until the piece ends: in registers they would
+        // take a thread past the 96 that let eight consumer warps run beside the producer
+        // (16 x 32768 keys of 8 heads: 129 us instead of 123)
         uint2 *sq = reinterpret_cast<uint2 *>(merge + warp * C::kRecFloats) + lane;  // [NT][kSteps][32]
         float sc[NT][2];   // score scale of this lane's columns 2t, 2t + 1
         int pos[NT][2];    // their positions

@@ -9,13 +9,16 @@
 // The row is read once, 16 bytes a load, by the CTAs of one cluster (one CTA
 // when there are many rows); every thread keeps a running (m, l, t) of its
 // elements.  The top comes out of the same maxima: the k-th largest of the
-// threads' maxima is a lower bound of the row part's k-th largest element,
-// and only threads whose maximum reaches it can hold one of the top k, about
-// k of the 512.  Of their elements those in pieces (an eighth or so) whose
-// maximum reaches the bound are read again, from L2, and what reaches the
-// bound is ranked in shared memory.  Rows of
-// equals, such as masked ones, whose equals at the bound do not fit there
-// take an ordered scan that stops when it has enough.
+// maxima of disjoint groups of threads is a lower bound of the row part's
+// k-th largest element.  The pieces (an eighth or so of a thread's elements)
+// whose maximum reaches it are read again, from L2, and what reaches the
+// bound is ranked in shared memory.  Rows of equals, such as masked ones,
+// whose equals at the bound do not fit there take an ordered scan that stops
+// when it has enough.
+//
+// Bound by HBM in bytes (floor 92 us for 2048 rows of 152064 bf16 at the
+// measured copy rate), by instruction issue as built: 102 us without the top,
+// 123 us with the top 20 (5.1 TB/s).
 #include "common.cuh"
 #include "internal.h"
 
@@ -627,9 +630,12 @@ cudaError_t launch_rows(const LogprobArgs &a, int splits, cudaStream_t stream) {
 
 cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
     const int splits = pick_row_split(a);
-    // Few rows: 512 threads a CTA, more of a row in flight (one row of 152064 bf16, top 20: 11.2 us, 13.8 with 256).
-    // Many: 256, so that four CTAs of an SM read while one looks for its top (2048 rows: 123 us, 136 with 512).
-    if (splits > 1) return a.f32 ? launch_rows<true, 512>(a, splits, stream) : launch_rows<false, 512>(a, splits, stream);
+    // Few rows: 512 threads a CTA, more of a row in flight (one row of 152064 bf16, top 20: 11.2 us, 13.8 with 256;
+    // 300 rows: 23 us and 26, but of 32003 9.8 us and 9.3).  Many: 256, so that four CTAs of an SM read while one
+    // looks for its top (2048 rows: 123 us, 136 with 512).
+    const bool one_wave = a.rows <= 2 * static_cast<int64_t>(device_sm_count());
+    if (splits > 1 || (one_wave && a.vocab / (a.f32 ? 4 : 8) >= 2 * kFlight * 512))
+        return a.f32 ? launch_rows<true, 512>(a, splits, stream) : launch_rows<false, 512>(a, splits, stream);
     return a.f32 ? launch_rows<true, 256>(a, 1, stream) : launch_rows<false, 256>(a, 1, stream);
 }
 

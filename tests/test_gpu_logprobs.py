@@ -100,6 +100,17 @@ def test_many_rows(pkg, m, v, top, dtype):
     check(pkg, x, np.random.default_rng(m).integers(0, v, m), top)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,v,top", [(160, 50003, 20), (290, 49152, 0)])
+def test_rows_of_one_block_each_in_one_wave(pkg, m, v, top, dtype):
+    x = logits(m, v, m, dtype, pad=3).clone()
+    x[3::50] = torch.finfo(dtype).min
+    x[4::50] = -np.inf
+    x[5::50] = 0.25
+    x[8::50, v // 2:] = -np.inf
+    check(pkg, x, np.random.default_rng(m).integers(0, v, m), top)
+
+
 @pytest.mark.parametrize("v", [70, 5000, 152064])
 @pytest.mark.parametrize("low", [-np.inf, "lowest"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
