@@ -33,7 +33,10 @@ __device__ uint32_t g_kv4_err;
 // ------------------------------------------------------- append and gather
 // A thread has 32 consecutive elements of a head vector (two groups): 64 bytes
 // of bf16, 16 of codes and 2 of scales; a warp's accesses are contiguous.  Both
-// are bound by HBM (read 2 B, write 9/16 B an element, or the reverse).
+// are bound by HBM (read 2 B, write 9/16 B an element, or the reverse).  K and V
+// of 8 heads of 128: 8191 tokens are written in 8.3 us (5.2 TB/s; 11.6 with IEEE
+// divisions) and read back in 7.1 (6.1), 65536 are read in 60 (5.7; L2 no longer
+// holds what is written; 65 with half the bytes a thread and a division for its place).
 constexpr int kCopyThreads = 256;
 
 __device__ __forceinline__ void ld_nc_v8(const void *p, uint32_t (&v)[8]) {
@@ -235,9 +238,9 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
 // two tiles, as pages of 16 allow, it did not keep up (16 x 32768 keys of 8
 // heads: 143 us, 134 with the gather; 123 with the steps after it).
 // It is pieces ahead of the consumers, so table lookups and copies cost no
-// time between them.  The consumers of a piece take its units in turn and join their
-// (m, l, o) in shared memory; a segment of one unit is one warp's alone, beside
-// others.  Per unit:
+// time between them.  The consumers of a piece take its units in turn and join
+// their (m, l, o) in shared memory; a segment of one unit is one warp's alone,
+// beside others.  Per unit:
 //   S^T[32 keys, R rows] = K q^T with f16 mma.sync m16n8k16.  The order of
 //   the contraction is free: lane t of a quad takes elements 32 t .. 32 t + 31
 //   of a key (D = 128), so its codes are one 16-byte load; codes convert to
@@ -245,8 +248,12 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
 //   O^T[D, R] += V^T P^T: row group g of the product is 16 consecutive
 //   elements, column pair t the keys kv4_row(t, j), so a lane's codes are 8
 //   bytes of each of four keys; pair_f16 interleaves two keys' values and
-//   multiplies with their scales.  P^T comes from the S^T fragments by movmatrix, because key m
-//   of S^T is key m of the product.
+//   multiplies with their scales.  P^T comes from the S^T fragments by
+//   movmatrix, because key m of S^T is key m of the product.
+// Bytes would take 89 us at 16 x 32768 keys of 8 heads (groups of 4) at the
+// measured copy rate; it takes 123 us, 4.9 TB/s: the dequantization beside the
+// matrix products keeps the ALU and FMA pipes and the issue slots that busy
+// (127 us when a cache that fits L2 was read).
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.0f;
@@ -393,6 +400,13 @@ __device__ __forceinline__ uint32_t pair_f16(uint32_t a, uint32_t b, uint32_t sa
     const __half2 r =
         __hfma2(x, *reinterpret_cast<const __half2 *>(&sa), __hmul2(y, *reinterpret_cast<const __half2 *>(&sb)));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Where 16 bytes of a row of a warp's o are in shared memory: the eight lanes of
+// a store (two values of g, four rows two apart) and of a load meet no bank twice.
+template <int D>
+__device__ __forceinline__ int merge_chunk(int r, int chunk) {
+    return chunk ^ (D == 128 ? (r >> 1) & 3 : ((r >> 1) & 1) | (r & 4));
 }
 
 // Key of a tile that is row m (and m + 8) of the score product, and column
@@ -885,9 +899,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     rec[R + r] = l_run[n][c];
                 }
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    *reinterpret_cast<float2 *>(rec + 2 * R + r * D + g * (D / 8) + 2 * i) =
-                        make_float2(o[n][i][c], o[n][i][c + 2]);
+                for (int i = 0; i < kSteps; i += 2)
+                    *reinterpret_cast<float4 *>(rec + 2 * R + r * D + 4 * merge_chunk<D>(r, g * (D / 32) + i / 2)) =
+                        make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
             }
         bar_consumers(W * 32);
         float *out_rec = records + static_cast<int64_t>(2 * cta + (starts ? 1 : 0)) * C::kRecFloats;
@@ -905,7 +919,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 const float mw = src[r];
                 if (mw == -INFINITY) continue;
                 const float f = ex2(mw - M);
-                const float4 v = *reinterpret_cast<const float4 *>(src + 2 * R + r * D + d4 * 4);
+                const float4 v = *reinterpret_cast<const float4 *>(src + 2 * R + r * D + 4 * merge_chunk<D>(r, d4));
                 L += f * src[R + r];
                 O.x += f * v.x, O.y += f * v.y, O.z += f * v.z, O.w += f * v.w;
             }
@@ -934,7 +948,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         if (tid == 0) {
             // the line's step of the segment's first unit, and whose share a step is in
             const int64_t at = starts ? s_line.hi - kept.u1 : s_line.lo - kept.u0;
-            auto owner = [&](int64_t step) { return static_cast<int>(((step + 1) * s_line.ctas + s_line.total - 1) / s_line.total - 1); };
+            auto owner = [&](int64_t step) {
+                return static_cast<int>(((step + 1) * s_line.ctas + s_line.total - 1) / s_line.total - 1);
+            };
             const int c0 = owner(at), parts = owner(at + kept.w.units - 1) - c0 + 1;
             const uint32_t before = atomicInc(arrived + c0, static_cast<uint32_t>(parts - 1));  // wraps to 0
             s_first = c0;

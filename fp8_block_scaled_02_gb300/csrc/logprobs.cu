@@ -296,7 +296,7 @@ __device__ int find_candidates(const Row<F32> &row, int v0, int v1, int top, flo
     constexpr int VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // ---- a bound at or below the top-th largest of the threads' maxima, by the upper half of its key (bf16 has no
-    // more): the top-th largest of the two largest of each warp, which every warp finds for itself
+    // more): the top-th largest of the kBest largest of each warp, which every warp finds for itself
     uint32_t left = order_key(m);
 #pragma unroll
     for (int i = 0; i < kBest; ++i) {
