@@ -326,6 +326,12 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int gro
     return w;
 }
 
+// a / b of non-negative numbers, by the 32-bit division where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // A CTA's walk along its share: pieces of segments, in order.  On the line a
 // segment is kSegCost steps and then its units.
 template <int R, int UT, int kSegCost>
@@ -342,9 +348,9 @@ struct Walk {
         left = steps;
         w = seq_work<R, UT>(a, b, group);
         const int seg_cost = w.units + kSegCost;
-        const int64_t seg = p / seg_cost;
+        const int64_t seg = quotient(p, seg_cost);
         at = static_cast<int>(p - seg * seg_cost);
-        kvh = static_cast<int>(seg / w.row_tiles);
+        kvh = static_cast<int>(quotient(seg, w.row_tiles));
         row_tile = static_cast<int>(seg - static_cast<int64_t>(kvh) * w.row_tiles);
     }
     __device__ __forceinline__ bool next(const Kv4AttnArgs &a, int hkv, int group) {
@@ -400,6 +406,59 @@ __device__ __forceinline__ uint32_t pair_f16(uint32_t a, uint32_t b, uint32_t sa
     const __half2 r =
         __hfma2(x, *reinterpret_cast<const __half2 *>(&sa), __hmul2(y, *reinterpret_cast<const __half2 *>(&sb)));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <int E>
+__device__ __forceinline__ void load_floats(const float *p, float (&v)[E]) {
+    if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void load_floats_cg(const float *p, float (&v)[E]) {
+    if constexpr (E == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void store_floats(float *p, const float (&v)[E]) {
+    if constexpr (E == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+
+template <int E>
+__device__ __forceinline__ void fma_floats(float (&o)[E], float f, const float (&v)[E]) {
+#pragma unroll
+    for (int d = 0; d < E; ++d) o[d] += f * v[d];
+}
+
+// Releases this CTA's earlier writes and acquires the others' to the GPU.
+__device__ __forceinline__ uint32_t atomic_inc_acq_rel(uint32_t *p, uint32_t limit) {
+    uint32_t before;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(before) : "l"(p), "r"(limit) : "memory");
+    return before;
 }
 
 // Where 16 bytes of a row of a warp's o are in shared memory: the eight lanes of
@@ -477,7 +536,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     }
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + kMinShare - 1) / kMinShare);
     if (cta >= ctas) return;
-    const int64_t lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
+    const int64_t lo = quotient(total * cta, ctas), hi = quotient(total * (cta + 1), ctas);
     if (tid == 0) s_line.total = total, s_line.ctas = ctas, s_line.lo = lo, s_line.hi = hi;
     if (lo >= before && lo < before + mine) {
         int64_t at = before;
@@ -532,7 +591,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         uint32_t place, place_next;
         int n = look_up(place);
         while (n > 0 && ok) {
-            const int n_next = look_up(place_next);
+            int n_next = -1;  // not looked up yet
+            place_next = kNoTile;
             // lanes 2 j and 2 j + 1 copy K and V of pair j: four tiles each, rows of the caches' maps
             int32_t row[2 * UT];
 #pragma unroll
@@ -559,6 +619,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     tma_gather4_2d(dst, lane % 2 ? &tm_v : &tm_k, &full[st], 0, row);
                 }
                 __syncwarp();
+                // with copies under way, what comes after this window
+                if (n_next < 0 && (first == 2 || first + 2 >= window_pairs)) n_next = look_up(place_next);
             }
             if (ok) pairs += static_cast<uint32_t>(window_pairs);
             n = n_next;
@@ -577,6 +639,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
     const float base = a.sm_scale * __ldg(a.k_scale) * kLog2e;
     const float v_scale = __ldg(a.v_scale);
     constexpr int kLaneCodes = D / 4;  // codes of a key a lane holds for S^T
+    constexpr int E = D / 32;          // of a row, when a warp joins its parts
     constexpr int kSteps = D / 16;
     static_assert(NT * kSteps * 32 * 8 <= C::kRecFloats * 4, "a record holds q");
     uint32_t count = 0;  // units of the pieces before this one
@@ -904,106 +967,103 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                         make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
             }
         bar_consumers(W * 32);
+        // ---- joined, a warp per row; a lane has D / 32 elements of it
         float *out_rec = records + static_cast<int64_t>(2 * cta + (starts ? 1 : 0)) * C::kRecFloats;
-        for (int e = tid; e < R * D / 4; e += W * 32) {
-            const int r = e / (D / 4), d4 = e - r * (D / 4);
-            if (r >= rows) break;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < W; ++w) M = fmaxf(M, merge[w * C::kRecFloats + r]);
-            float L = 0.0f;
-            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int live = min(rows, R);
+        auto finish_row = [&](int r, float M, float L, const float (&O)[E]) {
+            const int tok = n_q > 1 ? (row0 + r) / group : 0, h = row0 + r - tok * group;
+            const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
+            const float inv = L > 0.0f ? v_scale / L : 0.0f;
+            uint32_t *dst =
+                reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E);
+            if constexpr (E == 4)
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(f32x2_to_bf16x2(O[0] * inv, O[1] * inv), f32x2_to_bf16x2(O[2] * inv, O[3] * inv));
+            else
+                *dst = f32x2_to_bf16x2(O[0] * inv, O[1] * inv);
+            if (a.lse && lane == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+        };
+#pragma unroll 1
+        for (int r = warp; r < live; r += W) {
+            const float m = lane < W ? merge[lane * C::kRecFloats + r] : -INFINITY;
+            const float l = lane < W ? merge[lane * C::kRecFloats + R + r] : 0.0f;
+            const float M = warp_max(m), f = m == -INFINITY ? 0.0f : ex2(m - M), L = warp_sum(f * l);
+            const uint32_t some = __ballot_sync(0xffffffffu, m != -INFINITY);
+            float O[E] = {};
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float *src = merge + w * C::kRecFloats;
-                const float mw = src[r];
-                if (mw == -INFINITY) continue;
-                const float f = ex2(mw - M);
-                const float4 v = *reinterpret_cast<const float4 *>(src + 2 * R + r * D + 4 * merge_chunk<D>(r, d4));
-                L += f * src[R + r];
-                O.x += f * v.x, O.y += f * v.y, O.z += f * v.z, O.w += f * v.w;
+                const float fw = __shfl_sync(0xffffffffu, f, w);
+                float v[E];
+                load_floats(merge + w * C::kRecFloats + 2 * R + r * D + 4 * merge_chunk<D>(r, lane * E / 4) + lane * E % 4, v);
+                // a part without keys has no sum that is a number
+                if ((some >> w) & 1) fma_floats(O, fw, v);
             }
             if (starts && ends) {
-                const int tok = (row0 + r) / group, h = row0 + r - tok * group;
-                const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
-                const float inv = L > 0.0f ? v_scale / L : 0.0f;
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d4 * 4) =
-                    make_uint2(f32x2_to_bf16x2(O.x * inv, O.y * inv), f32x2_to_bf16x2(O.z * inv, O.w * inv));
-                if (a.lse && d4 == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+                finish_row(r, M, L, O);
             } else {
-                if (d4 == 0) {
-                    out_rec[r] = M;
-                    out_rec[R + r] = L;
-                }
-                *reinterpret_cast<float4 *>(out_rec + 2 * R + r * D + d4 * 4) = O;
+                if (lane == 0) out_rec[r] = M, out_rec[R + r] = L;
+                store_floats(out_rec + 2 * R + r * D + lane * E, O);
             }
         }
-        if (starts && ends) {
-            bar_consumers(W * 32);  // the records are free again
-            continue;
-        }
+        bar_consumers(W * 32);  // the warps' records are free again
+        if (starts && ends) continue;
         // ---- a part of a split segment: the last of its CTAs to come here joins them, in their order
-        __threadfence();
-        bar_consumers(W * 32);
         if (tid == 0) {
             // the line's step of the segment's first unit, and whose share a step is in
             const int64_t at = starts ? s_line.hi - kept.u1 : s_line.lo - kept.u0;
             auto owner = [&](int64_t step) {
-                return static_cast<int>(((step + 1) * s_line.ctas + s_line.total - 1) / s_line.total - 1);
+                return static_cast<int>(quotient((step + 1) * s_line.ctas + s_line.total - 1, s_line.total) - 1);
             };
             const int c0 = owner(at), parts = owner(at + kept.w.units - 1) - c0 + 1;
-            const uint32_t before = atomicInc(arrived + c0, static_cast<uint32_t>(parts - 1));  // wraps to 0
+            // releases what the barrier has ordered before it, the whole CTA's record; wraps to 0
+            const uint32_t before = atomic_inc_acq_rel(arrived + c0, static_cast<uint32_t>(parts - 1));
             s_first = c0;
             s_parts = before == static_cast<uint32_t>(parts - 1) ? parts : 0;
         }
         bar_consumers(W * 32);
         const int parts = s_parts;
-        if (parts == 0) continue;  // merge, s_first and s_parts are written after the next piece's barriers only
-        __threadfence();
-        auto part = [&](int j) { return records + static_cast<int64_t>(2 * (s_first + j) + (j == 0)) * C::kRecFloats; };
-        const int live = min(rows, R);
-        // weights of the parts, and v_scale / l, per row
-        static_assert(2 + kMaxSms * C::kRes <= W * (D + 2), "merge holds them");
+        if (parts == 0) continue;  // s_first and s_parts are written after the next piece's barriers only
+        const int first_cta = s_first;
+        auto part = [&](int j) {
+            return records + static_cast<int64_t>(2 * (first_cta + j) + (j == 0)) * C::kRecFloats;
+        };
+#pragma unroll 1
         for (int r = warp; r < live; r += W) {
-            float M = -INFINITY;
-            for (int j = lane; j < parts; j += 32) M = fmaxf(M, __ldcg(part(j) + r));
+            float M = -INFINITY, L = 0.0f;
+            float O[E] = {};
+            for (int j0 = 0; j0 < parts; j0 += 32) {  // lane j: part j0 + j's m and l
+                constexpr int kAhead = 8;
+                const int count = min(32, parts - j0);
+                float m = -INFINITY, l = 0.0f;
+                if (lane < count) m = __ldcg(part(j0 + lane) + r), l = __ldcg(part(j0 + lane) + R + r);
+                float v[kAhead][E];
+                auto load = [&](int i) {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-            float L = 0.0f;
-            for (int j = lane; j < parts; j += 32) {
-                const float m = __ldcg(part(j) + r), f = m == -INFINITY ? 0.0f : ex2(m - M);
-                L += f * __ldcg(part(j) + R + r);
-                merge[2 * R + j * R + r] = f;
-            }
+                    for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-            if (lane == 0) {
-                merge[r] = L > 0.0f ? v_scale / L : 0.0f;
-                if (a.lse) {
-                    const int tok = (row0 + r) / group, h = row0 + r - tok * group;
-                    a.lse[static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h] =
-                        L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+                        for (int d = 0; d < E; ++d) v[u][d] = 0.0f;
+                        if (i + u < count) load_floats_cg(part(j0 + i + u) + 2 * R + r * D + lane * E, v[u]);
+                    }
+                };
+                load(0);  // on their way beside m and l
+                const float M_new = fmaxf(M, warp_max(m));
+                const float f = m == -INFINITY ? 0.0f : ex2(m - M_new), keep = M == -INFINITY ? 0.0f : ex2(M - M_new);
+                L = L * keep + warp_sum(f * l);
+#pragma unroll
+                for (int d = 0; d < E; ++d) O[d] *= keep;
+                const uint32_t some = __ballot_sync(0xffffffffu, m != -INFINITY);
+                for (int i = 0; i < count; i += kAhead) {
+                    if (i > 0) load(i);
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const float fu = __shfl_sync(0xffffffffu, f, (i + u) & 31);
+                        if (i + u < count && ((some >> (i + u)) & 1)) fma_floats(O, fu, v[u]);
+                    }
                 }
+                M = M_new;
             }
+            finish_row(r, M, L, O);
         }
-        bar_consumers(W * 32);
-        for (int e = tid; e < live * D / 4; e += W * 32) {
-            const int r = e / (D / 4), d4 = e - r * (D / 4);
-            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int j = 0; j < parts; ++j) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(j) + 2 * R + r * D + d4 * 4));
-                const float f = merge[2 * R + j * R + r];
-                // a part without keys has no sum that is a number
-                if (f > 0.0f) O.x += f * v.x, O.y += f * v.y, O.z += f * v.z, O.w += f * v.w;
-            }
-            const int tok = (row0 + r) / group, h = row0 + r - tok * group;
-            const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
-            const float inv = merge[r];
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d4 * 4) =
-                make_uint2(f32x2_to_bf16x2(O.x * inv, O.y * inv), f32x2_to_bf16x2(O.z * inv, O.w * inv));
-        }
-        bar_consumers(W * 32);
     }
 }
 
