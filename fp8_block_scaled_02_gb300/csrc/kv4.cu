@@ -408,15 +408,18 @@ __device__ __forceinline__ uint32_t pair_f16(uint32_t a, uint32_t b, uint32_t sa
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// Over groups of `width` lanes.
+template <int width>
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int o = width / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
 
+template <int width>
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = width / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
@@ -983,26 +986,34 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 *dst = f32x2_to_bf16x2(O[0] * inv, O[1] * inv);
             if (a.lse && lane == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
         };
-#pragma unroll 1
-        for (int r = warp; r < live; r += W) {
-            const float m = lane < W ? merge[lane * C::kRecFloats + r] : -INFINITY;
-            const float l = lane < W ? merge[lane * C::kRecFloats + R + r] : 0.0f;
-            const float M = warp_max(m), f = m == -INFINITY ? 0.0f : ex2(m - M), L = warp_sum(f * l);
-            const uint32_t some = __ballot_sync(0xffffffffu, m != -INFINITY);
-            float O[E] = {};
+        // eight lanes find the weights of the warps' parts of one of four rows
+        for (int r0 = warp; r0 < live; r0 += 4 * W) {
+            const int mine = r0 + (lane >> 3) * W, w_mine = lane & 7;
+            const bool there = w_mine < W && mine < live;
+            const float m = there ? merge[w_mine * C::kRecFloats + mine] : -INFINITY;
+            const float l = there ? merge[w_mine * C::kRecFloats + R + mine] : 0.0f;
+            const float M = warp_max<8>(m), f = m == -INFINITY ? 0.0f : ex2(m - M), L = warp_sum<8>(f * l);
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float fw = __shfl_sync(0xffffffffu, f, w);
-                float v[E];
-                load_floats(merge + w * C::kRecFloats + 2 * R + r * D + 4 * merge_chunk<D>(r, lane * E / 4) + lane * E % 4, v);
-                // a part without keys has no sum that is a number
-                if ((some >> w) & 1) fma_floats(O, fw, v);
-            }
-            if (starts && ends) {
-                finish_row(r, M, L, O);
-            } else {
-                if (lane == 0) out_rec[r] = M, out_rec[R + r] = L;
-                store_floats(out_rec + 2 * R + r * D + lane * E, O);
+            for (int k = 0; k < 4 && k * W < R; ++k) {
+                const int r = r0 + k * W;
+                if (r >= live) break;
+                float O[E] = {};
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float fw = __shfl_sync(0xffffffffu, f, 8 * k + w);
+                    float v[E];
+                    load_floats(merge + w * C::kRecFloats + 2 * R + r * D + 4 * merge_chunk<D>(r, lane * E / 4) +
+                                    lane * E % 4, v);
+                    // a part without keys has no weight and no sum that is a number
+                    if (fw != 0.0f) fma_floats(O, fw, v);
+                }
+                const float Mr = __shfl_sync(0xffffffffu, M, 8 * k), Lr = __shfl_sync(0xffffffffu, L, 8 * k);
+                if (starts && ends) {
+                    finish_row(r, Mr, Lr, O);
+                } else {
+                    if (lane == 0) out_rec[r] = Mr, out_rec[R + r] = Lr;
+                    store_floats(out_rec + 2 * R + r * D + lane * E, O);
+                }
             }
         }
         bar_consumers(W * 32);  // the warps' records are free again
@@ -1046,9 +1057,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     }
                 };
                 load(0);  // on their way beside m and l
-                const float M_new = fmaxf(M, warp_max(m));
+                const float M_new = fmaxf(M, warp_max<32>(m));
                 const float f = m == -INFINITY ? 0.0f : ex2(m - M_new), keep = M == -INFINITY ? 0.0f : ex2(M - M_new);
-                L = L * keep + warp_sum(f * l);
+                L = L * keep + warp_sum<32>(f * l);
 #pragma unroll
                 for (int d = 0; d < E; ++d) O[d] *= keep;
                 const uint32_t some = __ballot_sync(0xffffffffu, m != -INFINITY);
