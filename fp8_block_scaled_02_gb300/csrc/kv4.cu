@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
 // tiles for K and one for V wherever they lie (a tile is a row of the cache's
 // map); a warp issues a bulk copy in some 235 clocks, and with copies of one or
 // two tiles, as pages of 16 allow, it did not keep up (16 x 32768 keys of 8
-// heads: 143 us, 134 with the gather; 123 with the steps after it).
+// heads: 143 us, 134 with the gather; 121 with the steps after it).
 // It is pieces ahead of the consumers, so table lookups and copies cost no
 // time between them.  The consumers of a piece take its units in turn and join
 // their (m, l, o) in shared memory; a segment of one unit is one warp's alone,
@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
 //   multiplies with their scales.  P^T comes from the S^T fragments by
 //   movmatrix, because key m of S^T is key m of the product.
 // Bytes would take 89 us at 16 x 32768 keys of 8 heads (groups of 4) at the
-// measured copy rate; it takes 123 us, 4.9 TB/s: the dequantization beside the
+// measured copy rate; it takes 121 us, 5.0 TB/s: the dequantization beside the
 // matrix products keeps the ALU and FMA pipes and the issue slots that busy
-// (127 us when a cache that fits L2 was read).
+// (reading a cache that fits L2 saved 3% when tried).
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.0f;
