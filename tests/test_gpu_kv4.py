@@ -277,6 +277,18 @@ def test_attention_longer(pkg, batch, length, hq, hkv):
     check(o, lse, q, range(batch + 1), kc, vc, table, lens, sm, pkg=pkg)
 
 
+@pytest.mark.parametrize("hq,d,nq", [(8, 128, 1), (4, 64, 1), (16, 128, 1), (6, 128, 4), (8, 64, 3), (8, 128, 4)])
+@pytest.mark.parametrize("peaked", [False, True])
+def test_one_sequence_over_many_blocks(pkg, hq, d, nq, peaked):
+    """One kv head, more parts than a warp has lanes; with peaked scores a few of them hold all the weight."""
+    lens = [30011]
+    kc, vc, table = layer(lens, 1, d, 64, 41, extra=0)
+    q = normal((nq, hq, d), 42, 30.0 if peaked else 1.0)
+    sm = 0.3 if peaked else d ** -0.5
+    o, lse = attend(pkg, q, kc, vc, table, lens, sm, cu_q=[0, nq], max_q=nq)
+    check(o, lse, q, [0, nq], kc, vc, table, lens, sm, pkg=pkg)
+
+
 def test_many_sequences(pkg):
     rng = np.random.default_rng(30)
     lens = [int(v) for v in rng.integers(0, 300, 300)]
