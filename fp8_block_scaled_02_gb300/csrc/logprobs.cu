@@ -629,13 +629,17 @@ cudaError_t launch_rows(const LogprobArgs &a, int splits, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
-    const int splits = pick_row_split(a);
-    // Few rows: 512 threads a CTA, more of a row in flight (one row of 152064 bf16, top 20: 11.2 us, 13.8 with 256;
+    // Threads a CTA.  Few rows: 512, more of a row in flight (one row of 152064 bf16, top 20: 11.2 us, 13.8 with 256;
     // 300 rows: 23 us and 26, but of 32003 9.8 us and 9.3).  Many: 256, so that four CTAs of an SM read while one
-    // looks for its top (2048 rows: 123 us, 136 with 512).
-    const bool one_wave = a.rows <= 2 * static_cast<int64_t>(device_sm_count());
-    if (splits > 1 || (one_wave && a.vocab / (a.f32 ? 4 : 8) >= 2 * kFlight * 512))
+    // looks for its top (2048 rows: 123 us, 136 with 512, 129 with 128).  Many short ones, whose tops weigh more:
+    // 128 and eight CTAs (4096 rows of 32003, top 20: 75 us, 90 with 256; of 65536 120 and 121; 3000 of 100003 127
+    // and 123); also where those take all the rows at once and four do not (1000 rows of 152064: 63 us, 69 with 256).
+    const int splits = pick_row_split(a);
+    const int64_t sms = device_sm_count(), vecs = a.vocab / (a.f32 ? 4 : 8);
+    if (splits > 1 || (a.rows <= 2 * sms && vecs >= 2 * kFlight * 512))
         return a.f32 ? launch_rows<true, 512>(a, splits, stream) : launch_rows<false, 512>(a, splits, stream);
+    if (a.rows > 4 * sms && (vecs <= 8192 || a.rows <= 8 * sms))
+        return a.f32 ? launch_rows<true, 128>(a, 1, stream) : launch_rows<false, 128>(a, 1, stream);
     return a.f32 ? launch_rows<true, 256>(a, 1, stream) : launch_rows<false, 256>(a, 1, stream);
 }
 

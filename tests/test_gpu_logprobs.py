@@ -111,6 +111,18 @@ def test_rows_of_one_block_each_in_one_wave(pkg, m, v, top, dtype):
     check(pkg, x, np.random.default_rng(m).integers(0, v, m), top)
 
 
+@pytest.mark.parametrize("dtype,v", [(torch.bfloat16, 66003), (torch.float32, 33003)])
+@pytest.mark.parametrize("m,top", [(613, 20), (1230, 0), (1230, 20)])
+def test_many_long_rows(pkg, dtype, v, m, top):
+    x = logits(m, v, v, dtype, pad=1).clone()
+    x[3::50] = torch.finfo(dtype).min
+    x[3::50, 7:13] = 1.0
+    x[4::50] = -np.inf
+    x[5::50] = 0.25
+    x[8::50, v // 2:] = -np.inf
+    check(pkg, x, np.random.default_rng(v).integers(0, v, m), top)
+
+
 @pytest.mark.parametrize("v", [70, 5000, 152064])
 @pytest.mark.parametrize("low", [-np.inf, "lowest"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
