@@ -715,9 +715,12 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
 def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
                    stream=None):
     """Log probabilities of the targets [M] under logits [M, V] (bf16 or fp32,
-    rows may be padded), each row's entropy and its `top` best tokens
-    (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
+    rows may be padded, or one row expanded to M), each row's entropy and its
+    `top` best tokens (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
     m, v = _shape2(logits, "logits")
+    stride = logits.stride(0) if m > 1 else v
+    if 0 < stride < v:
+        raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")
     top = int(top)
     f32 = logits.dtype == torch.float32
     given = [spec for spec in (("logprobs", logprobs, torch.float32, m, False), ("entropy", entropy, torch.float32, m, False),
@@ -734,7 +737,7 @@ def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, t
     if top_logprobs is None:
         top_logprobs = _empty(stream, device, (m, top), torch.float32)
     _call(device, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs,
-          (logits.data_ptr(), int(f32), max(_row_stride(logits), v), m, v, targets.data_ptr(), top,
+          (logits.data_ptr(), int(f32), stride, m, v, targets.data_ptr(), top,
            logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr()), stream)
     return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
 

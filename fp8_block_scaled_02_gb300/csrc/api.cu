@@ -585,7 +585,7 @@ int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride, const int32_t *
 int fp8bs_token_logprobs(const void *logits, int logits_f32, int64_t row_stride, int64_t rows, int64_t vocab,
                          const int32_t *targets, int64_t top, float *logprobs, float *entropy, int32_t *top_ids,
                          float *top_logprobs, void *stream) {
-    if (rows < 0 || rows >= kMaxDim || vocab <= 0 || vocab >= kMaxDim || row_stride < vocab ||
+    if (rows < 0 || rows >= kMaxDim || vocab <= 0 || vocab >= kMaxDim || (row_stride < vocab && row_stride != 0) ||
         row_stride >= (int64_t{1} << 40) || top < 0 || top > kLogprobsMaxTop || top > vocab)
         return FP8BS_ERR_SHAPE;
     if (rows == 0) return FP8BS_OK;

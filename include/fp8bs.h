@@ -693,8 +693,8 @@ int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride,
  * #636 serves the lm_head whose logits these are).
  *
  *   logits        device, [rows, vocab], rows row_stride elements apart
- *                 (>= vocab); bf16, or fp32 if logits_f32 is non-zero;
- *                 aligned to its element size
+ *                 (>= vocab, or 0: one row for every target); bf16, or
+ *                 fp32 if logits_f32 is non-zero; aligned to its element size
  *   targets       device, [rows] int32; a negative target gives logprob 0,
  *                 one >= vocab too, with bit 4 of the device error word
  *   top           0..32, <= vocab (0: top_ids and top_logprobs may be NULL)
