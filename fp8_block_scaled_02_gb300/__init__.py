@@ -48,7 +48,18 @@ import ctypes
 import os
 import threading
 
-import torch
+
+class _OnFirstUse:
+    """torch, imported when a call first needs it: building and the calls that
+    only ask the library need none.  The module then takes this name."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _OnFirstUse()
 
 PATH_AUTO, PATH_DECODE, PATH_PREFILL, PATH_GENERIC = 0, 1, 2, 3
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DECODE: "decode", PATH_PREFILL: "prefill", PATH_GENERIC: "generic"}
