@@ -14,7 +14,7 @@
 //
 // A tile is 16 tokens of one kv head: codes, then scales, contiguous, so a
 // whole tile is one aligned copy of 9 D bytes.
-#include "common.cuh"
+#include "serving.cuh"
 #include "fp8bs.h"
 #include "internal.h"
 

@@ -15,7 +15,7 @@
 // shared memory (no exchange between CTAs), then the CTAs share the tokens.
 // The cluster barrier between the scan and the first store lets seq_lens and
 // free_head_out be the arrays they were read from.
-#include "common.cuh"
+#include "serving.cuh"
 #include "internal.h"
 
 #include <mutex>

@@ -19,7 +19,7 @@
 // Bound by HBM in bytes (floor 92 us for 2048 rows of 152064 bf16 at the
 // measured copy rate), by instruction issue as built: 102 us without the top,
 // 123 us with the top 20 (5.1 TB/s).
-#include "common.cuh"
+#include "serving.cuh"
 #include "internal.h"
 
 namespace fp8bs {
