@@ -39,12 +39,6 @@ __device__ uint32_t g_kv4_err;
 // holds what is written; 65 with half the bytes a thread and a division for its place).
 constexpr int kCopyThreads = 256;
 
-__device__ __forceinline__ void ld_nc_v8(const void *p, uint32_t (&v)[8]) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(p));
-}
-
 __device__ __forceinline__ void st_v8(void *p, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -138,7 +132,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_append_kernel(Kv4CopyArgs a,
     pdl_launch_dependents();
     pdl_wait();
     if (it.token >= a.tokens) return;
-    const int64_t slot = __ldg(a.slots + it.token);
+    const int64_t slot = a.slots[it.token];
     if (slot < 0 || slot >= a.num_slots) {
         if (slot != -1 && it.pair == 0 && !is_v) atomicOr(&g_kv4_err, ERRBIT_INDEX);
         return;
@@ -146,17 +140,17 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_append_kernel(Kv4CopyArgs a,
     const __nv_bfloat16 *src = x + it.token * stride + it.pair * 32;
     uint32_t u[2][8];
     if (wide) {
-        ld_nc_v8(src, u[0]);
-        ld_nc_v8(src + 16, u[1]);
+        ld_v8(src, u[0]);
+        ld_v8(src + 16, u[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 w = ld_nc_v4(src + 8 * i);
+            const uint4 w = ld_v4(src + 8 * i);
             uint32_t *d = u[i / 2] + 4 * (i & 1);
             d[0] = w.x, d[1] = w.y, d[2] = w.z, d[3] = w.w;
         }
     }
-    const float s = __ldg(is_v ? a.v_scale : a.k_scale), six_s = 6.0f * s;
+    const float s = *(is_v ? a.v_scale : a.k_scale), six_s = 6.0f * s;
     uint2 c0, c1;
     const uint32_t s0 = encode_group(u[0], s, six_s, c0), s1 = encode_group(u[1], s, six_s, c1);
     uint8_t *scales;
@@ -176,7 +170,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
     pdl_launch_dependents();
     pdl_wait();
     if (it.token >= a.tokens) return;
-    const int64_t slot = __ldg(a.slots + it.token);
+    const int64_t slot = a.slots[it.token];
     uint32_t r[2][8] = {};
     if (slot < 0 || slot >= a.num_slots) {
         if (slot != -1 && it.pair == 0 && !is_v) atomicOr(&g_kv4_err, ERRBIT_INDEX);
@@ -184,9 +178,9 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
         uint8_t *scales;
         const uint8_t *codes = slot_codes<D>(cache, static_cast<uint32_t>(slot), it.pair / (D / 32), it.pair % (D / 32),
                                              kv_heads, tpp, &scales);
-        const uint4 c = ld_nc_v4(codes);
+        const uint4 c = ld_v4(codes);
         const uint32_t sc = *reinterpret_cast<const uint16_t *>(scales);
-        const float s = __ldg(is_v ? a.v_scale : a.k_scale);
+        const float s = *(is_v ? a.v_scale : a.k_scale);
         const uint32_t s2 = e4m3x2_to_f16x2(sc), w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -306,7 +300,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int gro
     w.q0 = b;
     w.n_q = 1;
     if (a.cu_q) {
-        const int64_t q0 = __ldg(a.cu_q + b), n = static_cast<int64_t>(__ldg(a.cu_q + b + 1)) - q0;
+        const int64_t q0 = a.cu_q[b], n = static_cast<int64_t>(a.cu_q[b + 1]) - q0;
         if (q0 < 0 || n < 0 || n > a.max_q || q0 + n > a.tokens) {
             w.err = ERRBIT_INDEX;
             w.n_q = 0;
@@ -315,7 +309,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnArgs &a, int b, int gro
         }
         w.q0 = static_cast<int32_t>(q0);
     }
-    const int32_t len = __ldg(a.seq_lens + b), cap = static_cast<int32_t>(a.max_seq_len);
+    const int32_t len = a.seq_lens[b], cap = static_cast<int32_t>(a.max_seq_len);
     if (len < 0 || len > cap) w.err = ERRBIT_INDEX;
     w.len = min(max(len, 0), cap);
     const int64_t lo = a.window > 0 ? static_cast<int64_t>(w.len) - w.n_q - a.window + 1 : 0;
@@ -574,7 +568,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 const int tile = walk.w.tile0 + ub * UT + lane - n * UT;
                 if (lane >= n * UT && lane < (n + take) * UT && tile < walk.w.tiles) {
                     const int pg = tile / tpp;
-                    const int32_t blk = __ldg(a.block_table + static_cast<int64_t>(walk.b) * a.max_blocks + pg);
+                    const int32_t blk = a.block_table[static_cast<int64_t>(walk.b) * a.max_blocks + pg];
                     if (blk >= 0 && blk < a.num_blocks)
                         place =
                             static_cast<uint32_t>((static_cast<int64_t>(blk) * hkv + walk.kvh) * tpp + (tile - pg * tpp));
@@ -639,8 +633,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
 
     // ==================================================== consumers
     const int g = lane >> 2, t = lane & 3;
-    const float base = a.sm_scale * __ldg(a.k_scale) * kLog2e;
-    const float v_scale = __ldg(a.v_scale);
+    const float base = a.sm_scale * *a.k_scale * kLog2e;
+    const float v_scale = *a.v_scale;
     constexpr int kLaneCodes = D / 4;  // codes of a key a lane holds for S^T
     constexpr int E = D / 32;          // of a row, when a warp joins its parts
     constexpr int kSteps = D / 16;

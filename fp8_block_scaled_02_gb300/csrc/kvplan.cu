@@ -74,19 +74,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a) {
     if (tid == 0) s_taken = 0;
     pdl_wait();  // the lengths and the tables may come from the previous kernel
 
-    const int64_t head = __ldcg(a.free_head);
+    const int64_t head = *a.free_head;
     const bool head_ok = head >= 0 && head <= a.num_free;
     if (!head_ok) err |= ERRBIT_INDEX;
 
     // ---- the token axis
     int64_t tokens = 0;
-    for (int b = b0; b < b1; ++b) tokens += max(0, __ldcg(a.new_lens + b));
+    for (int b = b0; b < b1; ++b) tokens += max(0, a.new_lens[b]);
     int64_t total_tokens, at = block_exclusive(tokens, sums, total_tokens);
 
     // ---- blocks asked for, in request order
     int64_t asked = 0;
     for (int b = b0; b < b1; ++b) {
-        const int64_t c = __ldcg(a.ctx_lens + b), n = __ldcg(a.new_lens + b);
+        const int64_t c = a.ctx_lens[b], n = a.new_lens[b];
         cu[b] = clamp_i32(at);
         ctx[b] = static_cast<int32_t>(c);
         at += n > 0 ? n : 0;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(KvPlanArgs a) {
                 if (pg < have) {
                     blk = *entry;
                 } else {
-                    blk = __ldg(a.free_blocks + base[lo] + (pg - have));
+                    blk = a.free_blocks[base[lo] + (pg - have)];
                     if (blk < 0 || blk >= a.num_blocks) blk = -1;
                     if (p == pg * page) *entry = blk;  // the block's first token opens it
                 }

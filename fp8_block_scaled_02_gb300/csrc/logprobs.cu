@@ -106,7 +106,7 @@ struct Row {
     __device__ __forceinline__ void load(int vec, float (&x)[VE]) const {
         const char *p = base + static_cast<int64_t>(vec) * 16;
         if (whole(vec)) {
-            unpack(ld_nc_v4(p), x);
+            unpack(ld_v4(p), x);
             return;
         }
 #pragma unroll
@@ -472,7 +472,7 @@ __device__ __forceinline__ Sums read_row(const Row<F32> &row, int v0, int v1, in
         const bool ragged = !row.whole(v);
 #pragma unroll
         for (int j = 0; j < kFlight; ++j)
-            if (j > 0 || !ragged) w[j] = ld_nc_v4(row.base + static_cast<int64_t>(v + j * TH) * 16);
+            if (j > 0 || !ragged) w[j] = ld_v4(row.base + static_cast<int64_t>(v + j * TH) * 16);
         if (ragged) {
             float x[VE];
             row.load(v, x);
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) logprobs_kernel(const LogprobAr
     int64_t target = -1;
     float x_target = 0.0f;
     if (part == 0 && tid == 0) {
-        target = __ldg(a.targets + r);
+        target = a.targets[r];
         if (target >= 0 && target < a.vocab) x_target = row.at(target);
     }
     const Sums s = read_row<F32, TH>(row, v0, v1, tid, Pieces<TH>(v1 - v0), top > 0, sh);

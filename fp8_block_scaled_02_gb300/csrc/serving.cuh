@@ -11,6 +11,24 @@ namespace fp8bs {
 // Beside common.cuh's bits of a kernel's error word.
 constexpr uint32_t ERRBIT_CAPACITY = 1u << 5;  // a request found no free cache blocks
 
+// Loads of what the kernels before this one wrote.  A kernel here may be on
+// the GPU while they still write (programmatic dependent launch), so it does
+// not promise, as ld.global.nc and __ldg do, that nothing changes while it
+// lives: griddepcontrol.wait orders ordinary loads.  Not kept in L1.
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void ld_v8(const void *p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+
 // Four rows of a 2-D map whose box is one row, from column x: row[0 .. 3] one
 // after the other in shared memory (128-byte aligned).  A row out of range
 // reads zeros.
