@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     if (r >= rows) continue;
                     const int tok = n_q > 1 ? (row0 + r) / group : 0, h = row0 + r - tok * group;
                     const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
-                    const float L = l_run[n][c], inv = L > 0.0f ? v_scale / L : 0.0f;
+                    const float L = l_run[n][c], inv = L == 0.0f ? 0.0f : v_scale / L;  // 0: no key; may be NaN
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + g * (D / 8));
 #pragma unroll
                     for (int i = 0; i < kSteps; i += 4)
@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                                                 f32x2_to_bf16x2(o[n][i + 2][c] * inv, o[n][i + 2][c + 2] * inv),
                                                 f32x2_to_bf16x2(o[n][i + 3][c] * inv, o[n][i + 3][c + 2] * inv));
                     if (a.lse && g == 0)
-                        a.lse[row] = L > 0.0f ? (m_run[n][c] - kPShift + log2f(L)) * kLn2 : -INFINITY;
+                        a.lse[row] = L == 0.0f ? -INFINITY : (m_run[n][c] - kPShift + log2f(L)) * kLn2;
                 }
             continue;
         }
@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
         auto finish_row = [&](int r, float M, float L, const float (&O)[E]) {
             const int tok = n_q > 1 ? (row0 + r) / group : 0, h = row0 + r - tok * group;
             const int64_t row = static_cast<int64_t>(q0 + tok) * a.q_heads + head0 + h;
-            const float inv = L > 0.0f ? v_scale / L : 0.0f;
+            const float inv = L == 0.0f ? 0.0f : v_scale / L;
             uint32_t *dst =
                 reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E);
             if constexpr (E == 4)
@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     make_uint2(f32x2_to_bf16x2(O[0] * inv, O[1] * inv), f32x2_to_bf16x2(O[2] * inv, O[3] * inv));
             else
                 *dst = f32x2_to_bf16x2(O[0] * inv, O[1] * inv);
-            if (a.lse && lane == 0) a.lse[row] = L > 0.0f ? (M - kPShift + log2f(L)) * kLn2 : -INFINITY;
+            if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M - kPShift + log2f(L)) * kLn2;
         };
         // eight lanes find the weights of the warps' parts of one of four rows
         for (int r0 = warp; r0 < live; r0 += 4 * W) {
@@ -986,7 +986,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             const bool there = w_mine < W && mine < live;
             const float m = there ? merge[w_mine * C::kRecFloats + mine] : -INFINITY;
             const float l = there ? merge[w_mine * C::kRecFloats + R + mine] : 0.0f;
-            const float M = warp_max<8>(m), f = m == -INFINITY ? 0.0f : ex2(m - M), L = warp_sum<8>(f * l);
+            // a part without keys has weight -1 and is left out; its l is 0, or NaN where its scores are
+            const float M = warp_max<8>(m), f = m == -INFINITY ? -1.0f : ex2(m - M);
+            const float L = warp_sum<8>(f < 0.0f ? l : f * l);
 #pragma unroll
             for (int k = 0; k < 4 && k * W < R; ++k) {
                 const int r = r0 + k * W;
@@ -998,8 +1000,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     float v[E];
                     load_floats(merge + w * C::kRecFloats + 2 * R + r * D + 4 * merge_chunk<D>(r, lane * E / 4) +
                                     lane * E % 4, v);
-                    // a part without keys has no weight and no sum that is a number
-                    if (fw != 0.0f) fma_floats(O, fw, v);
+                    if (fw >= 0.0f) fma_floats(O, fw, v);
                 }
                 const float Mr = __shfl_sync(0xffffffffu, M, 8 * k), Lr = __shfl_sync(0xffffffffu, L, 8 * k);
                 if (starts && ends) {

@@ -580,7 +580,8 @@ int fp8bs_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens,
  *   scale = e4m3(fl32(amax / fl32(6 s))), den = fl32(s * scale),
  *   code = e2m1(fl32(x / den)), code = 0 where den = 0
  * (nearest-even, saturating), stored at slot slots[t] = block * page_size +
- * offset.  Slot -1 stores nothing (padding, refused requests); any other
+ * offset.  A group with NaN in it is stored as a NaN scale: all of it reads
+ * as NaN.  Slot -1 stores nothing (padding, refused requests); any other
  * slot outside [0, num_blocks * page_size) stores nothing and sets the
  * device error word (bit 4).  Two tokens of one call may not share a slot.
  *
@@ -625,10 +626,11 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  *   lse[i, h] = log sum_l exp(sm_scale * q[i, h, :] . dec(K[l, g]))
  * over keys l <= p (with window > 0: p - window < l <= p),
  * g = h / (num_q_heads / num_kv_heads).  A row that sees no key gives o = 0,
- * lse = -inf.  K and V decode exactly to f16 (code * scale); scores, the
- * softmax and all sums are fp32 (the weights enter the V sum as f16, held
- * against the running maximum so that 2^-39 of it is the smallest); one
- * bf16 rounding at the end.
+ * lse = -inf.  NaN that a row sees goes the formula's way: in q or a key to
+ * the whole row and its lse, in a value to the elements of its group.
+ * K and V decode exactly to f16 (code * scale); scores, the softmax and all
+ * sums are fp32 (the weights enter the V sum as f16, held against the running
+ * maximum so that 2^-39 of it is the smallest); one bf16 rounding at the end.
  *
  * Defined by: InfiniLM PR #586 (Benchmark: split-KV decode attention over
  * the paged cache) for the decode form; several query tokens, the window and
