@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
             const uint32_t have = static_cast<uint32_t>(holds[st]);
             const uint8_t *kt = ring + st / 2 * (2 * C::kStageBytes) + st % 2 * (UT * T), *vt = kt + C::kStageBytes;
             const int key0 = piece_key + u * C::kKeys;
-            const bool ragged = have != (1u << UT) - 1 || key0 + C::kKeys > len;
+            // some row does not see some key, or a key is not there
+            const bool partial = have != (1u << UT) - 1 || key0 + C::kKeys > min(len, clear_hi) || key0 < clear_lo;
 
             // ---- S^T: lane holds keys kv4_row(g), + 8 of each tile, rows 2t, 2t + 1 of each n
             float s[UT][NT][4];
@@ -798,7 +799,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[h][n][j] *= sc[n][j & 1];
-            if (ragged || key0 + C::kKeys > clear_hi || key0 < clear_lo) {
+            if (partial) {
 #pragma unroll
                 for (int h = 0; h < UT; ++h)
 #pragma unroll
@@ -882,11 +883,30 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::kThreads, AttnCfg<D, NT>::kRes
                     }
                     sb[j] = vt[h * T + 8 * D + row * (D / 16) + g * D / 128];
                 }
-                if (ragged) {  // keys past the end and tiles left out have weight 0, but old bytes there may be NaN
+                if (partial) {
+                    // What a row does not see has weight 0, which does not hide NaN: not the old bytes past the end and
+                    // in tiles left out, nor a stored NaN scale, which goes to the rows that see its key by hand.
+                    uint32_t nan = 0;  // the tile's keys with NaN in this lane's elements
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int row = kv4_row(2 * t + (j & 1)) + 8 * (j >> 1);
                         if (!((have >> h) & 1) || key0 + h * kKv4Tile + row >= len) sb[j] = 0;
+                        if ((sb[j] & 0x7Fu) == 0x7Fu) sb[j] = 0, nan |= 1u << row;
+                    }
+                    if (__any_sync(0xffffffffu, nan != 0)) {
+                        nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
+                        nan |= __shfl_xor_sync(0xffffffffu, nan, 2);
+                        for (; nan != 0; nan &= nan - 1) {
+                            const int key = key0 + h * kKv4Tile + __ffs(nan) - 1;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    if (key > pos[n][c] || (a.window > 0 && key <= pos[n][c] - a.window)) continue;
+#pragma unroll
+                                    for (int i = 0; i < kSteps; ++i) o[n][i][c] = o[n][i][c + 2] = NAN;
+                                }
+                        }
                     }
                 }
                 const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));

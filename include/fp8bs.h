@@ -626,8 +626,9 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  *   lse[i, h] = log sum_l exp(sm_scale * q[i, h, :] . dec(K[l, g]))
  * over keys l <= p (with window > 0: p - window < l <= p),
  * g = h / (num_q_heads / num_kv_heads).  A row that sees no key gives o = 0,
- * lse = -inf.  NaN that a row sees goes the formula's way: in q or a key to
- * the whole row and its lse, in a value to the elements of its group.
+ * lse = -inf.  A row takes nothing from a key that it does not see, whatever
+ * is stored there; NaN that it does see goes the formula's way: in q or a key
+ * to the whole row and its lse, in a value to the elements of its group.
  * K and V decode exactly to f16 (code * scale); scores, the softmax and all
  * sums are fp32 (the weights enter the V sum as f16, held against the running
  * maximum so that 2^-39 of it is the smallest); one bf16 rounding at the end.

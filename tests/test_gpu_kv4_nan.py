@@ -57,7 +57,7 @@ CASES = [([20, 33], [4, 1], 0, [(0, 18), (0, 19), (0, 3), (1, 32)]),
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (8, 1, 128), (12, 2, 128), (16, 1, 64), (4, 2, 64)])
 @pytest.mark.parametrize("lens,qls,window,keys", CASES)
-@pytest.mark.parametrize("where", ["k"])
+@pytest.mark.parametrize("where", ["k", "v"])
 def test_nan_keys_and_values(pkg, where, lens, qls, window, keys, hq, hkv, d):
     cu = np.concatenate([[0], np.cumsum(qls)])
     kc, vc, table = layer(lens, hkv, d, 16, 71)
