@@ -11,6 +11,12 @@
 Prompts and decoding are the same step: a prompt is a step with several new
 tokens per request.  Decode steps are captured once into a CUDA graph; the
 plan runs inside it, on lengths and a free list that live on the device.
+
+A request that finds no free blocks is refused for the step: its tokens keep
+their rows, with slot -1, but are not in the cache, so what the step computes
+in those rows means nothing.  Here its next token is -1 then; decoding gives
+it the same token again until blocks have come back, and leaves out a request
+that never got its prompt in.
 Random weights; run on a GPU:
 
     python examples/serving_step.py
@@ -57,27 +63,30 @@ class Decoder:
         self.free_head = torch.zeros(1, dtype=torch.int32, device=device)
 
     def step(self, tokens, new_lens, max_q):
-        """tokens [T]: new_lens[b] of each request, one after the other.
-        Returns the plan, the logits [T, vocab], the likeliest next tokens [T]
-        and the TokenLogprobs of them."""
+        """tokens [T]: new_lens[b] of each request, one after the other (what
+        comes after them is padding).  Returns the plan, the logits [T, vocab],
+        the likeliest next tokens [T], -1 where a token has no slot, and the
+        TokenLogprobs of them."""
         t, hq, hkv, d = tokens.numel(), self.hq, self.hkv, self.d
         plan = fp8bs.kv_plan(self.lens, new_lens, self.table, self.free, self.free_head, self.page, self.num_blocks, t,
                              seq_lens=self.lens, free_head_out=self.free_head)
-        x = self.embed[tokens.long()]
+        x = self.embed[tokens.long().clamp(min=0)]
         for (wq, sq), (wo, so), (kc, vc) in zip(self.qkv, self.out, self.caches):
             qkv = fp8bs.gemv(torch.nn.functional.rms_norm(x, x.shape[1:]), wq, sq)
             q = qkv[:, :hq * d].unflatten(1, (hq, d))
             k, v = (qkv[:, i * d:(i + hkv) * d].unflatten(1, (hkv, d)) for i in (hq, hq + hkv))
             fp8bs.kv4_append(k, v, plan.slots, self.scale, self.scale, kc, vc)
             o = fp8bs.kv4_decode_attention(q, kc, vc, self.scale, self.scale, self.table, plan.seq_lens, self.max_len,
-                                           d ** -0.5, self.workspace, cu_q=plan.cu_new, max_q=max_q)
+                                           d ** -0.5, self.workspace, cu_q=plan.cu_new, max_q=max_q,
+                                           out=x.new_zeros((t, hq, d)))  # rows of padding are not written
             x = x + fp8bs.gemv(o.view(t, -1), wo, so)
         logits = fp8bs.gemv(torch.nn.functional.rms_norm(x, x.shape[1:]), *self.head)
-        best = logits.argmax(dim=1).to(torch.int32)
+        best = torch.where(plan.slots >= 0, logits.argmax(dim=1).to(torch.int32), -1)
         return plan, logits, best, fp8bs.token_logprobs(logits, best, self.top)
 
     def prompt(self, prompts):
-        """Runs the requests' prompts (lists of tokens); returns each one's next token."""
+        """Runs the requests' prompts (lists of tokens); returns each one's
+        next token, -1 for a refused request."""
         lens = [len(p) for p in prompts]
         tokens = torch.tensor([t for p in prompts for t in p], dtype=torch.int32, device=self.device)
         new = torch.tensor(lens, dtype=torch.int32, device=self.device)
@@ -85,16 +94,23 @@ class Decoder:
         return best[plan.cu_new[1:].long() - 1].contiguous()
 
     def decode(self, tokens, steps):
-        """Greedy decoding: `steps` tokens a request, every step one replay of
-        a graph.  Yields (next tokens, log probabilities, entropies)."""
-        ones = torch.ones(self.batch, dtype=torch.int32, device=self.device)
+        """Greedy decoding from each request's last token (-1: leave it out),
+        every step one replay of a graph.  Yields (next tokens, log
+        probabilities, entropies), -1, 0 and 0 for a request that was refused
+        or left out."""
         state = [self.lens, self.table, self.free_head]
         tokens = tokens.clone()
 
         def one():
-            _, _, best, lp = self.step(tokens, ones, 1)
-            tokens.copy_(best)
-            return best, lp
+            live = tokens >= 0
+            row = torch.where(live, live.cumsum(0) - 1, live.sum() + (~live).cumsum(0) - 1)  # of each request
+            packed = torch.empty_like(tokens)
+            packed[row] = tokens
+            _, _, best, lp = self.step(packed, live.to(torch.int32), 1)
+            best, logprobs, entropy = best[row], lp.logprobs[row], lp.entropy[row]
+            done = best >= 0
+            tokens.copy_(torch.where(done, best, tokens))
+            return best, logprobs, torch.where(done, entropy, 0.0)
 
         kept = [s.clone() for s in state] + [tokens.clone()]
         one()                                                   # warm up, then put the requests back
@@ -102,10 +118,10 @@ class Decoder:
             s.copy_(was)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            best, lp = one()
+            out = one()
         for _ in range(steps):
             graph.replay()
-            yield best.clone(), lp.logprobs.clone(), lp.entropy.clone()
+            yield tuple(t.clone() for t in out)
 
 
 def main():

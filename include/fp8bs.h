@@ -531,7 +531,12 @@ int w8a8_gemm_ex(const uint8_t *x_codes, int64_t m, const float *x_scale,
  * every later request that needs a block is refused too; sets
  * bit 5 of the device error word), or when its lengths cannot be: c or n
  * negative, c + n > max_blocks_per_seq * page_size, cu_new[b + 1] >
- * num_tokens (sets bit 4; seq_lens[b] is c clamped to the table's range).  A
+ * num_tokens (sets bit 4; seq_lens[b] is c clamped to the table's range).
+ * Nothing of a refused request's tokens is stored, but cu_new counts them:
+ * attention that is given cu_new and seq_lens takes their rows for the last n
+ * of the c cached tokens, so what it writes there means nothing.  Give up the
+ * results of tokens whose slot is -1, and offer the tokens again once there
+ * are blocks.  A
  * block id outside [0, num_blocks) gives slots -1 (a free-list id also a
  * table entry -1) and sets bit 4, as does a *free_head outside
  * [0, num_free], for which every request that needs a block is refused.
@@ -541,7 +546,10 @@ int w8a8_gemm_ex(const uint8_t *x_codes, int64_t m, const float *x_scale,
  *   block_table          device, [batch, max_blocks_per_seq] int32; entries
  *                        below `have` are read, the new ones written
  *   free_blocks          device, [num_free] int32 (may be NULL if num_free is 0)
- *   free_head            device, 1 int32: blocks of the list already taken
+ *   free_head            device, 1 int32: blocks of the list already taken.
+ *                        A finished request's k blocks come back by writing
+ *                        their ids to free_blocks[head - k .. head - 1] and
+ *                        head - k to the head, between steps on the stream
  *   page_size            1..65536, num_blocks * page_size < 2^31
  *   num_tokens           size of the token arrays (>= the step's tokens)
  *   seq_lens             device, [batch] int32, written; may be ctx_lens
@@ -640,8 +648,9 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  *   q_bf16       device, [num_q_tokens, num_q_heads, head_dim] bf16, 16-byte
  *                aligned, tokens q_stride elements apart, a multiple of 8
  *   cu_q         device, [batch + 1] int32: sequence b's query tokens are
- *                cu_q[b] .. cu_q[b + 1] - 1 (fp8bs_kv_plan's cu_new), at most
- *                max_q of them; NULL: one per sequence, num_q_tokens = batch.
+ *                cu_q[b] .. cu_q[b + 1] - 1 (fp8bs_kv_plan's cu_new; the rows
+ *                of a request that it refused mean nothing), at most max_q of
+ *                them; NULL: one per sequence, num_q_tokens = batch.
  *                A range outside [0, num_q_tokens] or longer than max_q is
  *                skipped (its rows are not written) and sets bit 4 of the
  *                device error word.  Rows of no sequence are not written
