@@ -32,11 +32,13 @@ __device__ uint32_t g_kv4_err;
 
 // ------------------------------------------------------- append and gather
 // A thread has 32 consecutive elements of a head vector (two groups): 64 bytes
-// of bf16, 16 of codes and 2 of scales; a warp's accesses are contiguous.  Both
-// are bound by HBM (read 2 B, write 9/16 B an element, or the reverse).  K and V
-// of 8 heads of 128: 8191 tokens are written in 8.3 us (5.2 TB/s; 11.6 with IEEE
-// divisions) and read back in 7.1 (6.1), 65536 are read in 60 (5.7; L2 no longer
-// holds what is written; 65 with half the bytes a thread and a division for its place).
+// of bf16, 16 of codes and 2 of scales; a warp's accesses are contiguous.  An
+// element is 2 B read and 9/16 B written, or the reverse.  K and V of 8 heads of
+// 128: 65536 tokens are read in 60 us (5.7 TB/s, bound by HBM; 65 with half the
+// bytes a thread and a division for its place).  8191 tokens, 43 MB, stay in L2
+// when the same buffers are used again: written in 8.3 us (11.6 with IEEE
+// divisions), read back in 7.1.  With the caches flushed, under a profiler, 12.7
+// and 10.8 us for 6.3 us of bytes: one wave, a third of it launch and first loads.
 constexpr int kCopyThreads = 256;
 
 __device__ __forceinline__ void st_v8(void *p, const uint32_t (&v)[8]) {
@@ -245,9 +247,14 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_gather_kernel(Kv4CopyArgs a,
 //   multiplies with their scales.  P^T comes from the S^T fragments by
 //   movmatrix, because key m of S^T is key m of the product.
 // Bytes would take 89 us at 16 x 32768 keys of 8 heads (groups of 4) at the
-// measured copy rate; it takes 121 us, 5.0 TB/s: the dequantization beside the
-// matrix products keeps the ALU and FMA pipes and the issue slots that busy
-// (reading a cache that fits L2 saved 3% when tried).
+// measured copy rate; it takes 120 us, 5.0 TB/s.  Neither HBM (a cache that fits
+// L2 saved 3% when tried) nor a pipe is at its limit: on a ragged batch ALU 44%,
+// FMA 25%, tensor 21%, issue slots 60%.  A unit is a chain of dependent steps
+// (copy, conversions, product, maximum, exponentials, transpose, product) and 18
+// warps an SM do not cover its latency (stalled warps per issue: long scoreboard
+// 1.25, fixed latency 1.13, not selected 1.05), so every instruction of the chain
+// counts: without the conversions it took 107 us of 131 then.  An eighth of the
+// SMs' time is idle, at the start and where the shares end.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.0f;
@@ -255,7 +262,8 @@ constexpr int kMaxSms = 160;  // CTAs the workspace has records for: two per SM 
 constexpr int kMinShare = 8;  // a CTA's share at least, in steps of the line
 
 // A producer warp, W consumer warps and a ring of S units per CTA, kRes CTAs
-// per SM.
+// per SM: measured at D = 128.  D = 64, with stages and accumulators half as
+// large, takes the same (16 x 32768: 92 us for 44 us of bytes).
 template <int D, int NT>
 struct AttnCfg {
     static constexpr int kRes = NT <= 2 ? 2 : 1;

@@ -16,9 +16,11 @@
 // whose equals at the bound do not fit there take an ordered scan that stops
 // when it has enough.
 //
-// Bound by HBM in bytes (floor 92 us for 2048 rows of 152064 bf16 at the
-// measured copy rate), by instruction issue as built: 102 us without the top,
-// 123 us with the top 20 (5.1 TB/s).
+// In bytes 92 us for 2048 rows of 152064 bf16 at the measured copy rate: 100 us
+// without the top, 121 us with the top 20 (5.2 TB/s).  The difference is the
+// choice of the top, in which a CTA reads little.  No unit is at its limit (issue
+// slots 68%, ALU 38%, FMA 32%, XU 29%): 64 registers leave 32 warps an SM, 29 at
+// work, and loads that are awaited are by far the first stall.
 #include "serving.cuh"
 #include "internal.h"
 
@@ -634,6 +636,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream) {
     // looks for its top (2048 rows: 123 us, 136 with 512, 129 with 128).  Many short ones, whose tops weigh more:
     // 128 and eight CTAs (4096 rows of 32003, top 20: 75 us, 90 with 256; of 65536 120 and 121; 3000 of 100003 127
     // and 123); also where those take all the rows at once and four do not (1000 rows of 152064: 63 us, 69 with 256).
+    // All of bf16; fp32 rows, of twice the vectors, go by the same numbers of vectors (1024 rows of 152064: 107 us for
+    // 92 of bytes).
     const int splits = pick_row_split(a);
     const int64_t sms = device_sm_count(), vecs = a.vocab / (a.f32 ? 4 : 8);
     if (splits > 1 || (a.rows <= 2 * sms && vecs >= 2 * kFlight * 512))

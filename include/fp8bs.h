@@ -637,7 +637,9 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  * lse = -inf.  A row takes nothing from a key that it does not see, whatever
  * is stored there; NaN that it does see goes the formula's way: in q or a key
  * to the whole row and its lse, in a value to the elements of its group.
- * K and V decode exactly to f16 (code * scale); scores, the softmax and all
+ * K and V decode exactly to f16 (code * scale); q enters as f16, each row
+ * brought to the type's range by a power of two, which is exact for elements
+ * down to 2^-31 of the row's largest; scores, the softmax and all
  * sums are fp32 (the weights enter the V sum as f16, held against the running
  * maximum so that 2^-39 of it is the smallest); one bf16 rounding at the end.
  *
