@@ -35,6 +35,9 @@ Functions (names follow the C entry points):
     kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                          max_seq_len, sm_scale, workspace) -> o bf16 [T, Hq, D]   (fp4kv_decode_attention)
         4-bit caches are uint8 of kv4_cache_shape(num_blocks, page_size, kv_heads, head_dim)
+    kv_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache) -> q bf16 [T, Hq, D]
+    kv4_rope_append(...)   norm and rotation of q and k, q out, k and v into the FP8 / 4-bit cache
+                           (fp8kv_rope_append, fp4kv_rope_append)
     token_logprobs(logits, targets, top) -> TokenLogprobs: log probabilities of given tokens, entropy,
                            top alternatives   (fp8bs_token_logprobs)
     check_device_error()   -> the kernels' error word (synchronises; reading clears it)
@@ -134,6 +137,9 @@ def lib() -> ctypes.CDLL:
         L.fp4kv_attention_ws_bytes.restype = i64
         L.fp4kv_decode_attention.argtypes = [p, i64, p, i64, i64, p, p, p, p, p, i64, p, i64, i64, i64, i64, i64, i64,
                                              i64, i64, ctypes.c_float, p, p, p, i64, p]
+        rope = [p, i64, p, i64, p, i64, i64, i64, i64, i64, p, p, p, i64, i64, i32, p, p, ctypes.c_float, p, p, p, p, p]
+        L.fp8kv_rope_append.argtypes = rope + [i64, p]
+        L.fp4kv_rope_append.argtypes = rope + [i64, i64, p]
         L.fp8bs_token_logprobs.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, p, p, p]
         L.w8a8_gemm.argtypes = [p, i64, p, p, p, i64, i64, p, p]
         L.w8a8_gemm_ex.argtypes = [p, i64, p, p, p, i64, i64, p, i32, p]
@@ -151,6 +157,7 @@ def lib() -> ctypes.CDLL:
                   "fp8tensor_gemv", "fp8tensor_gemv_ex", "fp8act_quantize", "w8a8_gemm", "w8a8_gemm_ex",
                   "fp8bs_moe_gemv", "fp8bs_moe_gemv_ws", "fp8kv_append", "fp8kv_decode_attention",
                   "fp8bs_kv_plan", "fp4kv_append", "fp4kv_gather", "fp4kv_decode_attention", "fp8bs_token_logprobs",
+                  "fp8kv_rope_append", "fp4kv_rope_append",
                   "fp8bs_select_path", "fp8bs_check_device_error", "fp8bs_debug_wait_expiry",
                   "fp8bs_debug_encode_f32", "fp8bs_version"):
             getattr(L, f).restype = ctypes.c_int
@@ -721,6 +728,62 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
            seq_lens.data_ptr(), b, hq, hkv, d, page, nb, int(max_seq_len), int(window), float(sm_scale), out.data_ptr(),
            lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.numel()), stream)
     return (out, lse) if return_lse else out
+
+
+def _rope_append(what, fn, q, k, v, positions, slots, cos_sin, cache_specs, cache_args, ptrs, q_norm, k_norm, eps,
+                 interleaved, out, stream):
+    t, hq, d = q.shape
+    max_pos, rot = _shape2(cos_sin, "cos_sin")
+    bf16, i32 = torch.bfloat16, torch.int32
+    given = [spec for spec in (("q_norm", q_norm, bf16, d, False), ("k_norm", k_norm, bf16, d, False),
+                               ("out", out, bf16, t * hq * d, False)) if spec[1] is not None]
+    device = _checked(*cache_specs, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
+                      ("cos_sin", cos_sin, torch.float32, None, False), *given, ("q", q, bf16, None, True),
+                      ("k", k, bf16, None, True), ("v", v, bf16, None, True))
+    if out is None:
+        out = _empty(stream, device, (t, hq, d), bf16)
+    _call(device, what, fn,
+          (q.data_ptr(), _row_stride(q), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), t, hq, k.shape[1], d,
+           positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, int(interleaved),
+           q_norm.data_ptr() if q_norm is not None else None, k_norm.data_ptr() if k_norm is not None else None,
+           float(eps), out.data_ptr(), *(x.data_ptr() for x in ptrs), *cache_args), stream)
+    return out
+
+
+def _rope_shapes(q, k, v):
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D]")
+
+
+def kv_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm=None, k_norm=None,
+                   eps: float = 1e-6, interleaved: bool = False, out=None, stream=None):
+    """Norm (RMS, per head, with the weights q_norm and k_norm [D] bf16 where
+    they are given) and rotate q and k [T, H, 128] bf16 by their positions,
+    then write k and v into the FP8 caches [num_blocks, page_size, Hkv, 128]
+    at flat token slots (fp8kv_rope_append).  cos_sin [max_pos, rot_dim] fp32
+    holds cos of a position's pairs, then sin.  q, k and v may be slices of a
+    fused projection.  Returns q [T, Hq, 128]; rows at position -1 are left as
+    they were."""
+    _rope_shapes(q, k, v)
+    if k_cache.dim() != 4 or k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [num_blocks, page_size, Hkv, D] of k")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
+    u8, f32 = torch.uint8, torch.float32
+    specs = (("k_cache", k_cache, u8, None, False), ("v_cache", v_cache, u8, None, False),
+             ("k_scale", k_scale, f32, 1, False), ("v_scale", v_scale, f32, 1, False))
+    return _rope_append("fp8kv_rope_append", lib().fp8kv_rope_append, q, k, v, positions, slots, cos_sin, specs,
+                        (k_cache.shape[0] * k_cache.shape[1],), (k_scale, v_scale, k_cache, v_cache), q_norm, k_norm, eps,
+                        interleaved, out, stream)
+
+
+def kv4_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm=None, k_norm=None,
+                    eps: float = 1e-6, interleaved: bool = False, out=None, stream=None):
+    """kv_rope_append into 4-bit caches (fp4kv_rope_append); head size 64 or 128."""
+    _rope_shapes(q, k, v)
+    specs, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, k.shape[1], k.shape[2])
+    return _rope_append("fp4kv_rope_append", lib().fp4kv_rope_append, q, k, v, positions, slots, cos_sin, specs, (page, nb),
+                        (k_scale, v_scale, k_cache, v_cache), q_norm, k_norm, eps, interleaved, out, stream)
 
 
 def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,

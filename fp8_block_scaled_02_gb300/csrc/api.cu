@@ -582,6 +582,66 @@ int fp4kv_decode_attention(const void *q_bf16, int64_t q_stride, const int32_t *
     return cuda_status(launch_kv4_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+int check_rope(const KvRopeArgs &a) {
+    if (a.tokens < 0 || a.tokens >= kMaxDim || a.q_heads <= 0 || a.q_heads >= 65536) return FP8BS_ERR_SHAPE;
+    if (a.tokens * a.q_heads >= (int64_t{1} << 40) || a.tokens * (a.q_heads + 2 * a.kv_heads) >= (int64_t{1} << 33))
+        return FP8BS_ERR_SHAPE;
+    if (a.max_pos <= 0 || a.max_pos >= kMaxDim || a.rot_dim < 16 || a.rot_dim % 16 != 0 || a.rot_dim > a.head_dim)
+        return FP8BS_ERR_SHAPE;
+    if (!stride_ok(a.q_stride, a.q_heads * a.head_dim) || !stride_ok(a.k_stride, a.kv_heads * a.head_dim) ||
+        !stride_ok(a.v_stride, a.kv_heads * a.head_dim))
+        return FP8BS_ERR_SHAPE;
+    if (!(a.eps >= 0.0f) || a.eps > 3.0e38f) return FP8BS_ERR_SHAPE;
+    if (a.tokens == 0) return FP8BS_OK;
+    if (!a.q || !a.k || !a.v || !a.positions || !a.slots || !a.cos_sin || !a.q_out || !a.k_scale || !a.v_scale ||
+        !a.k_cache || !a.v_cache)
+        return FP8BS_ERR_NULL;
+    if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || a.q_stride % 8 != 0 || a.k_stride % 8 != 0 ||
+        a.v_stride % 8 != 0 || !aligned(a.positions, 4) || !aligned(a.slots, 4) || !aligned(a.cos_sin, 16) ||
+        !aligned(a.q_weight, 16) || !aligned(a.k_weight, 16) || !aligned(a.q_out, 16) || !aligned(a.k_scale, 4) ||
+        !aligned(a.v_scale, 4) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16))
+        return FP8BS_ERR_ALIGN;
+    return FP8BS_OK;
+}
+
+int run_rope(const KvRopeArgs &a, bool four_bit, void *stream) {
+    const int st = check_rope(a);
+    if (st != FP8BS_OK || a.tokens == 0) return st;
+    return cuda_status(launch_kv_rope(a, four_bit, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+int fp8kv_rope_append(const void *q_bf16, int64_t q_stride, const void *k_bf16, int64_t k_stride, const void *v_bf16,
+                      int64_t v_stride, int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                      int64_t head_dim, const int32_t *positions, const int32_t *slots, const float *cos_sin,
+                      int64_t max_pos, int64_t rot_dim, int interleaved, const void *q_weight, const void *k_weight,
+                      float eps, void *q_out, const float *k_scale, const float *v_scale, uint8_t *k_cache,
+                      uint8_t *v_cache, int64_t num_slots, void *stream) {
+    if (num_kv_heads <= 0 || num_kv_heads >= 4096 || num_slots <= 0 || head_dim != 128) return FP8BS_ERR_SHAPE;
+    if (num_slots >= kMaxDim || num_slots * num_kv_heads * head_dim >= (int64_t{1} << 40)) return FP8BS_ERR_SHAPE;
+    const KvRopeArgs a{q_bf16, k_bf16, v_bf16, positions, slots, cos_sin, q_weight, k_weight, q_out, k_scale, v_scale,
+                       k_cache, v_cache, q_stride, k_stride, v_stride, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                       max_pos, rot_dim, 0, num_slots, eps, interleaved != 0};
+    return run_rope(a, false, stream);
+}
+
+int fp4kv_rope_append(const void *q_bf16, int64_t q_stride, const void *k_bf16, int64_t k_stride, const void *v_bf16,
+                      int64_t v_stride, int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                      int64_t head_dim, const int32_t *positions, const int32_t *slots, const float *cos_sin,
+                      int64_t max_pos, int64_t rot_dim, int interleaved, const void *q_weight, const void *k_weight,
+                      float eps, void *q_out, const float *k_scale, const float *v_scale, uint8_t *k_cache,
+                      uint8_t *v_cache, int64_t page_size, int64_t num_blocks, void *stream) {
+    const int st = check_kv4_cache(num_kv_heads, head_dim, page_size, num_blocks);
+    if (st != FP8BS_OK) return st;
+    const KvRopeArgs a{q_bf16, k_bf16, v_bf16, positions, slots, cos_sin, q_weight, k_weight, q_out, k_scale, v_scale,
+                       k_cache, v_cache, q_stride, k_stride, v_stride, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                       max_pos, rot_dim, page_size, num_blocks * page_size, eps, interleaved != 0};
+    return run_rope(a, true, stream);
+}
+
 int fp8bs_token_logprobs(const void *logits, int logits_f32, int64_t row_stride, int64_t rows, int64_t vocab,
                          const int32_t *targets, int64_t top, float *logprobs, float *entropy, int32_t *top_ids,
                          float *top_logprobs, void *stream) {
@@ -620,7 +680,8 @@ int fp8bs_debug_encode_f32(uint32_t first_bits, int64_t count, uint8_t *codes_u8
 int fp8bs_check_device_error(void *stream, uint32_t *word_out) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8BS_ERR_CUDA;
     const uint32_t w = take_decode_error() | take_prefill_error() | take_w8a8_error() | take_kv_error() |
-                       take_moe_error() | take_plan_error() | take_kv4_error() | take_logprobs_error();
+                       take_moe_error() | take_plan_error() | take_kv4_error() | take_logprobs_error() |
+                       take_rope_error();
     if (word_out) *word_out = w;
     return w ? FP8BS_ERR_DEVICE : FP8BS_OK;
 }

@@ -227,6 +227,22 @@ int64_t kv4_attention_ws_bytes(int64_t head_dim);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t stream);
 uint32_t take_kv4_error();
 
+// kvrope.cu -- norm and rotation of q and k, q out, k and v into a paged cache.
+struct KvRopeArgs {
+    const void *q, *k, *v;       // bf16 [tokens, heads, head_dim], rows *_stride elements apart
+    const int32_t *positions, *slots;  // [tokens]
+    const float *cos_sin;        // [max_pos, rot_dim]: cos of the pairs, then sin
+    const void *q_weight, *k_weight;   // bf16 [head_dim], or nullptr: no norm
+    void *q_out;                 // bf16 [tokens, q_heads, head_dim]
+    const float *k_scale, *v_scale;
+    uint8_t *k_cache, *v_cache;
+    int64_t q_stride, k_stride, v_stride, tokens, q_heads, kv_heads, head_dim, max_pos, rot_dim, page_size, num_slots;
+    float eps;
+    bool interleaved;
+};
+cudaError_t launch_kv_rope(const KvRopeArgs &a, bool four_bit, cudaStream_t stream);
+uint32_t take_rope_error();
+
 // logprobs.cu -- log probabilities of given tokens, entropy, top alternatives.
 constexpr int64_t kLogprobsMaxTop = 32;
 struct LogprobArgs {

@@ -3,8 +3,9 @@
  * per-tensor FP8 weight quantization, the W8A16 GEMV / skinny GEMM /
  * prefill GEMM that consumes it, the W8A8 route (dynamic per-tensor
  * activation quantization + e4m3 x e4m3 GEMM), the grouped MoE GEMV, FP8
- * E4M3 and 4-bit paged KV caches with split-KV decode attention, the step's
- * paging plan and token log probabilities, for NVIDIA GB300 (sm_103a).
+ * E4M3 and 4-bit paged KV caches with split-KV decode attention, the norm and
+ * rotation of q and k on their way there, the step's paging plan and token
+ * log probabilities, for NVIDIA GB300 (sm_103a).
  *
  * Common conventions
  * ------------------
@@ -622,6 +623,67 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
                  int64_t num_blocks, const float *k_scale,
                  const float *v_scale, void *k_bf16, void *v_bf16,
                  void *stream);
+
+/*
+ * fp8kv_rope_append / fp4kv_rope_append: the rows of a fused q, k, v
+ * projection made ready for the attention in one pass: each query and key head
+ * normed and rotated by its token's position, q written out in bf16, k and v
+ * written into the paged cache (the FP8 cache of fp8kv_append, the 4-bit cache
+ * of fp4kv_append).  Of a head vector a with norm weights w, each fl one fp32
+ * rounding:
+ *   r = fl(1 / sqrt(mean a^2 + eps)),  n_i = fl(fl(a_i * r) * w_i)
+ * (n = a where the weights are NULL; |a| below 2^60 where they are not); of a
+ * pair (n1, n2) with the cos c and the sin s of the token's position:
+ *   o1 = fl(fl(n1 * c) - fl(n2 * s)),  o2 = fl(fl(n2 * c) + fl(n1 * s))
+ * over the first rot_dim elements, the others o = n.  q_out = bf16(o); k is
+ * stored as o is by the cache's own rule (e4m3(fl(o / k_scale)), or the group
+ * rule of fp4kv_append with x = o), v as the append stores it.
+ *
+ * Defined by: no passage of the source pages has a counterpart for the norm
+ * and the rotation; the FP8 cache and its scales are InfiniLM PR #586's.
+ *
+ *   q_bf16, k_bf16, v_bf16   device, [num_tokens, heads, head_dim] bf16, 16-byte
+ *                aligned, tokens *_stride elements apart, a multiple of 8
+ *   head_dim     128; fp4kv_rope_append 64 too
+ *   positions    device, [num_tokens] int32; a token at -1 (padding, a refused
+ *                request) stores nothing and leaves its row of q_out as it was,
+ *                one outside [-1, max_pos) too, with bit 4 of the device error word
+ *   slots        device, [num_tokens] int32, as fp4kv_append: slot -1 stores
+ *                nothing, any other one out of range too, with bit 4 (q_out is
+ *                written).  Two tokens of one call may not share a slot
+ *   cos_sin      device, [max_pos, rot_dim] fp32, 16-byte aligned: the cos of a
+ *                position's rot_dim / 2 pairs, then the sin
+ *   rot_dim      16..head_dim, a multiple of 16
+ *   interleaved  0: pair j is elements j and j + rot_dim / 2; else 2j and 2j + 1
+ *   q_weight, k_weight   device, [head_dim] bf16, 16-byte aligned, or NULL
+ *   eps          >= 0, finite (a head of zeros with eps = 0 gives NaN)
+ *   q_out        device, [num_tokens, num_q_heads, head_dim] bf16, 16-byte aligned;
+ *                may be q_bf16 itself where q_stride is num_q_heads * head_dim
+ *   k_scale, v_scale   device, 1 positive float each
+ *   k_cache, v_cache   device, 16-byte aligned, written at the slots
+ */
+int fp8kv_rope_append(const void *q_bf16, int64_t q_stride, const void *k_bf16,
+                      int64_t k_stride, const void *v_bf16, int64_t v_stride,
+                      int64_t num_tokens, int64_t num_q_heads,
+                      int64_t num_kv_heads, int64_t head_dim,
+                      const int32_t *positions, const int32_t *slots,
+                      const float *cos_sin, int64_t max_pos, int64_t rot_dim,
+                      int interleaved, const void *q_weight,
+                      const void *k_weight, float eps, void *q_out,
+                      const float *k_scale, const float *v_scale,
+                      uint8_t *k_cache, uint8_t *v_cache, int64_t num_slots,
+                      void *stream);
+int fp4kv_rope_append(const void *q_bf16, int64_t q_stride, const void *k_bf16,
+                      int64_t k_stride, const void *v_bf16, int64_t v_stride,
+                      int64_t num_tokens, int64_t num_q_heads,
+                      int64_t num_kv_heads, int64_t head_dim,
+                      const int32_t *positions, const int32_t *slots,
+                      const float *cos_sin, int64_t max_pos, int64_t rot_dim,
+                      int interleaved, const void *q_weight,
+                      const void *k_weight, float eps, void *q_out,
+                      const float *k_scale, const float *v_scale,
+                      uint8_t *k_cache, uint8_t *v_cache, int64_t page_size,
+                      int64_t num_blocks, void *stream);
 
 /*
  * fp4kv_decode_attention: attention of the newest tokens of each sequence
