@@ -25,6 +25,8 @@ Functions (names follow the C entry points):
     moe_gemv(x, ids, codes, scales) -> y bf16 [M, topk, N]            (fp8bs_moe_gemv)
     moe_gemv_ws(x, ids, codes, scales, workspace) -> y                (fp8bs_moe_gemv_ws)
         codes [E,N,K], scales [E, ceil(N/128), ceil(K/128)], ids int32 [M, topk]
+    moe_route(logits, topk) -> (ids int32 [M, topk], weights f32 [M, topk])   (fp8bs_moe_route)
+    moe_combine(y, weights) -> out bf16 [M, N]: sum over topk of weights * y [M, topk, N]   (fp8bs_moe_combine)
     kv_append(x, slots, scale, cache)    FP8 KV cache append (fp8kv_append), in place
     kv_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                         max_seq_len, sm_scale) -> o bf16 [B, Hq, 128]   (fp8kv_decode_attention)
@@ -140,6 +142,8 @@ def lib() -> ctypes.CDLL:
         rope = [p, i64, p, i64, p, i64, i64, i64, i64, i64, p, p, p, i64, i64, i32, p, p, ctypes.c_float, p, p, p, p, p]
         L.fp8kv_rope_append.argtypes = rope + [i64, p]
         L.fp4kv_rope_append.argtypes = rope + [i64, i64, p]
+        L.fp8bs_moe_route.argtypes = [p, i32, i64, i64, i64, i64, i32, p, i64, i64, i64, i32, ctypes.c_float, p, p, p]
+        L.fp8bs_moe_combine.argtypes = [p, p, p, i64, p, i64, i64, i64, p, p]
         L.fp8bs_token_logprobs.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, p, p, p]
         L.w8a8_gemm.argtypes = [p, i64, p, p, p, i64, i64, p, p]
         L.w8a8_gemm_ex.argtypes = [p, i64, p, p, p, i64, i64, p, i32, p]
@@ -157,7 +161,7 @@ def lib() -> ctypes.CDLL:
                   "fp8tensor_gemv", "fp8tensor_gemv_ex", "fp8act_quantize", "w8a8_gemm", "w8a8_gemm_ex",
                   "fp8bs_moe_gemv", "fp8bs_moe_gemv_ws", "fp8kv_append", "fp8kv_decode_attention",
                   "fp8bs_kv_plan", "fp4kv_append", "fp4kv_gather", "fp4kv_decode_attention", "fp8bs_token_logprobs",
-                  "fp8kv_rope_append", "fp4kv_rope_append",
+                  "fp8kv_rope_append", "fp4kv_rope_append", "fp8bs_moe_route", "fp8bs_moe_combine",
                   "fp8bs_select_path", "fp8bs_check_device_error", "fp8bs_debug_wait_expiry",
                   "fp8bs_debug_encode_f32", "fp8bs_version"):
             getattr(L, f).restype = ctypes.c_int
@@ -570,6 +574,61 @@ def kv_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     return out
 
 
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits, topk: int, scoring: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The experts of each token and their weights from the router's logits
+    [M, E], bf16 or fp32 (fp8bs_moe_route): the topk of softmax or sigmoid
+    scores plus `bias` [E] fp32, in the topk_groups best of `groups` groups,
+    each scored by its group_top best experts.  Returns ids int32 [M, topk]
+    (what moe_gemv takes) and weights fp32 [M, topk] (what moe_combine takes)."""
+    m, e = _shape2(logits, "logits")
+    topk = int(topk)
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
+    if not 1 <= topk <= e:
+        raise ValueError(f"topk is {topk}, the experts are {e}")
+    stride = logits.stride(0) if m > 1 else e
+    if 0 < stride < e:
+        raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {e} long")
+    i32, f32 = torch.int32, torch.float32
+    is_f32 = logits.dtype == f32
+    given = [spec for spec in (("bias", bias, f32, e, False), ("ids", ids, i32, m * topk, False),
+                               ("weights", weights, f32, m * topk, False)) if spec[1] is not None]
+    device = _checked(("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), *given)
+    if ids is None:
+        ids = _empty(stream, device, (m, topk), i32)
+    if weights is None:
+        weights = _empty(stream, device, (m, topk), f32)
+    _call(device, "fp8bs_moe_route", lib().fp8bs_moe_route,
+          (logits.data_ptr(), int(is_f32), stride, m, e, topk, _SCORING[scoring],
+           bias.data_ptr() if bias is not None else None, int(groups), int(topk_groups), int(group_top),
+           int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr()), stream)
+    return ids, weights
+
+
+def moe_combine(y, weights, ids=None, num_experts: int = 0, residual=None, out=None, stream=None):
+    """The weighted sum of the experts' outputs y [M, topk, N] bf16
+    (fp8bs_moe_combine): out [M, N] bf16 = residual + sum_j weights[:, j] y[:, j].
+    With ids (int32 [M, topk]) a slot whose id is outside [0, num_experts) adds
+    nothing.  out may be residual."""
+    if y.dim() != 3:
+        raise ValueError("y must be [M, topk, N]")
+    m, topk, n = y.shape
+    bf16 = torch.bfloat16
+    given = [spec for spec in (("ids", ids, torch.int32, m * topk, False), ("residual", residual, bf16, m * n, False),
+                               ("out", out, bf16, m * n, False)) if spec[1] is not None]
+    device = _checked(("y", y, bf16, None, False), ("weights", weights, torch.float32, m * topk, False), *given)
+    if out is None:
+        out = _empty(stream, device, (m, n), bf16)
+    _call(device, "fp8bs_moe_combine", lib().fp8bs_moe_combine,
+          (y.data_ptr(), weights.data_ptr(), ids.data_ptr() if ids is not None else None, int(num_experts),
+           residual.data_ptr() if residual is not None else None, m, topk, n, out.data_ptr()), stream)
+    return out
+
+
 KvPlan = collections.namedtuple("KvPlan", "seq_lens cu_new slots positions requests free_head")
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs entropy top_ids top_logprobs")
 
@@ -587,7 +646,7 @@ def _empty(stream, device, shape, dtype):
 
 def _row_stride(t):
     """Elements from one row of the first dimension to the next."""
-    return t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else 0
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1:].numel() if t.shape[0] else 0
 
 
 def kv_plan(ctx_lens, new_lens, block_table, free_blocks, free_head, page_size: int, num_blocks: int,

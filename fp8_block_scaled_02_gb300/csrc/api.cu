@@ -642,6 +642,45 @@ int fp4kv_rope_append(const void *q_bf16, int64_t q_stride, const void *k_bf16, 
     return run_rope(a, true, stream);
 }
 
+int fp8bs_moe_route(const void *logits, int logits_f32, int64_t row_stride, int64_t num_tokens, int64_t num_experts,
+                    int64_t topk, int scoring, const float *bias, int64_t groups, int64_t topk_groups,
+                    int64_t group_top, int renormalize, float scale, int32_t *expert_ids, float *weights,
+                    void *stream) {
+    if (num_tokens < 0 || num_tokens >= kMaxDim || num_experts < 1 || num_experts > kRouteMaxExperts || topk < 1 ||
+        topk > kRouteMaxTopk || num_tokens * topk >= kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if ((row_stride < num_experts && row_stride != 0) || row_stride >= (int64_t{1} << 40)) return FP8BS_ERR_SHAPE;
+    if (groups < 1 || groups > kRouteMaxGroups || num_experts % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+        group_top < 1 || group_top > 2 || group_top > num_experts / groups ||
+        topk > topk_groups * (num_experts / groups))
+        return FP8BS_ERR_SHAPE;
+    if (scoring != FP8BS_SCORE_SOFTMAX && scoring != FP8BS_SCORE_SIGMOID) return FP8BS_ERR_SHAPE;
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return FP8BS_ERR_SHAPE;
+    if (num_tokens == 0) return FP8BS_OK;
+    if (!logits || !expert_ids || !weights) return FP8BS_ERR_NULL;
+    if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(bias, 4) || !aligned(expert_ids, 4) || !aligned(weights, 4))
+        return FP8BS_ERR_ALIGN;
+    const MoeScoreArgs a{logits, logits_f32 != 0, scoring == FP8BS_SCORE_SOFTMAX, renormalize != 0, bias, expert_ids,
+                         weights, row_stride, num_tokens, num_experts, topk, groups, topk_groups, group_top, scale};
+    return cuda_status(launch_moe_scores(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8bs_moe_combine(const void *y_bf16, const float *weights, const int32_t *expert_ids, int64_t num_experts,
+                      const void *residual_bf16, int64_t num_tokens, int64_t topk, int64_t n, void *out_bf16,
+                      void *stream) {
+    if (num_tokens < 0 || num_tokens >= kMaxDim || topk < 1 || topk > 1024 || n < 1 || n >= kMaxDim ||
+        num_experts < 0 || num_experts >= kMaxDim || num_tokens * topk >= kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (num_tokens * ((n + 7) / 8) >= (int64_t{1} << 38)) return FP8BS_ERR_SHAPE;
+    if (num_tokens == 0) return FP8BS_OK;
+    if (!y_bf16 || !weights || !out_bf16) return FP8BS_ERR_NULL;
+    if (!aligned(y_bf16, 2) || !aligned(weights, 4) || !aligned(expert_ids, 4) || !aligned(residual_bf16, 2) ||
+        !aligned(out_bf16, 2))
+        return FP8BS_ERR_ALIGN;
+    const MoeCombineArgs a{y_bf16, weights, expert_ids, residual_bf16, out_bf16, num_tokens, topk, n, num_experts};
+    return cuda_status(launch_moe_combine(a, static_cast<cudaStream_t>(stream)));
+}
+
 int fp8bs_token_logprobs(const void *logits, int logits_f32, int64_t row_stride, int64_t rows, int64_t vocab,
                          const int32_t *targets, int64_t top, float *logprobs, float *entropy, int32_t *top_ids,
                          float *top_logprobs, void *stream) {

@@ -243,6 +243,29 @@ struct KvRopeArgs {
 cudaError_t launch_kv_rope(const KvRopeArgs &a, bool four_bit, cudaStream_t stream);
 uint32_t take_rope_error();
 
+// route.cu -- the experts of a token and their weights; the weighted sum of
+// the experts' outputs.
+constexpr int64_t kRouteMaxExperts = 1024, kRouteMaxTopk = 32, kRouteMaxGroups = 32;
+struct MoeScoreArgs {
+    const void *logits;          // bf16 or fp32 [tokens, experts], rows row_stride elements apart
+    bool f32, softmax, renormalize;
+    const float *bias;           // [experts] or nullptr
+    int32_t *ids;                // [tokens, topk]
+    float *weights;              // [tokens, topk]
+    int64_t row_stride, tokens, experts, topk, groups, topk_groups, group_top;
+    float scale;
+};
+cudaError_t launch_moe_scores(const MoeScoreArgs &a, cudaStream_t stream);
+struct MoeCombineArgs {
+    const void *y;               // bf16 [tokens, topk, n]
+    const float *weights;        // [tokens, topk]
+    const int32_t *ids;          // [tokens, topk] or nullptr: every slot counts
+    const void *residual;        // bf16 [tokens, n] or nullptr
+    void *out;                   // bf16 [tokens, n] (may be residual)
+    int64_t tokens, topk, n, experts;
+};
+cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t stream);
+
 // logprobs.cu -- log probabilities of given tokens, entropy, top alternatives.
 constexpr int64_t kLogprobsMaxTop = 32;
 struct LogprobArgs {

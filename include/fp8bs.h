@@ -2,7 +2,8 @@
  * fp8bs.h -- C ABI of libfp8bs: block-scaled FP8 (E4M3), MXFP8 and per-row /
  * per-tensor FP8 weight quantization, the W8A16 GEMV / skinny GEMM /
  * prefill GEMM that consumes it, the W8A8 route (dynamic per-tensor
- * activation quantization + e4m3 x e4m3 GEMM), the grouped MoE GEMV, FP8
+ * activation quantization + e4m3 x e4m3 GEMM), the grouped MoE GEMV with
+ * its routing and the weighted sum of the experts' outputs, FP8
  * E4M3 and 4-bit paged KV caches with split-KV decode attention, the norm and
  * rotation of q and k on their way there, the step's paging plan and token
  * log probabilities, for NVIDIA GB300 (sm_103a).
@@ -405,6 +406,73 @@ int fp8bs_moe_gemv_ws(const void *x_bf16, int64_t m, const int32_t *expert_ids,
                       int64_t topk, const uint8_t *codes, const float *scales,
                       int64_t num_experts, int64_t n, int64_t k, void *y_bf16,
                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * fp8bs_moe_route -- which experts each token goes to and with which weights,
+ * from the router's logits x: the ids that fp8bs_moe_gemv takes, on the device.
+ *   s_e = softmax(x)_e (FP8BS_SCORE_SOFTMAX) or 1 / (1 + e^-x_e) (FP8BS_SCORE_SIGMOID)
+ *   c_e = s_e + bias_e
+ * The experts stand in `groups` groups of equal size, one after the other; a
+ * group's score is the sum of the group_top (1 or 2) largest c in it, the
+ * topk_groups groups with the highest scores are open, and of their experts
+ * the topk with the largest c are chosen, largest first:
+ *   expert_ids[t, j],  weights[t, j] = scale * s_e,  divided by the sum of the
+ *   chosen s where renormalize is not 0 (0 where that sum is 0).
+ * Equals go to the lowest index.  c and groups' scores are compared in multiples
+ * of 2^-44 (c held within 2^-43 of its value, biases taken as at most 65536 in
+ * magnitude); without a bias experts are compared by x itself, which is the same
+ * order.  Weights within 2^-20 of themselves; e^-|x| below 2^-126 counts as 0.
+ *
+ * Defined by: no passage of the source pages has a counterpart (Atlas
+ * spark_model/weight_map/quantize_fp8_bs.rs: decode reads the top-12 of 256
+ * experts per token, with the choice as given).
+ *
+ *   logits       device, [num_tokens, num_experts] bf16, or fp32 if logits_f32 is
+ *                non-zero, rows row_stride elements apart (>= num_experts, or 0:
+ *                one row for every token); aligned to its element size.  -inf
+ *                shuts an expert out of the softmax (all of them: s = 0).  An
+ *                expert whose c is NaN comes after every other; the ids are
+ *                distinct and in range whatever the logits
+ *   num_experts  1..1024;  topk 1..32, <= topk_groups * num_experts / groups
+ *   bias         device, [num_experts] fp32, or NULL
+ *   groups       1..32, a divisor of num_experts;  topk_groups 1..groups;
+ *                group_top 1 or 2, <= num_experts / groups
+ *   expert_ids   device, [num_tokens, topk] int32, written
+ *   weights      device, [num_tokens, topk] fp32, written
+ */
+#define FP8BS_SCORE_SOFTMAX 0
+#define FP8BS_SCORE_SIGMOID 1
+int fp8bs_moe_route(const void *logits, int logits_f32, int64_t row_stride,
+                    int64_t num_tokens, int64_t num_experts, int64_t topk,
+                    int scoring, const float *bias, int64_t groups,
+                    int64_t topk_groups, int64_t group_top, int renormalize,
+                    float scale, int32_t *expert_ids, float *weights,
+                    void *stream);
+
+/*
+ * fp8bs_moe_combine -- the experts' outputs y [num_tokens, topk, n]
+ * (fp8bs_moe_gemv's) brought together:
+ *   out[t, :] = bf16_rn( residual[t, :] + sum_j weights[t, j] * y[t, j, :] )
+ * summed in fp32 in the order of j, from the residual on.
+ *
+ * Defined by: no passage of the source pages has a counterpart; y is that of
+ * Atlas' grouped MoE GEMM (spark_model/weight_map/quantize_fp8_bs.rs).
+ *
+ *   y_bf16       device, [num_tokens, topk, n] bf16
+ *   weights      device, [num_tokens, topk] fp32
+ *   expert_ids   device, [num_tokens, topk] int32, or NULL; a slot whose id is
+ *                outside [0, num_experts) adds nothing, and its y, which
+ *                fp8bs_moe_gemv does not write, is not read
+ *   residual_bf16  device, [num_tokens, n] bf16, or NULL (0)
+ *   topk         1..1024
+ *   out_bf16     device, [num_tokens, n] bf16, written; may be residual_bf16
+ * Any alignment of 2 bytes; 16-byte aligned tensors with n % 8 == 0 are read
+ * 16 bytes at a time, with the same results.
+ */
+int fp8bs_moe_combine(const void *y_bf16, const float *weights,
+                      const int32_t *expert_ids, int64_t num_experts,
+                      const void *residual_bf16, int64_t num_tokens,
+                      int64_t topk, int64_t n, void *out_bf16, void *stream);
 
 /*
  * FP8 E4M3 KV cache for paged decode attention.

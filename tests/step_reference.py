@@ -85,26 +85,24 @@ def route(x, topk, scoring, bias=None, groups=1, topk_groups=1, group_top=1, ren
     ids, weights = np.zeros((m, topk), dtype=np.int64), np.zeros((m, topk))
     for t in range(m):
         if scoring == "softmax":
-            top = np.nanmax(x[t]) if not np.isnan(x[t]).all() else np.nan
-            s = np.exp(x[t] - top) if top != -math.inf else np.zeros(e)
-            s = s / s.sum() if s.sum() != 0 else s
+            with np.errstate(invalid="ignore"):
+                top = np.max(x[t])                              # NaN if there is one
+                s = np.exp(x[t] - top) if top != -math.inf else np.zeros(e)
+                s = s / s.sum() if s.sum() != 0 else s
         else:
             with np.errstate(over="ignore"):
                 s = 1.0 / (1.0 + np.exp(-x[t]))
-        c = np.rint(np.clip(s + (0.0 if bias is None else np.clip(np.asarray(bias, dtype=np.float64), -65536, 65536)),
-                            -65536, 65536) * UNIT)
-        choice = c.copy() if bias is not None else x[t].copy()
-        choice[np.isnan(choice)] = -math.inf
+        b = 0.0 if bias is None else np.clip(np.asarray(bias, dtype=np.float64), -65536, 65536)
+        c = np.rint((s + b) * UNIT)
+        choice = c if bias is not None else x[t]
         live = list(range(e))
         if groups > 1:
             per = e // groups
-            best = [sum(sorted(np.where(np.isnan(c), -65536 * UNIT, c)[g * per:(g + 1) * per])[::-1][:group_top])
-                    for g in range(groups)]
+            low = np.where(np.isnan(c), -2.0 ** 61 + 1, c)
+            best = [sum(sorted(low[g * per:(g + 1) * per])[::-1][:group_top]) for g in range(groups)]
             chosen = sorted(range(groups), key=lambda g: (-best[g], g))[:topk_groups]
             live = [i for i in range(e) if i // per in chosen]
-        # NaN after everything else, -inf included
-        nan = np.isnan(x[t])
-        picked = sorted(live, key=lambda i: (bool(nan[i]), -choice[i], i))[:topk]
+        picked = sorted(live, key=lambda i: (1, 0, i) if np.isnan(choice[i]) else (0, -choice[i], i))[:topk]
         w = s[picked]
         if renormalize:
             w = w / w.sum() if w.sum() != 0 else np.zeros(topk)

@@ -1,0 +1,18 @@
+"""Error bounds of the two-fp32 arithmetic (csrc/twofloat.cuh), compiled for the host.  No GPU."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_bounds(tmp_path):
+    exe = tmp_path / "twofloat_bounds"
+    subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", "-ffp-contract=off", "-I",
+                    os.path.join(ROOT, "fp8_block_scaled_02_gb300", "csrc"), "-o", str(exe),
+                    os.path.join(ROOT, "tests", "csrc", "twofloat_bounds.cpp"), "-lm"], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stdout
