@@ -42,6 +42,8 @@ Functions (names follow the C entry points):
                            (fp8kv_rope_append, fp4kv_rope_append)
     token_logprobs(logits, targets, top) -> TokenLogprobs: log probabilities of given tokens, entropy,
                            top alternatives   (fp8bs_token_logprobs)
+    sample_tokens(logits, u, temperature, top_k, top_p, min_p) -> SampledTokens: the next token of each row and
+                           its log probability, from given random numbers   (fp8bs_sample_tokens)
     check_device_error()   -> the kernels' error word (synchronises; reading clears it)
     select_path(m, n, k)   -> the kernel path an AUTO call takes (host only)
     debug_wait_expiry(), debug_encode_f32(first_bits, count)   test hooks (fp8bs_debug_*)
@@ -145,6 +147,7 @@ def lib() -> ctypes.CDLL:
         L.fp8bs_moe_route.argtypes = [p, i32, i64, i64, i64, i64, i32, p, i64, i64, i64, i32, ctypes.c_float, p, p, p]
         L.fp8bs_moe_combine.argtypes = [p, p, p, i64, p, i64, i64, i64, p, p]
         L.fp8bs_token_logprobs.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, p, p, p]
+        L.fp8bs_sample_tokens.argtypes = [p, i32, i64, i64, i64, p, p, p, p, p, p, p, p]
         L.w8a8_gemm.argtypes = [p, i64, p, p, p, i64, i64, p, p]
         L.w8a8_gemm_ex.argtypes = [p, i64, p, p, p, i64, i64, p, i32, p]
         L.fp8bs_select_path.argtypes = [i64, i64, i64, p, p, i32]
@@ -162,6 +165,7 @@ def lib() -> ctypes.CDLL:
                   "fp8bs_moe_gemv", "fp8bs_moe_gemv_ws", "fp8kv_append", "fp8kv_decode_attention",
                   "fp8bs_kv_plan", "fp4kv_append", "fp4kv_gather", "fp4kv_decode_attention", "fp8bs_token_logprobs",
                   "fp8kv_rope_append", "fp4kv_rope_append", "fp8bs_moe_route", "fp8bs_moe_combine",
+                  "fp8bs_sample_tokens",
                   "fp8bs_select_path", "fp8bs_check_device_error", "fp8bs_debug_wait_expiry",
                   "fp8bs_debug_encode_f32", "fp8bs_version"):
             getattr(L, f).restype = ctypes.c_int
@@ -873,6 +877,39 @@ def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, t
           (logits.data_ptr(), int(f32), stride, m, v, targets.data_ptr(), top,
            logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr()), stream)
     return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
+
+
+SampledTokens = collections.namedtuple("SampledTokens", "tokens logprobs")
+
+
+def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
+                  stream=None):
+    """The next token of each row of logits [M, V] (bf16 or fp32, rows may be
+    padded, or one row expanded to M), drawn with u [M, 2] fp32 from what
+    temperature, top_k (int32), top_p and min_p ([M] each, None: off) leave
+    (fp8bs_sample_tokens).  Returns a SampledTokens: int32 tokens [M], -1 for
+    a row that has none, and their log probabilities."""
+    m, v = _shape2(logits, "logits")
+    stride = logits.stride(0) if m > 1 else v
+    if 0 < stride < v:
+        raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")
+    f32, i32 = torch.float32, torch.int32
+    is_f32 = logits.dtype == f32
+    given = [spec for spec in (("temperature", temperature, f32, m, False), ("top_k", top_k, i32, m, False),
+                               ("top_p", top_p, f32, m, False), ("min_p", min_p, f32, m, False),
+                               ("tokens", tokens, i32, m, False), ("logprobs", logprobs, f32, m, False))
+             if spec[1] is not None]
+    device = _checked(("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), ("u", u, f32, 2 * m, False),
+                      *given)
+    if tokens is None:
+        tokens = _empty(stream, device, (m,), i32)
+    if logprobs is None:
+        logprobs = _empty(stream, device, (m,), f32)
+    _call(device, "fp8bs_sample_tokens", lib().fp8bs_sample_tokens,
+          (logits.data_ptr(), int(is_f32), stride, m, v, u.data_ptr(),
+           *(t.data_ptr() if t is not None else None for t in (temperature, top_k, top_p, min_p)), tokens.data_ptr(),
+           logprobs.data_ptr()), stream)
+    return SampledTokens(tokens, logprobs)
 
 
 def act_quantize(x, codes=None, scale=None, stream=None):

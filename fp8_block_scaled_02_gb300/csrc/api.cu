@@ -698,6 +698,21 @@ int fp8bs_token_logprobs(const void *logits, int logits_f32, int64_t row_stride,
     return cuda_status(launch_token_logprobs(a, static_cast<cudaStream_t>(stream)));
 }
 
+int fp8bs_sample_tokens(const void *logits, int logits_f32, int64_t row_stride, int64_t rows, int64_t vocab,
+                        const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
+                        const float *min_p, int32_t *tokens, float *logprobs, void *stream) {
+    if (rows < 0 || rows >= (int64_t{1} << 28) || vocab <= 0 || vocab > kSampleMaxVocab ||
+        (row_stride < vocab && row_stride != 0) || row_stride >= (int64_t{1} << 40))
+        return FP8BS_ERR_SHAPE;
+    if (rows == 0) return FP8BS_OK;
+    if (!logits || !u || !tokens) return FP8BS_ERR_NULL;
+    if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+        !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(tokens, 4) || !aligned(logprobs, 4))
+        return FP8BS_ERR_ALIGN;
+    const SampleArgs a{logits, logits_f32 != 0, u, temperature, top_k, top_p, min_p, tokens, logprobs, row_stride, rows, vocab};
+    return cuda_status(launch_sample(a, static_cast<cudaStream_t>(stream)));
+}
+
 int fp8bs_select_path(int64_t m, int64_t n, int64_t k, const void *x_bf16, const void *codes, int mx) {
     (void)n;
     if (m <= 0 || k <= 0) return FP8BS_ERR_SHAPE;
@@ -720,7 +735,7 @@ int fp8bs_check_device_error(void *stream, uint32_t *word_out) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8BS_ERR_CUDA;
     const uint32_t w = take_decode_error() | take_prefill_error() | take_w8a8_error() | take_kv_error() |
                        take_moe_error() | take_plan_error() | take_kv4_error() | take_logprobs_error() |
-                       take_rope_error();
+                       take_rope_error() | take_sample_error();
     if (word_out) *word_out = w;
     return w ? FP8BS_ERR_DEVICE : FP8BS_OK;
 }

@@ -280,6 +280,22 @@ struct LogprobArgs {
 cudaError_t launch_token_logprobs(const LogprobArgs &a, cudaStream_t stream);
 uint32_t take_logprobs_error();
 
+// sample.cu -- the next token of each row of logits.
+constexpr int64_t kSampleMaxVocab = 1 << 20;
+struct SampleArgs {
+    const void *logits;          // bf16 or fp32 [rows, vocab], rows row_stride elements apart
+    bool f32;
+    const float *u;              // [rows, 2]
+    const float *temperature;    // [rows] or nullptr (1)
+    const int32_t *top_k;        // [rows] or nullptr (off)
+    const float *top_p, *min_p;  // [rows] or nullptr (off)
+    int32_t *tokens;             // [rows]
+    float *logprobs;             // [rows] or nullptr
+    int64_t row_stride, rows, vocab;
+};
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
+uint32_t take_sample_error();
+
 // Multiprocessor count of the current device (cached per device).
 int device_sm_count();
 

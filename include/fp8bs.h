@@ -5,8 +5,8 @@
  * activation quantization + e4m3 x e4m3 GEMM), the grouped MoE GEMV with
  * its routing and the weighted sum of the experts' outputs, FP8
  * E4M3 and 4-bit paged KV caches with split-KV decode attention, the norm and
- * rotation of q and k on their way there, the step's paging plan and token
- * log probabilities, for NVIDIA GB300 (sm_103a).
+ * rotation of q and k on their way there, the step's paging plan, token log
+ * probabilities and sampling, for NVIDIA GB300 (sm_103a).
  *
  * Common conventions
  * ------------------
@@ -850,6 +850,51 @@ int fp8bs_token_logprobs(const void *logits, int logits_f32,
                          const int32_t *targets, int64_t top, float *logprobs,
                          float *entropy, int32_t *top_ids,
                          float *top_logprobs, void *stream);
+
+/*
+ * fp8bs_sample_tokens -- the next token of each row of logits x (e.g.
+ * fp8bs_gemv's lm_head output), drawn with given random numbers:
+ *   w_j = exp((x_j - max x) / T);  tokens stand in the order of value, highest
+ *   first, then index, lowest first; kept are the first of them that all allow:
+ *     top_k (> 0):  the first top_k,
+ *     top_p (< 1):  the fewest whose mass reaches top_p times that of the
+ *                   first top_k (of all without top_k); one at least,
+ *     min_p (> 0):  those with w_j >= min_p (> 1 counts as 1);
+ *   block b of 1024 tokens (1024 b .. 1024 b + 1023): the first one for which the kept mass
+ *     of the blocks to it exceeds u[r, 0] times the kept mass of all,
+ *   tokens[r] = the first kept token of the block for which the kept mass of
+ *     the block to it exceeds u[r, 1] times that of the block,
+ *   logprobs[r] = log(w_token / kept mass), the log probability of the draw.
+ * Two numbers a row, because one fp32 number in steps of 2^-24 cannot give
+ * 152064 tokens their probabilities, and the borders of as many tokens on
+ * one line would be moved by every rounding of a sum.  T = 0 is greedy (the
+ * first token, log probability 0).  Tokens lighter than 2^-63 of the first
+ * may count as not kept.  Sums: a weight in fp32 (2^-22), blocks and the tokens of a
+ * block in 2^-44 of the mass; a draw nearer to a border than their errors
+ * (some 2^-27 of the mass) may fall to either side.
+ *
+ * Defined by: no passage of the source pages has a counterpart (FreeToken PR
+ * #636 serves the lm_head whose logits these are).
+ *
+ *   logits        device, [rows, vocab], rows row_stride elements apart
+ *                 (>= vocab, or 0: one row for every draw); bf16, or fp32
+ *                 if logits_f32 is non-zero; aligned to its element size
+ *   vocab         1..1048576
+ *   u             device, [rows, 2] fp32 in [0, 1] (others are taken as the nearer end, NaN as 0)
+ *   temperature   device, [rows] fp32: 0, or 1e-30..1e30; NULL: 1
+ *   top_k         device, [rows] int32, <= 0 or >= vocab: off; NULL: off
+ *   top_p, min_p  device, [rows] fp32; NULL: off
+ *   tokens        device, [rows] int32, written
+ *   logprobs      device, [rows] fp32, written, or NULL
+ * A row of nothing but -inf gives token -1 and log probability 0.  So does one
+ * with NaN or +inf, or with a temperature out of range or a NaN setting, which
+ * also sets bit 4 of the device error word.
+ */
+int fp8bs_sample_tokens(const void *logits, int logits_f32, int64_t row_stride,
+                        int64_t rows, int64_t vocab, const float *u,
+                        const float *temperature, const int32_t *top_k,
+                        const float *top_p, const float *min_p,
+                        int32_t *tokens, float *logprobs, void *stream);
 
 /* Path FP8BS_PATH_AUTO would take for these shapes and pointers
  * (host-only, launches nothing).  `mx` selects the MXFP8 GEMV; the block,
