@@ -7,21 +7,26 @@
 // of its equals.  The first random number picks a block of 1024 tokens by the
 // kept mass, the second a token of the block.
 //
-// Whole numbers come out, so sums are made as exact as it is cheap to.  In a
-// block's fp32 sums the exponent is split into an integer and a rest below 1/2
-// that is within 2^-25, so that a weight is within the 2^-22 of ex2 and errors of
-// different values do not add up; blocks, cuts and the tokens of the drawn block
-// go by pairs of fp32 (2^-44).
+// Whole numbers come out, so masses are whole numbers too, in units of 2^-41 of
+// the largest weight: their sums and comparisons are exact and do not depend on
+// an order.  What rounds is a weight (ex2's 2^-22, with the exponent's own error
+// taken back out, so that the errors of different values do not add up) and a
+// lane's fp32 sum of 32; the drawn block's weights are pairs of fp32 (2^-44).
 //
 // The CTAs of a cluster (one CTA when there are many rows) have consecutive
-// blocks of a row each, a warp a block at a time.  The cut comes from histograms
-// over the values: counts, and the mass of each bin as its count times a weight of
-// the bin plus what its tokens differ from that, in whole numbers, so that the
-// order of the atomics does not matter.
+// blocks of a row each, a warp a block at a time.  One pass over the row gives the
+// largest logit and every block's mass.  A cut takes two more: a histogram over
+// the exponents of the weights, 32 bins to a factor of 2, whose masses are each
+// bin's count times its weight plus what its tokens differ from that; and, for the
+// bin that holds the cut, the tokens above it summed by block and its own tokens
+// gathered in shared memory, where histograms over their values end the search.
+// A bin that holds too many is first cut by histograms over its values.
 #include "twofloat.cuh"
 
 #include "serving.cuh"
 #include "internal.h"
+
+#include <mutex>
 
 namespace fp8bs {
 
@@ -32,12 +37,28 @@ __device__ uint32_t g_sample_err;
 constexpr int kBlock = 1024;                    // tokens of a block
 constexpr int kMaxBlocks = kSampleMaxVocab / kBlock;
 constexpr int kMaxSplit = 8;                    // CTAs a row
-constexpr int kBins = 2048;
-constexpr float kPerUnit = 32.0f;               // first-level bins in a factor 2 of the weight
-constexpr float kWindow = kBins / kPerUnit - 1; // in log2: lighter tokens are drawn with a chance below 2^-43
+constexpr int kBins = 2048;                     // of the exponents
+constexpr int kFine = 512;                      // of the values in a range
+constexpr int kGather = 2048;                   // tokens that the last histograms can take
+constexpr float kPerUnit = 32.0f;               // bins in a factor 2 of the weight
+constexpr float kWindow = kBins / kPerUnit - 1; // in log2: lighter tokens do not count
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23: adding it rounds to whole numbers
-constexpr float kResidual = 0.0225f;            // above 2^(1 / 32) - 1: what weights of one bin differ by
+constexpr uint32_t kMagicBits = 0x4B400000u;
+constexpr float kUnit = 0x1p41f;                // of masses
+constexpr uint32_t kKeyInf = 0xFF800000u, kKeyNegInf = 0x007FFFFFu;
+
+// 2^(62 - j / 32): a bin's weight
+__constant__ uint64_t kBinWeight[32] = {
+    0x4000000000000000ull, 0x3EA0ECB6DC8A80CFull, 0x3D495F454921B30Bull, 0x3BF92E66F736BD73ull,
+    0x3AB031B9F7490E4Cull, 0x396E41B9DF20D22Aull, 0x383337BB0AA53844ull, 0x36FEEDE5F6BC8DD5ull,
+    0x35D13F32B5A75ABDull, 0x34AA07647C4AB917ull, 0x3389230547E12039ull, 0x326E6F619B8BC9E9ull,
+    0x3159CA845541B6B7ull, 0x304B1332999C2516ull, 0x2F4228E7D6030DB0ull, 0x2E3EEBD1D8BEE7BAull,
+    0x2D413CCCFE779921ull, 0x2C48FD6074AB0964ull, 0x2B560FBA90A852B2ull, 0x2A6856AD3A9F03BEull,
+    0x297FB5AA6C544E3Bull, 0x289C10C0C3125A06ull, 0x27BD4C982468446Bull, 0x26E34E6E7553954Eull,
+    0x260DFC14636E2A5Cull, 0x253D3BEA3FBDC258ull, 0x2470F4DCEAC470CEull, 0x23A90E62D17354F0ull,
+    0x22E57078FAA2F5BAull, 0x222603A024B6A14Aull, 0x216AB0D9F3121EC5ull, 0x20B361A62B0AE876ull,
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -53,30 +74,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
-constexpr uint32_t kKeyInf = 0xFF800000u, kKeyNegInf = 0x007FFFFFu;
 
-__device__ __forceinline__ Two neg(Two a) { return Two{-a.h, -a.l}; }
-__device__ __forceinline__ bool above(Two a, Two b) { return add(a, neg(b)).h > 0.0f; }
-__device__ __forceinline__ Two shfl(Two a, int lane) {
-    return Two{__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
-}
-__device__ __forceinline__ Two shfl_up(Two a, int o) {
-    return Two{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
-}
-__device__ __forceinline__ Two warp_inclusive(Two v) {
+template <class T>
+__device__ __forceinline__ T warp_inclusive(T v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const Two y = shfl_up(v, o);
-        if (lane >= o) v = add(y, v);
-    }
-    return v;
-}
-__device__ __forceinline__ int warp_inclusive(int v) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        const T y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
     }
     return v;
@@ -90,6 +94,36 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Pairs of fp32, two results an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 
@@ -183,36 +217,34 @@ struct Row {
     }
 };
 
-// What a search for a cut has found so far: the tokens above value key_value(hi)
-// are count and mass; the cut lies among the values of keys lo .. hi.
-struct Found {
+// The values of keys lo .. hi, where the cut lies: `equals` tokens, under `count`
+// of them with `mass` above.
+struct Range {
     uint32_t lo, hi;
-    int count;     // of tokens above
-    int equals;    // of tokens at the cut's value, once lo == hi
-    Two mass;      // of tokens above
-    int state;     // 0: go on, 1: found (lo == hi), 2: there is no cut, every token is kept
+    int count, equals;
+    uint64_t mass;
+    int none;      // there is no cut: every token is kept
     int pad;
 };
 
 template <int TH>
 struct Shared {
     static constexpr int kWarps = TH / 32;
-    uint32_t n[kBins], q[kBins];  // a level's histogram: tokens, and what they weigh beside the bin's weight
-    uint32_t block_key[kMaxBlocks];
-    Two block_mass[kMaxBlocks];   // of the kept tokens above the cut's value; the first CTA has all blocks'
-    int block_equals[kMaxBlocks]; // tokens at the cut's value
-    Two fine[64], coarse[32];     // 2^-(j / 32), 2^-(2 i)
-    Found found;
-    Two c, warp_two[kWarps];
-    int warp_int[kWarps];
-    uint32_t part_key[kMaxSplit];
-    Two part_mass[kMaxSplit];
-    int bad, drawn, last, result_block, allowed;
-    Two total;
+    uint64_t block_mass[kMaxBlocks];  // the first CTA has all blocks' in the end
+    uint32_t block_key[kMaxBlocks];   // of the block's largest logit
+    int block_equals[kMaxBlocks];     // tokens at the cut's value
+    uint32_t n[kBins], q[kBins];      // tokens of a bin, and what they weigh beside its weight
+    uint32_t fine_n[kFine], fine_q[kFine];
+    uint32_t list_key[kGather], list_id[kGather];
+    Range range, inbox[2];
+    uint64_t warp_sum[kWarps], part_mass[kMaxSplit], total;
     double log_min_p;
-    uint32_t warp_key[kWarps];
+    int warp_int[kWarps];
+    uint32_t warp_key[kWarps], part_key[kMaxSplit];
+    int listed, drawn, last, block, allowed;
 };
 
+// To the shared memory of CTA `rank` of the cluster, at the place of *local.
 template <class T>
 __device__ __forceinline__ void dsmem_put(T *local, int rank, const T &v) {
     static_assert(sizeof(T) % 4 == 0, "words");
@@ -221,39 +253,31 @@ __device__ __forceinline__ void dsmem_put(T *local, int rank, const T &v) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T) / 4); ++i) dsmem_st_f32(to + 4 * i, w[i]);
 }
-
 __device__ __forceinline__ void dsmem_add(uint32_t *local, int rank, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(dsmem_map(smem_u32(local), rank)), "r"(v)
                  : "memory");
 }
-
-// The sums of the threads' values before this thread's, and of all.
-template <int TH>
-__device__ __forceinline__ Two cta_exclusive(Two v, Shared<TH> &sh, Two &all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Two upto = warp_inclusive(v);
-    __syncthreads();
-    if (lane == 31) sh.warp_two[warp] = upto;
-    __syncthreads();
-    const Two w = warp_inclusive(lane < TH / 32 ? sh.warp_two[lane] : Two{0.0f, 0.0f});
-    all = shfl(w, 31);
-    const Two before = shfl(w, warp > 0 ? warp - 1 : 0);
-    Two lanes = shfl_up(upto, 1);
-    if (lane == 0) lanes = Two{0.0f, 0.0f};
-    return warp > 0 ? add(before, lanes) : lanes;
+__device__ __forceinline__ uint32_t dsmem_next(int *local, int rank, uint32_t n) {
+    uint32_t r;
+    asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;"
+                 : "=r"(r)
+                 : "r"(dsmem_map(smem_u32(local), rank)), "r"(n)
+                 : "memory");
+    return r;
 }
 
-template <int TH>
-__device__ __forceinline__ int cta_exclusive(int v, Shared<TH> &sh, int &all) {
+// The sum of the values of the threads before this one, and of all.
+template <class T, int TH>
+__device__ __forceinline__ T cta_exclusive(T v, T *warps, T &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int upto = warp_inclusive(v);
+    const T upto = warp_inclusive(v);
     __syncthreads();
-    if (lane == 31) sh.warp_int[warp] = upto;
+    if (lane == 31) warps[warp] = upto;
     __syncthreads();
-    const int w = warp_inclusive(lane < TH / 32 ? sh.warp_int[lane] : 0);
+    const T w = warp_inclusive(lane < TH / 32 ? warps[lane] : T{0});
     all = __shfl_sync(0xffffffffu, w, 31);
-    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-    return (warp > 0 ? before : 0) + upto - v;
+    const T before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : T{0}) + upto - v;
 }
 
 // 2^(c (x - m)).
@@ -263,234 +287,477 @@ __device__ __forceinline__ Two weight(float x, float m, Two c) {
     const float t = d.h * c.h;
     return t > -125.0f ? two_exp2(mul(d, c)) : Two{0.0f, 0.0f};
 }
+// v * unit to the nearest whole number.
+__device__ __forceinline__ uint64_t fixed(Two v, float unit) {
+    const float h = v.h * unit, l = v.l * unit;
+    return h < 0x1p23f ? __float2ull_rn(h + l) : __float2ull_rn(h) + static_cast<uint64_t>(__float2ll_rn(l));
+}
+__device__ __forceinline__ uint64_t at_least_one(uint64_t v) { return v > 0 ? v : 1; }
+// floor(share * mass), for a share in [0, 1].
+__device__ __forceinline__ uint64_t part_of(uint64_t mass, float share) {
+    return share >= 1.0f ? mass : __umul64hi(mass, __float2ull_rz(share * 0x1p64f));
+}
 
-// A lane's sum of 2^(c (x - m)) of its elements for which keep(x) holds.
-template <bool F32, class Keep>
-__device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], float m, float floor, Two c, Keep keep) {
-    constexpr int VE = Row<F32>::VE;
-    float sum = 0.0f;
+// A lane's sum of 2^(c (x - m)), m the block's largest, of its elements with x
+// above `least`.  t = d c.h rounds; what it lost and d c.l, e together, come
+// back as the factor 1 + e ln 2.
+template <bool F32, bool ALL>
+__device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint32_t m_key, Two c, float least) {
+    const float m = key_value(m_key);
+    if (!(fabsf(m) < 1e37f && fabsf(m) * c.h < 1e30f)) {  // d c may not fit fp32
+        constexpr int VE = Row<F32>::VE;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Row<F32>::NV; ++i) {
+            float x[VE];
+            Row<F32>::unpack(w[i], x);
+            for (int j = 0; j < VE; ++j)
+                if (ALL || x[j] > least) sum += ex2(fmaxf(x[j] - m, -124.0f / c.h) * c.h);
+        }
+        return sum;
+    }
+    // below this a weight is none, but d c still a number; less than m itself
+    float floor = fminf(m - 124.0f / c.h, key_value(m_key - (F32 ? 1u : 0x10000u)));
+    const uint32_t fb = __float_as_uint(floor);
+    const uint32_t low = fb & 0x80000000u ? (fb + 0xFFFFu) >> 16 : fb >> 16;  // the next bf16 down
+    const uint64_t neg_m = pair(-m, -m), ch = pair(c.h, c.h), neg_ch = pair(-c.h, -c.h), neg_cl = pair(-c.l, -c.l);
+    const uint64_t neg_ln2 = pair(-kLn2, -kLn2);
+    uint64_t sum = 0;
 #pragma unroll
     for (int i = 0; i < Row<F32>::NV; ++i) {
-        float x[VE], part = 0.0f;
-        Row<F32>::unpack(w[i], x);
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            const float d = fmaxf(x[j] - m, floor);
-            const float r = fmaf(d, c.h, kMagic), n = r - kMagic;
-            const float f = fmaf(d, c.l, fmaf(d, c.h, -n));
-            // 2^n: the low bits of r are n; n >= -125 by the floor
-            const float v = ex2(f) * __uint_as_float((__float_as_uint(r) << 23) + 0x3F800000u);
-            part += keep(x[j]) ? v : 0.0f;
+        for (int j = 0; j < (F32 ? 2 : 4); ++j) {
+            float x0, x1;
+            if constexpr (F32) {
+                x0 = fmaxf(__uint_as_float(u[2 * j]), floor), x1 = fmaxf(__uint_as_float(u[2 * j + 1]), floor);
+            } else {
+                const uint32_t v = max_bf16x2(u[j], low | low << 16);
+                x0 = bf16lo_to_f32(v), x1 = bf16hi_to_f32(v);
+            }
+            const uint64_t d = add2(pair(x0, x1), neg_m), t = mul2(d, ch);
+            const uint64_t e = fma2(d, neg_cl, fma2(d, neg_ch, t));  // minus what is missing
+            float t0, t1;
+            unpair(t, t0, t1);
+            float w0 = ex2(t0), w1 = ex2(t1);
+            if constexpr (!ALL) {
+                w0 = x0 > least ? w0 : 0.0f;
+                w1 = x1 > least ? w1 : 0.0f;
+            }
+            const uint64_t v = pair(w0, w1);
+            sum = add2(sum, fma2(mul2(v, neg_ln2), e, v));
         }
-        sum += part;
     }
-    return sum;
+    float a, b;
+    unpair(sum, a, b);
+    return a + b;
 }
 
 struct Job {
     float m;       // the row's largest logit
-    uint32_t m_key;
+    uint32_t m_key, lowest;  // no token below `lowest` is kept
     Two c;
-    float floor;   // of x - m: below it a weight counts as 2^-125 or less
     int b0, b1, blocks, part, splits;
-    float inv_q;   // of the histogram's residuals
-    float q_scale;
+    int bits;      // of a residual in a histogram of the row
+    int turn;      // of share_range's boxes
 };
 
-// ------------------------------------------------------------ the cut's search
-// One level: a histogram of the tokens whose values' keys are in [lo, hi], over
-// the row's CTAs, and the bin in which `count` (mass = false) or `mass` is reached.
-// The first level has bins of equal ratio of weights, the others of equal numbers of values.
-template <bool F32, int TH>
-__device__ void level(const Row<F32> &row, const Job &job, Shared<TH> &sh, bool first, bool want_mass, bool by_mass,
-                      int count, Two mass) {
-    constexpr int VE = Row<F32>::VE, NV = Row<F32>::NV;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t lo = sh.found.lo, hi = sh.found.hi;
-    const int count0 = sh.found.count;
-    const Two mass0 = sh.found.mass;
-    int shift = 0;
-    while (((hi - lo) >> shift) >= kBins) ++shift;
-    const float top = key_value(hi);
-    const Two c = job.c;
-    const Two c32{c.h * kPerUnit, c.l * kPerUnit};
-    const float half_bin = 0.9892f;  // below 2^-(1 / 64), the lightest of a bin to its middle
-    for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
-    __syncthreads();
-    for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
-        if (sh.block_key[b] < lo) continue;
-        uint4 w[NV];
-        row.load(b, w);
+// The n-th token, or the first whose mass to it reaches `mass`.
+struct Target {
+    bool by_mass;
+    int count;
+    uint64_t mass;
+    __device__ __forceinline__ bool reached(int n, uint64_t v) const { return by_mass ? v >= mass : n >= count; }
+};
+
+// Among the bins of the threads in order, PER each (n tokens of mass v), the one
+// that reaches the target, or with MUST the last that holds a token: tell(bin of
+// the thread, tokens before, mass before) by the one thread that has it.  Returns
+// whether there is one.
+template <bool MUST, int PER, int TH, class Tell>
+__device__ __forceinline__ bool find_bin(const int (&n)[PER], const uint64_t (&v)[PER], int at_n, uint64_t at,
+                                         const Target &target, Shared<TH> &sh, Tell tell) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int hit = -1, last = -1, last_n = 0;
+    uint64_t last_at = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float x[VE];
-            Row<F32>::unpack(w[i], x);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                const uint32_t key = order_key(x[j]);
-                if (key < lo || key > hi) continue;
-                uint32_t bin;
-                float rest;  // weight / the bin's - its least, or 1 - weight / the range's largest
-                if (first) {
-                    const float d = job.m - x[j];
-                    const float r = fmaf(d, c32.h, kMagic), n = r - kMagic;
-                    const float f = fmaf(d, c32.l, fmaf(d, c32.h, -n)) * (kLn2 / kPerUnit);
-                    bin = __float_as_uint(r) & 0xFFFFu;
-                    rest = fmaf(f, fmaf(f, fmaf(f, -1.0f / 6.0f, 0.5f), -1.0f), 1.0f - half_bin);
-                } else {
-                    bin = (hi - key) >> shift;
-                    const float d = top - x[j];
-                    const float f = fmaf(d, c.l, d * c.h) * kLn2;
-                    rest = f * fmaf(f, fmaf(f, 1.0f / 6.0f, -0.5f), 1.0f);
-                }
-                if (bin >= kBins) continue;
-                atomicAdd(&sh.n[bin], 1u);
-                if (want_mass) atomicAdd(&sh.q[bin], static_cast<uint32_t>(__float2int_rn(rest * job.q_scale)));
+    for (int i = 0; i < PER; ++i) {
+        if (hit < 0 && n[i] > 0) {
+            if (target.reached(at_n + n[i], at + v[i])) {
+                hit = i;
+            } else {
+                if (MUST) last = i, last_n = at_n, last_at = at;
+                at_n += n[i], at += v[i];
             }
         }
     }
+    const uint32_t have = __ballot_sync(0xffffffffu, hit >= 0);
+    const uint32_t any = MUST ? __ballot_sync(0xffffffffu, last >= 0) : 0;
+    __syncthreads();
+    if (lane == 0) {
+        sh.warp_int[warp] = have ? __ffs(have) - 1 : -1;
+        sh.warp_key[warp] = any ? 31 - __clz(any) : 0xFFFFFFFFu;
+    }
+    __syncthreads();
+    int who = -1;
+#pragma unroll
+    for (int i = TH / 32 - 1; i >= 0; --i) who = sh.warp_int[i] >= 0 ? i * 32 + sh.warp_int[i] : who;
+    if (MUST && who < 0) {
+        for (int i = 0; i < TH / 32; ++i) who = sh.warp_key[i] != 0xFFFFFFFFu ? i * 32 + static_cast<int>(sh.warp_key[i]) : who;
+        hit = last, at_n = last_n, at = last_at;
+    }
+    if (static_cast<int>(threadIdx.x) == who) tell(hit, at_n, at);
+    __syncthreads();
+    return who >= 0;
+}
+
+// What a token of a range of values whose weights are within 2^-5 of the range's
+// largest weighs less than that, in units of 2^-25.
+__device__ __forceinline__ uint32_t fine_rest(float top, float x, Two c, float scale) {
+    const float d = top - x, f = fmaf(d, c.l, d * c.h) * kLn2;
+    return static_cast<uint32_t>(__float2int_rn(f * fmaf(f, fmaf(f, 1.0f / 6.0f, -0.5f), 1.0f) * scale));
+}
+
+// No number is -0's: ranges leave its key out, so that their ends compare as floats do.
+__device__ __forceinline__ Range tidy(Range r) {
+    if (r.hi == 0x7FFFFFFFu) --r.hi;
+    if (r.lo == 0x7FFFFFFFu) ++r.lo;
+    return r;
+}
+
+// From the histogram fine_n, fine_q of sh.range's values: the bin with the target
+// becomes sh.range.  By the first CTA.
+template <int TH>
+__device__ void narrow(const Job &job, Shared<TH> &sh, const Target &target, int shift, int bits) {
+    constexpr int kPer = kFine / TH > 0 ? kFine / TH : 1;
+    const Range r = sh.range;
+    const uint64_t w = fixed(weight(key_value(r.hi), job.m, job.c), 0x1p62f);
+    int n[kPer], sum_n = 0, all_n;
+    uint64_t v[kPer], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int bin = threadIdx.x * kPer + i;
+        n[i] = bin < kFine ? static_cast<int>(sh.fine_n[bin]) : 0;
+        // (n - q 2^-(5 + bits)) w
+        v[i] = n[i] ? __umul64hi(((static_cast<uint64_t>(n[i]) << (5 + bits)) - sh.fine_q[bin]) << (38 - bits), w) : 0;
+        sum_n += n[i], sum += v[i];
+    }
+    const int at_n = r.count + cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n);
+    const uint64_t at = r.mass + cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
+    // the bins' masses can miss by their units what their sum was one histogram before: the last bin has the cut then
+    const bool found = find_bin<true, kPer, TH>(n, v, at_n, at, target, sh, [&](int i, int before_n, uint64_t before) {
+        const uint32_t hi = r.hi - (static_cast<uint32_t>(threadIdx.x * kPer + i) << shift);
+        const uint32_t lo = hi - r.lo < (1u << shift) ? r.lo : hi - (1u << shift) + 1;
+        sh.range = tidy(Range{lo, hi, before_n, n[i], before, 0, 0});
+    });
+    if (!found) {  // a range holds a token; were it not so, this ends the search
+        if (threadIdx.x == 0) sh.range.lo = sh.range.hi;
+        __syncthreads();
+    }
+}
+
+// What the first CTA has found to all of the row's.  The boxes take turns: the
+// one that is written has been read before the last barrier.
+template <int TH>
+__device__ __forceinline__ void share_range(Job &job, Shared<TH> &sh) {
     __syncthreads();
     if (job.splits > 1) {
+        Range *box = &sh.inbox[job.turn];
+        job.turn ^= 1;
+        if (job.part == 0 && threadIdx.x > 0 && static_cast<int>(threadIdx.x) < job.splits)
+            dsmem_put(box, threadIdx.x, sh.range);
         cluster_sync_all();
-        if (job.part != 0) {
-            for (int i = tid; i < kBins; i += TH) {
-                const uint32_t n = sh.n[i];
-                if (n) {
-                    dsmem_add(&sh.n[i], 0, n);
-                    if (want_mass) dsmem_add(&sh.q[i], 0, sh.q[i]);
+        if (job.part != 0 && threadIdx.x == 0) sh.range = *box;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int fine_shift(uint32_t lo, uint32_t hi) {
+    const uint32_t over = (hi - lo) / kFine;  // bins of 1 << shift values: ((hi - lo) >> shift) < kFine
+    return over ? 32 - __clz(over) : 0;
+}
+
+// A CTA's histogram into the first one's.
+template <int TH>
+__device__ __forceinline__ void collect(const Job &job, uint32_t *n, uint32_t *q, int bins) {
+    if (job.splits > 1) {
+        cluster_sync_all();
+        if (job.part != 0)
+            for (int i = threadIdx.x; i < bins; i += TH)
+                if (n[i]) {
+                    dsmem_add(n + i, 0, n[i]);
+                    dsmem_add(q + i, 0, q[i]);
+                }
+        cluster_sync_all();
+    }
+}
+
+// The histogram of the row's exponents, in the first CTA's n and q.
+template <bool F32, int TH>
+__device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> &sh) {
+    const int tid = threadIdx.x, warp = tid >> 5;
+    for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
+    __syncthreads();
+    const float least = key_value(job.lowest), m = job.m, ch = job.c.h * kPerUnit, cl = job.c.l * kPerUnit;
+    // weight / bin's = 2^(-f / 32), f in [-1/2, 1/2], less 63/64, in units of 2^-(5 + bits): below 2^bits
+    const float unit = static_cast<float>(1 << (5 + job.bits)), y = kLn2 / kPerUnit;
+    const float q0 = unit / 64.0f + 0x1p23f, q1 = -unit * y, q2 = unit * y * y / 2.0f, q3 = -unit * y * y * y / 6.0f;
+    for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
+        if (sh.block_key[b] < job.lowest) continue;
+        uint4 w[Row<F32>::NV];
+        row.load(b, w);
+#pragma unroll
+        for (int i = 0; i < Row<F32>::NV; ++i) {
+            float x[Row<F32>::VE];
+            Row<F32>::unpack(w[i], x);
+#pragma unroll
+            for (int j = 0; j < Row<F32>::VE; ++j) {
+                const float d = m - x[j];
+                const float r = fmaf(d, ch, kMagic), n = r - kMagic;
+                const float f = fmaf(d, cl, fmaf(d, ch, -n));
+                const float q = fmaf(f, fmaf(f, fmaf(f, q3, q2), q1), q0);
+                const uint32_t bin = __float_as_uint(r) - kMagicBits;
+                if (x[j] >= least && bin < kBins) {
+                    atomicAdd(&sh.n[bin], 1u);
+                    atomicAdd(&sh.q[bin], __float_as_uint(q) & 0x7FFFFFu);
                 }
             }
         }
-        cluster_sync_all();
     }
+    __syncthreads();
+    collect<TH>(job, sh.n, sh.q, kBins);
+}
+
+// The range of values of the exponents' bin that holds the target: sh.range, the
+// same in all the row's CTAs; none if all the bins together do not reach it.
+template <int TH>
+__device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (job.part == 0) {
         constexpr int kPer = kBins / TH;
-        Two bin_mass[kPer], sum{0.0f, 0.0f};
-        int bin_n[kPer], sum_n = 0;
-        const Two range_top = want_mass && !first ? weight(top, job.m, c) : Two{0.0f, 0.0f};
+        int n[kPer], sum_n = 0, all_n;
+        uint64_t v[kPer], sum = 0, all;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int bin = tid * kPer + i;
-            bin_n[i] = static_cast<int>(sh.n[bin]);
-            sum_n += bin_n[i];
-            bin_mass[i] = Two{0.0f, 0.0f};
-            if (want_mass && bin_n[i] > 0) {
-                // the count (exact in fp32: at most 2^20) times the bin's weight, and the rest
-                const Two rest = mul(two_prod(1.0f, static_cast<float>(sh.q[bin] >> 12) * 4096.0f), Two{job.inv_q, 0.0f});
-                const Two rest2 = add(rest, static_cast<float>(sh.q[bin] & 4095u) * job.inv_q);
-                if (first)
-                    bin_mass[i] = mul(mul(sh.coarse[bin >> 6], sh.fine[bin & 63]),
-                                      add(two_prod(static_cast<float>(bin_n[i]), half_bin), rest2));
-                else
-                    bin_mass[i] = mul(range_top, add(neg(rest2), static_cast<float>(bin_n[i])));
-                sum = add(sum, bin_mass[i]);
-            }
+            n[i] = static_cast<int>(sh.n[bin]);
+            const uint64_t units = static_cast<uint64_t>(n[i]) * (63u << (job.bits - 1)) + sh.q[bin];
+            v[i] = n[i] ? __umul64hi(units << (38 - job.bits), kBinWeight[bin & 31] >> (bin >> 5)) : 0;
+            sum_n += n[i], sum += v[i];
         }
-        int all_n;
-        Two all;
-        int at_n = count0 + cta_exclusive(sum_n, sh, all_n);
-        Two at{0.0f, 0.0f};
-        if (want_mass) at = add(mass0, cta_exclusive(sum, sh, all));
-        if (tid == 0) sh.found.state = 2;
-        __syncthreads();
-        int hit = -1;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (bin_n[i] > 0 && hit < 0) {
-                const Two next = add(at, bin_mass[i]);
-                if (by_mass ? !above(mass, next) : at_n + bin_n[i] >= count) {
-                    hit = i;
-                } else {
-                    at_n += bin_n[i];
-                    at = next;
-                }
-            }
-        }
-        // the first thread that has a hit; threads before it ended below the target, those after began above it
-        const int hits = hit >= 0 ? tid : TH;
-        const int lowest = __reduce_min_sync(0xffffffffu, hits);
-        if (lane == 0) sh.warp_int[warp] = lowest;
-        __syncthreads();
-        int who = TH;
-        for (int i = 0; i < TH / 32; ++i) who = min(who, sh.warp_int[i]);
-        if (tid == who) {
-            const int bin = tid * kPer + hit;
-            Found f;
-            f.count = at_n;
-            f.mass = at;
-            f.equals = bin_n[hit];
-            f.pad = 0;
-            if (first) {
-                // the values of a bin: from its number's first key to its last (keys fall as bins rise)
-                f.lo = f.hi = bin;  // resolved below
-                f.state = 3;
-            } else {
-                f.hi = hi - (static_cast<uint32_t>(bin) << shift);
-                f.lo = f.hi - lo < (1u << shift) ? lo : f.hi - (1u << shift) + 1;
-                f.state = f.lo == f.hi ? 1 : 0;
-            }
-            sh.found = f;
-        }
-        __syncthreads();
-        if (sh.found.state == 3) {
-            // the first key from `lo` on whose bin is at most `bin` (warp 0), and the last whose bin is at least `bin`
-            const int bin = static_cast<int>(sh.found.hi);
-            __syncthreads();
+        const int at_n = cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n);
+        const uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
+        const bool found = find_bin<false, kPer, TH>(n, v, at_n, at, target, sh, [&](int i, int before_n, uint64_t before) {
+            sh.range = Range{static_cast<uint32_t>(tid * kPer + i), 0, before_n, n[i], before, 0, 0};
+        });
+        if (found) {
+            // the bin's least value (warp 0) and the next bin's above it (warp 1): the bins' numbers fall as values rise
+            const float ch = job.c.h * kPerUnit;
+            const int bin = static_cast<int>(sh.range.lo);
             if (warp < 2) {
-                const int want = warp == 0 ? bin : bin - 1;
-                int64_t from = static_cast<int64_t>(lo) - 1, to = static_cast<int64_t>(hi) + 1;  // (from, to] holds it
+                int64_t from = static_cast<int64_t>(job.lowest) - 1, to = static_cast<int64_t>(job.m_key) + 1;  // in (from, to]
                 while (to - from > 1) {
-                    const int64_t step = (to - from) / 33 + 1, probe = from + step * (lane + 1);
+                    const int64_t step = ((to - from) >> 5) + 1, probe = from + step * (lane + 1);
                     bool reached = true;
                     if (probe < to) {
-                        const float d = job.m - key_value(static_cast<uint32_t>(probe));
-                        const float r = fmaf(d, c32.h, kMagic);
-                        reached = static_cast<int>(__float_as_uint(r) & 0xFFFFu) <= want;
+                        const float r = fmaf(job.m - key_value(static_cast<uint32_t>(probe)), ch, kMagic);
+                        reached = static_cast<int>(__float_as_uint(r) - kMagicBits) <= bin - warp;
                     }
-                    const int k = __ffs(__ballot_sync(0xffffffffu, reached)) - 1;  // of the first, -1: none
-                    const int64_t base = from;
-                    from = k < 0 ? base + 32 * step : base + k * step;
-                    if (k >= 0) to = min(to, base + (k + 1) * step);
+                    const int k = __ffs(__ballot_sync(0xffffffffu, reached)) - 1;  // the last probe is past the end
+                    to = min(to, from + step * (k + 1));
+                    from += step * k;
                 }
                 if (lane == 0) sh.warp_key[warp] = static_cast<uint32_t>(to);
             }
             __syncthreads();
             if (tid == 0) {
-                sh.found.lo = sh.warp_key[0];
-                sh.found.hi = sh.warp_key[1] - 1;
-                sh.found.state = sh.found.lo == sh.found.hi ? 1 : 0;
+                sh.range.lo = sh.warp_key[0];
+                sh.range.hi = sh.warp_key[1] - 1;
+                sh.range = tidy(sh.range);
             }
-            __syncthreads();
+        } else if (tid == 0) {
+            sh.range.none = 1;
         }
-        if (job.splits > 1 && tid > 0 && tid < job.splits) dsmem_put(&sh.found, tid, sh.found);
+        __syncthreads();
     }
-    if (job.splits > 1) cluster_sync_all();
+    share_range(job, sh);
+}
+
+// By block, the mass of the tokens above value `hi`; and the tokens from `lo` to
+// it: gathered in the first CTA's list, or, one value, counted by block.
+template <bool F32, int TH>
+__device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, uint32_t lo, uint32_t hi, bool gather) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float least = key_value(lo), most = key_value(hi);
+    for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
+        const uint32_t key = sh.block_key[b];
+        float s = 0.0f;
+        int n = 0;
+        if (key >= lo) {
+            uint4 w[Row<F32>::NV];
+            row.load(b, w);
+            if (key > hi) s = block_sum<F32, false>(w, key, job.c, most);
+#pragma unroll
+            for (int i = 0; i < Row<F32>::NV; ++i) {
+                float x[Row<F32>::VE];
+                Row<F32>::unpack(w[i], x);
+#pragma unroll
+                for (int j = 0; j < Row<F32>::VE; ++j) {
+                    if (x[j] >= least && x[j] <= most) {
+                        ++n;
+                        if (gather) {
+                            const int id = b * kBlock + (lane + 32 * i) * Row<F32>::VE + j;
+                            const uint32_t at = job.splits > 1 ? dsmem_next(&sh.listed, 0, 1)
+                                                               : static_cast<uint32_t>(atomicAdd(&sh.listed, 1));
+                            if (at < kGather) {
+                                if (job.splits > 1) {
+                                    dsmem_put(&sh.list_key[at], 0, order_key(x[j]));
+                                    dsmem_put(&sh.list_id[at], 0, static_cast<uint32_t>(id));
+                                } else {
+                                    sh.list_key[at] = order_key(x[j]);
+                                    sh.list_id[at] = id;
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (!gather) n = __reduce_add_sync(0xffffffffu, n);
+        }
+        if (lane == 0) {
+            sh.block_mass[b] = __float_as_uint(s);
+            sh.block_equals[b] = gather ? 0 : n;
+        }
+    }
     __syncthreads();
 }
 
-template <bool F32, int TH>
-__device__ Found search(const Row<F32> &row, const Job &job, Shared<TH> &sh, bool want_mass, bool by_mass, int count,
-                        Two mass, uint32_t lowest) {
-    __syncthreads();
-    if (threadIdx.x == 0) sh.found = Found{lowest, job.m_key, 0, 0, Two{0.0f, 0.0f}, 0, 0};
-    __syncthreads();
-    bool first = true;
-    while (sh.found.state == 0) {
-        level<F32, TH>(row, job, sh, first, want_mass, by_mass, count, mass);
-        first = false;
+// sh.block_mass from sums relative to the block's largest logit to units of the row's.
+template <int TH>
+__device__ __forceinline__ uint64_t weigh_blocks(const Job &job, Shared<TH> &sh) {
+    uint64_t mine = 0;
+    for (int b = job.b0 + threadIdx.x; b < job.b1; b += TH) {
+        const float s = __uint_as_float(static_cast<uint32_t>(sh.block_mass[b]));
+        uint64_t v = 0;
+        if (s > 0.0f) v = fixed(mul(weight(key_value(sh.block_key[b]), job.m, job.c), Two{s, 0.0f}), kUnit);
+        sh.block_mass[b] = v;
+        mine += v;
     }
-    return sh.found;
+    return mine;
+}
+
+template <int TH>
+__device__ __forceinline__ void hand_over_blocks(const Job &job, Shared<TH> &sh) {
+    if (job.splits > 1) {
+        if (job.part != 0)
+            for (int b = job.b0 + threadIdx.x; b < job.b1; b += TH) {
+                dsmem_put(&sh.block_mass[b], 0, sh.block_mass[b]);
+                dsmem_put(&sh.block_key[b], 0, sh.block_key[b]);
+                dsmem_put(&sh.block_equals[b], 0, sh.block_equals[b]);
+            }
+        cluster_sync_all();
+    }
+    __syncthreads();
+}
+
+// The list's tokens whose keys are in sh.range, down to one value.  By the first CTA.
+template <int TH>
+__device__ void search_list(const Job &job, Shared<TH> &sh, const Target &target) {
+    constexpr int kBits = 20;  // kGather residuals of 2^20 fit 32 bits
+    while (sh.range.lo != sh.range.hi) {
+        const uint32_t lo = sh.range.lo, hi = sh.range.hi;
+        const int shift = fine_shift(lo, hi), n = min(sh.listed, kGather);
+        const float top = key_value(hi);
+        for (int i = threadIdx.x; i < kFine; i += TH) sh.fine_n[i] = sh.fine_q[i] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += TH) {
+            const uint32_t key = sh.list_key[i];
+            if (key >= lo && key <= hi) {
+                const uint32_t bin = (hi - key) >> shift;
+                atomicAdd(&sh.fine_n[bin], 1u);
+                atomicAdd(&sh.fine_q[bin], fine_rest(top, key_value(key), job.c, static_cast<float>(1 << (5 + kBits))));
+            }
+        }
+        __syncthreads();
+        narrow(job, sh, target, shift, kBits);
+    }
+}
+
+// From sh.range, the same in all the row's CTAs, to the cut: its value
+// (lo = hi), how many of its equals are kept, the mass of all that is.
+// `list`: the range whose tokens are gathered and above which blocks are summed.
+template <bool F32, int TH>
+__device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Target &target, Range &list) {
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const bool listed = list.lo == sh.range.lo && list.hi == sh.range.hi;
+    while (!listed && sh.range.equals > kGather && sh.range.lo != sh.range.hi) {
+        const uint32_t lo = sh.range.lo, hi = sh.range.hi;
+        const int shift = fine_shift(lo, hi);
+        const float top = key_value(hi), least = key_value(lo);
+        __syncthreads();
+        for (int i = tid; i < kFine; i += TH) sh.fine_n[i] = sh.fine_q[i] = 0;
+        __syncthreads();
+        for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
+            if (sh.block_key[b] < lo) continue;
+            uint4 w[Row<F32>::NV];
+            row.load(b, w);
+#pragma unroll
+            for (int i = 0; i < Row<F32>::NV; ++i) {
+                float x[Row<F32>::VE];
+                Row<F32>::unpack(w[i], x);
+                for (int j = 0; j < Row<F32>::VE; ++j)
+                    if (x[j] >= least && x[j] <= top) {
+                        const uint32_t bin = (hi - order_key(x[j])) >> shift;
+                        atomicAdd(&sh.fine_n[bin], 1u);
+                        atomicAdd(&sh.fine_q[bin], fine_rest(top, x[j], job.c, static_cast<float>(1 << (5 + job.bits))));
+                    }
+            }
+        }
+        __syncthreads();
+        collect<TH>(job, sh.fine_n, sh.fine_q, kFine);
+        if (job.part == 0) narrow(job, sh, target, shift, job.bits);
+        share_range(job, sh);
+    }
+    if (!listed && sh.range.lo != sh.range.hi) {
+        list = sh.range;
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        if (job.splits > 1) cluster_sync_all();
+        sum_blocks<F32, TH>(row, job, sh, list.lo, list.hi, true);
+        weigh_blocks(job, sh);
+        hand_over_blocks(job, sh);
+    }
+    if (job.part == 0) {
+        search_list(job, sh, target);
+        __syncthreads();
+        if (tid == 0) {
+            const uint64_t w = fixed(weight(key_value(sh.range.lo), job.m, job.c), kUnit);
+            int kept = target.count - sh.range.count;
+            if (target.by_mass) {
+                const uint64_t miss = target.mass > sh.range.mass ? target.mass - sh.range.mass : 0;
+                const uint64_t need = w > 0 ? (miss + w - 1) / w : static_cast<uint64_t>(sh.range.equals);
+                kept = need > static_cast<uint64_t>(sh.range.equals) ? sh.range.equals : need < 1 ? 1 : static_cast<int>(need);
+            }
+            sh.range.equals = kept;
+            sh.range.mass += w * static_cast<uint64_t>(kept);
+        }
+    }
+    share_range(job, sh);
 }
 
 // ------------------------------------------------------------------ the kernel
 template <bool F32, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs a, int splits) {
-    __shared__ Shared<TH> sh;
-    constexpr int kWarps = TH / 32, NV = Row<F32>::NV;
+    extern __shared__ uint4 sample_smem[];
+    Shared<TH> &sh = *reinterpret_cast<Shared<TH> *>(sample_smem);
+    constexpr int kWarps = TH / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / splits;
     Job job;
     job.splits = splits;
+    job.turn = 0;
     job.part = static_cast<int>(blockIdx.x - r * splits);
     if (splits > 1) cluster_arrive();  // shared memory of the others is there once all have
     pdl_wait();
@@ -506,22 +773,21 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     const bool greedy = temperature == 0.0f;
     bool bad = !(greedy || (temperature >= 1e-30f && temperature <= 1e30f)) || top_p != top_p || min_p != min_p;
     job.c = div(Two{0x1.715476p+0f, 0x1.4ae0cp-26f}, Two{greedy || bad ? 1.0f : temperature, 0.0f});
-    job.floor = -124.0f / job.c.h;
     if (min_p > 0.0f && tid == TH - 1) sh.log_min_p = log(static_cast<double>(fminf(min_p, 1.0f)));
 
     // ---- the blocks' largest logits and their masses relative to those
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
-        uint4 w[NV];
+        uint4 w[Row<F32>::NV];
         row.load(b, w);
         const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(Row<F32>::most(w)));
-        const float m = key_value(key);
         float s = 0.0f;
-        if (key > kKeyNegInf && key < kKeyInf) s = block_sum<F32>(w, m, job.floor, job.c, [](float) { return true; });
+        if (key > kKeyNegInf && key < kKeyInf && !greedy) s = block_sum<F32, true>(w, key, job.c, 0.0f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) {
             sh.block_key[b] = key;
-            sh.block_mass[b] = Two{s, 0.0f};
+            sh.block_mass[b] = __float_as_uint(s);
+            sh.block_equals[b] = 0;
         }
     }
     __syncthreads();
@@ -548,150 +814,119 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         }
         return;
     }
-    // ---- the blocks' masses relative to the row's largest
-    Two mine{0.0f, 0.0f};
-    for (int b = job.b0 + tid; b < job.b1; b += TH) {
-        const uint32_t bk = sh.block_key[b];
-        const Two v = bk == kKeyNegInf ? Two{0.0f, 0.0f} : mul(weight(key_value(bk), job.m, job.c), sh.block_mass[b]);
-        sh.block_mass[b] = v;
-        sh.block_equals[b] = 0;
-        mine = add(mine, v);
-    }
-    // ---- the cut
-    uint32_t cut = kKeyNegInf;  // tokens above it are kept, and `ties` equal to it
+    job.lowest = max(order_key(job.m - kWindow / job.c.h), kKeyNegInf + 1);
+    int log_v = 0;
+    while ((1 << log_v) < vocab) ++log_v;
+    job.bits = min(32 - log_v, 18);
+
+    // ---- the cut: tokens above its value are kept, and `ties` equal to it
+    uint32_t cut = kKeyNegInf;
     int ties = 0;
+    Range list{1, 0, 0, 0, 0, 0, 0};
+    const bool by_p = top_p < 1.0f, by_k = top_k < vocab;
     if (greedy || top_k == 1) {
         cut = job.m_key;
         ties = 1;
-    } else {
-        int log_v = 0;
-        while ((1 << log_v) < vocab) ++log_v;
-        const float q_max = static_cast<float>(1u << (31 - log_v > 24 ? 24 : 31 - log_v));
-        job.q_scale = q_max / kResidual;
-        job.inv_q = kResidual / q_max;
-        const bool by_p = top_p < 1.0f, by_k = top_k < vocab;
-        const float window = job.m - kWindow / job.c.h;
-        const uint32_t lowest = max(order_key(window), kKeyNegInf + 1);
-        if (by_p || by_k) {
-            if (tid < 64) sh.fine[tid] = two_exp2(Two{-static_cast<float>(tid) / kPerUnit, 0.0f});
-            else if (tid < 96) sh.coarse[tid - 64] = Two{exp2f(-2.0f * static_cast<float>(tid - 64)), 0.0f};
-            __syncthreads();
+    } else if (by_p || by_k) {
+        uint64_t whole = 0;  // the mass that top_p is a share of; the first CTA's counts
+        const uint64_t mine = weigh_blocks(job, sh);
+        cta_exclusive<uint64_t, TH>(mine, sh.warp_sum, whole);
+        if (splits > 1 && tid == 0) dsmem_put(&sh.part_mass[job.part], 0, whole);
+        count_exponents<F32, TH>(row, job, sh);
+        if (splits > 1) {
+            whole = 0;
+            for (int i = 0; i < splits; ++i) whole += sh.part_mass[i];
         }
-        Two whole{0.0f, 0.0f};  // the mass that top_p is a share of
         if (by_k) {
-            const Found f = search<F32, TH>(row, job, sh, by_p, false, top_k, Two{0.0f, 0.0f}, lowest);
-            if (f.state == 1) {
-                cut = f.lo;
-                ties = top_k - f.count;
-                whole = add(f.mass, mul(weight(key_value(f.lo), job.m, job.c), Two{static_cast<float>(ties), 0.0f}));
+            const Target target{false, top_k, 0};
+            find_exponent(job, sh, target);
+            if (!sh.range.none) {
+                find_cut<F32, TH>(row, job, sh, target, list);
+                cut = sh.range.lo;
+                ties = sh.range.equals;
+                whole = sh.range.mass;
+                __syncthreads();
             }
         }
         if (by_p) {
-            if (cut == kKeyNegInf) {
-                Two all;
-                cta_exclusive(mine, sh, all);
-                whole = all;
-                if (splits > 1) {
-                    if (tid < splits) dsmem_put(&sh.part_mass[job.part], tid, all);
-                    cluster_sync_all();
-                    whole = sh.part_mass[0];
-                    for (int i = 1; i < splits; ++i) whole = add(whole, sh.part_mass[i]);
-                }
-            }
-            const Two target = mul(whole, Two{fmaxf(top_p, 0.0f), 0.0f});
-            const Found f = search<F32, TH>(row, job, sh, true, true, 0, target, lowest);
-            if (f.state == 1) {
-                // the fewest equals that reach the target
-                const Two w = weight(key_value(f.lo), job.m, job.c);
-                const Two need = div(add(target, neg(f.mass)), w);
-                const float whole_need = ceilf(need.h) + (need.h == ceilf(need.h) && need.l > 0.0f ? 1.0f : 0.0f);
-                const int n = whole_need < 1.0f ? 1 : min(f.equals, static_cast<int>(whole_need));
-                if (f.lo > cut || (f.lo == cut && n < ties)) cut = f.lo, ties = n;
+            const uint64_t share = __float2ull_rz(fmaxf(top_p, 0.0f) * 0x1p64f);
+            const Target target{true, 0, at_least_one(__umul64hi(whole, share) + (whole * share != 0 ? 1 : 0))};
+            find_exponent(job, sh, target);
+            if (!sh.range.none) {
+                find_cut<F32, TH>(row, job, sh, target, list);
+                if (sh.range.lo > cut || (sh.range.lo == cut && sh.range.equals < ties)) cut = sh.range.lo, ties = sh.range.equals;
+                __syncthreads();
             }
         }
-        if (min_p > 0.0f) {
-            // the least value whose weight is min_p or more
-            const uint32_t k = order_key(__double2float_ru(job.m + temperature * sh.log_min_p));
-            if (k > cut) cut = k, ties = 0x7FFFFFFF;
-        }
+    } else if (min_p <= 0.0f) {
+        weigh_blocks(job, sh);
+        __syncthreads();
+        hand_over_blocks(job, sh);
+    }
+    if (min_p > 0.0f && !greedy) {
+        // the least value whose weight is min_p or more
+        const uint32_t k = order_key(__double2float_ru(job.m + temperature * sh.log_min_p));
+        if (k > cut) cut = k, ties = 0x7FFFFFFF;
     }
     const bool filtered = cut > kKeyNegInf;
     const float cut_value = key_value(cut);
-    // ---- the masses of the kept tokens above the cut's value, and its equals
-    if (filtered) {
+    const bool in_list = list.lo <= cut && cut <= list.hi;
+    if (filtered && !in_list) {
+        sum_blocks<F32, TH>(row, job, sh, cut, cut, false);
+        weigh_blocks(job, sh);
         __syncthreads();
-        for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
-            const uint32_t bk = sh.block_key[b];
-            float s = 0.0f;
-            int n = 0;
-            if (bk >= cut) {
-                uint4 w[NV];
-                row.load(b, w);
-                s = block_sum<F32>(w, key_value(bk), job.floor, job.c, [&](float x) { return x > cut_value; });
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    float x[Row<F32>::VE];
-                    Row<F32>::unpack(w[i], x);
-#pragma unroll
-                    for (int j = 0; j < Row<F32>::VE; ++j) n += x[j] == cut_value ? 1 : 0;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                n = __reduce_add_sync(0xffffffffu, n);
-            }
-            if (lane == 0) {
-                sh.block_mass[b] = s > 0.0f ? mul(weight(key_value(bk), job.m, job.c), Two{s, 0.0f}) : Two{0.0f, 0.0f};
-                sh.block_equals[b] = n;
-            }
-        }
+        hand_over_blocks(job, sh);
+    } else if (!filtered && (by_p || by_k)) {  // neither took a token away
+        sum_blocks<F32, TH>(row, job, sh, kKeyNegInf + 1, kKeyNegInf, false);
+        weigh_blocks(job, sh);
+        __syncthreads();
+        hand_over_blocks(job, sh);
     }
-    __syncthreads();
-    if (splits > 1) {
-        if (job.part != 0)
-            for (int b = job.b0 + tid; b < job.b1; b += TH) {
-                dsmem_put(&sh.block_mass[b], 0, sh.block_mass[b]);
-                dsmem_put(&sh.block_equals[b], 0, sh.block_equals[b]);
-            }
-        cluster_sync_all();
-        if (job.part != 0) return;
+    if (job.part != 0) return;
+    if (filtered && in_list) {  // what the list holds above the cut, and the cut's equals
+        const int n = min(sh.listed, kGather);
+        for (int i = tid; i < n; i += TH) {
+            const uint32_t k = sh.list_key[i], b = sh.list_id[i] / kBlock;
+            if (k > cut)
+                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.block_mass[b]),
+                          static_cast<unsigned long long>(fixed(weight(key_value(k), job.m, job.c), kUnit)));
+            else if (k == cut) atomicAdd(&sh.block_equals[b], 1);
+        }
+        __syncthreads();
     }
     // ---- the block
     const float u0 = fminf(fmaxf(a.u[2 * r], 0.0f), 1.0f), u1 = fminf(fmaxf(a.u[2 * r + 1], 0.0f), 1.0f);
-    const Two cut_weight = filtered ? weight(cut_value, job.m, job.c) : Two{0.0f, 0.0f};
     if (warp == 0) {
+        const uint64_t cut_weight = filtered ? fixed(weight(cut_value, job.m, job.c), kUnit) : 0;
         const int per = (job.blocks + 31) / 32, first = lane * per, end = min(first + per, job.blocks);
         int n = 0;
         for (int b = first; b < end; ++b) n += sh.block_equals[b];
-        const int before = warp_inclusive(n) - n;
-        Two sum{0.0f, 0.0f};
-        int seen = before;
+        int seen = warp_inclusive(n) - n;
+        uint64_t sum = 0;
         for (int b = first; b < end; ++b) {
             const int e = sh.block_equals[b], keep = min(max(ties - seen, 0), e);
             seen += e;
-            Two v = sh.block_mass[b];
-            if (keep > 0) v = add(v, mul(cut_weight, Two{static_cast<float>(keep), 0.0f}));
+            const uint64_t v = sh.block_mass[b] + cut_weight * static_cast<uint64_t>(keep);
             sh.block_mass[b] = v;
             sh.block_equals[b] = keep;
-            sum = add(sum, v);
+            sum += v;
         }
-        const Two upto = warp_inclusive(sum), all = shfl(upto, 31);
-        const Two target = mul(all, Two{u0, 0.0f});
-        Two at = shfl_up(upto, 1);
-        if (lane == 0) at = Two{0.0f, 0.0f};
+        const uint64_t upto = warp_inclusive(sum), all = __shfl_sync(0xffffffffu, upto, 31), target = part_of(all, u0);
+        uint64_t at = upto - sum;
         int hit = -1, last = -1;
         for (int b = first; b < end; ++b) {
-            const Two v = sh.block_mass[b];
-            if (v.h > 0.0f) {
-                at = add(at, v);
+            const uint64_t v = sh.block_mass[b];
+            at += v;
+            if (v > 0) {
                 last = b;
-                if (hit < 0 && above(at, target)) hit = b;
+                if (hit < 0 && at > target) hit = b;
             }
         }
         const uint32_t have = __ballot_sync(0xffffffffu, hit >= 0);
         last = __reduce_max_sync(0xffffffffu, last);
         hit = have ? __shfl_sync(0xffffffffu, hit, __ffs(have) - 1) : last;
         if (lane == 0) {
-            sh.result_block = hit;
+            sh.block = hit;
             sh.allowed = sh.block_equals[hit];
             sh.total = all;
             sh.drawn = 0x7FFFFFFF;
@@ -699,9 +934,10 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         }
     }
     __syncthreads();
-    // ---- the token
+    // ---- the token: weights relative to the block's largest logit, which is kept if any of the block is
     constexpr int kPer = kBlock / TH;
-    const int e0 = sh.result_block * kBlock + tid * kPer;
+    const float block_m = key_value(sh.block_key[sh.block]);
+    const int e0 = sh.block * kBlock + tid * kPer;
     float x[kPer];
     int eq = 0;
 #pragma unroll
@@ -710,50 +946,70 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         eq += filtered && x[j] == cut_value ? 1 : 0;
     }
     int all_eq, rank = 0;
-    if (filtered) rank = cta_exclusive(eq, sh, all_eq);
-    Two w[kPer], sum{0.0f, 0.0f};
+    if (filtered) rank = cta_exclusive<int, TH>(eq, sh.warp_int, all_eq);
+    uint64_t w[kPer], sum = 0, all;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         bool keep = !filtered || x[j] > cut_value;
         if (filtered && x[j] == cut_value) keep = rank++ < sh.allowed;
-        w[j] = keep ? weight(x[j], job.m, job.c) : Two{0.0f, 0.0f};
-        sum = add(sum, w[j]);
+        w[j] = keep ? fixed(weight(x[j], block_m, job.c), 0x1p45f) : 0;
+        sum += w[j];
     }
-    Two all;
-    Two at = cta_exclusive(sum, sh, all);
-    const Two target = mul(all, Two{u1, 0.0f});
+    uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
+    const uint64_t target = part_of(all, u1);
     int hit = 0x7FFFFFFF, last = -1;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        if (w[j].h > 0.0f) {
-            at = add(at, w[j]);
+        at += w[j];
+        if (w[j] > 0) {
             last = e0 + j;
-            if (hit == 0x7FFFFFFF && above(at, target)) hit = e0 + j;
+            if (hit == 0x7FFFFFFF && at > target) hit = e0 + j;
         }
     }
-    hit = static_cast<int>(__reduce_min_sync(0xffffffffu, hit));
+    hit = __reduce_min_sync(0xffffffffu, hit);
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) {
-        atomicMin(&sh.drawn, hit);
-        atomicMax(&sh.last, last);
+        if (hit != 0x7FFFFFFF) atomicMin(&sh.drawn, hit);
+        if (last >= 0) atomicMax(&sh.last, last);
     }
     __syncthreads();
     const int token = sh.drawn != 0x7FFFFFFF ? sh.drawn : sh.last;
     if (tid == 0) {
         a.tokens[r] = token;
         if (a.logprobs) {
-            // (x - m) / T - log W, with W = h (1 + l / h)
+            // (x - m) / T - log(mass / 2^41)
             const Two t = mul(mul(two_sum(row.at(token), -job.m), job.c), Two{kLn2, -0x1.05c61p-29f});
-            a.logprobs[r] = (t.h - logf(sh.total.h)) + (t.l - sh.total.l / sh.total.h);
+            const float mass = __ull2float_rn(sh.total) * (1.0f / kUnit);
+            a.logprobs[r] = (t.h - logf(mass)) + t.l;
         }
     }
 }
 
+struct SampleSetup {
+    std::mutex mu;
+    bool done[64] = {};
+    cudaError_t err[64] = {};
+};
+
 template <bool F32, int TH>
 cudaError_t launch_rows(const SampleArgs &a, int splits, cudaStream_t stream) {
+    static SampleSetup setup;
+    constexpr int kSmem = static_cast<int>(sizeof(Shared<TH>));
+    static_assert(kSmem * (1024 / TH) <= 227 * 1024, "shared memory per SM");
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(setup.mu);
+        if (!setup.done[dev]) {
+            setup.err[dev] = cudaFuncSetAttribute(sample_kernel<F32, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            setup.done[dev] = true;
+        }
+        if (setup.err[dev] != cudaSuccess) return setup.err[dev];
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * splits), 1, 1);
     cfg.blockDim = dim3(TH, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -868,10 +868,11 @@ int fp8bs_token_logprobs(const void *logits, int logits_f32,
  * Two numbers a row, because one fp32 number in steps of 2^-24 cannot give
  * 152064 tokens their probabilities, and the borders of as many tokens on
  * one line would be moved by every rounding of a sum.  T = 0 is greedy (the
- * first token, log probability 0).  Tokens lighter than 2^-63 of the first
- * may count as not kept.  Sums: a weight in fp32 (2^-22), blocks and the tokens of a
- * block in 2^-44 of the mass; a draw nearer to a border than their errors
- * (some 2^-27 of the mass) may fall to either side.
+ * first token, log probability 0).  A weight is within 2^-22 of itself, and masses
+ * are whole multiples of 2^-41 of the largest weight: what is below half of that
+ * may count as nothing.  Errors of single weights mostly cancel in a mass; a
+ * draw, or a top_p, nearer to a border than what is left of them (some 2^-27 of
+ * the mass) may fall to either side.
  *
  * Defined by: no passage of the source pages has a counterpart (FreeToken PR
  * #636 serves the lm_head whose logits these are).
