@@ -46,7 +46,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23: adding it rounds to whole numbers
 constexpr uint32_t kMagicBits = 0x4B400000u;
 constexpr float kUnit = 0x1p41f;                // of masses
-constexpr uint32_t kKeyInf = 0xFF800000u, kKeyNegInf = 0x007FFFFFu;
 
 // 2^(62 - j / 32): a bin's weight
 __constant__ uint64_t kBinWeight[32] = {
@@ -66,14 +65,29 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Order of the values as unsigned integers: -0 is +0, NaN above everything.
-__device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t u = __float_as_uint(x + 0.0f);
-    return x != x ? 0xFFFFFFFFu : u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
+// Order of the values as unsigned integers, of 16 bits for bf16: -0 is +0, NaN
+// above everything.
+template <bool F32>
+struct Key {
+    static constexpr uint32_t kInf = F32 ? 0xFF800000u : 0xFF80u, kNegInf = F32 ? 0x007FFFFFu : 0x007Fu;
+    static constexpr uint32_t kNegZero = F32 ? 0x7FFFFFFFu : 0x7FFFu;  // no value's
+    static __device__ __forceinline__ uint32_t of(float x) {
+        const uint32_t u = __float_as_uint(x + 0.0f);
+        const uint32_t k = x != x ? 0xFFFFFFFFu : u & 0x80000000u ? ~u : u | 0x80000000u;
+        return F32 ? k : k >> 16;
+    }
+    static __device__ __forceinline__ float value(uint32_t k) {
+        if (!F32) k = k & 0x8000u ? k << 16 : k << 16 | 0xFFFFu;
+        return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+    }
+    // Of the least value that is not below x, a finite fp32.
+    static __device__ __forceinline__ uint32_t from(float x) {
+        const uint32_t u = __float_as_uint(x + 0.0f);
+        if (F32) return of(x);
+        const uint32_t k = u & 0x80000000u ? ~u >> 16 : ((u | 0x80000000u) + 0xFFFFu) >> 16;
+        return k == kNegZero ? k + 1 : k;
+    }
+};
 
 template <class T>
 __device__ __forceinline__ T warp_inclusive(T v) {
@@ -241,7 +255,8 @@ struct Shared {
     double log_min_p;
     int warp_int[kWarps];
     uint32_t warp_key[kWarps], part_key[kMaxSplit];
-    int listed, drawn, last, block, allowed;
+    uint64_t bin_weight[32];          // kBinWeight: lanes ask for different ones
+    int listed, collected, drawn, last, block, allowed;
 };
 
 // To the shared memory of CTA `rank` of the cluster, at the place of *local.
@@ -303,7 +318,7 @@ __device__ __forceinline__ uint64_t part_of(uint64_t mass, float share) {
 // back as the factor 1 + e ln 2.
 template <bool F32, bool ALL>
 __device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint32_t m_key, Two c, float least) {
-    const float m = key_value(m_key);
+    const float m = Key<F32>::value(m_key);
     if (!(fabsf(m) < 1e37f && fabsf(m) * c.h < 1e30f)) {  // d c may not fit fp32
         constexpr int VE = Row<F32>::VE;
         float sum = 0.0f;
@@ -317,7 +332,7 @@ __device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint3
         return sum;
     }
     // below this a weight is none, but d c still a number; less than m itself
-    float floor = fminf(m - 124.0f / c.h, key_value(m_key - (F32 ? 1u : 0x10000u)));
+    float floor = fminf(m - 124.0f / c.h, Key<F32>::value(m_key - 1));
     const uint32_t fb = __float_as_uint(floor);
     const uint32_t low = fb & 0x80000000u ? (fb + 0xFFFFu) >> 16 : fb >> 16;  // the next bf16 down
     const uint64_t neg_m = pair(-m, -m), ch = pair(c.h, c.h), neg_ch = pair(-c.h, -c.h), neg_cl = pair(-c.l, -c.l);
@@ -419,19 +434,20 @@ __device__ __forceinline__ uint32_t fine_rest(float top, float x, Two c, float s
 }
 
 // No number is -0's: ranges leave its key out, so that their ends compare as floats do.
+template <bool F32>
 __device__ __forceinline__ Range tidy(Range r) {
-    if (r.hi == 0x7FFFFFFFu) --r.hi;
-    if (r.lo == 0x7FFFFFFFu) ++r.lo;
+    if (r.hi == Key<F32>::kNegZero) --r.hi;
+    if (r.lo == Key<F32>::kNegZero) ++r.lo;
     return r;
 }
 
 // From the histogram fine_n, fine_q of sh.range's values: the bin with the target
 // becomes sh.range.  By the first CTA.
-template <int TH>
+template <bool F32, int TH>
 __device__ void narrow(const Job &job, Shared<TH> &sh, const Target &target, int shift, int bits) {
     constexpr int kPer = kFine / TH > 0 ? kFine / TH : 1;
     const Range r = sh.range;
-    const uint64_t w = fixed(weight(key_value(r.hi), job.m, job.c), 0x1p62f);
+    const uint64_t w = fixed(weight(Key<F32>::value(r.hi), job.m, job.c), 0x1p62f);
     int n[kPer], sum_n = 0, all_n;
     uint64_t v[kPer], sum = 0, all;
 #pragma unroll
@@ -448,7 +464,7 @@ __device__ void narrow(const Job &job, Shared<TH> &sh, const Target &target, int
     const bool found = find_bin<true, kPer, TH>(n, v, at_n, at, target, sh, [&](int i, int before_n, uint64_t before) {
         const uint32_t hi = r.hi - (static_cast<uint32_t>(threadIdx.x * kPer + i) << shift);
         const uint32_t lo = hi - r.lo < (1u << shift) ? r.lo : hi - (1u << shift) + 1;
-        sh.range = tidy(Range{lo, hi, before_n, n[i], before, 0, 0});
+        sh.range = tidy<F32>(Range{lo, hi, before_n, n[i], before, 0, 0});
     });
     if (!found) {  // a range holds a token; were it not so, this ends the search
         if (threadIdx.x == 0) sh.range.lo = sh.range.hi;
@@ -492,16 +508,29 @@ __device__ __forceinline__ void collect(const Job &job, uint32_t *n, uint32_t *q
     }
 }
 
+// One token more in the bin at shared address `at`, of residual q.
+__device__ __forceinline__ void count_one(uint32_t at, uint32_t q) {
+    asm volatile("red.shared.add.u32 [%0], 1;\n\tred.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4)
+                 : "memory");
+}
+
 // The histogram of the row's exponents, in the first CTA's n and q.
 template <bool F32, int TH>
 __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> &sh) {
     const int tid = threadIdx.x, warp = tid >> 5;
     for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
     __syncthreads();
-    const float least = key_value(job.lowest), m = job.m, ch = job.c.h * kPerUnit, cl = job.c.l * kPerUnit;
-    // weight / bin's = 2^(-f / 32), f in [-1/2, 1/2], less 63/64, in units of 2^-(5 + bits): below 2^bits
+    const float least = Key<F32>::value(job.lowest), m = job.m;
+    // d = m - x; bin = round(32 c d), f the rest in [-1/2, 1/2]; weight / bin's = 2^(-f / 32), less 63/64, in units of
+    // 2^-(5 + bits): below 2^bits.  The low bits of r are the bin, those of q the units
     const float unit = static_cast<float>(1 << (5 + job.bits)), y = kLn2 / kPerUnit;
-    const float q0 = unit / 64.0f + 0x1p23f, q1 = -unit * y, q2 = unit * y * y / 2.0f, q3 = -unit * y * y * y / 6.0f;
+    const uint64_t m2 = pair(m, m), minus = pair(-1.0f, -1.0f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
+    const float chf = job.c.h * kPerUnit, clf = job.c.l * kPerUnit;
+    const uint64_t ch = pair(chf, chf), cl = pair(clf, clf);
+    const uint64_t q0 = pair(unit / 64.0f + 0x1p23f, unit / 64.0f + 0x1p23f), q1 = pair(-unit * y, -unit * y);
+    const uint64_t q2 = pair(unit * y * y / 2.0f, unit * y * y / 2.0f);
+    const uint64_t q3 = pair(-unit * y * y * y / 6.0f, -unit * y * y * y / 6.0f);
+    const uint32_t base = smem_u32(sh.n) - (kMagicBits << 2);
     for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
         if (sh.block_key[b] < job.lowest) continue;
         uint4 w[Row<F32>::NV];
@@ -511,16 +540,17 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
             float x[Row<F32>::VE];
             Row<F32>::unpack(w[i], x);
 #pragma unroll
-            for (int j = 0; j < Row<F32>::VE; ++j) {
-                const float d = m - x[j];
-                const float r = fmaf(d, ch, kMagic), n = r - kMagic;
-                const float f = fmaf(d, cl, fmaf(d, ch, -n));
-                const float q = fmaf(f, fmaf(f, fmaf(f, q3, q2), q1), q0);
-                const uint32_t bin = __float_as_uint(r) - kMagicBits;
-                if (x[j] >= least && bin < kBins) {
-                    atomicAdd(&sh.n[bin], 1u);
-                    atomicAdd(&sh.q[bin], __float_as_uint(q) & 0x7FFFFFu);
-                }
+            for (int j = 0; j < Row<F32>::VE; j += 2) {
+                const uint64_t d = fma2(pair(x[j], x[j + 1]), minus, m2), r = fma2(d, ch, magic);
+                const uint64_t n = add2(r, unmagic);
+                // 32 c d - n: the product's difference is exact but for one rounding
+                const uint64_t f = fma2(d, cl, fma2(d, ch, mul2(n, minus)));
+                const uint64_t q = fma2(f, fma2(f, fma2(f, q3, q2), q1), q0);
+                float r0, r1, u0, u1;
+                unpair(r, r0, r1);
+                unpair(q, u0, u1);
+                if (x[j] >= least) count_one(base + (__float_as_uint(r0) << 2), __float_as_uint(u0) & 0x7FFFFFu);
+                if (x[j + 1] >= least) count_one(base + (__float_as_uint(r1) << 2), __float_as_uint(u1) & 0x7FFFFFu);
             }
         }
     }
@@ -530,7 +560,7 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
 
 // The range of values of the exponents' bin that holds the target: sh.range, the
 // same in all the row's CTAs; none if all the bins together do not reach it.
-template <int TH>
+template <bool F32, int TH>
 __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (job.part == 0) {
@@ -542,7 +572,7 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
             const int bin = tid * kPer + i;
             n[i] = static_cast<int>(sh.n[bin]);
             const uint64_t units = static_cast<uint64_t>(n[i]) * (63u << (job.bits - 1)) + sh.q[bin];
-            v[i] = n[i] ? __umul64hi(units << (38 - job.bits), kBinWeight[bin & 31] >> (bin >> 5)) : 0;
+            v[i] = n[i] ? __umul64hi(units << (38 - job.bits), sh.bin_weight[bin & 31] >> (bin >> 5)) : 0;
             sum_n += n[i], sum += v[i];
         }
         const int at_n = cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n);
@@ -560,7 +590,7 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
                     const int64_t step = ((to - from) >> 5) + 1, probe = from + step * (lane + 1);
                     bool reached = true;
                     if (probe < to) {
-                        const float r = fmaf(job.m - key_value(static_cast<uint32_t>(probe)), ch, kMagic);
+                        const float r = fmaf(job.m - Key<F32>::value(static_cast<uint32_t>(probe)), ch, kMagic);
                         reached = static_cast<int>(__float_as_uint(r) - kMagicBits) <= bin - warp;
                     }
                     const int k = __ffs(__ballot_sync(0xffffffffu, reached)) - 1;  // the last probe is past the end
@@ -573,7 +603,7 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
             if (tid == 0) {
                 sh.range.lo = sh.warp_key[0];
                 sh.range.hi = sh.warp_key[1] - 1;
-                sh.range = tidy(sh.range);
+                sh.range = tidy<F32>(sh.range);
             }
         } else if (tid == 0) {
             sh.range.none = 1;
@@ -584,47 +614,48 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
 }
 
 // By block, the mass of the tokens above value `hi`; and the tokens from `lo` to
-// it: gathered in the first CTA's list, or, one value, counted by block.
+// it: gathered in this CTA's list, or, one value, counted by block.
 template <bool F32, int TH>
 __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, uint32_t lo, uint32_t hi, bool gather) {
+    constexpr int NV = Row<F32>::NV, VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const float least = key_value(lo), most = key_value(hi);
+    const float least = Key<F32>::value(lo), most = Key<F32>::value(hi);
     for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
         const uint32_t key = sh.block_key[b];
         float s = 0.0f;
         int n = 0;
         if (key >= lo) {
-            uint4 w[Row<F32>::NV];
+            uint4 w[NV];
             row.load(b, w);
             if (key > hi) s = block_sum<F32, false>(w, key, job.c, most);
+            uint32_t in = 0;  // bit i * VE + j: vector i's element j is in the range
 #pragma unroll
-            for (int i = 0; i < Row<F32>::NV; ++i) {
-                float x[Row<F32>::VE];
+            for (int i = 0; i < NV; ++i) {
+                float x[VE];
                 Row<F32>::unpack(w[i], x);
 #pragma unroll
-                for (int j = 0; j < Row<F32>::VE; ++j) {
-                    if (x[j] >= least && x[j] <= most) {
-                        ++n;
-                        if (gather) {
-                            const int id = b * kBlock + (lane + 32 * i) * Row<F32>::VE + j;
-                            const uint32_t at = job.splits > 1 ? dsmem_next(&sh.listed, 0, 1)
-                                                               : static_cast<uint32_t>(atomicAdd(&sh.listed, 1));
-                            if (at < kGather) {
-                                if (job.splits > 1) {
-                                    dsmem_put(&sh.list_key[at], 0, order_key(x[j]));
-                                    dsmem_put(&sh.list_id[at], 0, static_cast<uint32_t>(id));
-                                } else {
-                                    sh.list_key[at] = order_key(x[j]);
-                                    sh.list_id[at] = id;
-                                }
-                            }
+                for (int j = 0; j < VE; ++j) in |= x[j] >= least && x[j] <= most ? 1u << (i * VE + j) : 0u;
+            }
+            n = __popc(in);
+            if (gather) {
+                if (__any_sync(0xffffffffu, n > 0)) {
+                    const int upto = warp_inclusive(n);
+                    int at = 0;
+                    if (lane == 31) at = atomicAdd(&sh.listed, upto);
+                    at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
+                    for (; in; in &= in - 1, ++at) {
+                        const int k = __ffs(in) - 1, id = b * kBlock + (lane + 32 * (k / VE)) * VE + k % VE;
+                        if (at < kGather) {
+                            sh.list_key[at] = Key<F32>::of(row.at(id));
+                            sh.list_id[at] = id;
                         }
                     }
                 }
+            } else {
+                n = __reduce_add_sync(0xffffffffu, n);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (!gather) n = __reduce_add_sync(0xffffffffu, n);
         }
         if (lane == 0) {
             sh.block_mass[b] = __float_as_uint(s);
@@ -634,14 +665,29 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
     __syncthreads();
 }
 
-// sh.block_mass from sums relative to the block's largest logit to units of the row's.
+// The CTAs' lists into the first one's, behind one another.
 template <int TH>
+__device__ __forceinline__ void hand_over_list(const Job &job, Shared<TH> &sh) {
+    if (job.splits > 1 && job.part != 0) {
+        const int n = min(sh.listed, kGather);
+        if (threadIdx.x == 0 && n > 0) sh.drawn = static_cast<int>(dsmem_next(&sh.collected, 0, n));
+        __syncthreads();
+        if (n > 0)
+            for (int i = threadIdx.x; i < n && sh.drawn + i < kGather; i += TH) {
+                dsmem_put(&sh.list_key[sh.drawn + i], 0, sh.list_key[i]);
+                dsmem_put(&sh.list_id[sh.drawn + i], 0, sh.list_id[i]);
+            }
+    }
+}
+
+// sh.block_mass from sums relative to the block's largest logit to units of the row's.
+template <bool F32, int TH>
 __device__ __forceinline__ uint64_t weigh_blocks(const Job &job, Shared<TH> &sh) {
     uint64_t mine = 0;
     for (int b = job.b0 + threadIdx.x; b < job.b1; b += TH) {
         const float s = __uint_as_float(static_cast<uint32_t>(sh.block_mass[b]));
         uint64_t v = 0;
-        if (s > 0.0f) v = fixed(mul(weight(key_value(sh.block_key[b]), job.m, job.c), Two{s, 0.0f}), kUnit);
+        if (s > 0.0f) v = fixed(mul(weight(Key<F32>::value(sh.block_key[b]), job.m, job.c), Two{s, 0.0f}), kUnit);
         sh.block_mass[b] = v;
         mine += v;
     }
@@ -663,13 +709,13 @@ __device__ __forceinline__ void hand_over_blocks(const Job &job, Shared<TH> &sh)
 }
 
 // The list's tokens whose keys are in sh.range, down to one value.  By the first CTA.
-template <int TH>
+template <bool F32, int TH>
 __device__ void search_list(const Job &job, Shared<TH> &sh, const Target &target) {
     constexpr int kBits = 20;  // kGather residuals of 2^20 fit 32 bits
     while (sh.range.lo != sh.range.hi) {
         const uint32_t lo = sh.range.lo, hi = sh.range.hi;
         const int shift = fine_shift(lo, hi), n = min(sh.listed, kGather);
-        const float top = key_value(hi);
+        const float top = Key<F32>::value(hi);
         for (int i = threadIdx.x; i < kFine; i += TH) sh.fine_n[i] = sh.fine_q[i] = 0;
         __syncthreads();
         for (int i = threadIdx.x; i < n; i += TH) {
@@ -677,11 +723,11 @@ __device__ void search_list(const Job &job, Shared<TH> &sh, const Target &target
             if (key >= lo && key <= hi) {
                 const uint32_t bin = (hi - key) >> shift;
                 atomicAdd(&sh.fine_n[bin], 1u);
-                atomicAdd(&sh.fine_q[bin], fine_rest(top, key_value(key), job.c, static_cast<float>(1 << (5 + kBits))));
+                atomicAdd(&sh.fine_q[bin], fine_rest(top, Key<F32>::value(key), job.c, static_cast<float>(1 << (5 + kBits))));
             }
         }
         __syncthreads();
-        narrow(job, sh, target, shift, kBits);
+        narrow<F32>(job, sh, target, shift, kBits);
     }
 }
 
@@ -695,7 +741,7 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
     while (!listed && sh.range.equals > kGather && sh.range.lo != sh.range.hi) {
         const uint32_t lo = sh.range.lo, hi = sh.range.hi;
         const int shift = fine_shift(lo, hi);
-        const float top = key_value(hi), least = key_value(lo);
+        const float top = Key<F32>::value(hi), least = Key<F32>::value(lo);
         __syncthreads();
         for (int i = tid; i < kFine; i += TH) sh.fine_n[i] = sh.fine_q[i] = 0;
         __syncthreads();
@@ -709,7 +755,7 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
                 Row<F32>::unpack(w[i], x);
                 for (int j = 0; j < Row<F32>::VE; ++j)
                     if (x[j] >= least && x[j] <= top) {
-                        const uint32_t bin = (hi - order_key(x[j])) >> shift;
+                        const uint32_t bin = (hi - Key<F32>::of(x[j])) >> shift;
                         atomicAdd(&sh.fine_n[bin], 1u);
                         atomicAdd(&sh.fine_q[bin], fine_rest(top, x[j], job.c, static_cast<float>(1 << (5 + job.bits))));
                     }
@@ -717,23 +763,29 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
         }
         __syncthreads();
         collect<TH>(job, sh.fine_n, sh.fine_q, kFine);
-        if (job.part == 0) narrow(job, sh, target, shift, job.bits);
+        if (job.part == 0) narrow<F32>(job, sh, target, shift, job.bits);
         share_range(job, sh);
     }
     if (!listed && sh.range.lo != sh.range.hi) {
         list = sh.range;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        if (job.splits > 1) cluster_sync_all();
         sum_blocks<F32, TH>(row, job, sh, list.lo, list.hi, true);
-        weigh_blocks(job, sh);
+        if (job.splits > 1) {
+            if (tid == 0) sh.collected = sh.listed;  // the first CTA's own come first
+            cluster_sync_all();
+            hand_over_list(job, sh);
+        }
+        weigh_blocks<F32>(job, sh);
         hand_over_blocks(job, sh);
+        if (job.splits > 1 && job.part == 0 && tid == 0) sh.listed = sh.collected;
+        __syncthreads();
     }
     if (job.part == 0) {
-        search_list(job, sh, target);
+        search_list<F32>(job, sh, target);
         __syncthreads();
         if (tid == 0) {
-            const uint64_t w = fixed(weight(key_value(sh.range.lo), job.m, job.c), kUnit);
+            const uint64_t w = fixed(weight(Key<F32>::value(sh.range.lo), job.m, job.c), kUnit);
             int kept = target.count - sh.range.count;
             if (target.by_mass) {
                 const uint64_t miss = target.mass > sh.range.mass ? target.mass - sh.range.mass : 0;
@@ -752,6 +804,7 @@ template <bool F32, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs a, int splits) {
     extern __shared__ uint4 sample_smem[];
     Shared<TH> &sh = *reinterpret_cast<Shared<TH> *>(sample_smem);
+    using K = Key<F32>;
     constexpr int kWarps = TH / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / splits;
@@ -773,15 +826,16 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     const bool greedy = temperature == 0.0f;
     bool bad = !(greedy || (temperature >= 1e-30f && temperature <= 1e30f)) || top_p != top_p || min_p != min_p;
     job.c = div(Two{0x1.715476p+0f, 0x1.4ae0cp-26f}, Two{greedy || bad ? 1.0f : temperature, 0.0f});
+    if (tid < 32) sh.bin_weight[tid] = kBinWeight[tid];
     if (min_p > 0.0f && tid == TH - 1) sh.log_min_p = log(static_cast<double>(fminf(min_p, 1.0f)));
 
     // ---- the blocks' largest logits and their masses relative to those
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
         uint4 w[Row<F32>::NV];
         row.load(b, w);
-        const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(Row<F32>::most(w)));
+        const uint32_t key = __reduce_max_sync(0xffffffffu, K::of(Row<F32>::most(w)));
         float s = 0.0f;
-        if (key > kKeyNegInf && key < kKeyInf && !greedy) s = block_sum<F32, true>(w, key, job.c, 0.0f);
+        if (key > K::kNegInf && key < K::kInf && !greedy) s = block_sum<F32, true>(w, key, job.c, 0.0f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) {
@@ -804,9 +858,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         for (int i = 0; i < splits; ++i) key = max(key, sh.part_key[i]);
     }
     job.m_key = key;
-    job.m = key_value(key);
-    bad = bad || key >= kKeyInf;
-    if (bad || key == kKeyNegInf) {  // the same in all of the row's CTAs
+    job.m = K::value(key);
+    bad = bad || key >= K::kInf;
+    if (bad || key == K::kNegInf) {  // the same in all of the row's CTAs
         if (job.part == 0 && tid == 0) {
             a.tokens[r] = -1;
             if (a.logprobs) a.logprobs[r] = 0.0f;
@@ -814,13 +868,13 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         }
         return;
     }
-    job.lowest = max(order_key(job.m - kWindow / job.c.h), kKeyNegInf + 1);
+    job.lowest = max(K::from(job.m - kWindow / job.c.h), K::kNegInf + 1);
     int log_v = 0;
     while ((1 << log_v) < vocab) ++log_v;
     job.bits = min(32 - log_v, 18);
 
     // ---- the cut: tokens above its value are kept, and `ties` equal to it
-    uint32_t cut = kKeyNegInf;
+    uint32_t cut = K::kNegInf;
     int ties = 0;
     Range list{1, 0, 0, 0, 0, 0, 0};
     const bool by_p = top_p < 1.0f, by_k = top_k < vocab;
@@ -829,7 +883,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         ties = 1;
     } else if (by_p || by_k) {
         uint64_t whole = 0;  // the mass that top_p is a share of; the first CTA's counts
-        const uint64_t mine = weigh_blocks(job, sh);
+        const uint64_t mine = weigh_blocks<F32>(job, sh);
         cta_exclusive<uint64_t, TH>(mine, sh.warp_sum, whole);
         if (splits > 1 && tid == 0) dsmem_put(&sh.part_mass[job.part], 0, whole);
         count_exponents<F32, TH>(row, job, sh);
@@ -839,7 +893,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         }
         if (by_k) {
             const Target target{false, top_k, 0};
-            find_exponent(job, sh, target);
+            find_exponent<F32>(job, sh, target);
             if (!sh.range.none) {
                 find_cut<F32, TH>(row, job, sh, target, list);
                 cut = sh.range.lo;
@@ -851,7 +905,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         if (by_p) {
             const uint64_t share = __float2ull_rz(fmaxf(top_p, 0.0f) * 0x1p64f);
             const Target target{true, 0, at_least_one(__umul64hi(whole, share) + (whole * share != 0 ? 1 : 0))};
-            find_exponent(job, sh, target);
+            find_exponent<F32>(job, sh, target);
             if (!sh.range.none) {
                 find_cut<F32, TH>(row, job, sh, target, list);
                 if (sh.range.lo > cut || (sh.range.lo == cut && sh.range.equals < ties)) cut = sh.range.lo, ties = sh.range.equals;
@@ -859,26 +913,26 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             }
         }
     } else if (min_p <= 0.0f) {
-        weigh_blocks(job, sh);
+        weigh_blocks<F32>(job, sh);
         __syncthreads();
         hand_over_blocks(job, sh);
     }
     if (min_p > 0.0f && !greedy) {
         // the least value whose weight is min_p or more
-        const uint32_t k = order_key(__double2float_ru(job.m + temperature * sh.log_min_p));
+        const uint32_t k = K::from(__double2float_ru(job.m + temperature * sh.log_min_p));
         if (k > cut) cut = k, ties = 0x7FFFFFFF;
     }
-    const bool filtered = cut > kKeyNegInf;
-    const float cut_value = key_value(cut);
+    const bool filtered = cut > K::kNegInf;
+    const float cut_value = K::value(cut);
     const bool in_list = list.lo <= cut && cut <= list.hi;
     if (filtered && !in_list) {
         sum_blocks<F32, TH>(row, job, sh, cut, cut, false);
-        weigh_blocks(job, sh);
+        weigh_blocks<F32>(job, sh);
         __syncthreads();
         hand_over_blocks(job, sh);
     } else if (!filtered && (by_p || by_k)) {  // neither took a token away
-        sum_blocks<F32, TH>(row, job, sh, kKeyNegInf + 1, kKeyNegInf, false);
-        weigh_blocks(job, sh);
+        sum_blocks<F32, TH>(row, job, sh, K::kNegInf + 1, K::kNegInf, false);
+        weigh_blocks<F32>(job, sh);
         __syncthreads();
         hand_over_blocks(job, sh);
     }
@@ -889,54 +943,69 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             const uint32_t k = sh.list_key[i], b = sh.list_id[i] / kBlock;
             if (k > cut)
                 atomicAdd(reinterpret_cast<unsigned long long *>(&sh.block_mass[b]),
-                          static_cast<unsigned long long>(fixed(weight(key_value(k), job.m, job.c), kUnit)));
+                          static_cast<unsigned long long>(fixed(weight(K::value(k), job.m, job.c), kUnit)));
             else if (k == cut) atomicAdd(&sh.block_equals[b], 1);
         }
         __syncthreads();
     }
     // ---- the block
     const float u0 = fminf(fmaxf(a.u[2 * r], 0.0f), 1.0f), u1 = fminf(fmaxf(a.u[2 * r + 1], 0.0f), 1.0f);
-    if (warp == 0) {
+    {
+        constexpr int kPer = kMaxBlocks / TH;
         const uint64_t cut_weight = filtered ? fixed(weight(cut_value, job.m, job.c), kUnit) : 0;
-        const int per = (job.blocks + 31) / 32, first = lane * per, end = min(first + per, job.blocks);
-        int n = 0;
-        for (int b = first; b < end; ++b) n += sh.block_equals[b];
-        int seen = warp_inclusive(n) - n;
-        uint64_t sum = 0;
-        for (int b = first; b < end; ++b) {
-            const int e = sh.block_equals[b], keep = min(max(ties - seen, 0), e);
-            seen += e;
-            const uint64_t v = sh.block_mass[b] + cut_weight * static_cast<uint64_t>(keep);
-            sh.block_mass[b] = v;
-            sh.block_equals[b] = keep;
-            sum += v;
+        const int first = tid * kPer;
+        int n[kPer], sum_n = 0, all_n;
+        uint64_t v[kPer], sum = 0, all;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            n[i] = first + i < job.blocks ? sh.block_equals[first + i] : 0;
+            v[i] = first + i < job.blocks ? sh.block_mass[first + i] : 0;
+            sum_n += n[i];
         }
-        const uint64_t upto = warp_inclusive(sum), all = __shfl_sync(0xffffffffu, upto, 31), target = part_of(all, u0);
-        uint64_t at = upto - sum;
-        int hit = -1, last = -1;
-        for (int b = first; b < end; ++b) {
-            const uint64_t v = sh.block_mass[b];
-            at += v;
-            if (v > 0) {
-                last = b;
-                if (hit < 0 && at > target) hit = b;
-            }
+        int seen = filtered ? cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n) : 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int keep = min(max(ties - seen, 0), n[i]);
+            seen += n[i];
+            n[i] = keep;
+            v[i] += cut_weight * static_cast<uint64_t>(keep);
+            sum += v[i];
         }
-        const uint32_t have = __ballot_sync(0xffffffffu, hit >= 0);
-        last = __reduce_max_sync(0xffffffffu, last);
-        hit = have ? __shfl_sync(0xffffffffu, hit, __ffs(have) - 1) : last;
-        if (lane == 0) {
-            sh.block = hit;
-            sh.allowed = sh.block_equals[hit];
+        uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
+        const uint64_t target = part_of(all, u0);
+        if (tid == 0) {
             sh.total = all;
             sh.drawn = 0x7FFFFFFF;
-            sh.last = -1;
+            sh.last = sh.block = -1;
+        }
+        __syncthreads();
+        int last = -1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (v[i] > 0) {
+                if (at <= target && at + v[i] > target) {  // one block at most
+                    sh.block = first + i;
+                    sh.allowed = n[i];
+                }
+                last = first + i;
+            }
+            at += v[i];
+        }
+        if (u0 >= 1.0f) {  // past the last: it
+            last = __reduce_max_sync(0xffffffffu, last);
+            if (lane == 0 && last >= 0) atomicMax(&sh.last, last);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (first + i == sh.last) sh.block = first + i, sh.allowed = n[i];
+            __syncthreads();
+            if (tid == 0) sh.last = -1;
         }
     }
     __syncthreads();
     // ---- the token: weights relative to the block's largest logit, which is kept if any of the block is
     constexpr int kPer = kBlock / TH;
-    const float block_m = key_value(sh.block_key[sh.block]);
+    const float block_m = K::value(sh.block_key[sh.block]);
     const int e0 = sh.block * kBlock + tid * kPer;
     float x[kPer];
     int eq = 0;
