@@ -212,6 +212,15 @@ struct Row {
             }
         }
     }
+    // The largest of a vector's elements, none of which is NaN.
+    static __device__ __forceinline__ float largest(const uint4 v) {
+        if constexpr (F32) {
+            return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+        } else {
+            const uint32_t m = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
+            return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
+        }
+    }
     // The largest of a lane's elements; NaN if there is one.
     static __device__ __forceinline__ float most(const uint4 (&w)[NV]) {
         if constexpr (F32) {
@@ -237,7 +246,7 @@ struct Range {
     uint32_t lo, hi;
     int count, equals;
     uint64_t mass;
-    int none;      // there is no cut: every token is kept
+    int none;      // not 0: there is no cut
     int pad;
 };
 
@@ -251,10 +260,10 @@ struct Shared {
     uint32_t fine_n[kFine], fine_q[kFine];
     uint32_t list_key[kGather], list_id[kGather];
     Range range, inbox[2];
-    uint64_t warp_sum[kWarps], part_mass[kMaxSplit], total;
+    uint64_t warp_sum[kWarps], part_mass[kMaxSplit], part_in[kMaxSplit], total;
     double log_min_p;
     int warp_int[kWarps];
-    uint32_t warp_key[kWarps], part_key[kMaxSplit];
+    uint32_t warp_key[kWarps], part_key[kMaxSplit], part_bound[kMaxSplit], bound;
     uint64_t bin_weight[32];          // kBinWeight: lanes ask for different ones
     int listed, collected, drawn, last, block, allowed;
 };
@@ -508,92 +517,169 @@ __device__ __forceinline__ void collect(const Job &job, uint32_t *n, uint32_t *q
     }
 }
 
-// One token more in the bin at shared address `at`, of residual q.
+// What a row's histogram has to tell.  Two atomics a token where both are wanted;
+// for masses alone one does, a token's weight beside its bin's in units of 2^-20.
+// 4000 tokens of a bin fit 32 bits so, and if more wrap (rows of equals, far
+// temperatures) the bins do not add up to what went in: then both are counted.
+enum Counting : int { kCounts = 1, kMasses = 2, kBoth = 3 };
+constexpr int kMassBits = 20;
+
+template <int MODE>
 __device__ __forceinline__ void count_one(uint32_t at, uint32_t q) {
-    asm volatile("red.shared.add.u32 [%0], 1;\n\tred.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4)
-                 : "memory");
+    if constexpr (MODE == kCounts) {
+        asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(at) : "memory");
+    } else if constexpr (MODE == kMasses) {
+        asm volatile("red.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4) : "memory");
+    } else {
+        asm volatile("red.shared.add.u32 [%0], 1;\n\tred.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4)
+                     : "memory");
+    }
 }
 
 // The histogram of the row's exponents, in the first CTA's n and q.
-template <bool F32, int TH>
+template <bool F32, int TH, int MODE>
 __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> &sh) {
-    const int tid = threadIdx.x, warp = tid >> 5;
+    constexpr int NV = Row<F32>::NV, VE = Row<F32>::VE;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
     __syncthreads();
     const float least = Key<F32>::value(job.lowest), m = job.m;
-    // d = m - x; bin = round(32 c d), f the rest in [-1/2, 1/2]; weight / bin's = 2^(-f / 32), less 63/64, in units of
-    // 2^-(5 + bits): below 2^bits.  The low bits of r are the bin, those of q the units
-    const float unit = static_cast<float>(1 << (5 + job.bits)), y = kLn2 / kPerUnit;
+    // d = m - x; bin = round(32 c d), f the rest in [-1/2, 1/2]; weight / bin's = 2^(-f / 32), with the counts less 63/64
+    // and in units of 2^-(5 + bits): below 2^bits.  The low bits of r are the bin, those of q the units
+    const float unit = static_cast<float>(1 << (MODE == kMasses ? kMassBits : 5 + job.bits)), y = kLn2 / kPerUnit;
+    const float whole = (MODE == kMasses ? unit : unit / 64.0f) + 0x1p23f;
     const uint64_t m2 = pair(m, m), minus = pair(-1.0f, -1.0f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
     const float chf = job.c.h * kPerUnit, clf = job.c.l * kPerUnit;
     const uint64_t ch = pair(chf, chf), cl = pair(clf, clf);
-    const uint64_t q0 = pair(unit / 64.0f + 0x1p23f, unit / 64.0f + 0x1p23f), q1 = pair(-unit * y, -unit * y);
+    const uint64_t q0 = pair(whole, whole), q1 = pair(-unit * y, -unit * y);
     const uint64_t q2 = pair(unit * y * y / 2.0f, unit * y * y / 2.0f);
     const uint64_t q3 = pair(-unit * y * y * y / 6.0f, -unit * y * y * y / 6.0f);
     const uint32_t base = smem_u32(sh.n) - (kMagicBits << 2);
+    uint64_t went_in = 0;
     for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
         if (sh.block_key[b] < job.lowest) continue;
-        uint4 w[Row<F32>::NV];
+        uint4 w[NV];
         row.load(b, w);
+        uint32_t sum = 0;  // 32 tokens of 2^20 and a hundredth more
 #pragma unroll
-        for (int i = 0; i < Row<F32>::NV; ++i) {
-            float x[Row<F32>::VE];
+        for (int i = 0; i < NV; ++i) {
+            if (Row<F32>::largest(w[i]) < least) continue;
+            float x[VE];
             Row<F32>::unpack(w[i], x);
 #pragma unroll
-            for (int j = 0; j < Row<F32>::VE; j += 2) {
+            for (int j = 0; j < VE; j += 2) {
                 const uint64_t d = fma2(pair(x[j], x[j + 1]), minus, m2), r = fma2(d, ch, magic);
-                const uint64_t n = add2(r, unmagic);
-                // 32 c d - n: the product's difference is exact but for one rounding
-                const uint64_t f = fma2(d, cl, fma2(d, ch, mul2(n, minus)));
-                const uint64_t q = fma2(f, fma2(f, fma2(f, q3, q2), q1), q0);
-                float r0, r1, u0, u1;
+                float r0, r1, u0 = 0.0f, u1 = 0.0f;
                 unpair(r, r0, r1);
-                unpair(q, u0, u1);
-                if (x[j] >= least) count_one(base + (__float_as_uint(r0) << 2), __float_as_uint(u0) & 0x7FFFFFu);
-                if (x[j + 1] >= least) count_one(base + (__float_as_uint(r1) << 2), __float_as_uint(u1) & 0x7FFFFFu);
+                if constexpr (MODE != kCounts) {
+                    const uint64_t n = add2(r, unmagic);
+                    // 32 c d - n: the product's difference is exact but for one rounding
+                    const uint64_t f = fma2(d, cl, fma2(d, ch, mul2(n, minus)));
+                    unpair(fma2(f, fma2(f, fma2(f, q3, q2), q1), q0), u0, u1);
+                }
+                const uint32_t v0 = __float_as_uint(u0) & 0x7FFFFFu, v1 = __float_as_uint(u1) & 0x7FFFFFu;
+                if (x[j] >= least) {
+                    count_one<MODE>(base + (__float_as_uint(r0) << 2), v0);
+                    sum += v0;
+                }
+                if (x[j + 1] >= least) {
+                    count_one<MODE>(base + (__float_as_uint(r1) << 2), v1);
+                    sum += v1;
+                }
             }
         }
+        went_in += sum;
+    }
+    if constexpr (MODE == kMasses) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) went_in += __shfl_xor_sync(0xffffffffu, went_in, o);
+        if (lane == 0) sh.warp_sum[warp] = went_in;
     }
     __syncthreads();
-    collect<TH>(job, sh.n, sh.q, kBins);
+    if constexpr (MODE == kMasses) {
+        if (tid == 0) {
+            went_in = 0;
+            for (int i = 0; i < TH / 32; ++i) went_in += sh.warp_sum[i];
+            if (job.splits > 1) dsmem_put(&sh.part_in[job.part], 0, went_in);
+            else sh.part_in[0] = went_in;
+        }
+    }
+    if (job.splits > 1) {
+        cluster_sync_all();
+        if (job.part != 0)
+            for (int i = tid; i < kBins; i += TH) {
+                if (MODE != kMasses && sh.n[i]) dsmem_add(&sh.n[i], 0, sh.n[i]);
+                if (MODE != kCounts && sh.q[i]) dsmem_add(&sh.q[i], 0, sh.q[i]);
+            }
+        cluster_sync_all();
+    }
 }
 
 // The range of values of the exponents' bin that holds the target: sh.range, the
-// same in all the row's CTAs; none if all the bins together do not reach it.
+// same in all the row's CTAs; `none` is 1 if all the bins together do not reach
+// it, 2 if masses alone did not fit their bins.
 template <bool F32, int TH>
-__device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
+__device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target, int mode) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (job.part == 0) {
         constexpr int kPer = kBins / TH;
         int n[kPer], sum_n = 0, all_n;
-        uint64_t v[kPer], sum = 0, all;
+        uint64_t v[kPer], sum = 0, all, in_bins = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int bin = tid * kPer + i;
-            n[i] = static_cast<int>(sh.n[bin]);
-            const uint64_t units = static_cast<uint64_t>(n[i]) * (63u << (job.bits - 1)) + sh.q[bin];
-            v[i] = n[i] ? __umul64hi(units << (38 - job.bits), sh.bin_weight[bin & 31] >> (bin >> 5)) : 0;
+            const uint32_t q = sh.q[bin];
+            const uint64_t w = sh.bin_weight[bin & 31] >> (bin >> 5);
+            if (mode == kMasses) {
+                n[i] = static_cast<int>(q / ((1u << kMassBits) * 63 / 64)) + (q > 0 ? 1 : 0);  // no fewer than there are
+                v[i] = __umul64hi(static_cast<uint64_t>(q) << (43 - kMassBits), w);
+                in_bins += q;
+            } else {
+                n[i] = static_cast<int>(sh.n[bin]);
+                const uint64_t units = static_cast<uint64_t>(n[i]) * (63u << (job.bits - 1)) + q;
+                v[i] = n[i] && mode == kBoth ? __umul64hi(units << (38 - job.bits), w) : 0;
+            }
             sum_n += n[i], sum += v[i];
         }
         const int at_n = cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n);
         const uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
-        const bool found = find_bin<false, kPer, TH>(n, v, at_n, at, target, sh, [&](int i, int before_n, uint64_t before) {
-            sh.range = Range{static_cast<uint32_t>(tid * kPer + i), 0, before_n, n[i], before, 0, 0};
-        });
+        bool wrapped = false;
+        if (mode == kMasses) {
+            cta_exclusive<uint64_t, TH>(in_bins, sh.warp_sum, all);
+            uint64_t went_in = 0;
+            for (int i = 0; i < job.splits; ++i) went_in += sh.part_in[i];
+            wrapped = all != went_in;
+        }
+        bool found = false;
+        if (!wrapped)
+            found = find_bin<false, kPer, TH>(n, v, at_n, at, target, sh, [&](int i, int before_n, uint64_t before) {
+                sh.range = Range{static_cast<uint32_t>(tid * kPer + i), 0, before_n, n[i], before, 0, 0};
+            });
         if (found) {
             // the bin's least value (warp 0) and the next bin's above it (warp 1): the bins' numbers fall as values rise
             const float ch = job.c.h * kPerUnit;
             const int bin = static_cast<int>(sh.range.lo);
             if (warp < 2) {
+                const int want = bin - warp;
+                auto reached = [&](int64_t key) {
+                    const float r = fmaf(job.m - Key<F32>::value(static_cast<uint32_t>(key)), ch, kMagic);
+                    return static_cast<int>(__float_as_uint(r) - kMagicBits) <= want;
+                };
                 int64_t from = static_cast<int64_t>(job.lowest) - 1, to = static_cast<int64_t>(job.m_key) + 1;  // in (from, to]
+                {
+                    // most often it is near where the numbers say
+                    const int64_t guess = Key<F32>::of(job.m - (want + 0.5f) / ch);
+                    const int64_t probe = guess - 16 + lane;
+                    const bool yes = probe >= to || (probe > from && reached(probe));
+                    const uint32_t votes = __ballot_sync(0xffffffffu, yes);
+                    if (votes & 1u) to = min(to, max(guess - 16, from + 1));
+                    else if (votes) to = min(to, guess - 16 + (__ffs(votes) - 1)), from = max(from, to - 1);
+                    else from = max(from, guess + 15);
+                }
                 while (to - from > 1) {
                     const int64_t step = ((to - from) >> 5) + 1, probe = from + step * (lane + 1);
-                    bool reached = true;
-                    if (probe < to) {
-                        const float r = fmaf(job.m - Key<F32>::value(static_cast<uint32_t>(probe)), ch, kMagic);
-                        reached = static_cast<int>(__float_as_uint(r) - kMagicBits) <= bin - warp;
-                    }
-                    const int k = __ffs(__ballot_sync(0xffffffffu, reached)) - 1;  // the last probe is past the end
+                    const bool yes = probe >= to || reached(probe);
+                    const int k = __ffs(__ballot_sync(0xffffffffu, yes)) - 1;  // the last probe is past the end
                     to = min(to, from + step * (k + 1));
                     from += step * k;
                 }
@@ -606,7 +692,7 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target) {
                 sh.range = tidy<F32>(sh.range);
             }
         } else if (tid == 0) {
-            sh.range.none = 1;
+            sh.range.none = wrapped ? 2 : 1;
         }
         __syncthreads();
     }
@@ -805,7 +891,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     extern __shared__ uint4 sample_smem[];
     Shared<TH> &sh = *reinterpret_cast<Shared<TH> *>(sample_smem);
     using K = Key<F32>;
-    constexpr int kWarps = TH / 32;
+    constexpr int kWarps = TH / 32, kBoundShift = F32 ? 21 : 5;  // keys to kBins
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / splits;
     Job job;
@@ -829,11 +915,18 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     if (tid < 32) sh.bin_weight[tid] = kBinWeight[tid];
     if (min_p > 0.0f && tid == TH - 1) sh.log_min_p = log(static_cast<double>(fminf(min_p, 1.0f)));
 
+    const bool by_p = top_p < 1.0f, by_k = top_k < vocab && top_k > 1 && !greedy && !bad;
+    if (by_k) {
+        for (int i = tid; i < kBins; i += TH) sh.n[i] = 0;
+        if (tid == 0) sh.bound = 0;
+        __syncthreads();
+    }
     // ---- the blocks' largest logits and their masses relative to those
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
         uint4 w[Row<F32>::NV];
         row.load(b, w);
-        const uint32_t key = __reduce_max_sync(0xffffffffu, K::of(Row<F32>::most(w)));
+        const uint32_t lane_key = K::of(Row<F32>::most(w)), key = __reduce_max_sync(0xffffffffu, lane_key);
+        if (by_k) atomicAdd(&sh.n[lane_key >> kBoundShift], 1u);
         float s = 0.0f;
         if (key > K::kNegInf && key < K::kInf && !greedy) s = block_sum<F32, true>(w, key, job.c, 0.0f);
 #pragma unroll
@@ -851,11 +944,31 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     if (lane == 0) sh.warp_key[warp] = key;
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) key = max(key, sh.warp_key[i]);
+    uint32_t bound = 0;
+    if (by_k) {
+        // the top_k-th largest of the lanes' largest is no larger than the top_k-th of all: the least of its bin
+        constexpr int kPer = kBins / TH;
+        int n[kPer], sum = 0, all;
+        uint64_t none[kPer] = {};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) n[i] = static_cast<int>(sh.n[kBins - 1 - (tid * kPer + i)]), sum += n[i];
+        const int at = cta_exclusive<int, TH>(sum, sh.warp_int, all);
+        find_bin<false, kPer, TH>(n, none, at, 0, Target{false, top_k, 0}, sh, [&](int i, int, uint64_t) {
+            sh.bound = static_cast<uint32_t>(kBins - 1 - (tid * kPer + i)) << kBoundShift;
+        });
+        bound = sh.bound;
+    }
     if (splits > 1) {
         cluster_wait();
-        if (tid < splits) dsmem_put(&sh.part_key[job.part], tid, key);
+        if (tid < splits) {
+            dsmem_put(&sh.part_key[job.part], tid, key);
+            dsmem_put(&sh.part_bound[job.part], tid, bound);
+        }
         cluster_sync_all();
-        for (int i = 0; i < splits; ++i) key = max(key, sh.part_key[i]);
+        for (int i = 0; i < splits; ++i) {
+            key = max(key, sh.part_key[i]);
+            bound = max(bound, sh.part_bound[i]);
+        }
     }
     job.m_key = key;
     job.m = K::value(key);
@@ -868,16 +981,13 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         }
         return;
     }
-    job.lowest = max(K::from(job.m - kWindow / job.c.h), K::kNegInf + 1);
-    int log_v = 0;
-    while ((1 << log_v) < vocab) ++log_v;
-    job.bits = min(32 - log_v, 18);
+    job.lowest = max(max(K::from(job.m - kWindow / job.c.h), K::kNegInf + 1), bound);
+    job.bits = min(32 - (vocab > 1 ? 32 - __clz(vocab - 1) : 0), 18);  // 2^bits residuals of `vocab` tokens fit 32 bits
 
     // ---- the cut: tokens above its value are kept, and `ties` equal to it
     uint32_t cut = K::kNegInf;
     int ties = 0;
     Range list{1, 0, 0, 0, 0, 0, 0};
-    const bool by_p = top_p < 1.0f, by_k = top_k < vocab;
     if (greedy || top_k == 1) {
         cut = job.m_key;
         ties = 1;
@@ -886,14 +996,17 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         const uint64_t mine = weigh_blocks<F32>(job, sh);
         cta_exclusive<uint64_t, TH>(mine, sh.warp_sum, whole);
         if (splits > 1 && tid == 0) dsmem_put(&sh.part_mass[job.part], 0, whole);
-        count_exponents<F32, TH>(row, job, sh);
+        int mode = !by_k ? kMasses : by_p ? kBoth : kCounts;
+        if (mode == kMasses) count_exponents<F32, TH, kMasses>(row, job, sh);
+        else if (mode == kBoth) count_exponents<F32, TH, kBoth>(row, job, sh);
+        else count_exponents<F32, TH, kCounts>(row, job, sh);
         if (splits > 1) {
             whole = 0;
             for (int i = 0; i < splits; ++i) whole += sh.part_mass[i];
         }
         if (by_k) {
             const Target target{false, top_k, 0};
-            find_exponent<F32>(job, sh, target);
+            find_exponent<F32>(job, sh, target, mode);
             if (!sh.range.none) {
                 find_cut<F32, TH>(row, job, sh, target, list);
                 cut = sh.range.lo;
@@ -905,7 +1018,12 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         if (by_p) {
             const uint64_t share = __float2ull_rz(fmaxf(top_p, 0.0f) * 0x1p64f);
             const Target target{true, 0, at_least_one(__umul64hi(whole, share) + (whole * share != 0 ? 1 : 0))};
-            find_exponent<F32>(job, sh, target);
+            find_exponent<F32>(job, sh, target, mode);
+            if (sh.range.none == 2) {
+                count_exponents<F32, TH, kBoth>(row, job, sh);
+                mode = kBoth;
+                find_exponent<F32>(job, sh, target, mode);
+            }
             if (!sh.range.none) {
                 find_cut<F32, TH>(row, job, sh, target, list);
                 if (sh.range.lo > cut || (sh.range.lo == cut && sh.range.equals < ties)) cut = sh.range.lo, ties = sh.range.equals;
