@@ -26,6 +26,7 @@
 #include "serving.cuh"
 #include "internal.h"
 
+#include <cstddef>
 #include <mutex>
 
 namespace fp8bs {
@@ -113,6 +114,12 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -221,6 +228,14 @@ struct Row {
             return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
         }
     }
+    static __device__ __forceinline__ float smallest(const uint4 v) {
+        if constexpr (F32) {
+            return fminf(fminf(__uint_as_float(v.x), __uint_as_float(v.y)), fminf(__uint_as_float(v.z), __uint_as_float(v.w)));
+        } else {
+            const uint32_t m = min_bf16x2(min_bf16x2(v.x, v.y), min_bf16x2(v.z, v.w));
+            return fminf(bf16lo_to_f32(m), bf16hi_to_f32(m));
+        }
+    }
     // The largest of a lane's elements; NaN if there is one.
     static __device__ __forceinline__ float most(const uint4 (&w)[NV]) {
         if constexpr (F32) {
@@ -256,16 +271,17 @@ struct Shared {
     uint64_t block_mass[kMaxBlocks];  // the first CTA has all blocks' in the end
     uint32_t block_key[kMaxBlocks];   // of the block's largest logit
     int block_equals[kMaxBlocks];     // tokens at the cut's value
-    uint32_t n[kBins], q[kBins];      // tokens of a bin, and what they weigh beside its weight
-    uint32_t fine_n[kFine], fine_q[kFine];
-    uint32_t list_key[kGather], list_id[kGather];
     Range range, inbox[2];
     uint64_t warp_sum[kWarps], part_mass[kMaxSplit], part_in[kMaxSplit], total;
     double log_min_p;
     int warp_int[kWarps];
     uint32_t warp_key[kWarps], part_key[kMaxSplit], part_bound[kMaxSplit], bound;
     uint64_t bin_weight[32];          // kBinWeight: lanes ask for different ones
-    int listed, collected, drawn, last, block, allowed;
+    int listed, collected, last, block, allowed;
+    // from here on for the search of a cut only
+    uint32_t n[kBins], q[kBins];      // tokens of a bin, and what they weigh beside its weight
+    uint32_t fine_n[kFine], fine_q[kFine];
+    uint32_t list_key[kGather], list_id[kGather];
 };
 
 // To the shared memory of CTA `rank` of the cluster, at the place of *local.
@@ -298,10 +314,35 @@ __device__ __forceinline__ T cta_exclusive(T v, T *warps, T &all) {
     __syncthreads();
     if (lane == 31) warps[warp] = upto;
     __syncthreads();
-    const T w = warp_inclusive(lane < TH / 32 ? warps[lane] : T{0});
-    all = __shfl_sync(0xffffffffu, w, 31);
-    const T before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-    return (warp > 0 ? before : T{0}) + upto - v;
+    T before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < TH / 32; ++w) {
+        if (w == warp) before = sum;
+        sum += warps[w];
+    }
+    all = sum;
+    return before + upto - v;
+}
+// The same of a count and a mass at once: n and v become the sums before.
+template <int TH>
+__device__ __forceinline__ void cta_exclusive2(int &n, uint64_t &v, int *warps_n, uint64_t *warps_v, uint64_t &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int upto_n = warp_inclusive(n);
+    const uint64_t upto = warp_inclusive(v);
+    __syncthreads();
+    if (lane == 31) warps_n[warp] = upto_n, warps_v[warp] = upto;
+    __syncthreads();
+    int before_n = 0, sum_n = 0;
+    uint64_t before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < TH / 32; ++w) {
+        if (w == warp) before_n = sum_n, before = sum;
+        sum_n += warps_n[w];
+        sum += warps_v[w];
+    }
+    all = sum;
+    n = before_n + upto_n - n;
+    v = before + upto - v;
 }
 
 // 2^(c (x - m)).
@@ -457,7 +498,7 @@ __device__ void narrow(const Job &job, Shared<TH> &sh, const Target &target, int
     constexpr int kPer = kFine / TH > 0 ? kFine / TH : 1;
     const Range r = sh.range;
     const uint64_t w = fixed(weight(Key<F32>::value(r.hi), job.m, job.c), 0x1p62f);
-    int n[kPer], sum_n = 0, all_n;
+    int n[kPer], sum_n = 0;
     uint64_t v[kPer], sum = 0, all;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -467,8 +508,9 @@ __device__ void narrow(const Job &job, Shared<TH> &sh, const Target &target, int
         v[i] = n[i] ? __umul64hi(((static_cast<uint64_t>(n[i]) << (5 + bits)) - sh.fine_q[bin]) << (38 - bits), w) : 0;
         sum_n += n[i], sum += v[i];
     }
-    const int at_n = r.count + cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n);
-    const uint64_t at = r.mass + cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
+    cta_exclusive2<TH>(sum_n, sum, sh.warp_int, sh.warp_sum, all);
+    const int at_n = r.count + sum_n;
+    const uint64_t at = r.mass + sum;
     // the bins' masses can miss by their units what their sum was one histogram before: the last bin has the cut then
     const bool found = find_bin<true, kPer, TH>(n, v, at_n, at, target, sh, [&](int i, int before_n, uint64_t before) {
         const uint32_t hi = r.hi - (static_cast<uint32_t>(threadIdx.x * kPer + i) << shift);
@@ -527,12 +569,11 @@ constexpr int kMassBits = 20;
 template <int MODE>
 __device__ __forceinline__ void count_one(uint32_t at, uint32_t q) {
     if constexpr (MODE == kCounts) {
-        asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(at) : "memory");
+        asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(at));
     } else if constexpr (MODE == kMasses) {
-        asm volatile("red.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4) : "memory");
+        asm volatile("red.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4));
     } else {
-        asm volatile("red.shared.add.u32 [%0], 1;\n\tred.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4)
-                     : "memory");
+        asm volatile("red.shared.add.u32 [%0], 1;\n\tred.shared.add.u32 [%0 + %2], %1;" ::"r"(at), "r"(q), "n"(kBins * 4));
     }
 }
 
@@ -548,12 +589,11 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
     // and in units of 2^-(5 + bits): below 2^bits.  The low bits of r are the bin, those of q the units
     const float unit = static_cast<float>(1 << (MODE == kMasses ? kMassBits : 5 + job.bits)), y = kLn2 / kPerUnit;
     const float whole = (MODE == kMasses ? unit : unit / 64.0f) + 0x1p23f;
-    const uint64_t m2 = pair(m, m), minus = pair(-1.0f, -1.0f), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic);
+    const uint64_t m2 = pair(m, m), minus = pair(-1.0f, -1.0f), magic = pair(kMagic, kMagic);
     const float chf = job.c.h * kPerUnit, clf = job.c.l * kPerUnit;
     const uint64_t ch = pair(chf, chf), cl = pair(clf, clf);
     const uint64_t q0 = pair(whole, whole), q1 = pair(-unit * y, -unit * y);
     const uint64_t q2 = pair(unit * y * y / 2.0f, unit * y * y / 2.0f);
-    const uint64_t q3 = pair(-unit * y * y * y / 6.0f, -unit * y * y * y / 6.0f);
     const uint32_t base = smem_u32(sh.n) - (kMagicBits << 2);
     uint64_t went_in = 0;
     for (int b = job.b0 + warp; b < job.b1; b += TH / 32) {
@@ -565,6 +605,7 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
         for (int i = 0; i < NV; ++i) {
             if (Row<F32>::largest(w[i]) < least) continue;
             float x[VE];
+            uint32_t at[VE], v[VE];
             Row<F32>::unpack(w[i], x);
 #pragma unroll
             for (int j = 0; j < VE; j += 2) {
@@ -572,20 +613,27 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
                 float r0, r1, u0 = 0.0f, u1 = 0.0f;
                 unpair(r, r0, r1);
                 if constexpr (MODE != kCounts) {
-                    const uint64_t n = add2(r, unmagic);
-                    // 32 c d - n: the product's difference is exact but for one rounding
-                    const uint64_t f = fma2(d, cl, fma2(d, ch, mul2(n, minus)));
-                    unpair(fma2(f, fma2(f, fma2(f, q3, q2), q1), q0), u0, u1);
+                    // 32 c d - n, of which the product's part is exact but for one rounding; the third power of
+                    // f ln 2 / 32 is at most 2^-22, as often up as down
+                    const uint64_t f = fma2(d, cl, fma2(d, ch, fma2(r, minus, magic)));
+                    unpair(fma2(f, fma2(f, q2, q1), q0), u0, u1);
                 }
-                const uint32_t v0 = __float_as_uint(u0) & 0x7FFFFFu, v1 = __float_as_uint(u1) & 0x7FFFFFu;
-                if (x[j] >= least) {
-                    count_one<MODE>(base + (__float_as_uint(r0) << 2), v0);
-                    sum += v0;
+                at[j] = base + (__float_as_uint(r0) << 2), at[j + 1] = base + (__float_as_uint(r1) << 2);
+                v[j] = __float_as_uint(u0) & 0x7FFFFFu, v[j + 1] = __float_as_uint(u1) & 0x7FFFFFu;
+            }
+            if (MODE == kMasses && Row<F32>::smallest(w[i]) >= least) {
+#pragma unroll
+                for (int j = 0; j < VE; ++j) {
+                    count_one<MODE>(at[j], v[j]);
+                    sum += v[j];
                 }
-                if (x[j + 1] >= least) {
-                    count_one<MODE>(base + (__float_as_uint(r1) << 2), v1);
-                    sum += v1;
-                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    if (x[j] >= least) {
+                        count_one<MODE>(at[j], v[j]);
+                        sum += v[j];
+                    }
             }
         }
         went_in += sum;
@@ -623,7 +671,7 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target, in
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (job.part == 0) {
         constexpr int kPer = kBins / TH;
-        int n[kPer], sum_n = 0, all_n;
+        int n[kPer], sum_n = 0;
         uint64_t v[kPer], sum = 0, all, in_bins = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -641,14 +689,21 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target, in
             }
             sum_n += n[i], sum += v[i];
         }
-        const int at_n = cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n);
-        const uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
+        cta_exclusive2<TH>(sum_n, sum, sh.warp_int, sh.warp_sum, all);
+        const int at_n = sum_n;
+        const uint64_t at = sum;
         bool wrapped = false;
         if (mode == kMasses) {
-            cta_exclusive<uint64_t, TH>(in_bins, sh.warp_sum, all);
+            // each thread's part of what is in the bins fits 35 bits, and their sum is off by a multiple of 2^32 or not at all
             uint64_t went_in = 0;
             for (int i = 0; i < job.splits; ++i) went_in += sh.part_in[i];
-            wrapped = all != went_in;
+            const uint32_t low = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(in_bins & 0xFFFFu));
+            const uint32_t high = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(in_bins >> 16));
+            __syncthreads();
+            if (lane == 0) sh.warp_sum[warp] = (static_cast<uint64_t>(high) << 16) + low;
+            __syncthreads();
+            for (int i = 0; i < TH / 32; ++i) went_in -= sh.warp_sum[i];
+            wrapped = went_in != 0;
         }
         bool found = false;
         if (!wrapped)
@@ -701,8 +756,8 @@ __device__ void find_exponent(Job &job, Shared<TH> &sh, const Target &target, in
 
 // By block, the mass of the tokens above value `hi`; and the tokens from `lo` to
 // it: gathered in this CTA's list, or, one value, counted by block.
-template <bool F32, int TH>
-__device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, uint32_t lo, uint32_t hi, bool gather) {
+template <bool GATHER, bool F32, int TH>
+__device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, uint32_t lo, uint32_t hi) {
     constexpr int NV = Row<F32>::NV, VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float least = Key<F32>::value(lo), most = Key<F32>::value(hi);
@@ -723,7 +778,7 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
                 for (int j = 0; j < VE; ++j) in |= x[j] >= least && x[j] <= most ? 1u << (i * VE + j) : 0u;
             }
             n = __popc(in);
-            if (gather) {
+            if constexpr (GATHER) {
                 if (__any_sync(0xffffffffu, n > 0)) {
                     const int upto = warp_inclusive(n);
                     int at = 0;
@@ -745,7 +800,7 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
         }
         if (lane == 0) {
             sh.block_mass[b] = __float_as_uint(s);
-            sh.block_equals[b] = gather ? 0 : n;
+            sh.block_equals[b] = GATHER ? 0 : n;
         }
     }
     __syncthreads();
@@ -756,12 +811,12 @@ template <int TH>
 __device__ __forceinline__ void hand_over_list(const Job &job, Shared<TH> &sh) {
     if (job.splits > 1 && job.part != 0) {
         const int n = min(sh.listed, kGather);
-        if (threadIdx.x == 0 && n > 0) sh.drawn = static_cast<int>(dsmem_next(&sh.collected, 0, n));
+        if (threadIdx.x == 0 && n > 0) sh.last = static_cast<int>(dsmem_next(&sh.collected, 0, n));
         __syncthreads();
         if (n > 0)
-            for (int i = threadIdx.x; i < n && sh.drawn + i < kGather; i += TH) {
-                dsmem_put(&sh.list_key[sh.drawn + i], 0, sh.list_key[i]);
-                dsmem_put(&sh.list_id[sh.drawn + i], 0, sh.list_id[i]);
+            for (int i = threadIdx.x; i < n && sh.last + i < kGather; i += TH) {
+                dsmem_put(&sh.list_key[sh.last + i], 0, sh.list_key[i]);
+                dsmem_put(&sh.list_id[sh.last + i], 0, sh.list_id[i]);
             }
     }
 }
@@ -856,7 +911,7 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
         list = sh.range;
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        sum_blocks<F32, TH>(row, job, sh, list.lo, list.hi, true);
+        sum_blocks<true, F32, TH>(row, job, sh, list.lo, list.hi);
         if (job.splits > 1) {
             if (tid == 0) sh.collected = sh.listed;  // the first CTA's own come first
             cluster_sync_all();
@@ -886,7 +941,8 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
 }
 
 // ------------------------------------------------------------------ the kernel
-template <bool F32, int TH>
+// PLAIN: nothing but temperatures are given.
+template <bool F32, int TH, bool PLAIN>
 __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs a, int splits) {
     extern __shared__ uint4 sample_smem[];
     Shared<TH> &sh = *reinterpret_cast<Shared<TH> *>(sample_smem);
@@ -906,27 +962,36 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     job.b1 = static_cast<int>(static_cast<int64_t>(job.blocks) * (job.part + 1) / splits);
     const Row<F32> row(static_cast<const char *>(a.logits) + r * a.row_stride * (F32 ? 4 : 2), vocab);
     const float temperature = a.temperature ? a.temperature[r] : 1.0f;
-    const float top_p = a.top_p ? a.top_p[r] : 1.0f, min_p = a.min_p ? a.min_p[r] : 0.0f;
-    int top_k = a.top_k ? a.top_k[r] : 0;
+    const float top_p = !PLAIN && a.top_p ? a.top_p[r] : 1.0f, min_p = !PLAIN && a.min_p ? a.min_p[r] : 0.0f;
+    int top_k = !PLAIN && a.top_k ? a.top_k[r] : 0;
     if (top_k <= 0 || top_k > vocab) top_k = vocab;
     const bool greedy = temperature == 0.0f;
     bool bad = !(greedy || (temperature >= 1e-30f && temperature <= 1e30f)) || top_p != top_p || min_p != min_p;
     job.c = div(Two{0x1.715476p+0f, 0x1.4ae0cp-26f}, Two{greedy || bad ? 1.0f : temperature, 0.0f});
-    if (tid < 32) sh.bin_weight[tid] = kBinWeight[tid];
-    if (min_p > 0.0f && tid == TH - 1) sh.log_min_p = log(static_cast<double>(fminf(min_p, 1.0f)));
+    if (!PLAIN && tid < 32) sh.bin_weight[tid] = kBinWeight[tid];
+    if (!PLAIN && min_p > 0.0f && tid == TH - 1) sh.log_min_p = log(static_cast<double>(fminf(min_p, 1.0f)));
 
-    const bool by_p = top_p < 1.0f, by_k = top_k < vocab && top_k > 1 && !greedy && !bad;
-    if (by_k) {
+    const bool by_p = !PLAIN && top_p < 1.0f, by_k = !PLAIN && top_k < vocab && top_k > 1 && !greedy && !bad;
+    if (!PLAIN && by_k) {
         for (int i = tid; i < kBins; i += TH) sh.n[i] = 0;
         if (tid == 0) sh.bound = 0;
         __syncthreads();
     }
     // ---- the blocks' largest logits and their masses relative to those
+    uint4 ahead[Row<F32>::NV];
+    constexpr bool kAhead = !F32;  // the next block's loads in flight beside this one's sums, where registers allow it
+    if (kAhead && job.b0 + warp < job.b1) row.load(job.b0 + warp, ahead);
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
         uint4 w[Row<F32>::NV];
-        row.load(b, w);
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < Row<F32>::NV; ++i) w[i] = ahead[i];
+            if (b + kWarps < job.b1) row.load(b + kWarps, ahead);
+        } else {
+            row.load(b, w);
+        }
         const uint32_t lane_key = K::of(Row<F32>::most(w)), key = __reduce_max_sync(0xffffffffu, lane_key);
-        if (by_k) atomicAdd(&sh.n[lane_key >> kBoundShift], 1u);
+        if (!PLAIN && by_k) atomicAdd(&sh.n[lane_key >> kBoundShift], 1u);
         float s = 0.0f;
         if (key > K::kNegInf && key < K::kInf && !greedy) s = block_sum<F32, true>(w, key, job.c, 0.0f);
 #pragma unroll
@@ -945,7 +1010,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) key = max(key, sh.warp_key[i]);
     uint32_t bound = 0;
-    if (by_k) {
+    if (!PLAIN && by_k) {
         // the top_k-th largest of the lanes' largest is no larger than the top_k-th of all: the least of its bin
         constexpr int kPer = kBins / TH;
         int n[kPer], sum = 0, all;
@@ -991,7 +1056,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     if (greedy || top_k == 1) {
         cut = job.m_key;
         ties = 1;
-    } else if (by_p || by_k) {
+    } else if (!PLAIN && (by_p || by_k)) {
         uint64_t whole = 0;  // the mass that top_p is a share of; the first CTA's counts
         const uint64_t mine = weigh_blocks<F32>(job, sh);
         cta_exclusive<uint64_t, TH>(mine, sh.warp_sum, whole);
@@ -1035,27 +1100,27 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         __syncthreads();
         hand_over_blocks(job, sh);
     }
-    if (min_p > 0.0f && !greedy) {
+    if (!PLAIN && min_p > 0.0f && !greedy) {
         // the least value whose weight is min_p or more
         const uint32_t k = K::from(__double2float_ru(job.m + temperature * sh.log_min_p));
         if (k > cut) cut = k, ties = 0x7FFFFFFF;
     }
     const bool filtered = cut > K::kNegInf;
     const float cut_value = K::value(cut);
-    const bool in_list = list.lo <= cut && cut <= list.hi;
+    const bool in_list = !PLAIN && list.lo <= cut && cut <= list.hi;
     if (filtered && !in_list) {
-        sum_blocks<F32, TH>(row, job, sh, cut, cut, false);
+        sum_blocks<false, F32, TH>(row, job, sh, cut, cut);
         weigh_blocks<F32>(job, sh);
         __syncthreads();
         hand_over_blocks(job, sh);
-    } else if (!filtered && (by_p || by_k)) {  // neither took a token away
-        sum_blocks<F32, TH>(row, job, sh, K::kNegInf + 1, K::kNegInf, false);
+    } else if (!PLAIN && !filtered && (by_p || by_k)) {  // neither took a token away
+        sum_blocks<false, F32, TH>(row, job, sh, K::kNegInf + 1, K::kNegInf);
         weigh_blocks<F32>(job, sh);
         __syncthreads();
         hand_over_blocks(job, sh);
     }
     if (job.part != 0) return;
-    if (filtered && in_list) {  // what the list holds above the cut, and the cut's equals
+    if (!PLAIN && filtered && in_list) {  // what the list holds above the cut, and the cut's equals
         const int n = min(sh.listed, kGather);
         for (int i = tid; i < n; i += TH) {
             const uint32_t k = sh.list_key[i], b = sh.list_id[i] / kBlock;
@@ -1068,16 +1133,18 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     }
     // ---- the block
     const float u0 = fminf(fmaxf(a.u[2 * r], 0.0f), 1.0f), u1 = fminf(fmaxf(a.u[2 * r + 1], 0.0f), 1.0f);
+    uint64_t total;
     {
         constexpr int kPer = kMaxBlocks / TH;
         const uint64_t cut_weight = filtered ? fixed(weight(cut_value, job.m, job.c), kUnit) : 0;
-        const int first = tid * kPer;
+        const int per = (job.blocks + TH - 1) / TH, first = tid * per;  // of this thread
         int n[kPer], sum_n = 0, all_n;
-        uint64_t v[kPer], sum = 0, all;
+        uint64_t v[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            n[i] = first + i < job.blocks ? sh.block_equals[first + i] : 0;
-            v[i] = first + i < job.blocks ? sh.block_mass[first + i] : 0;
+            const bool have = i < per && first + i < job.blocks;
+            n[i] = have && filtered ? sh.block_equals[first + i] : 0;
+            v[i] = have ? sh.block_mass[first + i] : 0;
             sum_n += n[i];
         }
         int seen = filtered ? cta_exclusive<int, TH>(sum_n, sh.warp_int, all_n) : 0;
@@ -1089,35 +1156,16 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             v[i] += cut_weight * static_cast<uint64_t>(keep);
             sum += v[i];
         }
-        uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
-        const uint64_t target = part_of(all, u0);
-        if (tid == 0) {
-            sh.total = all;
-            sh.drawn = 0x7FFFFFFF;
-            sh.last = sh.block = -1;
-        }
-        __syncthreads();
-        int last = -1;
+        uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, total);
+        uint64_t target = part_of(total, u0);
+        if (target >= total) target = total - 1;  // u0 = 1: the last block
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            if (v[i] > 0) {
-                if (at <= target && at + v[i] > target) {  // one block at most
-                    sh.block = first + i;
-                    sh.allowed = n[i];
-                }
-                last = first + i;
+            if (at <= target && at + v[i] > target) {  // one block
+                sh.block = first + i;
+                sh.allowed = n[i];
             }
             at += v[i];
-        }
-        if (u0 >= 1.0f) {  // past the last: it
-            last = __reduce_max_sync(0xffffffffu, last);
-            if (lane == 0 && last >= 0) atomicMax(&sh.last, last);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (first + i == sh.last) sh.block = first + i, sh.allowed = n[i];
-            __syncthreads();
-            if (tid == 0) sh.last = -1;
         }
     }
     __syncthreads();
@@ -1143,32 +1191,19 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         sum += w[j];
     }
     uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
-    const uint64_t target = part_of(all, u1);
-    int hit = 0x7FFFFFFF, last = -1;
+    uint64_t target = part_of(all, u1);
+    if (target >= all) target = all - 1;  // u1 = 1: the last token
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+        if (at <= target && at + w[j] > target) {  // one token
+            a.tokens[r] = e0 + j;
+            if (a.logprobs) {
+                // (x - m) / T - log(mass / 2^41)
+                const Two t = mul(mul(two_sum(x[j], -job.m), job.c), Two{kLn2, -0x1.05c61p-29f});
+                a.logprobs[r] = (t.h - logf(__ull2float_rn(total) * (1.0f / kUnit))) + t.l;
+            }
+        }
         at += w[j];
-        if (w[j] > 0) {
-            last = e0 + j;
-            if (hit == 0x7FFFFFFF && at > target) hit = e0 + j;
-        }
-    }
-    hit = __reduce_min_sync(0xffffffffu, hit);
-    last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0) {
-        if (hit != 0x7FFFFFFF) atomicMin(&sh.drawn, hit);
-        if (last >= 0) atomicMax(&sh.last, last);
-    }
-    __syncthreads();
-    const int token = sh.drawn != 0x7FFFFFFF ? sh.drawn : sh.last;
-    if (tid == 0) {
-        a.tokens[r] = token;
-        if (a.logprobs) {
-            // (x - m) / T - log(mass / 2^41)
-            const Two t = mul(mul(two_sum(row.at(token), -job.m), job.c), Two{kLn2, -0x1.05c61p-29f});
-            const float mass = __ull2float_rn(sh.total) * (1.0f / kUnit);
-            a.logprobs[r] = (t.h - logf(mass)) + t.l;
-        }
     }
 }
 
@@ -1178,17 +1213,18 @@ struct SampleSetup {
     cudaError_t err[64] = {};
 };
 
-template <bool F32, int TH>
+template <bool F32, int TH, bool PLAIN>
 cudaError_t launch_rows(const SampleArgs &a, int splits, cudaStream_t stream) {
     static SampleSetup setup;
-    constexpr int kSmem = static_cast<int>(sizeof(Shared<TH>));
+    constexpr int kSmem = static_cast<int>(PLAIN ? offsetof(Shared<TH>, n) : sizeof(Shared<TH>));
     static_assert(kSmem * (1024 / TH) <= 227 * 1024, "shared memory per SM");
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     {
         std::lock_guard<std::mutex> lock(setup.mu);
         if (!setup.done[dev]) {
-            setup.err[dev] = cudaFuncSetAttribute(sample_kernel<F32, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            setup.err[dev] =
+                cudaFuncSetAttribute(sample_kernel<F32, TH, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             setup.done[dev] = true;
         }
         if (setup.err[dev] != cudaSuccess) return setup.err[dev];
@@ -1207,7 +1243,7 @@ cudaError_t launch_rows(const SampleArgs &a, int splits, cudaStream_t stream) {
     attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<F32, TH>, a, splits);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<F32, TH, PLAIN>, a, splits);
 }
 
 }  // namespace
@@ -1216,7 +1252,12 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     const int64_t blocks = (a.vocab + kBlock - 1) / kBlock, sms = device_sm_count();
     int splits = 1;
     while (splits < kMaxSplit && 2 * splits * a.rows <= 2 * sms && blocks / (2 * splits) >= 8) splits *= 2;
-    return a.f32 ? launch_rows<true, 512>(a, splits, stream) : launch_rows<false, 512>(a, splits, stream);
+    if (!a.top_k && !a.top_p && !a.min_p) {
+        if (splits == 1 && a.rows > 2 * sms)
+            return a.f32 ? launch_rows<true, 256, true>(a, splits, stream) : launch_rows<false, 256, true>(a, splits, stream);
+        return a.f32 ? launch_rows<true, 512, true>(a, splits, stream) : launch_rows<false, 512, true>(a, splits, stream);
+    }
+    return a.f32 ? launch_rows<true, 512, false>(a, splits, stream) : launch_rows<false, 512, false>(a, splits, stream);
 }
 
 uint32_t take_sample_error() {
