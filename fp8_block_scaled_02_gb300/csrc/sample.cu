@@ -345,8 +345,8 @@ __device__ __forceinline__ void cta_exclusive2(int &n, uint64_t &v, int *warps_n
     v = before + upto - v;
 }
 
-// 2^(c (x - m)).
-__device__ __forceinline__ Two weight(float x, float m, Two c) {
+// 2^(c (x - m)).  One copy of its code: what runs once waits for its instructions.
+__device__ __noinline__ Two weight(float x, float m, Two c) {
     if (!(x > -INFINITY)) return Two{0.0f, 0.0f};
     const Two d = two_sum(x, -m);
     const float t = d.h * c.h;
@@ -577,13 +577,12 @@ __device__ __forceinline__ void count_one(uint32_t at, uint32_t q) {
     }
 }
 
-// The histogram of the row's exponents, in the first CTA's n and q.
+// The histogram of the row's exponents, in the first CTA's n and q; they are
+// zero in all CTAs before a cluster barrier before this.
 template <bool F32, int TH, int MODE>
 __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> &sh) {
     constexpr int NV = Row<F32>::NV, VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
-    __syncthreads();
     const float least = Key<F32>::value(job.lowest), m = job.m;
     // d = m - x; bin = round(32 c d), f the rest in [-1/2, 1/2]; weight / bin's = 2^(-f / 32), with the counts less 63/64
     // and in units of 2^-(5 + bits): below 2^bits.  The low bits of r are the bin, those of q the units
@@ -653,7 +652,6 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
         }
     }
     if (job.splits > 1) {
-        cluster_sync_all();
         if (job.part != 0)
             for (int i = tid; i < kBins; i += TH) {
                 if (MODE != kMasses && sh.n[i]) dsmem_add(&sh.n[i], 0, sh.n[i]);
@@ -806,7 +804,7 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
     __syncthreads();
 }
 
-// The CTAs' lists into the first one's, behind one another.
+// The CTAs' lists into the first one's, from its end down; its own are at its start.
 template <int TH>
 __device__ __forceinline__ void hand_over_list(const Job &job, Shared<TH> &sh) {
     if (job.splits > 1 && job.part != 0) {
@@ -815,8 +813,8 @@ __device__ __forceinline__ void hand_over_list(const Job &job, Shared<TH> &sh) {
         __syncthreads();
         if (n > 0)
             for (int i = threadIdx.x; i < n && sh.last + i < kGather; i += TH) {
-                dsmem_put(&sh.list_key[sh.last + i], 0, sh.list_key[i]);
-                dsmem_put(&sh.list_id[sh.last + i], 0, sh.list_id[i]);
+                dsmem_put(&sh.list_key[kGather - 1 - sh.last - i], 0, sh.list_key[i]);
+                dsmem_put(&sh.list_id[kGather - 1 - sh.last - i], 0, sh.list_id[i]);
             }
     }
 }
@@ -849,24 +847,30 @@ __device__ __forceinline__ void hand_over_blocks(const Job &job, Shared<TH> &sh)
     __syncthreads();
 }
 
+template <int TH, class Each>
+__device__ __forceinline__ void for_list(const Shared<TH> &sh, Each each) {
+    const int own = min(sh.listed, kGather), n = min(own + sh.collected, kGather);
+    for (int i = threadIdx.x; i < n; i += TH) each(i < own ? i : kGather - 1 - (i - own));
+}
+
 // The list's tokens whose keys are in sh.range, down to one value.  By the first CTA.
 template <bool F32, int TH>
 __device__ void search_list(const Job &job, Shared<TH> &sh, const Target &target) {
     constexpr int kBits = 20;  // kGather residuals of 2^20 fit 32 bits
     while (sh.range.lo != sh.range.hi) {
         const uint32_t lo = sh.range.lo, hi = sh.range.hi;
-        const int shift = fine_shift(lo, hi), n = min(sh.listed, kGather);
+        const int shift = fine_shift(lo, hi);
         const float top = Key<F32>::value(hi);
         for (int i = threadIdx.x; i < kFine; i += TH) sh.fine_n[i] = sh.fine_q[i] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += TH) {
+        for_list(sh, [&](int i) {
             const uint32_t key = sh.list_key[i];
             if (key >= lo && key <= hi) {
                 const uint32_t bin = (hi - key) >> shift;
                 atomicAdd(&sh.fine_n[bin], 1u);
                 atomicAdd(&sh.fine_q[bin], fine_rest(top, Key<F32>::value(key), job.c, static_cast<float>(1 << (5 + kBits))));
             }
-        }
+        });
         __syncthreads();
         narrow<F32>(job, sh, target, shift, kBits);
     }
@@ -875,8 +879,10 @@ __device__ void search_list(const Job &job, Shared<TH> &sh, const Target &target
 // From sh.range, the same in all the row's CTAs, to the cut: its value
 // (lo = hi), how many of its equals are kept, the mass of all that is.
 // `list`: the range whose tokens are gathered and above which blocks are summed.
+// After the last search only the first CTA has more than the range that it began
+// with, or the one that is in the list.
 template <bool F32, int TH>
-__device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Target &target, Range &list) {
+__device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Target &target, Range &list, bool last) {
     const int tid = threadIdx.x, warp = tid >> 5;
     const bool listed = list.lo == sh.range.lo && list.hi == sh.range.hi;
     while (!listed && sh.range.equals > kGather && sh.range.lo != sh.range.hi) {
@@ -908,19 +914,18 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
         share_range(job, sh);
     }
     if (!listed && sh.range.lo != sh.range.hi) {
+        const bool again = list.lo <= list.hi;
         list = sh.range;
-        if (tid == 0) sh.listed = 0;
-        __syncthreads();
-        sum_blocks<true, F32, TH>(row, job, sh, list.lo, list.hi);
-        if (job.splits > 1) {
-            if (tid == 0) sh.collected = sh.listed;  // the first CTA's own come first
-            cluster_sync_all();
-            hand_over_list(job, sh);
+        if (tid == 0) {
+            sh.listed = 0;
+            if (again) sh.collected = 0;
         }
+        __syncthreads();
+        if (again && job.splits > 1) cluster_sync_all();
+        sum_blocks<true, F32, TH>(row, job, sh, list.lo, list.hi);
+        hand_over_list(job, sh);
         weigh_blocks<F32>(job, sh);
         hand_over_blocks(job, sh);
-        if (job.splits > 1 && job.part == 0 && tid == 0) sh.listed = sh.collected;
-        __syncthreads();
     }
     if (job.part == 0) {
         search_list<F32>(job, sh, target);
@@ -929,15 +934,23 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
             const uint64_t w = fixed(weight(Key<F32>::value(sh.range.lo), job.m, job.c), kUnit);
             int kept = target.count - sh.range.count;
             if (target.by_mass) {
+                // the fewest whose mass reaches what is missing: a quotient in fp32, put right by products
                 const uint64_t miss = target.mass > sh.range.mass ? target.mass - sh.range.mass : 0;
-                const uint64_t need = w > 0 ? (miss + w - 1) / w : static_cast<uint64_t>(sh.range.equals);
-                kept = need > static_cast<uint64_t>(sh.range.equals) ? sh.range.equals : need < 1 ? 1 : static_cast<int>(need);
+                const uint64_t most = static_cast<uint64_t>(sh.range.equals);
+                uint64_t need = most;
+                if (w > 0 && miss < most * w) {
+                    need = static_cast<uint64_t>(__fdividef(__ull2float_rn(miss), __ull2float_rn(w)));
+                    while (need * w < miss) ++need;
+                    while (need > 0 && (need - 1) * w >= miss) --need;
+                }
+                kept = need < 1 ? 1 : static_cast<int>(need < most ? need : most);
             }
             sh.range.equals = kept;
             sh.range.mass += w * static_cast<uint64_t>(kept);
         }
     }
-    share_range(job, sh);
+    if (!last) share_range(job, sh);
+    else __syncthreads();
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -1023,6 +1036,12 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         });
         bound = sh.bound;
     }
+    if (!PLAIN && (by_k || by_p)) {
+        __syncthreads();
+        for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
+        if (tid == 0) sh.collected = 0;
+        __syncthreads();
+    }
     if (splits > 1) {
         cluster_wait();
         if (tid < splits) {
@@ -1073,7 +1092,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             const Target target{false, top_k, 0};
             find_exponent<F32>(job, sh, target, mode);
             if (!sh.range.none) {
-                find_cut<F32, TH>(row, job, sh, target, list);
+                find_cut<F32, TH>(row, job, sh, target, list, !by_p);
                 cut = sh.range.lo;
                 ties = sh.range.equals;
                 whole = sh.range.mass;
@@ -1085,12 +1104,15 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             const Target target{true, 0, at_least_one(__umul64hi(whole, share) + (whole * share != 0 ? 1 : 0))};
             find_exponent<F32>(job, sh, target, mode);
             if (sh.range.none == 2) {
+                for (int i = tid; i < kBins; i += TH) sh.n[i] = sh.q[i] = 0;
+                __syncthreads();
+                if (splits > 1) cluster_sync_all();
                 count_exponents<F32, TH, kBoth>(row, job, sh);
                 mode = kBoth;
                 find_exponent<F32>(job, sh, target, mode);
             }
             if (!sh.range.none) {
-                find_cut<F32, TH>(row, job, sh, target, list);
+                find_cut<F32, TH>(row, job, sh, target, list, true);
                 if (sh.range.lo > cut || (sh.range.lo == cut && sh.range.equals < ties)) cut = sh.range.lo, ties = sh.range.equals;
                 __syncthreads();
             }
@@ -1121,14 +1143,13 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     }
     if (job.part != 0) return;
     if (!PLAIN && filtered && in_list) {  // what the list holds above the cut, and the cut's equals
-        const int n = min(sh.listed, kGather);
-        for (int i = tid; i < n; i += TH) {
+        for_list(sh, [&](int i) {
             const uint32_t k = sh.list_key[i], b = sh.list_id[i] / kBlock;
             if (k > cut)
                 atomicAdd(reinterpret_cast<unsigned long long *>(&sh.block_mass[b]),
                           static_cast<unsigned long long>(fixed(weight(K::value(k), job.m, job.c), kUnit)));
             else if (k == cut) atomicAdd(&sh.block_equals[b], 1);
-        }
+        });
         __syncthreads();
     }
     // ---- the block
