@@ -183,28 +183,43 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // Elements e0 .. e0 + VE - 1 of a row that is off a boundary, from the two vectors that hold them.
-    __device__ __forceinline__ uint4 shifted(int e0) const {
-        const char *p = base + static_cast<int64_t>(e0) * ES - off;
+    // Elements e0 .. e0 + VE - 1 of a row that is 4 Q bytes and `bits` off a boundary, from the two vectors that hold them.
+    template <int Q>
+    __device__ __forceinline__ uint4 shifted(const char *p, int bits) const {
         const uint4 a = ld_v4_cached(p), b = ld_v4_cached(p + 16);
-        uint32_t w[5];
-        switch (off >> 2) {
-            case 0: w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x; break;
-            case 1: w[0] = a.y, w[1] = a.z, w[2] = a.w, w[3] = b.x, w[4] = b.y; break;
-            case 2: w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z; break;
-            default: w[0] = a.w, w[1] = b.x, w[2] = b.y, w[3] = b.z, w[4] = b.w; break;
-        }
-        const int bits = (off & 3) * 8;
-        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if constexpr (F32) return make_uint4(u[Q], u[Q + 1], u[Q + 2], u[Q + 3]);
+        return make_uint4(__funnelshift_r(u[Q], u[Q + 1], bits), __funnelshift_r(u[Q + 1], u[Q + 2], bits),
+                          __funnelshift_r(u[Q + 2], u[Q + 3], bits),
+                          __funnelshift_r(u[Q + 3], Q < 3 ? u[Q < 3 ? Q + 4 : 0] : b.w, bits));
+    }
+    template <int Q>
+    __device__ __forceinline__ void load_shifted(int first, uint4 (&w)[NV]) const {
+        const char *p = base + static_cast<int64_t>(first) * ES - off;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) w[i] = shifted<Q>(p + i * 512, (off & 3) * 8);
     }
     __device__ __forceinline__ void load(int b, uint4 (&w)[NV]) const {
         const int first = b * kBlock + (threadIdx.x & 31) * VE;
+        if (off == 0 && (b + 1) * kBlock <= vocab) {  // a whole block: the most
+            const char *p = base + static_cast<int64_t>(first) * ES;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) w[i] = ld_v4(p + i * 512);
+            return;
+        }
+        if (off != 0 && b > 0 && (b + 1) * kBlock + VE <= vocab) {  // with the vectors before and behind it in the row
+            switch (off >> 2) {
+                case 0: load_shifted<0>(first, w); break;
+                case 1: load_shifted<1>(first, w); break;
+                case 2: load_shifted<2>(first, w); break;
+                default: load_shifted<3>(first, w); break;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e0 = first + i * 32 * VE;
-            if (off == 0) w[i] = e0 + VE <= vocab ? ld_v4(base + static_cast<int64_t>(e0) * ES) : slow(e0);
-            else w[i] = e0 * ES >= off && e0 + 2 * VE <= vocab ? shifted(e0) : slow(e0);
+            w[i] = off == 0 && e0 + VE <= vocab ? ld_v4(base + static_cast<int64_t>(e0) * ES) : slow(e0);
         }
     }
     static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[VE]) {
