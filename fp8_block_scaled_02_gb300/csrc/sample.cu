@@ -219,7 +219,15 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e0 = first + i * 32 * VE;
-            w[i] = off == 0 && e0 + VE <= vocab ? ld_v4(base + static_cast<int64_t>(e0) * ES) : slow(e0);
+            const char *p = base + static_cast<int64_t>(e0) * ES;
+            if (e0 >= vocab) w[i] = F32 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                                        : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+            else if (off == 0 && e0 + VE <= vocab) w[i] = ld_v4(p);
+            else if (off == 0 || e0 * ES < off || e0 + 2 * VE > vocab) w[i] = slow(e0);
+            else if (off < 4) w[i] = shifted<0>(p - off, (off & 3) * 8);
+            else if (off < 8) w[i] = shifted<1>(p - off, (off & 3) * 8);
+            else if (off < 12) w[i] = shifted<2>(p - off, (off & 3) * 8);
+            else w[i] = shifted<3>(p - off, (off & 3) * 8);
         }
     }
     static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[VE]) {
@@ -287,15 +295,20 @@ struct Shared {
     uint32_t block_key[kMaxBlocks];   // of the block's largest logit
     int block_equals[kMaxBlocks];     // tokens at the cut's value
     Range range, inbox[2];
-    uint64_t warp_sum[kWarps], part_mass[kMaxSplit], part_in[kMaxSplit], total;
+    uint64_t warp_sum[kWarps], part_mass[kMaxSplit], part_in[kMaxSplit];
     double log_min_p;
     int warp_int[kWarps];
-    uint32_t warp_key[kWarps], part_key[kMaxSplit], part_bound[kMaxSplit], bound;
+    uint32_t warp_key[kWarps], part_key[kMaxSplit], part_bound[kMaxSplit], bound, min_key;
     uint64_t bin_weight[32];          // kBinWeight: lanes ask for different ones
     int listed, collected, last, block, allowed;
     // from here on for the search of a cut only
-    uint32_t n[kBins], q[kBins];      // tokens of a bin, and what they weigh beside its weight
-    uint32_t fine_n[kFine], fine_q[kFine];
+    alignas(16) uint32_t n[kBins], q[kBins];  // tokens of a bin, and what they weigh beside its weight
+    union {
+        struct {
+            uint32_t fine_n[kFine], fine_q[kFine];
+        };
+        uint64_t list_weight[kFine];  // of a short list's tokens
+    };
     uint32_t list_key[kGather], list_id[kGather];
 };
 
@@ -891,6 +904,43 @@ __device__ void search_list(const Job &job, Shared<TH> &sh, const Target &target
     }
 }
 
+// The same of a short list, to the end: every token's place among them and the
+// mass to it, by comparing all.  The token with the target has the cut.
+constexpr int kShort = 256;
+static_assert(kShort <= kFine, "list_weight holds a short list");
+template <bool F32, int TH>
+__device__ void rank_list(const Job &job, Shared<TH> &sh, const Target &target) {
+    static_assert(TH >= kShort, "a thread a token");
+    const int own = min(sh.listed, kGather), n = own + sh.collected, i = threadIdx.x;
+    auto at = [&](int j) { return j < own ? j : kGather - 1 - (j - own); };
+    const Range r = sh.range;
+    uint32_t key = 0, id = 0;
+    uint64_t w = 0;
+    if (i < n) {
+        key = sh.list_key[at(i)], id = sh.list_id[at(i)];
+        w = fixed(weight(Key<F32>::value(key), job.m, job.c), kUnit);
+        sh.list_weight[i] = w;
+    }
+    __syncthreads();
+    if (i < n) {
+        int before = 0, equals = 0;
+        uint64_t mass = 0;
+        for (int j = 0; j < n; ++j) {
+            const uint32_t k = sh.list_key[at(j)];
+            const bool same = k == key && sh.list_id[at(j)] < id, ahead = k > key || same;
+            before += ahead ? 1 : 0;
+            equals += same ? 1 : 0;
+            mass += ahead ? sh.list_weight[j] : 0;
+        }
+        mass += r.mass;
+        const bool last = before == n - 1;
+        const bool mine = target.by_mass ? (mass < target.mass || before == 0) && (mass + w >= target.mass || last)
+                                         : r.count + before + 1 == target.count || (last && r.count + n < target.count);
+        if (mine) sh.range = Range{key, key, r.count + before - equals, equals + 1, mass + w, 0, 0};
+    }
+    __syncthreads();
+}
+
 // From sh.range, the same in all the row's CTAs, to the cut: its value
 // (lo = hi), how many of its equals are kept, the mass of all that is.
 // `list`: the range whose tokens are gathered and above which blocks are summed.
@@ -942,7 +992,9 @@ __device__ void find_cut(const Row<F32> &row, Job &job, Shared<TH> &sh, const Ta
         weigh_blocks<F32>(job, sh);
         hand_over_blocks(job, sh);
     }
-    if (job.part == 0) {
+    if (job.part == 0 && sh.range.lo != sh.range.hi && sh.listed + sh.collected <= kShort) {
+        rank_list<F32>(job, sh, target);
+    } else if (job.part == 0) {
         search_list<F32>(job, sh, target);
         __syncthreads();
         if (tid == 0) {
@@ -991,6 +1043,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     const Row<F32> row(static_cast<const char *>(a.logits) + r * a.row_stride * (F32 ? 4 : 2), vocab);
     const float temperature = a.temperature ? a.temperature[r] : 1.0f;
     const float top_p = !PLAIN && a.top_p ? a.top_p[r] : 1.0f, min_p = !PLAIN && a.min_p ? a.min_p[r] : 0.0f;
+    const float u0 = fminf(fmaxf(a.u[2 * r], 0.0f), 1.0f), u1 = fminf(fmaxf(a.u[2 * r + 1], 0.0f), 1.0f);
     int top_k = !PLAIN && a.top_k ? a.top_k[r] : 0;
     if (top_k <= 0 || top_k > vocab) top_k = vocab;
     const bool greedy = temperature == 0.0f;
@@ -1072,6 +1125,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     job.m_key = key;
     job.m = K::value(key);
     bad = bad || key >= K::kInf;
+    if (!PLAIN && min_p > 0.0f && tid == 0)  // the least value whose weight is min_p or more
+        sh.min_key = K::from(__double2float_ru(job.m + temperature * sh.log_min_p));
     if (bad || key == K::kNegInf) {  // the same in all of the row's CTAs
         if (job.part == 0 && tid == 0) {
             a.tokens[r] = -1;
@@ -1138,8 +1193,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         hand_over_blocks(job, sh);
     }
     if (!PLAIN && min_p > 0.0f && !greedy) {
-        // the least value whose weight is min_p or more
-        const uint32_t k = K::from(__double2float_ru(job.m + temperature * sh.log_min_p));
+        __syncthreads();
+        const uint32_t k = sh.min_key;
         if (k > cut) cut = k, ties = 0x7FFFFFFF;
     }
     const bool filtered = cut > K::kNegInf;
@@ -1168,7 +1223,6 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         __syncthreads();
     }
     // ---- the block
-    const float u0 = fminf(fmaxf(a.u[2 * r], 0.0f), 1.0f), u1 = fminf(fmaxf(a.u[2 * r + 1], 0.0f), 1.0f);
     uint64_t total;
     {
         constexpr int kPer = kMaxBlocks / TH;
