@@ -3,7 +3,10 @@
 //
 // Route, a warp a token.  s = softmax(x) or 1 / (1 + e^-x); experts are chosen
 // by c = s + bias.  Whole numbers come out, so near ties have to be decided as
-// the definition decides them: c is compared in multiples of 2^-44.
+// the definition decides them: c is compared in multiples of 2^-44.  The choice
+// is made in fp32 first, and stands if what it told apart is further apart than
+// c can be off; else (one token in some thousands) it is made again with pairs
+// of fp32.  Without a bias or groups it goes by the logits themselves.
 #include "twofloat.cuh"
 
 #include "serving.cuh"
@@ -44,14 +47,10 @@ __device__ __forceinline__ float load_logit(const void *row, int e) {
 }
 
 // Lane l has experts l * EPL .. l * EPL + EPL - 1, so that the lowest lane among
-// equals has the lowest expert.
+// equals has the lowest expert.  sc: [experts] in shared memory, with groups.
 template <bool F32, int EPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const MoeScoreArgs a) {
-    extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-    pdl_wait();
-    if (token >= a.tokens) return;
+__device__ __noinline__ void route_exactly(const MoeScoreArgs &a, int64_t token, uint64_t *sc) {
+    const int lane = threadIdx.x & 31;
     const int experts = static_cast<int>(a.experts), topk = static_cast<int>(a.topk), e0 = lane * EPL;
     const void *row = static_cast<const char *>(a.logits) + token * a.row_stride * (F32 ? 4 : 2);
     float x[EPL];
@@ -104,7 +103,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const MoeScoreA
     for (int i = 0; i < EPL; ++i) mine |= e0 + i < experts ? 1u << i : 0u;
     if (a.groups > 1) {
         const int groups = static_cast<int>(a.groups), per = experts / groups;
-        uint64_t *sc = sh_scores + static_cast<int64_t>(warp) * experts;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (e0 + i < experts) sc[e0 + i] = key[i];
@@ -165,6 +163,217 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const MoeScoreA
         a.ids[token * topk + lane] = id;
         a.weights[token * topk + lane] = w * a.scale;
     }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// e^(x - m) within 2^-21 of itself, x - m in [-104, 0]: the exponent's own error goes back in.
+__device__ __forceinline__ float exp_near(float x, float m) {
+    const Two t = times_log2e(two_sum(x, -m));
+    const float e = ex2(t.h);
+    return fmaf(e, t.l * 0.6931471805599453f, e);
+}
+
+// A token's experts by fp32 scores; false if they do not tell them apart.
+template <bool F32, int EPL>
+__device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t token) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const int lane = threadIdx.x & 31, experts = static_cast<int>(a.experts), topk = static_cast<int>(a.topk);
+    const int e0 = lane * EPL, groups = static_cast<int>(a.groups), per = groups > 1 ? experts / groups : experts;
+    const int lanes = per / EPL;  // of a group
+    if (groups > 1 && (lanes * EPL != per || (lanes & (lanes - 1)) != 0)) return false;
+    const char *row = static_cast<const char *>(a.logits) + token * a.row_stride * (F32 ? 4 : 2);
+    float x[EPL];
+    constexpr int kBytes = EPL * (F32 ? 4 : 2);
+    bool vector = false;
+    if constexpr (kBytes >= 16) vector = (reinterpret_cast<uintptr_t>(row) & 15) == 0 && e0 + EPL <= experts;
+    if (vector) {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 v = ld_v4(row + static_cast<int64_t>(lane) * kBytes + 16 * i);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (F32) x[4 * i + j] = __uint_as_float(u[j]);
+                    else x[8 * i + 2 * j] = bf16lo_to_f32(u[j]), x[8 * i + 2 * j + 1] = bf16hi_to_f32(u[j]);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) x[i] = e0 + i < experts ? load_logit<F32>(row, e0 + i) : -INFINITY;
+    }
+    float m = 0.0f, z = 1.0f;
+    if (a.softmax) {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!(fabsf(m) < INFINITY)) return false;
+    }
+    // ---- what the experts are ordered by: c, or the logit itself; 0: not there, or its group is not open
+    const bool scored = a.bias != nullptr || groups > 1;
+    uint32_t key[EPL];
+    float c[EPL];
+    float slack = 0.0f;  // c is within slack + 2^-22 |c|
+    if (a.softmax || scored) {
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            if (a.softmax) {
+                c[i] = ex2((x[i] - m) * kLog2e);
+                z += c[i];
+            } else {
+                c[i] = __frcp_rn(1.0f + ex2(-x[i] * kLog2e));
+            }
+        }
+        if (a.softmax) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        }
+        if (z != z) return false;
+    }
+    if (scored) {
+        // Softmax: e^-d, d = m - x, is off by 2.5 2^-24 d and ex2's 2^-22 of itself, below 2^-21 of the largest; z by 2^-22,
+        // 2^-23 and half a step for each of EPL + 5 additions; the quotient by 2^-22: to 256 experts 2^-19 of the largest
+        // score.  Sigmoid, with u = e^-x: u / (1 + u) of u's 2.2 2^-24 |x| + 2^-22 reach s, 1 + u and the quotient round
+        // once each: 2^-22.
+        const float to_score = a.softmax ? __fdividef(1.0f, z) : 1.0f;
+        slack = a.softmax ? (EPL <= 8 ? 0x1p-19f : 0x1p-18f) * to_score : 0x1p-22f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            float b = 0.0f;
+            if (a.bias && e0 + i < experts) b = fminf(fmaxf(a.bias[e0 + i], -kMostBias), kMostBias);
+            c[i] = fmaf(c[i], to_score, b);
+        }
+    }
+    bool open = true;
+    if (groups > 1) {
+        // ---- the groups' scores: the two best of the lane's experts, then of the group's lanes
+        float b1 = -INFINITY, b2 = -INFINITY;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const float v = e0 + i < experts ? c[i] : -INFINITY;
+            nan |= v != v;
+            b2 = fmaxf(b2, fminf(b1, v));
+            b1 = fmaxf(b1, v);
+        }
+        if (__any_sync(0xffffffffu, nan)) return false;
+        for (int o = 1; o < lanes; o <<= 1) {
+            const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+            b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+            b1 = fmaxf(b1, o1);
+        }
+        const int mine = lane / lanes;
+        const float score = a.group_top == 2 ? b1 + b2 : b1;
+        int before = 0;
+        for (int g = 0; g < groups; ++g) {
+            const float other = __shfl_sync(0xffffffffu, score, g * lanes);
+            before += other > score || (other == score && g < mine) ? 1 : 0;
+        }
+        open = mine < groups && before < static_cast<int>(a.topk_groups);
+        if (a.topk_groups < a.groups) {
+            // the last that is open and the first that is not
+            const uint32_t in = __reduce_min_sync(0xffffffffu, open ? logit_key(score) : 0xFFFFFFFFu);
+            const uint32_t out = __reduce_max_sync(0xffffffffu, mine < groups && !open ? logit_key(score) : 0u);
+            const float low = __uint_as_float(in & 0x80000000u ? in & 0x7FFFFFFFu : ~in);
+            const float high = __uint_as_float(out & 0x80000000u ? out & 0x7FFFFFFFu : ~out);
+            if (!(low - high > 4.0f * (slack + 0x1p-22f * (fabsf(low) + fabsf(high))))) return false;
+        }
+    }
+    const bool by_score = a.bias != nullptr;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = open && e0 + i < experts ? logit_key(by_score ? c[i] : x[i]) : 0u;
+    // ---- the best that is left, topk times, and by scores as long as one may yet be before the topk-th; lane j keeps the j-th
+    auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); };
+    int id = 0, n = 0, place = lane;
+    uint32_t got = 0;
+    float last = 0.0f;
+    bool close = false;
+    for (; n < 33; ++n) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        if (n >= topk && !by_score) break;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (by_score) {
+            const float v = value(top);
+            if (top == 0) break;
+            if (v != v) return false;
+            const bool apart = n == 0 || last - v > 2.0f * (slack + 0x1p-22f * (fabsf(last) + fabsf(v)));
+            if (n >= topk && apart) break;
+            if (n == 32) return false;
+            close |= !apart;
+            if (n < topk) last = v;
+        }
+        const int winner = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+        const int e = __shfl_sync(0xffffffffu, e0 + at, winner);
+        if (lane == n) id = e, got = top;
+        if (lane == winner) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (i == at) key[i] = 0;
+        }
+    }
+    if (close) {
+        // ---- scores that fp32 does not tell apart: those of the candidates again, and their places by them
+        if (a.softmax) return false;  // would need the sum of all again
+        uint64_t exact = 0;
+        if (lane < n) {
+            const float v = load_logit<F32>(row, id), d = -fabsf(v);
+            const Two u = d > kNoScore ? two_exp2(times_log2e(Two{d, 0.0f})) : Two{0.0f, 0.0f}, one{1.0f, 0.0f};
+            exact = score_key(add(div(v < 0.0f ? u : one, add(u, 1.0f)), fminf(fmaxf(a.bias[id], -kMostBias), kMostBias)));
+        }
+        place = 0;
+        for (int j = 0; j < n; ++j) {
+            const uint64_t other = __shfl_sync(0xffffffffu, exact, j);
+            const int other_id = __shfl_sync(0xffffffffu, id, j);
+            place += other > exact || (other == exact && other_id < id) ? 1 : 0;
+        }
+        if (lane >= n) place = 32;
+    }
+    // ---- the weights, from the chosen experts' logits
+    float w = 0.0f;
+    if (place < topk) {
+        float v = value(got);
+        if (by_score) v = load_logit<F32>(row, id);
+        if (a.softmax) {
+            w = v - m > kNoScore ? exp_near(v, m) / z : 0.0f;
+        } else {
+            const float e = fabsf(v) < -kNoScore ? exp_near(-fabsf(v), 0.0f) : 0.0f;
+            w = (v < 0.0f ? e : 1.0f) / (1.0f + e);
+        }
+        if (v != v) w = v;
+    }
+    if (a.renormalize) {
+        float sum = w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        w = sum == 0.0f ? 0.0f : w / sum;
+    }
+    if (place < topk) {
+        a.ids[token * topk + place] = id;
+        a.weights[token * topk + place] = w * a.scale;
+    }
+    return true;
+}
+
+template <bool F32, int EPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ MoeScoreArgs a) {
+    extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    pdl_wait();
+    if (token >= a.tokens) return;
+    if (!route_quickly<F32, EPL>(a, token)) route_exactly<F32, EPL>(a, token, sh_scores + (threadIdx.x >> 5) * a.experts);
 }
 
 template <bool F32, int EPL>

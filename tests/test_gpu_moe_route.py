@@ -1,8 +1,11 @@
 """GPU tests of fp8bs_moe_route and fp8bs_moe_combine against float64.
 
-Ids have to be equal.  Weights: the scores are held in two fp32 numbers and
-rounded once (2^-24), their sum's five additions, the quotient and the product
-with the scale round by half a step each: 9 * 2^-24 < 2^-20 of the weight.
+Ids have to be equal.  Weights: the exponential is within 2^-22 (ex2) + 2^-23,
+the sum over all experts by as much and the roundings of its 32 + 5 additions at
+most (E = 1024), half a step each and each of a part of the sum only (8 + 5 of
+them to E = 256); the quotient, the sum of the chosen by five additions, its quotient and the
+product with the scale round by half a step: (4 + 2 + 37 + 8) 2^-24 < 2^-18 of the
+weight, below 2^-19 to E = 256.
 Combine: topk fused multiply-adds round by 2^-24 of the running sum, below
 the sum of the magnitudes; one bf16 rounding, 2^-8 of the result at most.
 """
@@ -37,7 +40,7 @@ def check(pkg, x, topk, bias=None, **kw):
     nan = np.isnan(want_w)
     assert np.array_equal(np.isnan(w), nan)
     e = np.abs(w - want_w)[~nan]
-    assert np.all(e <= 2.0 ** -20 * np.abs(want_w)[~nan] + 2.0 ** -126), e.max()
+    assert np.all(e <= 2.0 ** (-19 if x.shape[1] <= 256 else -18) * np.abs(want_w)[~nan] + 2.0 ** -126), e.max()
     assert pkg.check_device_error() == 0
     return ids
 
