@@ -171,6 +171,12 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // e^(x - m) within 2^-21 of itself, x - m in [-104, 0]: the exponent's own error goes back in.
 __device__ __forceinline__ float exp_near(float x, float m) {
     const Two t = times_log2e(two_sum(x, -m));
@@ -230,7 +236,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
                 c[i] = ex2((x[i] - m) * kLog2e);
                 z += c[i];
             } else {
-                c[i] = __frcp_rn(1.0f + ex2(-x[i] * kLog2e));
+                c[i] = reciprocal(1.0f + ex2(-x[i] * kLog2e));
             }
         }
         if (a.softmax) {
@@ -242,16 +248,27 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     if (scored) {
         // Softmax: e^-d, d = m - x, is off by 2.5 2^-24 d and ex2's 2^-22 of itself, below 2^-21 of the largest; z by 2^-22,
         // 2^-23 and half a step for each of EPL + 5 additions; the quotient by 2^-22: to 256 experts 2^-19 of the largest
-        // score.  Sigmoid, with u = e^-x: u / (1 + u) of u's 2.2 2^-24 |x| + 2^-22 reach s, 1 + u and the quotient round
-        // once each: 2^-22.
+        // score.  Sigmoid, with u = e^-x: u / (1 + u) of u's 2.2 2^-24 |x| + 2^-22 reach s, 1 + u rounds once, the
+        // reciprocal is within 2^-23: below 2^-21.
         const float to_score = a.softmax ? __fdividef(1.0f, z) : 1.0f;
-        slack = a.softmax ? (EPL <= 8 ? 0x1p-19f : 0x1p-18f) * to_score : 0x1p-22f;
+        slack = a.softmax ? (EPL <= 8 ? 0x1p-19f : 0x1p-18f) * to_score : 0x1p-21f;
+        float b[EPL] = {};
+        bool wide = false;
+        if constexpr (EPL >= 4) wide = a.bias && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0 && e0 + EPL <= experts;
+        if (wide) {
+            if constexpr (EPL >= 4) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            float b = 0.0f;
-            if (a.bias && e0 + i < experts) b = fminf(fmaxf(a.bias[e0 + i], -kMostBias), kMostBias);
-            c[i] = fmaf(c[i], to_score, b);
+                for (int i = 0; i < EPL; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
+                    b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+                }
+            }
+        } else if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) b[i] = e0 + i < experts ? a.bias[e0 + i] : 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] = fmaf(c[i], to_score, fminf(fmaxf(b[i], -kMostBias), kMostBias));
     }
     bool open = true;
     if (groups > 1) {
@@ -297,12 +314,16 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     uint32_t got = 0;
     float last = 0.0f;
     bool close = false;
-    for (; n < 33; ++n) {
-        uint32_t best = 0;
-        int at = 0;
+    uint32_t best = 0;
+    int at = 0;
+    auto look = [&]() {
+        best = 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (key[i] > best) best = key[i], at = i;
+    };
+    look();
+    for (; n < 33; ++n) {
         if (n >= topk && !by_score) break;
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         if (by_score) {
@@ -322,6 +343,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 if (i == at) key[i] = 0;
+            look();
         }
     }
     if (close) {
@@ -368,7 +390,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
 }
 
 template <bool F32, int EPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ MoeScoreArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kernel(const __grid_constant__ MoeScoreArgs a) {
     extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
     pdl_wait();
