@@ -252,6 +252,9 @@ class _Args:
 
 def _rows_contiguous(t):
     """Whether every t[i] is contiguous."""
+    if t.dim() == 3:
+        (_, h, d), (_, by_head, by_element) = t.shape, t.stride()
+        return (by_element == 1 or d == 1) and (by_head == d or h == 1)
     n = 1
     for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
         if size != 1 and stride != n:
@@ -263,14 +266,18 @@ def _rows_contiguous(t):
 def _checked(*specs):
     """_Args' checks of (name, tensor, dtype, numel or None, rows) in one
     quick pass; raises what _Args raises.  Returns the call's device."""
-    first = getattr(specs[0][1], "device", None)
-    for _, t, dtype, numel, rows in specs:
-        if (getattr(t, "device", None) != first or t.dtype != dtype or (numel is not None and t.numel() != numel)
-                or not (t.is_contiguous() or (rows and _rows_contiguous(t)))):
-            break
-    else:
-        if first.type == "cuda":
-            return first
+    try:
+        first = specs[0][1]
+        index = first.get_device()  # -1: not a GPU
+        if index >= 0:
+            for _, t, dtype, numel, rows in specs:
+                if (t.dtype is not dtype or t.get_device() != index or (numel is not None and t.numel() != numel)
+                        or not (t.is_contiguous() or (rows and _rows_contiguous(t)))):
+                    break
+            else:
+                return first.device
+    except (AttributeError, RuntimeError):  # not a tensor, or of a kind that is on no device
+        pass
     a = _Args()
     for name, t, dtype, numel, rows in specs:
         a.need(name, t, dtype, numel=numel, rows=rows)
@@ -793,23 +800,31 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
     return (out, lse) if return_lse else out
 
 
-def _rope_append(what, fn, q, k, v, positions, slots, cos_sin, cache_specs, cache_args, ptrs, q_norm, k_norm, eps,
-                 interleaved, out, stream):
+def _rope_append(what, fn, q, k, v, positions, slots, cos_sin, cache_specs, cache_args, k_scale, v_scale, k_cache, v_cache,
+                 q_norm, k_norm, eps, interleaved, out, stream):
     t, hq, d = q.shape
     max_pos, rot = _shape2(cos_sin, "cos_sin")
     bf16, i32 = torch.bfloat16, torch.int32
-    given = [spec for spec in (("q_norm", q_norm, bf16, d, False), ("k_norm", k_norm, bf16, d, False),
-                               ("out", out, bf16, t * hq * d, False)) if spec[1] is not None]
-    device = _checked(*cache_specs, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
-                      ("cos_sin", cos_sin, torch.float32, None, False), *given, ("q", q, bf16, None, True),
-                      ("k", k, bf16, None, True), ("v", v, bf16, None, True))
+    specs = [*cache_specs, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
+             ("cos_sin", cos_sin, torch.float32, None, False), ("q", q, bf16, None, True), ("k", k, bf16, None, True),
+             ("v", v, bf16, None, True)]
+    q_ptr = k_ptr = None
+    if q_norm is not None:
+        specs.append(("q_norm", q_norm, bf16, d, False))
+        q_ptr = q_norm.data_ptr()
+    if k_norm is not None:
+        specs.append(("k_norm", k_norm, bf16, d, False))
+        k_ptr = k_norm.data_ptr()
+    if out is not None:
+        specs.append(("out", out, bf16, t * hq * d, False))
+    device = _checked(*specs)
     if out is None:
         out = _empty(stream, device, (t, hq, d), bf16)
     _call(device, what, fn,
           (q.data_ptr(), _row_stride(q), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), t, hq, k.shape[1], d,
-           positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, int(interleaved),
-           q_norm.data_ptr() if q_norm is not None else None, k_norm.data_ptr() if k_norm is not None else None,
-           float(eps), out.data_ptr(), *(x.data_ptr() for x in ptrs), *cache_args), stream)
+           positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, interleaved, q_ptr, k_ptr, eps,
+           out.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *cache_args),
+          stream)
     return out
 
 
@@ -836,8 +851,8 @@ def kv_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache
     specs = (("k_cache", k_cache, u8, None, False), ("v_cache", v_cache, u8, None, False),
              ("k_scale", k_scale, f32, 1, False), ("v_scale", v_scale, f32, 1, False))
     return _rope_append("fp8kv_rope_append", lib().fp8kv_rope_append, q, k, v, positions, slots, cos_sin, specs,
-                        (k_cache.shape[0] * k_cache.shape[1],), (k_scale, v_scale, k_cache, v_cache), q_norm, k_norm, eps,
-                        interleaved, out, stream)
+                        (k_cache.shape[0] * k_cache.shape[1],), k_scale, v_scale, k_cache, v_cache, q_norm, k_norm,
+                        float(eps), int(interleaved), out, stream)
 
 
 def kv4_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm=None, k_norm=None,
@@ -846,7 +861,7 @@ def kv4_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cach
     _rope_shapes(q, k, v)
     specs, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, k.shape[1], k.shape[2])
     return _rope_append("fp4kv_rope_append", lib().fp4kv_rope_append, q, k, v, positions, slots, cos_sin, specs, (page, nb),
-                        (k_scale, v_scale, k_cache, v_cache), q_norm, k_norm, eps, interleaved, out, stream)
+                        k_scale, v_scale, k_cache, v_cache, q_norm, k_norm, float(eps), int(interleaved), out, stream)
 
 
 def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,

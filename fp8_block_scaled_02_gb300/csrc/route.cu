@@ -432,54 +432,80 @@ cudaError_t launch_route_epl(const MoeScoreArgs &a, cudaStream_t stream) {
 
 // --------------------------------------------------------------- combination
 // A thread has 8 consecutive columns of a token, 16 bytes of each of its
-// slots; kInFlight of them are loaded before the first is used.
+// slots.  A warp's lanes load the token's ids and weights, a slot each, at
+// once; kInFlight slots are loaded before the first is used.
 constexpr int kCombineThreads = 256;
 constexpr int kInFlight = 4;
 
+// The 8 columns from p on, of which `cols` are there, as bf16; no load unless `want`.  Without a branch, so that
+// several are in flight.
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int n, float (&x)[8]) {
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p, int cols, bool want) {
     if constexpr (VEC) {
-        const uint4 v = ld_v4(p);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[2 * j] = bf16lo_to_f32(u[j]), x[2 * j + 1] = bf16hi_to_f32(u[j]);
+        uint4 v;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+            "@p ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n\t}"
+            : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+            : "l"(p), "r"(want ? 1u : 0u));
+        return v;
     } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < n ? __bfloat162float(p[j]) : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = want && 2 * j < cols ? q[2 * j] : 0u, hi = want && 2 * j + 1 < cols ? q[2 * j + 1] : 0u;
+            w[j] = lo | hi << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void add8(const uint4 v, float w, float (&acc)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        acc[2 * j] = fmaf(w, bf16lo_to_f32(u[j]), acc[2 * j]);
+        acc[2 * j + 1] = fmaf(w, bf16hi_to_f32(u[j]), acc[2 * j + 1]);
     }
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const MoeCombineArgs a, int64_t per_row) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kCombineThreads + threadIdx.x;
-    const int64_t token = item / per_row, col = 8 * (item - token * per_row);
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const MoeCombineArgs a, uint32_t chunks) {
+    const int lane = threadIdx.x & 31;
+    const int64_t token = blockIdx.x / chunks;
+    const int64_t col = 8 * (static_cast<int64_t>(blockIdx.x - token * chunks) * blockDim.x + threadIdx.x);
     pdl_wait();
-    if (token >= a.tokens) return;
     const int topk = static_cast<int>(a.topk), cols = static_cast<int>(a.n - col < 8 ? a.n - col : 8);
+    const bool in = cols > 0;
     const __nv_bfloat16 *y = static_cast<const __nv_bfloat16 *>(a.y) + token * topk * a.n + col;
-    float acc[8] = {};
-    if (a.residual) load8<VEC>(static_cast<const __nv_bfloat16 *>(a.residual) + token * a.n + col, cols, acc);
-    for (int j0 = 0; j0 < topk; j0 += kInFlight) {
-        float w[kInFlight], x[kInFlight][8];
-        bool live[kInFlight];
+    const uint4 base = load8<VEC>(static_cast<const __nv_bfloat16 *>(a.residual) + token * a.n + col, cols, in && a.residual);
+    float acc[8];
+    for (int j0 = 0; j0 < topk; j0 += 32) {
+        // lane j: slot j0 + j
+        const bool there = j0 + lane < topk;
+        const int id = there && a.ids ? a.ids[token * topk + j0 + lane] : 0;
+        const float weight = there ? a.weights[token * topk + j0 + lane] : 0.0f;
+        const uint32_t live = __ballot_sync(0xffffffffu, there && (!a.ids || (id >= 0 && id < a.experts)));
+        const int slots = topk - j0 < 32 ? topk - j0 : 32;
+        for (int j = 0; j < slots; j += kInFlight) {
+            uint4 x[kInFlight];
 #pragma unroll
-        for (int i = 0; i < kInFlight; ++i) {
-            live[i] = j0 + i < topk;
-            if (live[i] && a.ids) {
-                const int id = a.ids[token * topk + j0 + i];
-                live[i] = id >= 0 && id < a.experts;
+            for (int i = 0; i < kInFlight; ++i)
+                x[i] = load8<VEC>(y + (j0 + j + i) * a.n, cols, in && j + i < slots && ((live >> ((j + i) & 31)) & 1));
+            if (j0 + j == 0) {
+                const uint32_t u[4] = {base.x, base.y, base.z, base.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[2 * k] = bf16lo_to_f32(u[k]), acc[2 * k + 1] = bf16hi_to_f32(u[k]);
             }
-            if (live[i]) {
-                w[i] = a.weights[token * topk + j0 + i];
-                load8<VEC>(y + (j0 + i) * a.n, cols, x[i]);
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) {
+                const float w = __shfl_sync(0xffffffffu, weight, (j + i) & 31);
+                if (j + i < slots && ((live >> ((j + i) & 31)) & 1)) add8(x[i], w, acc);  // the same for the whole warp
             }
         }
-#pragma unroll
-        for (int i = 0; i < kInFlight; ++i)
-            if (live[i])
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] = fmaf(w[i], x[i][j], acc[j]);
     }
+    if (!in) return;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.n + col;
     if constexpr (VEC) {
         *reinterpret_cast<uint4 *>(out) = make_uint4(f32x2_to_bf16x2(acc[0], acc[1]), f32x2_to_bf16x2(acc[2], acc[3]),
@@ -500,21 +526,23 @@ cudaError_t launch_moe_scores(const MoeScoreArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t stream) {
-    const int64_t per_row = (a.n + 7) / 8, items = a.tokens * per_row;
-    const int64_t blocks = (items + kCombineThreads - 1) / kCombineThreads;
+    // a CTA has one token's columns: as few warps as hold a short row
+    const int64_t per_row = (a.n + 7) / 8;
+    const int64_t threads = per_row >= kCombineThreads ? kCombineThreads : (per_row + 31) / 32 * 32;
+    const int64_t chunks = (per_row + threads - 1) / threads, blocks = a.tokens * chunks;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     const bool vec = a.n % 8 == 0 && aligned16(a.y) && aligned16(a.residual) && aligned16(a.out);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(kCombineThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return vec ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a, per_row)
-               : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a, per_row);
+    return vec ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a, static_cast<uint32_t>(chunks))
+               : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a, static_cast<uint32_t>(chunks));
 }
 
 }  // namespace fp8bs
