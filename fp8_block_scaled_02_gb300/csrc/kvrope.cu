@@ -24,6 +24,9 @@ namespace {
 __device__ uint32_t g_rope_err;
 
 constexpr int kRopeThreads = 256;
+#ifndef ROPE_B
+#define ROPE_B 4
+#endif
 
 // 1 / sqrt(h + l), |l| <= ulp(h): one rounding of y + y (1 - (h + l) y^2) / 2,
 // with y = rsqrtf(h) and the residual exact to 2^-24 of itself.
@@ -36,26 +39,20 @@ __device__ __forceinline__ float rsqrt_once(float h, float l) {
     return fma1(mul1(0.5f, y), e, y);
 }
 
-__device__ __forceinline__ uint2 ld_v2(const void *p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
-
 // The codes of x / s without a division: q = x (1 / s) is within 2^-23 of the
 // quotient, so if q (1 - 2^-21) and q (1 + 2^-21) have one code, the rounded
 // quotient has it too; a value near a border between codes is divided (one in
 // some hundred thousand).  encode(v) gives the codes of v[0 .. 7]; `recip` is RN(1 / s) for
 // s in [2^-100, 2^100], or 0: every value is divided.
 template <class Word, class Encode>
-__device__ __forceinline__ Word codes_of(const float (&x)[8], float s, float recip, Encode encode) {
+__device__ __forceinline__ Word codes_of(const uint64_t *x, float s, float recip, Encode encode) {
     float lo[8], hi[8];
     if (recip != 0.0f) {
         const uint64_t y2 = pair(recip, recip), down = pair(1.0f - 0x1p-21f, 1.0f - 0x1p-21f);
         const uint64_t up = pair(1.0f + 0x1p-21f, 1.0f + 0x1p-21f);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const uint64_t q = mul2(pair(x[j], x[j + 1]), y2);
+            const uint64_t q = mul2(x[j / 2], y2);
             unpair(mul2(q, down), lo[j], lo[j + 1]);
             unpair(mul2(q, up), hi[j], hi[j + 1]);
         }
@@ -63,39 +60,41 @@ __device__ __forceinline__ Word codes_of(const float (&x)[8], float s, float rec
         if (a == b) return a;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) lo[j] = __fdiv_rn(x[j], s);
+    for (int j = 0; j < 8; j += 2) {
+        float a, b;
+        unpair(x[j / 2], a, b);
+        lo[j] = __fdiv_rn(a, s), lo[j + 1] = __fdiv_rn(b, s);
+    }
     return encode(lo);
 }
 __device__ __forceinline__ float safe_reciprocal(float s) { return s >= 0x1p-100f && s <= 0x1p100f ? __frcp_rn(s) : 0.0f; }
 
 enum RopeKind : int { kRopeQ = 0, kRopeK = 1, kRopeV = 2 };
 
-// A lane has 8 elements of each of its heads, in pairs of four: of a query, or
-// of pairs that are neighbours, the elements that turn together; of a key with
-// halves, and of a value, 8 consecutive ones, because a group of a 4-bit cache
-// is 16.  first, second: where the lane's two fours begin.
-struct Fours {
-    int first, second;
-    bool turns;
-};
-template <int D, bool NEXT>
-__device__ __forceinline__ Fours fours_of(int kind, int l, int rot) {
-    const int half = rot / 2;
-    if (kind == kRopeQ && !NEXT) {
-        if (4 * l < half) return Fours{4 * l, half + 4 * l, true};
-        return Fours{8 * l, 8 * l + 4, false};  // 8 (l - half / 4) past the rotated ones
-    }
-    return Fours{8 * l, 8 * l + 4, 8 * l < rot};
+// Eight bf16 numbers to pairs of fp32: (0, 1), (2, 3), ...
+__device__ __forceinline__ void unpack8(uint4 u, uint64_t *x) {
+    x[0] = pair(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x)), x[1] = pair(bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+    x[2] = pair(bf16lo_to_f32(u.z), bf16hi_to_f32(u.z)), x[3] = pair(bf16lo_to_f32(u.w), bf16hi_to_f32(u.w));
 }
-
-__device__ __forceinline__ void unpack4(uint2 u, uint64_t &a, uint64_t &b) {
-    a = pair(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x));
-    b = pair(bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+// Sixteen to the even ones, (0, 2), (4, 6), ..., and the odd ones.
+__device__ __forceinline__ void unpack_apart(uint4 u, uint4 v, uint64_t *even, uint64_t *odd) {
+    even[0] = pair(bf16lo_to_f32(u.x), bf16lo_to_f32(u.y)), odd[0] = pair(bf16hi_to_f32(u.x), bf16hi_to_f32(u.y));
+    even[1] = pair(bf16lo_to_f32(u.z), bf16lo_to_f32(u.w)), odd[1] = pair(bf16hi_to_f32(u.z), bf16hi_to_f32(u.w));
+    even[2] = pair(bf16lo_to_f32(v.x), bf16lo_to_f32(v.y)), odd[2] = pair(bf16hi_to_f32(v.x), bf16hi_to_f32(v.y));
+    even[3] = pair(bf16lo_to_f32(v.z), bf16lo_to_f32(v.w)), odd[3] = pair(bf16hi_to_f32(v.z), bf16hi_to_f32(v.w));
 }
 __device__ __forceinline__ uint32_t pack2(uint64_t v) {
     float a, b;
     unpair(v, a, b);
     return f32x2_to_bf16x2(a, b);
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t *x) { return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3])); }
+// (x0, y0), (x1, y1) of the pairs (x0, x1), (y0, y1)
+__device__ __forceinline__ void pack_together(uint64_t x, uint64_t y, uint32_t &a, uint32_t &b) {
+    float x0, x1, y0, y1;
+    unpair(x, x0, x1);
+    unpair(y, y0, y1);
+    a = f32x2_to_bf16x2(x0, y0), b = f32x2_to_bf16x2(x1, y1);
 }
 __device__ __forceinline__ uint64_t neg2(uint64_t v) { return v ^ 0x8000000080000000ull; }
 
@@ -107,123 +106,152 @@ __device__ __forceinline__ uint64_t add_apart(uint64_t a, uint64_t b) {
     unpair(b, b0, b1);
     return pair(add1(a0, b0), add1(a1, b1));
 }
-
-// Queries.  x: the pairs' first elements, y: their second ones, two and two.
-template <int D, int N, bool NEXT>
-__device__ __forceinline__ void rope_queries(const KvRopeArgs &a, const uint4 (&raw)[N], const uint4 weights, const Fours at,
-                                             int64_t token, int position, int head0) {
-    constexpr int kLanes = D / 8, kTeams = 32 / kLanes;
-    const int lane = threadIdx.x & 31, l = lane % kLanes, team = lane / kLanes;
-    const int heads = static_cast<int>(a.q_heads), rot = static_cast<int>(a.rot_dim);
-    uint64_t c[2] = {}, s[2] = {}, wx[2] = {}, wy[2] = {};
-    if (at.turns) {
-        const float *row = a.cos_sin + static_cast<int64_t>(position) * rot + 4 * l;
-        const float4 cc = *reinterpret_cast<const float4 *>(row), ss = *reinterpret_cast<const float4 *>(row + rot / 2);
-        c[0] = pair(cc.x, cc.y), c[1] = pair(cc.z, cc.w), s[0] = pair(ss.x, ss.y), s[1] = pair(ss.z, ss.w);
-    }
-    // neighbours: (x0, y0), (x1, y1), ... to (x0, x1), (y0, y1), ...
-    auto split = [&](uint4 u, uint64_t (&x)[2], uint64_t (&y)[2]) {
-        if constexpr (NEXT) {
-            x[0] = pair(bf16lo_to_f32(u.x), bf16lo_to_f32(u.y)), y[0] = pair(bf16hi_to_f32(u.x), bf16hi_to_f32(u.y));
-            x[1] = pair(bf16lo_to_f32(u.z), bf16lo_to_f32(u.w)), y[1] = pair(bf16hi_to_f32(u.z), bf16hi_to_f32(u.w));
-        } else {
-            unpack4(make_uint2(u.x, u.y), x[0], x[1]);
-            unpack4(make_uint2(u.z, u.w), y[0], y[1]);
-        }
-    };
-    const bool norm = a.q_weight != nullptr;
-    if (norm) split(weights, wx, wy);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int h = head0 + i * kTeams + team;
-        uint64_t x[2], y[2];
-        split(raw[i], x, y);
-        if (norm) {
-            const uint64_t sq = fma2(y[1], y[1], fma2(y[0], y[0], fma2(x[1], x[1], mul2(x[0], x[0]))));
-            float s0, s1;
-            unpair(sq, s0, s1);
-            float sum = s0 + s1;
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float r = rsqrt_once(fmaf(sum, 1.0f / D, a.eps), 0.0f);
-            const uint64_t r2 = pair(r, r);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], r2), wx[j]), y[j] = mul2(mul2(y[j], r2), wy[j]);
-        }
-        if (at.turns) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint64_t o1 = add_apart(mul2(x[j], c[j]), neg2(mul2(y[j], s[j])));
-                y[j] = add_apart(mul2(y[j], c[j]), mul2(x[j], s[j]));
-                x[j] = o1;
-            }
-        }
-        if (h < heads) {
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.q_out) + (token * heads + h) * D;
-            if constexpr (NEXT) {
-                float x0, x1, x2, x3, y0, y1, y2, y3;
-                unpair(x[0], x0, x1), unpair(x[1], x2, x3), unpair(y[0], y0, y1), unpair(y[1], y2, y3);
-                *reinterpret_cast<uint4 *>(out + at.first) =
-                    make_uint4(f32x2_to_bf16x2(x0, y0), f32x2_to_bf16x2(x1, y1), f32x2_to_bf16x2(x2, y2), f32x2_to_bf16x2(x3, y3));
-            } else {
-                *reinterpret_cast<uint2 *>(out + at.first) = make_uint2(pack2(x[0]), pack2(x[1]));
-                *reinterpret_cast<uint2 *>(out + at.second) = make_uint2(pack2(y[0]), pack2(y[1]));
-            }
-        }
-    }
+__device__ __forceinline__ uint64_t sub_apart(uint64_t a, uint64_t b) {
+    float a0, a1, b0, b1;
+    unpair(a, a0, a1);
+    unpair(b, b0, b1);
+    return pair(sub1(a0, b0), sub1(a1, b1));
+}
+__device__ __forceinline__ void load_pairs8(const float *p, uint64_t *x) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = pair(a.x, a.y), x[1] = pair(a.z, a.w), x[2] = pair(b.x, b.y), x[3] = pair(b.z, b.w);
 }
 
-// Keys and values: 8 consecutive elements a lane.
-template <int D, int N, bool F4, bool KEYS, bool NEXT>
-__device__ __forceinline__ void rope_cached(const KvRopeArgs &a, const uint4 (&raw)[N], const uint4 weights, float scale,
-                                            int64_t token, int64_t slot, int position, int head0) {
-    constexpr int kLanes = D / 8, kTeams = 32 / kLanes;
-    const int lane = threadIdx.x & 31, l = lane % kLanes, team = lane / kLanes;
-    const int heads = static_cast<int>(a.kv_heads), rot = static_cast<int>(a.rot_dim), half = rot / 2;
-    const bool norm = KEYS && a.k_weight != nullptr, turns = KEYS && 8 * l < rot, low = 8 * l < half;
-    uint64_t w[4] = {}, c[4] = {}, s[4] = {};
-    if (norm) {
-        unpack4(make_uint2(weights.x, weights.y), w[0], w[1]);
-        unpack4(make_uint2(weights.z, weights.w), w[2], w[3]);
+// A head is D / 16 lanes' of 16 elements each.  Of a query with halves a lane has
+// eight elements and the eight that turn with them; else 16 consecutive ones,
+// neighbours that turn together or, of a key or value, a group of the 4-bit cache.
+template <int D>
+struct Lanes {
+    static constexpr int kPerHead = D / 16, kHeads = 32 / kPerHead;
+    int l, head;  // lane of the head, head of the warp
+    __device__ __forceinline__ Lanes() : l(threadIdx.x % kPerHead), head((threadIdx.x & 31) / kPerHead) {}
+};
+
+template <int D, bool NEXT>
+__device__ __forceinline__ void rope_queries(const KvRopeArgs &a, int64_t token, int part) {
+    using L = Lanes<D>;
+    const L me;
+    const int heads = static_cast<int>(a.q_heads), h = part * L::kHeads + me.head, rot = static_cast<int>(a.rot_dim);
+    const int half = rot / 2;
+    const bool turns = 8 * me.l < half, there = h < heads;
+    const int first = NEXT || !turns ? 16 * me.l : 8 * me.l, second = NEXT || !turns ? first + 8 : half + 8 * me.l;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + token * a.q_stride + h * D;
+    const int position = a.positions[token];
+    uint4 u = make_uint4(0, 0, 0, 0), v = u, wu = u, wv = u;
+    if (there) u = ld_v4(src + first), v = ld_v4(src + second);
+    const __nv_bfloat16 *wp = static_cast<const __nv_bfloat16 *>(a.q_weight);
+    if (wp) wu = *reinterpret_cast<const uint4 *>(wp + first), wv = *reinterpret_cast<const uint4 *>(wp + second);
+    if (position < 0 || position >= a.max_pos) {
+        if (position != -1 && part == 0 && (threadIdx.x & 31) == 0) atomicOr(&g_rope_err, ERRBIT_INDEX);
+        return;
+    }
+    uint64_t c[4], s[4], x[4], y[4];
+    if (turns) {
+        const float *row = a.cos_sin + static_cast<int64_t>(position) * rot + 8 * me.l;
+        load_pairs8(row, c);
+        load_pairs8(row + half, s);
+    }
+    if constexpr (NEXT) {
+        unpack_apart(u, v, x, y);
+    } else {
+        unpack8(u, x);
+        unpack8(v, y);
+    }
+    if (wp) {
+        uint64_t sq = mul2(x[0], x[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) sq = fma2(x[j], x[j], sq);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sq = fma2(y[j], y[j], sq);
+        float s0, s1;
+        unpair(sq, s0, s1);
+        float sum = s0 + s1;
+#pragma unroll
+        for (int o = L::kPerHead / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = rsqrt_once(fmaf(sum, 1.0f / D, a.eps), 0.0f);
+        const uint64_t r2 = pair(r, r);
+        uint64_t wx[4], wy[4];
+        if constexpr (NEXT) {
+            unpack_apart(wu, wv, wx, wy);
+        } else {
+            unpack8(wu, wx);
+            unpack8(wv, wy);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], r2), wx[j]), y[j] = mul2(mul2(y[j], r2), wy[j]);
     }
     if (turns) {
-        const float *row = a.cos_sin + static_cast<int64_t>(position) * rot;
-        if constexpr (NEXT) {
-            const float4 cc = *reinterpret_cast<const float4 *>(row + 4 * l);
-            const float4 ss = *reinterpret_cast<const float4 *>(row + half + 4 * l);
-            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = pair(cv[j], cv[j]), s[j] = pair(-sv[j], sv[j]);
-        } else {
-            const float *p = row + (low ? 8 * l : 8 * l - half);
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const float4 cc = *reinterpret_cast<const float4 *>(p + 2 * j);
-                const float4 ss = *reinterpret_cast<const float4 *>(p + half + 2 * j);
-                c[j] = pair(cc.x, cc.y), c[j + 1] = pair(cc.z, cc.w);
-                s[j] = pair(ss.x, ss.y), s[j + 1] = pair(ss.z, ss.w);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = low ? neg2(s[j]) : s[j];
+        for (int j = 0; j < 4; ++j) {
+            const uint64_t o1 = sub_apart(mul2(x[j], c[j]), mul2(y[j], s[j]));
+            y[j] = add_apart(mul2(y[j], c[j]), mul2(x[j], s[j]));
+            x[j] = o1;
         }
     }
-    // the lane with the other elements of this lane's pairs
-    const int partner = !turns ? lane : low ? lane + half / 8 : lane - half / 8;
-    uint8_t *cache = KEYS ? a.k_cache : a.v_cache;
-    const float recip = safe_reciprocal(scale);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int h = head0 + i * kTeams + team;
-        uint64_t v[4];
-        unpack4(make_uint2(raw[i].x, raw[i].y), v[0], v[1]);
-        unpack4(make_uint2(raw[i].z, raw[i].w), v[2], v[3]);
-        if (norm) {
+    if (!there) return;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.q_out) + (token * heads + h) * D;
+    if constexpr (NEXT) {
+        pack_together(x[0], y[0], u.x, u.y), pack_together(x[1], y[1], u.z, u.w);
+        pack_together(x[2], y[2], v.x, v.y), pack_together(x[3], y[3], v.z, v.w);
+    } else {
+        u = pack8(x), v = pack8(y);
+    }
+    *reinterpret_cast<uint4 *>(out + first) = u;
+    *reinterpret_cast<uint4 *>(out + second) = v;
+}
+
+// ODD: halves of an odd number of eights, whose lanes have eights that turn with another lane's other eight.
+template <int D, bool F4, bool KEYS, bool NEXT, bool ODD>
+__device__ __forceinline__ void rope_cached(const KvRopeArgs &a, int64_t token, int part) {
+    using L = Lanes<D>;
+    const L me;
+    const int heads = static_cast<int>(a.kv_heads), h = part * L::kHeads + me.head, rot = static_cast<int>(a.rot_dim);
+    const int half = rot / 2, lane = threadIdx.x & 31;
+    const bool there = h < heads, turns = KEYS && 16 * me.l < rot;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(KEYS ? a.k : a.v) +
+                               token * (KEYS ? a.k_stride : a.v_stride) + h * D + 16 * me.l;
+    const int position = a.positions[token];
+    const int64_t slot = a.slots[token];
+    const float scale = *(KEYS ? a.k_scale : a.v_scale);
+    uint4 u = make_uint4(0, 0, 0, 0), v = u, wu = u, wv = u;
+    if (there) u = ld_v4(src), v = ld_v4(src + 8);
+    const __nv_bfloat16 *wp = KEYS ? static_cast<const __nv_bfloat16 *>(a.k_weight) : nullptr;
+    if (wp) wu = *reinterpret_cast<const uint4 *>(wp + 16 * me.l), wv = *reinterpret_cast<const uint4 *>(wp + 16 * me.l + 8);
+    if (position < 0 || position >= a.max_pos) return;
+    if (slot < 0 || slot >= a.num_slots) {
+        if (KEYS && slot != -1 && part == 0 && lane == 0) atomicOr(&g_rope_err, ERRBIT_INDEX);
+        return;
+    }
+    uint64_t x[8];
+    if (KEYS && NEXT) {
+        unpack_apart(u, v, x, x + 4);  // the even ones, then the odd ones
+    } else {
+        unpack8(u, x);
+        unpack8(v, x + 4);
+    }
+    if (KEYS) {
+        uint64_t c[8], s[8];
+        const float *row = a.cos_sin + static_cast<int64_t>(position) * rot;
+        const bool low = 16 * me.l < half;
+        if (turns) {
+            if (NEXT) {
+                load_pairs8(row + 8 * me.l, c);
+                load_pairs8(row + half + 8 * me.l, s);
+            } else {
+                const int e0 = 16 * me.l, e1 = e0 + 8, at0 = e0 < half ? e0 : e0 - half, at1 = e1 < half ? e1 : e1 - half;
+                load_pairs8(row + at0, c);
+                load_pairs8(row + half + at0, s);
+                load_pairs8(row + at1, c + 4);
+                load_pairs8(row + half + at1, s + 4);
+            }
+        }
+        if (wp) {
             // two sums of exact squares, each with what its roundings lost
-            uint64_t sum = mul2(v[0], v[0]), rest = 0;
+            uint64_t sum = mul2(x[0], x[0]), rest = 0;
 #pragma unroll
-            for (int j = 1; j < 4; ++j) {
-                const uint64_t t = fma2(v[j], v[j], sum), z = add2(t, neg2(sum));
-                rest = add2(rest, add2(add2(sum, neg2(add2(t, neg2(z)))), fma2(v[j], v[j], neg2(z))));
+            for (int j = 1; j < 8; ++j) {
+                const uint64_t t = fma2(x[j], x[j], sum), z = add2(t, neg2(sum));
+                rest = add2(rest, add2(add2(sum, neg2(add2(t, neg2(z)))), fma2(x[j], x[j], neg2(z))));
                 sum = t;
             }
             float s0, s1, r0, r1;
@@ -232,7 +260,7 @@ __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, const uint4 (&r
             Two all = two_sum(s0, s1);
             all.l += r0 + r1;
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) {
+            for (int o = L::kPerHead / 2; o > 0; o >>= 1) {
                 const float oh = __shfl_xor_sync(0xffffffffu, all.h, o), ol = __shfl_xor_sync(0xffffffffu, all.l, o);
                 const Two t = two_sum(all.h, oh);
                 all = Two{t.h, add1(add1(all.l, ol), t.l)};
@@ -240,126 +268,138 @@ __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, const uint4 (&r
             const Two m = two_sum(mul1(all.h, 1.0f / D), a.eps);
             const float r = rsqrt_once(m.h, fma1(all.l, 1.0f / D, m.l));
             const uint64_t r2 = pair(r, r);
+            uint64_t w[8];
+            if (NEXT) {
+                unpack_apart(wu, wv, w, w + 4);
+            } else {
+                unpack8(wu, w);
+                unpack8(wv, w + 4);
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(v[j], r2), w[j]);
+            for (int j = 0; j < 8; ++j) x[j] = mul2(mul2(x[j], r2), w[j]);
         }
-        float x[8];
+        if constexpr (NEXT) {
+            if (turns) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) unpair(v[j], x[2 * j], x[2 * j + 1]);
-        if (KEYS) {
+                for (int j = 0; j < 4; ++j) {
+                    const uint64_t o1 = sub_apart(mul2(x[j], c[j]), mul2(x[j + 4], s[j]));
+                    x[j + 4] = add_apart(mul2(x[j + 4], c[j]), mul2(x[j], s[j]));
+                    x[j] = o1;
+                }
+            }
+            // back to the elements' order
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint64_t other;
-                if constexpr (NEXT) other = pair(x[2 * j + 1], x[2 * j]);
-                else other = pair(__shfl_sync(0xffffffffu, x[2 * j], partner), __shfl_sync(0xffffffffu, x[2 * j + 1], partner));
-                v[j] = turns ? add_apart(mul2(v[j], c[j]), mul2(other, s[j])) : v[j];
+                float x0, x1, y0, y1;
+                unpair(x[j], x0, x1);
+                unpair(x[j + 4], y0, y1);
+                x[j] = pair(x0, y0), x[j + 4] = pair(x1, y1);
             }
+            const uint64_t t[8] = {x[0], x[4], x[1], x[5], x[2], x[6], x[3], x[7]};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) unpair(v[j], x[2 * j], x[2 * j + 1]);
-        }
-        if constexpr (F4) {
-            // a group is two lanes; NaN is above every magnitude
-            uint32_t mx = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            const uint32_t sc = f32x2_to_e4m3x2(__fdiv_rn(__uint_as_float(mx), mul1(6.0f, scale)), 0.0f) & 0xFFu;
-            const float den = mul1(f16x2_to_f32x2(e4m3x2_to_f16x2(sc)).x, scale);
-            uint32_t codes = 0;
-            if (den > 0.0f)
-                codes = codes_of<uint32_t>(x, den, safe_reciprocal(den), [](const float (&q)[8]) { return f32x8_to_e2m1x8(q); });
-            if (h < heads) {
-                const uint32_t tpp = static_cast<uint32_t>(a.page_size / kKv4Tile);
-                const uint32_t tile = static_cast<uint32_t>(slot) / kKv4Tile, row = static_cast<uint32_t>(slot) % kKv4Tile;
-                const uint32_t blk = tile / tpp;
-                uint8_t *t = cache + ((static_cast<int64_t>(blk) * heads + h) * tpp + (tile - blk * tpp)) * kv4_tile_bytes(D);
-                *reinterpret_cast<uint32_t *>(t + row * (D / 2) + 4 * l) = codes;
-                if ((l & 1) == 0) t[8 * D + row * (D / 16) + l / 2] = static_cast<uint8_t>(sc);
-            }
+            for (int j = 0; j < 8; ++j) x[j] = t[j];
         } else {
-            const uint64_t codes = codes_of<uint64_t>(x, scale, recip, [](const float (&q)[8]) {
-                uint32_t o[2];
+            // the other elements of the pairs: eight of this lane's are with eight half a rotation away
+            const int apart = half / 8;  // in eights; a lane has two of them
+            uint64_t o[8];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    o[j] = f32x2_to_e4m3x2(q[4 * j], q[4 * j + 1]) |
-                           static_cast<uint32_t>(f32x2_to_e4m3x2(q[4 * j + 2], q[4 * j + 3])) << 16;
-                return static_cast<uint64_t>(o[1]) << 32 | o[0];
-            });
-            if (h < heads) *reinterpret_cast<uint64_t *>(cache + (slot * heads + h) * D + 8 * l) = codes;
+            for (int k = 0; k < 2; ++k) {
+                const int mine = 2 * me.l + k, partner = mine < apart ? mine + apart : mine - apart;
+                const int from = turns ? (lane - me.l) + (partner >> 1) : lane;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float a0, a1;
+                    unpair(x[4 * (ODD ? 1 - k : k) + j], a0, a1);
+                    o[4 * k + j] = pair(__shfl_sync(0xffffffffu, a0, from), __shfl_sync(0xffffffffu, a1, from));
+                }
+            }
+            if (turns) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool first = ODD ? 2 * me.l + (j >> 2) < apart : low;
+                    const uint64_t p = mul2(o[j], s[j]);
+                    x[j] = add_apart(mul2(x[j], c[j]), first ? neg2(p) : p);
+                }
+            }
         }
+    }
+    uint8_t *cache = KEYS ? a.k_cache : a.v_cache;
+    if constexpr (F4) {
+        // a lane has a group; NaN is above every magnitude
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float a0, a1;
+            unpair(x[j], a0, a1);
+            mx = max(mx, max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(a1) & 0x7FFFFFFFu));
+        }
+        const uint32_t sc = f32x2_to_e4m3x2(__fdiv_rn(__uint_as_float(mx), mul1(6.0f, scale)), 0.0f) & 0xFFu;
+        const float den = mul1(f16x2_to_f32x2(e4m3x2_to_f16x2(sc)).x, scale);
+        uint2 codes = make_uint2(0, 0);
+        if (den > 0.0f) {
+            const float recip = safe_reciprocal(den);
+            auto encode = [](const float (&q)[8]) { return f32x8_to_e2m1x8(q); };
+            codes.x = codes_of<uint32_t>(x, den, recip, encode);
+            codes.y = codes_of<uint32_t>(x + 4, den, recip, encode);
+        }
+        if (there) {
+            const uint32_t tpp = static_cast<uint32_t>(a.page_size / kKv4Tile);
+            const uint32_t tile = static_cast<uint32_t>(slot) / kKv4Tile, row = static_cast<uint32_t>(slot) % kKv4Tile;
+            const uint32_t blk = tile / tpp;
+            uint8_t *t = cache + ((static_cast<int64_t>(blk) * heads + h) * tpp + (tile - blk * tpp)) * kv4_tile_bytes(D);
+            *reinterpret_cast<uint2 *>(t + row * (D / 2) + 8 * me.l) = codes;
+            t[8 * D + row * (D / 16) + me.l] = static_cast<uint8_t>(sc);
+        }
+    } else {
+        const float recip = safe_reciprocal(scale);
+        auto encode = [](const float (&q)[8]) {
+            uint32_t o[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                o[j] = f32x2_to_e4m3x2(q[4 * j], q[4 * j + 1]) |
+                       static_cast<uint32_t>(f32x2_to_e4m3x2(q[4 * j + 2], q[4 * j + 3])) << 16;
+            return static_cast<uint64_t>(o[1]) << 32 | o[0];
+        };
+        const uint64_t c0 = codes_of<uint64_t>(x, scale, recip, encode), c1 = codes_of<uint64_t>(x + 4, scale, recip, encode);
+        if (there)
+            *reinterpret_cast<uint4 *>(cache + (slot * heads + h) * D + 16 * me.l) =
+                make_uint4(static_cast<uint32_t>(c0), static_cast<uint32_t>(c0 >> 32), static_cast<uint32_t>(c1),
+                           static_cast<uint32_t>(c1 >> 32));
     }
 }
 
-// A warp has up to N * (256 / D) heads of one kind of one token; q_warps and
-// kv_warps of them make a token's q, k and v.  `inverse` = ceil(2^64 / warps a
-// token) divides every warp number below 2^47 exactly by a multiplication.  The
-// heads are loaded before the token's place is known: two loads one after the
-// other to the cos and sin instead of three.
-template <int D, int N, bool F4, bool NEXT>
-__global__ void __launch_bounds__(kRopeThreads, 6) kv_rope_kernel(const KvRopeArgs a, uint64_t inverse, int q_warps, int kv_warps) {
-    constexpr int kHeads = N * (256 / D), kLanes = D / 8, kTeams = 32 / kLanes;
-    const int lane = threadIdx.x & 31, l = lane % kLanes, team = lane / kLanes;
-    const uint64_t warp = static_cast<uint64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    const int64_t token = static_cast<int64_t>(__umul64hi(warp, inverse));
-    const int part = static_cast<int>(warp - token * (q_warps + 2 * kv_warps));
-    const int kind = part < q_warps ? kRopeQ : part < q_warps + kv_warps ? kRopeK : kRopeV;
-    const int at = kind == kRopeQ ? part : kind == kRopeK ? part - q_warps : part - q_warps - kv_warps;
+// A warp has 512 / D heads of one kind of one token: 2 * kv_blocks CTAs of keys
+// and values, which take longer, come before those of queries.  The inverses are
+// ceil(2^64 / warps a token), which divide every warp number below 2^47 exactly by
+// a multiplication (0: one warp).  A token's place, its heads and the weights are
+// one round trip, cos and sin the second.
+template <int D, bool F4, bool NEXT, bool ODD>
+__global__ void __launch_bounds__(kRopeThreads, ROPE_B) kv_rope_kernel(const __grid_constant__ KvRopeArgs a, uint32_t kv_blocks,
+                                                                       uint64_t kv_inverse, uint64_t q_inverse) {
+    using L = Lanes<D>;
+    const bool q = blockIdx.x >= 2 * kv_blocks;
+    const uint32_t block = q ? blockIdx.x - 2 * kv_blocks : blockIdx.x >> 1;
+    const uint64_t warp = static_cast<uint64_t>(block) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const uint64_t inverse = q ? q_inverse : kv_inverse;
+    const int64_t token = static_cast<int64_t>(inverse ? __umul64hi(warp, inverse) : warp);
+    const uint32_t heads = static_cast<uint32_t>(q ? a.q_heads : a.kv_heads), per = (heads + L::kHeads - 1) / L::kHeads;
+    const int part = static_cast<int>(warp - token * per);
     pdl_wait();
     if (token >= a.tokens) return;
-    const int heads = static_cast<int>(kind == kRopeQ ? a.q_heads : a.kv_heads), head0 = at * kHeads;
-    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(kind == kRopeQ ? a.q : kind == kRopeK ? a.k : a.v) +
-                               token * (kind == kRopeQ ? a.q_stride : kind == kRopeK ? a.k_stride : a.v_stride);
-    const int position = a.positions[token];
-    const int64_t slot = a.slots[token];
-    const Fours f = fours_of<D, NEXT>(kind, l, static_cast<int>(a.rot_dim));
-    uint4 raw[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int h = head0 + i * kTeams + team;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (h < heads) {
-            if (f.second == f.first + 4) {
-                raw[i] = ld_v4(src + h * D + f.first);
-            } else {
-                const uint2 u = ld_v2(src + h * D + f.first), v = ld_v2(src + h * D + f.second);
-                raw[i] = make_uint4(u.x, u.y, v.x, v.y);
-            }
-        }
-    }
-    // what all tokens share, in the same round trip
-    const __nv_bfloat16 *wp = static_cast<const __nv_bfloat16 *>(kind == kRopeQ ? a.q_weight : kind == kRopeK ? a.k_weight : nullptr);
-    uint4 weights = make_uint4(0, 0, 0, 0);
-    if (wp) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(wp + f.first), v = *reinterpret_cast<const uint2 *>(wp + f.second);
-        weights = make_uint4(u.x, u.y, v.x, v.y);
-    }
-    const float scale = *(kind == kRopeV ? a.v_scale : a.k_scale);
-    if (position < 0 || position >= a.max_pos) {
-        if (position != -1 && part == 0 && lane == 0) atomicOr(&g_rope_err, ERRBIT_INDEX);
-        return;
-    }
-    if (kind == kRopeQ) {
-        rope_queries<D, N, NEXT>(a, raw, weights, f, token, position, head0);
-        return;
-    }
-    if (slot < 0 || slot >= a.num_slots) {
-        if (slot != -1 && at == 0 && kind == kRopeK && lane == 0) atomicOr(&g_rope_err, ERRBIT_INDEX);
-        return;
-    }
-    if (kind == kRopeK) rope_cached<D, N, F4, true, NEXT>(a, raw, weights, scale, token, slot, position, head0);
-    else rope_cached<D, N, F4, false, NEXT>(a, raw, weights, scale, token, slot, position, head0);
+    if (q) rope_queries<D, NEXT>(a, token, part);
+    else if (blockIdx.x & 1) rope_cached<D, F4, false, NEXT, ODD>(a, token, part);
+    else rope_cached<D, F4, true, NEXT, ODD>(a, token, part);
 }
 
-template <int D, int N, bool F4, bool NEXT>
-cudaError_t launch_rope(const KvRopeArgs &a, cudaStream_t stream) {
-    constexpr int64_t kHeads = N * (256 / D);
-    const int64_t q_warps = (a.q_heads + kHeads - 1) / kHeads, kv_warps = (a.kv_heads + kHeads - 1) / kHeads;
-    const int64_t per_token = q_warps + 2 * kv_warps, warps = a.tokens * per_token, per = kRopeThreads / 32;
-    const int64_t blocks = (warps + per - 1) / per;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const uint64_t inverse = ~uint64_t{0} / static_cast<uint64_t>(per_token) + 1;  // per_token >= 3
+template <int D, bool F4, bool NEXT, bool ODD>
+cudaError_t launch_rope_t(const KvRopeArgs &a, cudaStream_t stream) {
+    constexpr int64_t kHeads = Lanes<D>::kHeads, kWarps = kRopeThreads / 32;
+    const int64_t q_per = (a.q_heads + kHeads - 1) / kHeads, kv_per = (a.kv_heads + kHeads - 1) / kHeads;
+    const int64_t q_blocks = (a.tokens * q_per + kWarps - 1) / kWarps, kv_blocks = (a.tokens * kv_per + kWarps - 1) / kWarps;
+    if (q_blocks + 2 * kv_blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    auto inverse = [](int64_t per) { return per == 1 ? uint64_t{0} : ~uint64_t{0} / static_cast<uint64_t>(per) + 1; };
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(q_blocks + 2 * kv_blocks), 1, 1);
     cfg.blockDim = dim3(kRopeThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -367,22 +407,21 @@ cudaError_t launch_rope(const KvRopeArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_rope_kernel<D, N, F4, NEXT>, a, inverse, static_cast<int>(q_warps),
-                              static_cast<int>(kv_warps));
+    return cudaLaunchKernelEx(&cfg, kv_rope_kernel<D, F4, NEXT, ODD>, a, static_cast<uint32_t>(kv_blocks), inverse(kv_per),
+                              inverse(q_per));
 }
 
-template <int D, bool F4, bool NEXT>
-cudaError_t launch_rope_split(const KvRopeArgs &a, cudaStream_t stream) {
-    return a.tokens >= 512 ? launch_rope<D, 2, F4, NEXT>(a, stream) : launch_rope<D, 1, F4, NEXT>(a, stream);
+template <int D, bool F4>
+cudaError_t launch_rope(const KvRopeArgs &a, cudaStream_t stream) {
+    if (a.interleaved) return launch_rope_t<D, F4, true, false>(a, stream);
+    return a.rot_dim % 32 == 0 ? launch_rope_t<D, F4, false, false>(a, stream) : launch_rope_t<D, F4, false, true>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_rope(const KvRopeArgs &a, bool four_bit, cudaStream_t stream) {
-    if (!four_bit) return a.interleaved ? launch_rope_split<128, false, true>(a, stream) : launch_rope_split<128, false, false>(a, stream);
-    if (a.head_dim == 128)
-        return a.interleaved ? launch_rope_split<128, true, true>(a, stream) : launch_rope_split<128, true, false>(a, stream);
-    return a.interleaved ? launch_rope_split<64, true, true>(a, stream) : launch_rope_split<64, true, false>(a, stream);
+    if (!four_bit) return launch_rope<128, false>(a, stream);
+    return a.head_dim == 128 ? launch_rope<128, true>(a, stream) : launch_rope<64, true>(a, stream);
 }
 
 uint32_t take_rope_error() {
