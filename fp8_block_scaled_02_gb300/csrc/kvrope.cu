@@ -23,10 +23,7 @@ namespace {
 
 __device__ uint32_t g_rope_err;
 
-constexpr int kRopeThreads = 256;
-#ifndef ROPE_B
-#define ROPE_B 4
-#endif
+constexpr int kRopeThreads = 128;
 
 // 1 / sqrt(h + l), |l| <= ulp(h): one rounding of y + y (1 - (h + l) y^2) / 2,
 // with y = rsqrtf(h) and the residual exact to 2^-24 of itself.
@@ -117,9 +114,9 @@ __device__ __forceinline__ void load_pairs8(const float *p, uint64_t *x) {
     x[0] = pair(a.x, a.y), x[1] = pair(a.z, a.w), x[2] = pair(b.x, b.y), x[3] = pair(b.z, b.w);
 }
 
-// A head is D / 16 lanes' of 16 elements each.  Of a query with halves a lane has
-// eight elements and the eight that turn with them; else 16 consecutive ones,
-// neighbours that turn together or, of a key or value, a group of the 4-bit cache.
+// A head is D / 16 lanes' of 16 elements each.  With halves a lane whose elements
+// turn has eight and the eight that turn with them; else 16 consecutive ones,
+// neighbours that turn together or, of a value, a group of the 4-bit cache.
 template <int D>
 struct Lanes {
     static constexpr int kPerHead = D / 16, kHeads = 32 / kPerHead;
@@ -200,50 +197,44 @@ __device__ __forceinline__ void rope_queries(const KvRopeArgs &a, int64_t token,
     *reinterpret_cast<uint4 *>(out + second) = v;
 }
 
-// ODD: halves of an odd number of eights, whose lanes have eights that turn with another lane's other eight.
-template <int D, bool F4, bool KEYS, bool NEXT, bool ODD>
+// KEYS with halves: a lane's eights can be of two groups of the 4-bit cache, whose
+// other eights are another lane's; its largest magnitudes come by shuffles.
+template <int D, bool F4, bool KEYS, bool NEXT>
 __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, int64_t token, int part) {
     using L = Lanes<D>;
+    constexpr bool kApart = KEYS && !NEXT;
     const L me;
     const int heads = static_cast<int>(a.kv_heads), h = part * L::kHeads + me.head, rot = static_cast<int>(a.rot_dim);
     const int half = rot / 2, lane = threadIdx.x & 31;
-    const bool there = h < heads, turns = KEYS && 16 * me.l < rot;
+    const bool there = h < heads, turns = KEYS && 8 * me.l < half;
+    const int first = kApart && turns ? 8 * me.l : 16 * me.l, second = kApart && turns ? half + 8 * me.l : first + 8;
     const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(KEYS ? a.k : a.v) +
-                               token * (KEYS ? a.k_stride : a.v_stride) + h * D + 16 * me.l;
+                               token * (KEYS ? a.k_stride : a.v_stride) + h * D;
     const int position = a.positions[token];
     const int64_t slot = a.slots[token];
     const float scale = *(KEYS ? a.k_scale : a.v_scale);
     uint4 u = make_uint4(0, 0, 0, 0), v = u, wu = u, wv = u;
-    if (there) u = ld_v4(src), v = ld_v4(src + 8);
+    if (there) u = ld_v4(src + first), v = ld_v4(src + second);
     const __nv_bfloat16 *wp = KEYS ? static_cast<const __nv_bfloat16 *>(a.k_weight) : nullptr;
-    if (wp) wu = *reinterpret_cast<const uint4 *>(wp + 16 * me.l), wv = *reinterpret_cast<const uint4 *>(wp + 16 * me.l + 8);
+    if (wp) wu = *reinterpret_cast<const uint4 *>(wp + first), wv = *reinterpret_cast<const uint4 *>(wp + second);
     if (position < 0 || position >= a.max_pos) return;
     if (slot < 0 || slot >= a.num_slots) {
         if (KEYS && slot != -1 && part == 0 && lane == 0) atomicOr(&g_rope_err, ERRBIT_INDEX);
         return;
     }
-    uint64_t x[8];
+    uint64_t x[8];  // what turns together: x[j] and x[j + 4]
     if (KEYS && NEXT) {
-        unpack_apart(u, v, x, x + 4);  // the even ones, then the odd ones
+        unpack_apart(u, v, x, x + 4);
     } else {
         unpack8(u, x);
         unpack8(v, x + 4);
     }
     if (KEYS) {
-        uint64_t c[8], s[8];
-        const float *row = a.cos_sin + static_cast<int64_t>(position) * rot;
-        const bool low = 16 * me.l < half;
+        uint64_t c[4], s[4];
         if (turns) {
-            if (NEXT) {
-                load_pairs8(row + 8 * me.l, c);
-                load_pairs8(row + half + 8 * me.l, s);
-            } else {
-                const int e0 = 16 * me.l, e1 = e0 + 8, at0 = e0 < half ? e0 : e0 - half, at1 = e1 < half ? e1 : e1 - half;
-                load_pairs8(row + at0, c);
-                load_pairs8(row + half + at0, s);
-                load_pairs8(row + at1, c + 4);
-                load_pairs8(row + half + at1, s + 4);
-            }
+            const float *row = a.cos_sin + static_cast<int64_t>(position) * rot + 8 * me.l;
+            load_pairs8(row, c);
+            load_pairs8(row + half, s);
         }
         if (wp) {
             // two sums of exact squares, each with what its roundings lost
@@ -278,77 +269,80 @@ __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, int64_t token, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = mul2(mul2(x[j], r2), w[j]);
         }
-        if constexpr (NEXT) {
-            if (turns) {
+        if (turns) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint64_t o1 = sub_apart(mul2(x[j], c[j]), mul2(x[j + 4], s[j]));
-                    x[j + 4] = add_apart(mul2(x[j + 4], c[j]), mul2(x[j], s[j]));
-                    x[j] = o1;
-                }
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t o1 = sub_apart(mul2(x[j], c[j]), mul2(x[j + 4], s[j]));
+                x[j + 4] = add_apart(mul2(x[j + 4], c[j]), mul2(x[j], s[j]));
+                x[j] = o1;
             }
+        }
+        if constexpr (NEXT) {
             // back to the elements' order
+            uint64_t t[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float x0, x1, y0, y1;
                 unpair(x[j], x0, x1);
                 unpair(x[j + 4], y0, y1);
-                x[j] = pair(x0, y0), x[j + 4] = pair(x1, y1);
+                t[2 * j] = pair(x0, y0), t[2 * j + 1] = pair(x1, y1);
             }
-            const uint64_t t[8] = {x[0], x[4], x[1], x[5], x[2], x[6], x[3], x[7]};
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = t[j];
-        } else {
-            // the other elements of the pairs: eight of this lane's are with eight half a rotation away
-            const int apart = half / 8;  // in eights; a lane has two of them
-            uint64_t o[8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int mine = 2 * me.l + k, partner = mine < apart ? mine + apart : mine - apart;
-                const int from = turns ? (lane - me.l) + (partner >> 1) : lane;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float a0, a1;
-                    unpair(x[4 * (ODD ? 1 - k : k) + j], a0, a1);
-                    o[4 * k + j] = pair(__shfl_sync(0xffffffffu, a0, from), __shfl_sync(0xffffffffu, a1, from));
-                }
-            }
-            if (turns) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool first = ODD ? 2 * me.l + (j >> 2) < apart : low;
-                    const uint64_t p = mul2(o[j], s[j]);
-                    x[j] = add_apart(mul2(x[j], c[j]), first ? neg2(p) : p);
-                }
-            }
         }
     }
     uint8_t *cache = KEYS ? a.k_cache : a.v_cache;
     if constexpr (F4) {
-        // a lane has a group; NaN is above every magnitude
-        uint32_t mx = 0;
+        // NaN is above every magnitude
+        uint32_t mx[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float a0, a1;
             unpair(x[j], a0, a1);
-            mx = max(mx, max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(a1) & 0x7FFFFFFFu));
+            mx[j / 4] = max(mx[j / 4], max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(a1) & 0x7FFFFFFFu));
         }
-        const uint32_t sc = f32x2_to_e4m3x2(__fdiv_rn(__uint_as_float(mx), mul1(6.0f, scale)), 0.0f) & 0xFFu;
-        const float den = mul1(f16x2_to_f32x2(e4m3x2_to_f16x2(sc)).x, scale);
-        uint2 codes = make_uint2(0, 0);
-        if (den > 0.0f) {
-            const float recip = safe_reciprocal(den);
-            auto encode = [](const float (&q)[8]) { return f32x8_to_e2m1x8(q); };
-            codes.x = codes_of<uint32_t>(x, den, recip, encode);
-            codes.y = codes_of<uint32_t>(x + 4, den, recip, encode);
+        if constexpr (kApart) {
+            const int firsts = turns ? half / 8 : 0;  // eights that are lanes' first ones
+            uint32_t other[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int eight = (turns ? (k ? second : first) / 8 : 2 * me.l + k) ^ 1;
+                const bool is_second = turns ? eight >= firsts : k == 0;
+                const int from = lane - me.l + (turns ? eight - (is_second ? firsts : 0) : me.l);
+                const uint32_t m0 = __shfl_sync(0xffffffffu, mx[0], from), m1 = __shfl_sync(0xffffffffu, mx[1], from);
+                other[k] = is_second ? m1 : m0;
+            }
+            mx[0] = max(mx[0], other[0]), mx[1] = max(mx[1], other[1]);
+        } else {
+            mx[0] = mx[1] = max(mx[0], mx[1]);
+        }
+        const float scale6 = mul1(6.0f, scale);
+        uint32_t sc[2], codes[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k == 0 || kApart) sc[k] = f32x2_to_e4m3x2(__fdiv_rn(__uint_as_float(mx[k]), scale6), 0.0f) & 0xFFu;
+            else sc[k] = sc[0];
+            const float den = mul1(f16x2_to_f32x2(e4m3x2_to_f16x2(sc[k])).x, scale);
+            codes[k] = 0;
+            if (den > 0.0f)
+                codes[k] = codes_of<uint32_t>(x + 4 * k, den, safe_reciprocal(den),
+                                              [](const float (&q)[8]) { return f32x8_to_e2m1x8(q); });
         }
         if (there) {
             const uint32_t tpp = static_cast<uint32_t>(a.page_size / kKv4Tile);
             const uint32_t tile = static_cast<uint32_t>(slot) / kKv4Tile, row = static_cast<uint32_t>(slot) % kKv4Tile;
             const uint32_t blk = tile / tpp;
             uint8_t *t = cache + ((static_cast<int64_t>(blk) * heads + h) * tpp + (tile - blk * tpp)) * kv4_tile_bytes(D);
-            *reinterpret_cast<uint2 *>(t + row * (D / 2) + 8 * me.l) = codes;
-            t[8 * D + row * (D / 16) + me.l] = static_cast<uint8_t>(sc);
+            uint8_t *to = t + row * (D / 2), *to_scale = t + 8 * D + row * (D / 16);
+            if constexpr (kApart) {
+                *reinterpret_cast<uint32_t *>(to + first / 2) = codes[0];
+                *reinterpret_cast<uint32_t *>(to + second / 2) = codes[1];
+                if (first % 16 == 0) to_scale[first / 16] = static_cast<uint8_t>(sc[0]);
+                if (second % 16 == 0) to_scale[second / 16] = static_cast<uint8_t>(sc[1]);
+            } else {
+                *reinterpret_cast<uint2 *>(to + 8 * me.l) = make_uint2(codes[0], codes[1]);
+                to_scale[me.l] = static_cast<uint8_t>(sc[0]);
+            }
         }
     } else {
         const float recip = safe_reciprocal(scale);
@@ -361,10 +355,17 @@ __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, int64_t token, 
             return static_cast<uint64_t>(o[1]) << 32 | o[0];
         };
         const uint64_t c0 = codes_of<uint64_t>(x, scale, recip, encode), c1 = codes_of<uint64_t>(x + 4, scale, recip, encode);
-        if (there)
-            *reinterpret_cast<uint4 *>(cache + (slot * heads + h) * D + 16 * me.l) =
-                make_uint4(static_cast<uint32_t>(c0), static_cast<uint32_t>(c0 >> 32), static_cast<uint32_t>(c1),
-                           static_cast<uint32_t>(c1 >> 32));
+        if (there) {
+            uint8_t *to = cache + (slot * heads + h) * D;
+            if constexpr (kApart) {
+                *reinterpret_cast<uint64_t *>(to + first) = c0;
+                *reinterpret_cast<uint64_t *>(to + second) = c1;
+            } else {
+                *reinterpret_cast<uint4 *>(to + first) =
+                    make_uint4(static_cast<uint32_t>(c0), static_cast<uint32_t>(c0 >> 32), static_cast<uint32_t>(c1),
+                               static_cast<uint32_t>(c1 >> 32));
+            }
+        }
     }
 }
 
@@ -373,9 +374,20 @@ __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, int64_t token, 
 // ceil(2^64 / warps a token), which divide every warp number below 2^47 exactly by
 // a multiplication (0: one warp).  A token's place, its heads and the weights are
 // one round trip, cos and sin the second.
-template <int D, bool F4, bool NEXT, bool ODD>
-__global__ void __launch_bounds__(kRopeThreads, ROPE_B) kv_rope_kernel(const __grid_constant__ KvRopeArgs a, uint32_t kv_blocks,
-                                                                       uint64_t kv_inverse, uint64_t q_inverse) {
+//
+// Floor: every byte of q, k, v read once, q's written, the cache's rows written.
+// At D = 128, 32 query and 8 key and value heads, 8191 tokens into the FP8 cache
+// (189 MB): 43.7 us, 4.3 TB/s; 4099 tokens of 64 and 8, half of each rotated, no norms (161 MB): 32.9 us, 4.9 TB/s;
+// 64 tokens 2.15 us.  What bounds it is latency: two dependent round
+// trips and some 200 instructions a warp, 32 warps an SM.  Warps an SM, at 8191
+// tokens: 24 53.6 us, 32 45.8, 40 47.0 (48 registers, which spill).  Threads a CTA:
+// 64 43.3 us, 128 43.7, 256 45.8, 512 49.6, since a CTA's registers are free when
+// its last warp is done; at 64 tokens 64 takes 2.3 us, 128 2.15.  A lane with 8
+// elements (a third more instructions a byte, 48 warps an SM) took 51.6 us, a warp
+// with several tokens one after the other, the next one's heads loaded ahead, 52 to 106.
+template <int D, bool F4, bool NEXT>
+__global__ void __launch_bounds__(kRopeThreads, 8) kv_rope_kernel(const __grid_constant__ KvRopeArgs a, uint32_t kv_blocks,
+                                                                  uint64_t kv_inverse, uint64_t q_inverse) {
     using L = Lanes<D>;
     const bool q = blockIdx.x >= 2 * kv_blocks;
     const uint32_t block = q ? blockIdx.x - 2 * kv_blocks : blockIdx.x >> 1;
@@ -387,11 +399,11 @@ __global__ void __launch_bounds__(kRopeThreads, ROPE_B) kv_rope_kernel(const __g
     pdl_wait();
     if (token >= a.tokens) return;
     if (q) rope_queries<D, NEXT>(a, token, part);
-    else if (blockIdx.x & 1) rope_cached<D, F4, false, NEXT, ODD>(a, token, part);
-    else rope_cached<D, F4, true, NEXT, ODD>(a, token, part);
+    else if (blockIdx.x & 1) rope_cached<D, F4, false, NEXT>(a, token, part);
+    else rope_cached<D, F4, true, NEXT>(a, token, part);
 }
 
-template <int D, bool F4, bool NEXT, bool ODD>
+template <int D, bool F4, bool NEXT>
 cudaError_t launch_rope_t(const KvRopeArgs &a, cudaStream_t stream) {
     constexpr int64_t kHeads = Lanes<D>::kHeads, kWarps = kRopeThreads / 32;
     const int64_t q_per = (a.q_heads + kHeads - 1) / kHeads, kv_per = (a.kv_heads + kHeads - 1) / kHeads;
@@ -407,14 +419,13 @@ cudaError_t launch_rope_t(const KvRopeArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_rope_kernel<D, F4, NEXT, ODD>, a, static_cast<uint32_t>(kv_blocks), inverse(kv_per),
+    return cudaLaunchKernelEx(&cfg, kv_rope_kernel<D, F4, NEXT>, a, static_cast<uint32_t>(kv_blocks), inverse(kv_per),
                               inverse(q_per));
 }
 
 template <int D, bool F4>
 cudaError_t launch_rope(const KvRopeArgs &a, cudaStream_t stream) {
-    if (a.interleaved) return launch_rope_t<D, F4, true, false>(a, stream);
-    return a.rot_dim % 32 == 0 ? launch_rope_t<D, F4, false, false>(a, stream) : launch_rope_t<D, F4, false, true>(a, stream);
+    return a.interleaved ? launch_rope_t<D, F4, true>(a, stream) : launch_rope_t<D, F4, false>(a, stream);
 }
 
 }  // namespace
