@@ -628,6 +628,8 @@ def moe_combine(y, weights, ids=None, num_experts: int = 0, residual=None, out=N
     if y.dim() != 3:
         raise ValueError("y must be [M, topk, N]")
     m, topk, n = y.shape
+    if ids is not None and num_experts < 1:
+        raise ValueError("ids need num_experts: a slot whose id is outside [0, num_experts) adds nothing")
     bf16 = torch.bfloat16
     given = [spec for spec in (("ids", ids, torch.int32, m * topk, False), ("residual", residual, bf16, m * n, False),
                                ("out", out, bf16, m * n, False)) if spec[1] is not None]
@@ -905,6 +907,8 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     (fp8bs_sample_tokens).  Returns a SampledTokens: int32 tokens [M], -1 for
     a row that has none, and their log probabilities."""
     m, v = _shape2(logits, "logits")
+    if u.shape[-1:] != (2,):
+        raise ValueError(f"u has shape {tuple(u.shape)}, expected ({m}, 2)")
     stride = logits.stride(0) if m > 1 else v
     if 0 < stride < v:
         raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")

@@ -7,6 +7,14 @@
 // is made in fp32 first, and stands if what it told apart is further apart than
 // c can be off; else (one token in some thousands) it is made again with pairs
 // of fp32.  Without a bias or groups it goes by the logits themselves.
+//
+// Floor: the logits read once (8192 tokens of 256 experts in fp32: 8.9 MB, 1.3 us).
+// Measured 18.9 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 13.8 (softmax,
+// 12 of 256, no bias), and 4.3 for 32 tokens, most of it the launch and the topk
+// rounds, each a dependent chain of a warp's maximum, a ballot and two shuffles.
+// What bounds the prompt is instructions: the scores' exponents, and the rounds.
+// With pairs of fp32 for every token it took 36.5 us; with 16 warps an SM instead of
+// 32, 20.0; CTAs of 8 warps 19.2, and 4.5 for 32 tokens, 2 warps as 4.
 #include "twofloat.cuh"
 
 #include "serving.cuh"
@@ -16,7 +24,7 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kRouteWarps = 8;
+constexpr int kRouteWarps = 4;
 constexpr float kMostBias = 65536.0f;
 constexpr float kNoScore = -104.0f;  // e^x below two_exp2's range
 
@@ -389,8 +397,9 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     return true;
 }
 
+// 64 registers to 256 experts: 32 warps an SM, in CTAs of 4
 template <bool F32, int EPL>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kernel(const __grid_constant__ MoeScoreArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 8 : 1) route_kernel(const __grid_constant__ MoeScoreArgs a) {
     extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
     pdl_wait();
@@ -401,12 +410,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1) route_kern
 template <bool F32, int EPL>
 cudaError_t launch_route_t(const MoeScoreArgs &a, cudaStream_t stream) {
     const int64_t blocks = (a.tokens + kRouteWarps - 1) / kRouteWarps;
+    static_assert(kRouteWarps * kRouteMaxExperts * 8 <= 48 * 1024, "shared memory of a launch");
     const size_t smem = a.groups > 1 ? static_cast<size_t>(kRouteWarps * a.experts * 8) : 0;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(route_kernel<F32, EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
     cfg.blockDim = dim3(kRouteWarps * 32, 1, 1);
@@ -434,7 +439,15 @@ cudaError_t launch_route_epl(const MoeScoreArgs &a, cudaStream_t stream) {
 // A thread has 8 consecutive columns of a token, 16 bytes of each of its
 // slots.  A warp's lanes load the token's ids and weights, a slot each, at
 // once; kInFlight slots are loaded before the first is used.
-constexpr int kCombineThreads = 256;
+//
+// Floor: y, the residual and the result once.  2048 tokens of 12 x 4096 (235 MB):
+// 36.2 us, 6.5 TB/s, 0.97 of a copy's rate; 512 of 8 x 7168 (73 MB, within L2) 13.4;
+// 32 tokens 2.4.  DRAM bounds it.  Slots in flight, for these three: 2 38.7, 15.2, 3.1
+// (CTAs of 256); 4 36.2, 13.4, 2.4; 6 35.8, 14.1, 2.2; 8 36.6, 13.0, 2.3: 6 and 8 each
+// gain where they divide topk and lose elsewhere.  Threads a CTA: 64 36.2, 13.4, 2.7;
+// 128 36.2, 13.4, 2.4; 256 36.8, 13.7, 2.9; 512 39.7, 15.5, 3.1.  With branches around
+// the loads, which the compiler then waits for one by one, 51.
+constexpr int kCombineThreads = 128;
 constexpr int kInFlight = 4;
 
 // The 8 columns from p on, of which `cols` are there, as bf16; no load unless `want`.  Without a branch, so that

@@ -21,6 +21,13 @@
 // bin that holds the cut, the tokens above it summed by block and its own tokens
 // gathered in shared memory, where histograms over their values end the search.
 // A bin that holds too many is first cut by histograms over its values.
+//
+// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 46 us,
+// 3.4 TB/s; by top-p 174, by top-k 106; 64 rows of mixed settings 39; 256 fp32 rows of
+// 32003 49; one row by top-p 23, by temperature 8.5.  The passes are bound by the
+// instructions they issue, 512 rows also by their count on 152 SMs; what lies between
+// the passes by the latency of steps that a whole CTA or cluster takes together, about
+// 0.7 us for each exchange in a cluster.
 #include "twofloat.cuh"
 
 #include "serving.cuh"
@@ -1315,9 +1322,18 @@ cudaError_t launch_rows(const SampleArgs &a, int splits, cudaStream_t stream) {
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     const int64_t blocks = (a.vocab + kBlock - 1) / kBlock, sms = device_sm_count();
+    const bool plain = !a.top_k && !a.top_p && !a.min_p;
+    // CTAs a row: as many as still give each 8 blocks, and the SMs at most two CTAs, or one without a cut, whose one
+    // pass gains less from a second than another exchange costs.  Rows of 152064, us at one CTA and at two an SM:
+    // temperature alone 32 rows 9.8 and 11.4, 64 12.2 and 13.6, 100 15.7 and 18.1; with cuts 64 43.8 and 39.1, 100
+    // 63.1 and 55.2 (four an SM: 51.4 for 64).  Rows of 12000 with cuts, 32 of them: 8 blocks 20.4, 4 blocks 23.5;
+    // rows of 32003: 8 blocks 26.0, 16 blocks 27.5.
     int splits = 1;
-    while (splits < kMaxSplit && 2 * splits * a.rows <= 2 * sms && blocks / (2 * splits) >= 8) splits *= 2;
-    if (!a.top_k && !a.top_p && !a.min_p) {
+    while (splits < kMaxSplit && 2 * splits * a.rows <= (plain ? sms : 2 * sms) && blocks / (2 * splits) >= 8) splits *= 2;
+    // 512 threads a CTA, two an SM (registers).  Without a cut and with more rows than those, 256, four an SM: a row's
+    // end leaves fewer idle, 2048 rows of 32003 60.4 and not 82 us, 512 of 152064 46.2 and not 47.7.  With cuts CTAs of
+    // 256 are slower: 64 rows 40.0 and not 39.1, 256 fp32 rows of 32003 53.7 and not 49.2.
+    if (plain) {
         if (splits == 1 && a.rows > 2 * sms)
             return a.f32 ? launch_rows<true, 256, true>(a, splits, stream) : launch_rows<false, 256, true>(a, splits, stream);
         return a.f32 ? launch_rows<true, 512, true>(a, splits, stream) : launch_rows<false, 512, true>(a, splits, stream);

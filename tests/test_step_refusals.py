@@ -61,7 +61,8 @@ def sample(**kw):
     lambda: route(logits=t(16, F32)), lambda: route(topk=0), lambda: route(topk=17), lambda: route(scoring="relu"),
     lambda: route(bias=t(15, F32)), lambda: route(ids=t((3, 3))), lambda: route(weights=t((2, 2), F32)),
     lambda: route(logits=torch.as_strided(t(64, F32), (3, 16), (8, 1))),
-    lambda: combine(y=t((3, 128), BF)), lambda: combine(weights=t((3, 3), F32)), lambda: combine(ids=t((2, 2))),
+    lambda: combine(y=t((3, 128), BF)), lambda: combine(weights=t((3, 3), F32)), lambda: combine(ids=t((2, 2)), num_experts=4),
+    lambda: combine(ids=t((3, 2))), lambda: sample(u=t((2, 3), F32)),
     lambda: combine(residual=t((3, 63), BF)), lambda: combine(residual=t(64, BF)), lambda: combine(out=t((2, 64), BF)),
     lambda: sample(logits=t(50, BF)), lambda: sample(u=t((3, 1), F32)), lambda: sample(temperature=t(2, F32)),
     lambda: sample(top_k=t(4)), lambda: sample(top_p=t(1, F32)), lambda: sample(min_p=t(1, F32)),
@@ -82,7 +83,7 @@ def test_right_sizes_on_the_cpu_are_refused_as_not_cuda(call):
 @pytest.mark.parametrize("call", [
     lambda: rope8(q=t((4, 8, 128), F32)), lambda: rope4(positions=t(4, torch.int64)), lambda: rope8(cos_sin=t((50, 64), BF)),
     lambda: rope8(k_norm=t(128, F32)), lambda: route(logits=t((3, 16), torch.float16)), lambda: route(bias=t(16, BF)),
-    lambda: combine(weights=t((3, 2), BF)), lambda: combine(ids=t((3, 2), torch.int64)), lambda: sample(temperature=0.7),
+    lambda: combine(weights=t((3, 2), BF)), lambda: combine(ids=t((3, 2), torch.int64), num_experts=4), lambda: sample(temperature=0.7),
     lambda: sample(top_k=t(3, torch.int64)), lambda: sample(top_p=t(3, torch.float64)), lambda: sample(u=t((3, 2), BF)),
     lambda: combine(y=t((3, 4, 64), BF)[:, ::2]), lambda: sample(logits=t((3, 100), BF)[:, ::2]),
     lambda: rope8(q=t((4, 16, 128), BF)[:, ::2]),
@@ -94,7 +95,7 @@ def test_other_types_and_layouts_raise(call):
 
 def test_tensors_on_different_devices_raise():
     for call in (lambda: rope4(slots=t(4, I32, "meta")), lambda: route(bias=t(16, F32, "meta")),
-                 lambda: combine(ids=t((3, 2), I32, "meta")), lambda: sample(top_p=t(3, F32, "meta"))):
+                 lambda: combine(ids=t((3, 2), I32, "meta"), num_experts=4), lambda: sample(top_p=t(3, F32, "meta"))):
         with pytest.raises(ValueError, match="is on"):
             call()
 
