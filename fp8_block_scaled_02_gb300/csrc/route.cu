@@ -192,9 +192,14 @@ __device__ __forceinline__ float exp_near(float x, float m) {
     return fmaf(e, t.l * 0.6931471805599453f, e);
 }
 
+struct Candidates {  // of a warp
+    alignas(16) uint32_t key[32];
+    int id[32];
+};
+
 // A token's experts by fp32 scores; false if they do not tell them apart.
 template <bool F32, int EPL>
-__device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t token) {
+__device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t token, Candidates &sh) {
     constexpr float kLog2e = 1.4426950408889634f;
     const int lane = threadIdx.x & 31, experts = static_cast<int>(a.experts), topk = static_cast<int>(a.topk);
     const int e0 = lane * EPL, groups = static_cast<int>(a.groups), per = groups > 1 ? experts / groups : experts;
@@ -316,43 +321,67 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     const bool by_score = a.bias != nullptr;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = open && e0 + i < experts ? logit_key(by_score ? c[i] : x[i]) : 0u;
-    // ---- the best that is left, topk times, and by scores as long as one may yet be before the topk-th; lane j keeps the j-th
+    // ---- candidates: what is not below the topk-th largest of the lanes' largest, which is no larger than the topk-th of
+    // all; by scores not below what may yet be before it.  To lane j the j-th of them by key, then expert.
     auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); };
-    int id = 0, n = 0, place = lane;
-    uint32_t got = 0;
-    float last = 0.0f;
+    uint32_t best = 0, least = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
+    for (int seen = 0; seen < topk;) {
+        least = __reduce_max_sync(0xffffffffu, best);
+        if (least == 0) break;
+        seen += __popc(__ballot_sync(0xffffffffu, best == least));
+        if (best == least) best = 0;
+    }
+    if (by_score) {
+        if (least <= 1) return false;  // not one in each of topk lanes, or NaN
+        const float v = value(least);
+        least = logit_key(v - 4.0f * (slack + 0x1p-21f * fabsf(v)));
+    }
+    if (least == 0) least = 1;
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) mine += key[i] >= least ? 1 : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    const int n = __shfl_sync(0xffffffffu, upto, 31);
+    if (n > 32) return false;
+    sh.key[lane] = 0;
+    __syncwarp();
+    int to = upto - mine;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (key[i] >= least) {
+            sh.key[to] = key[i];
+            sh.id[to++] = e0 + i;
+        }
+    __syncwarp();
+    uint32_t got = sh.key[lane];
+    int id = sh.id[lane], rank = 0;
+    for (int k = 0; k < n; k += 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(sh.key + k);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) rank += u[q] > got || (u[q] == got && k + q < lane) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < n) {
+        sh.key[rank] = got;
+        sh.id[rank] = id;
+    }
+    __syncwarp();
+    got = sh.key[lane];
+    id = sh.id[lane];
+    int place = lane < n ? lane : 32;
     bool close = false;
-    uint32_t best = 0;
-    int at = 0;
-    auto look = [&]() {
-        best = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) best = key[i], at = i;
-    };
-    look();
-    for (; n < 33; ++n) {
-        if (n >= topk && !by_score) break;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (by_score) {
-            const float v = value(top);
-            if (top == 0) break;
-            if (v != v) return false;
-            const bool apart = n == 0 || last - v > 2.0f * (slack + 0x1p-22f * (fabsf(last) + fabsf(v)));
-            if (n >= topk && apart) break;
-            if (n == 32) return false;
-            close |= !apart;
-            if (n < topk) last = v;
-        }
-        const int winner = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-        const int e = __shfl_sync(0xffffffffu, e0 + at, winner);
-        if (lane == n) id = e, got = top;
-        if (lane == winner) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i == at) key[i] = 0;
-            look();
-        }
+    if (by_score) {
+        const float v = value(got), above = value(sh.key[lane > 0 ? lane - 1 : 0]);
+        const bool apart = above - v > 2.0f * (slack + 0x1p-22f * (fabsf(above) + fabsf(v)));
+        close = __any_sync(0xffffffffu, lane > 0 && lane <= topk && lane < n && !apart);
     }
     if (close) {
         // ---- scores that fp32 does not tell apart: those of the candidates again, and their places by them
@@ -402,9 +431,11 @@ template <bool F32, int EPL>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 8 : 1) route_kernel(const __grid_constant__ MoeScoreArgs a) {
     extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    __shared__ Candidates candidates[kRouteWarps];
     pdl_wait();
     if (token >= a.tokens) return;
-    if (!route_quickly<F32, EPL>(a, token)) route_exactly<F32, EPL>(a, token, sh_scores + (threadIdx.x >> 5) * a.experts);
+    if (!route_quickly<F32, EPL>(a, token, candidates[threadIdx.x >> 5]))
+        route_exactly<F32, EPL>(a, token, sh_scores + (threadIdx.x >> 5) * a.experts);
 }
 
 template <bool F32, int EPL>
