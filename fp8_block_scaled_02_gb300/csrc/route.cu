@@ -9,12 +9,13 @@
 // of fp32.  Without a bias or groups it goes by the logits themselves.
 //
 // Floor: the logits read once (8192 tokens of 256 experts in fp32: 8.9 MB, 1.3 us).
-// Measured 18.9 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 13.8 (softmax,
-// 12 of 256, no bias), and 4.3 for 32 tokens, most of it the launch and the topk
-// rounds, each a dependent chain of a warp's maximum, a ballot and two shuffles.
-// What bounds the prompt is instructions: the scores' exponents, and the rounds.
-// With pairs of fp32 for every token it took 36.5 us; with 16 warps an SM instead of
-// 32, 20.0; CTAs of 8 warps 19.2, and 4.5 for 32 tokens, 2 warps as 4.
+// Measured 16.9 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 9.8 (softmax,
+// 12 of 256, no bias), and 3.4 for 32 tokens, most of it the launch and the chain of
+// dependent steps.  What bounds the prompt is instructions, 1110 and 860 a token, ALU
+// first: the scores, the groups, the order keys.  With pairs of fp32 for every token it
+// took 36.5 us; with the largest left taken topk times in place of a rank among the few
+// that can be chosen 18.9, 13.8 and 4.2.  Warps an SM: 16 20.0 us (those rounds), 32
+// 16.9 and 9.8, 40 17.1 and 9.7, 48 17.8 and 9.9.
 #include "twofloat.cuh"
 
 #include "serving.cuh"
