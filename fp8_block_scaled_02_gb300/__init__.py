@@ -802,37 +802,50 @@ def kv4_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
     return (out, lse) if return_lse else out
 
 
-def _rope_append(what, fn, q, k, v, positions, slots, cos_sin, cache_specs, cache_args, k_scale, v_scale, k_cache, v_cache,
-                 q_norm, k_norm, eps, interleaved, out, stream):
-    t, hq, d = q.shape
+def _rope_append(four_bit, q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm, k_norm, eps,
+                 interleaved, out, stream):
+    try:
+        (t, hq, d), (tk, hkv, dk) = q.shape, k.shape
+    except ValueError:
+        t, tk = -1, -2
+    if t != tk or d != dk or v.shape != k.shape:
+        raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D]")
     max_pos, rot = _shape2(cos_sin, "cos_sin")
-    bf16, i32 = torch.bfloat16, torch.int32
-    specs = [*cache_specs, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
-             ("cos_sin", cos_sin, torch.float32, None, False), ("q", q, bf16, None, True), ("k", k, bf16, None, True),
-             ("v", v, bf16, None, True)]
+    bf16, i32, u8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+    L = lib()
+    if four_bit:
+        caches, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, hkv, d)
+        what, fn, places = "fp4kv_rope_append", L.fp4kv_rope_append, (page, nb)
+    else:
+        shape = k_cache.shape
+        if len(shape) != 4 or shape[2] != hkv or shape[3] != d:
+            raise ValueError(f"k_cache has shape {tuple(shape)}, expected [num_blocks, page_size, Hkv, D] of k")
+        if v_cache.shape != shape:
+            raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(shape)}")
+        caches = (("k_cache", k_cache, u8, None, False), ("v_cache", v_cache, u8, None, False),
+                  ("k_scale", k_scale, f32, 1, False), ("v_scale", v_scale, f32, 1, False))
+        what, fn, places = "fp8kv_rope_append", L.fp8kv_rope_append, (shape[0] * shape[1],)
+    given = ()
     q_ptr = k_ptr = None
     if q_norm is not None:
-        specs.append(("q_norm", q_norm, bf16, d, False))
+        given = (("q_norm", q_norm, bf16, d, False),)
         q_ptr = q_norm.data_ptr()
     if k_norm is not None:
-        specs.append(("k_norm", k_norm, bf16, d, False))
+        given += (("k_norm", k_norm, bf16, d, False),)
         k_ptr = k_norm.data_ptr()
     if out is not None:
-        specs.append(("out", out, bf16, t * hq * d, False))
-    device = _checked(*specs)
+        given += (("out", out, bf16, t * hq * d, False),)
+    device = _checked(*caches, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
+                      ("cos_sin", cos_sin, f32, None, False), ("q", q, bf16, None, True), ("k", k, bf16, None, True),
+                      ("v", v, bf16, None, True), *given)
     if out is None:
         out = _empty(stream, device, (t, hq, d), bf16)
+    q_stride, k_stride, v_stride = (q.stride(0), k.stride(0), v.stride(0)) if t > 1 else (hq * d, hkv * d, hkv * d)
     _call(device, what, fn,
-          (q.data_ptr(), _row_stride(q), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), t, hq, k.shape[1], d,
-           positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, interleaved, q_ptr, k_ptr, eps,
-           out.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *cache_args),
-          stream)
+          (q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, t, hq, hkv, d, positions.data_ptr(),
+           slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, int(interleaved), q_ptr, k_ptr, float(eps), out.data_ptr(),
+           k_scale.data_ptr(), v_scale.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *places), stream)
     return out
-
-
-def _rope_shapes(q, k, v):
-    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D]")
 
 
 def kv_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm=None, k_norm=None,
@@ -844,56 +857,15 @@ def kv_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache
     holds cos of a position's pairs, then sin.  q, k and v may be slices of a
     fused projection.  Returns q [T, Hq, 128]; rows at position -1 are left as
     they were."""
-    _rope_shapes(q, k, v)
-    if k_cache.dim() != 4 or k_cache.shape[2:] != k.shape[1:]:
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [num_blocks, page_size, Hkv, D] of k")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
-    u8, f32 = torch.uint8, torch.float32
-    specs = (("k_cache", k_cache, u8, None, False), ("v_cache", v_cache, u8, None, False),
-             ("k_scale", k_scale, f32, 1, False), ("v_scale", v_scale, f32, 1, False))
-    return _rope_append("fp8kv_rope_append", lib().fp8kv_rope_append, q, k, v, positions, slots, cos_sin, specs,
-                        (k_cache.shape[0] * k_cache.shape[1],), k_scale, v_scale, k_cache, v_cache, q_norm, k_norm,
-                        float(eps), int(interleaved), out, stream)
+    return _rope_append(False, q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm, k_norm, eps,
+                        interleaved, out, stream)
 
 
 def kv4_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm=None, k_norm=None,
                     eps: float = 1e-6, interleaved: bool = False, out=None, stream=None):
     """kv_rope_append into 4-bit caches (fp4kv_rope_append); head size 64 or 128."""
-    _rope_shapes(q, k, v)
-    specs, nb, page = _kv4_specs(k_cache, v_cache, k_scale, v_scale, k.shape[1], k.shape[2])
-    return _rope_append("fp4kv_rope_append", lib().fp4kv_rope_append, q, k, v, positions, slots, cos_sin, specs, (page, nb),
-                        k_scale, v_scale, k_cache, v_cache, q_norm, k_norm, float(eps), int(interleaved), out, stream)
-
-
-def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
-                   stream=None):
-    """Log probabilities of the targets [M] under logits [M, V] (bf16 or fp32,
-    rows may be padded, or one row expanded to M), each row's entropy and its
-    `top` best tokens (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
-    m, v = _shape2(logits, "logits")
-    stride = logits.stride(0) if m > 1 else v
-    if 0 < stride < v:
-        raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")
-    top = int(top)
-    f32 = logits.dtype == torch.float32
-    given = [spec for spec in (("logprobs", logprobs, torch.float32, m, False), ("entropy", entropy, torch.float32, m, False),
-                               ("top_ids", top_ids, torch.int32, m * top, False),
-                               ("top_logprobs", top_logprobs, torch.float32, m * top, False)) if spec[1] is not None]
-    device = _checked(("logits", logits, torch.float32 if f32 else torch.bfloat16, None, True),
-                      ("targets", targets, torch.int32, m, False), *given)
-    if logprobs is None:
-        logprobs = _empty(stream, device, (m,), torch.float32)
-    if entropy is None:
-        entropy = _empty(stream, device, (m,), torch.float32)
-    if top_ids is None:
-        top_ids = _empty(stream, device, (m, top), torch.int32)
-    if top_logprobs is None:
-        top_logprobs = _empty(stream, device, (m, top), torch.float32)
-    _call(device, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs,
-          (logits.data_ptr(), int(f32), stride, m, v, targets.data_ptr(), top,
-           logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr()), stream)
-    return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
+    return _rope_append(True, q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cache, v_cache, q_norm, k_norm, eps,
+                        interleaved, out, stream)
 
 
 SampledTokens = collections.namedtuple("SampledTokens", "tokens logprobs")
