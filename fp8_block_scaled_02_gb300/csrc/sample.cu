@@ -375,9 +375,9 @@ __device__ __forceinline__ uint64_t part_of(uint64_t mass, float share) {
 
 // A lane's sum of 2^(c (x - m)), m the block's largest, of its elements with x
 // above `least`.  t = d c.h rounds; what it lost and d c.l, e together, come
-// back as the factor 1 + e ln 2.
+// back as the factor 1 + e ln 2, its second part summed apart.
 template <bool F32, bool ALL>
-__device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint32_t m_key, Two c, float least) {
+__device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint32_t m_key, Two c, float reach, float least) {
     const float m = Key<F32>::value(m_key);
     if (!(fabsf(m) < 1e37f && fabsf(m) * c.h < 1e30f)) {  // d c may not fit fp32
         constexpr int VE = Row<F32>::VE;
@@ -387,17 +387,16 @@ __device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint3
             float x[VE];
             Row<F32>::unpack(w[i], x);
             for (int j = 0; j < VE; ++j)
-                if (ALL || x[j] > least) sum += ex2(fmaxf(x[j] - m, -124.0f / c.h) * c.h);
+                if (ALL || x[j] > least) sum += ex2(fmaxf(x[j] - m, -reach) * c.h);
         }
         return sum;
     }
     // below this a weight is none, but d c still a number; less than m itself
-    float floor = fminf(m - 124.0f / c.h, Key<F32>::value(m_key - 1));
+    float floor = fminf(m - reach, Key<F32>::value(m_key - 1));
     const uint32_t fb = __float_as_uint(floor);
     const uint32_t low = fb & 0x80000000u ? (fb + 0xFFFFu) >> 16 : fb >> 16;  // the next bf16 down
     const uint64_t neg_m = pair(-m, -m), ch = pair(c.h, c.h), neg_ch = pair(-c.h, -c.h), neg_cl = pair(-c.l, -c.l);
-    const uint64_t neg_ln2 = pair(-kLn2, -kLn2);
-    uint64_t sum = 0;
+    uint64_t sum = 0, missing = 0;
 #pragma unroll
     for (int i = 0; i < Row<F32>::NV; ++i) {
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -420,18 +419,21 @@ __device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint3
                 w1 = x1 > least ? w1 : 0.0f;
             }
             const uint64_t v = pair(w0, w1);
-            sum = add2(sum, fma2(mul2(v, neg_ln2), e, v));
+            sum = add2(sum, v);
+            missing = fma2(v, e, missing);
         }
     }
-    float a, b;
+    float a, b, p, q;
     unpair(sum, a, b);
-    return a + b;
+    unpair(missing, p, q);
+    return fmaf(p + q, -kLn2, a + b);
 }
 
 struct Job {
     float m;       // the row's largest logit
     uint32_t m_key, lowest;  // no token below `lowest` is kept
     Two c;
+    float reach;   // 124 / c: a weight that far below another is none beside it
     int b0, b1, blocks, part, splits;
     int bits;      // of a residual in a histogram of the row
     int turn;      // of share_range's boxes
@@ -776,7 +778,7 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
         if (key >= lo) {
             uint4 w[NV];
             row.load(b, w);
-            if (key > hi) s = block_sum<F32, false>(w, key, job.c, most);
+            if (key > hi) s = block_sum<F32, false>(w, key, job.c, job.reach, most);
             uint32_t in = 0;  // bit i * VE + j: vector i's element j is in the range
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -1042,6 +1044,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     }
     // ---- the blocks' largest logits and their masses relative to those
     uint4 ahead[Row<F32>::NV];
+    job.reach = 124.0f / job.c.h;
     constexpr bool kAhead = !F32;  // the next block's loads in flight beside this one's sums, where registers allow it
     if (kAhead && job.b0 + warp < job.b1) row.load(job.b0 + warp, ahead);
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
@@ -1056,7 +1059,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         const uint32_t lane_key = K::of(Row<F32>::most(w)), key = __reduce_max_sync(0xffffffffu, lane_key);
         if (!PLAIN && by_k) atomicAdd(&sh.n[lane_key >> kBoundShift], 1u);
         float s = 0.0f;
-        if (key > K::kNegInf && key < K::kInf && !greedy) s = block_sum<F32, true>(w, key, job.c, 0.0f);
+        if (key > K::kNegInf && key < K::kInf && !greedy) s = block_sum<F32, true>(w, key, job.c, job.reach, 0.0f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) {
