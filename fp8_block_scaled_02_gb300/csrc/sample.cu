@@ -34,6 +34,7 @@
 #include "internal.h"
 
 #include <cstddef>
+#include <cstring>
 #include <mutex>
 
 namespace fp8bs {
@@ -124,6 +125,20 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// 0xFFFF in the halves where a's number is at least b's.
+__device__ __forceinline__ uint32_t at_least_bf16x2(uint32_t a, uint32_t b) {
+    __nv_bfloat162 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    return __hge2_mask(x, y);
+}
+// v's two numbers and c, each sum one fp32 rounding.
+__device__ __forceinline__ void add_bf16x2(uint32_t v, float c, float &lo, float &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.rn.f32.bf16 %0, l, %3;\n\tadd.rn.f32.bf16 %1, h, %3;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v), "f"(c));
+}
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -241,6 +256,26 @@ struct Row {
             return fminf(bf16lo_to_f32(m), bf16hi_to_f32(m));
         }
     }
+    // Which of a lane's elements, none of which is NaN, are in [lo, hi], a bit each; and the element of a bit.
+    static __device__ __forceinline__ uint32_t between(const uint4 (&w)[NV], float lo, float hi) {
+        uint32_t in = 0;
+        const uint32_t l = __float_as_uint(lo) >> 16, h = __float_as_uint(hi) >> 16, low = l << 16 | l, high = h << 16 | h;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (F32) {
+                    const float x = __uint_as_float(u[j]);
+                    in |= x >= lo && x <= hi ? 1u << (4 * i + j) : 0u;
+                } else {
+                    in |= at_least_bf16x2(u[j], low) & at_least_bf16x2(high, u[j]) & (0x10001u << (4 * i + j));
+                }
+            }
+        }
+        return in;
+    }
+    static __device__ __forceinline__ int element(int bit) { return F32 ? bit : 2 * (bit & 15) + (bit >> 4); }
     // The largest of a lane's elements; NaN if there is one.
     static __device__ __forceinline__ float most(const uint4 (&w)[NV]) {
         if constexpr (F32) {
@@ -402,14 +437,15 @@ __device__ __forceinline__ float block_sum(const uint4 (&w)[Row<F32>::NV], uint3
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int j = 0; j < (F32 ? 2 : 4); ++j) {
-            float x0, x1;
+            float x0, x1, d0 = 0.0f, d1 = 0.0f;
             if constexpr (F32) {
                 x0 = fmaxf(__uint_as_float(u[2 * j]), floor), x1 = fmaxf(__uint_as_float(u[2 * j + 1]), floor);
             } else {
                 const uint32_t v = max_bf16x2(u[j], low | low << 16);
                 x0 = bf16lo_to_f32(v), x1 = bf16hi_to_f32(v);
+                add_bf16x2(v, -m, d0, d1);
             }
-            const uint64_t d = add2(pair(x0, x1), neg_m), t = mul2(d, ch);
+            const uint64_t d = F32 ? add2(pair(x0, x1), neg_m) : pair(d0, d1), t = mul2(d, ch);
             const uint64_t e = fma2(d, neg_cl, fma2(d, neg_ch, t));  // minus what is missing
             float t0, t1;
             unpair(t, t0, t1);
@@ -596,12 +632,12 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
     constexpr int NV = Row<F32>::NV, VE = Row<F32>::VE;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float least = Key<F32>::value(job.lowest), m = job.m;
-    // d = m - x; bin = round(32 c d), f the rest in [-1/2, 1/2]; weight / bin's = 2^(-f / 32), with the counts less 63/64
+    // d = x - m; bin = round(-32 c d), f the rest in [-1/2, 1/2]; weight / bin's = 2^(-f / 32), with the counts less 63/64
     // and in units of 2^-(5 + bits): below 2^bits.  The low bits of r are the bin, those of q the units
     const float unit = static_cast<float>(1 << (MODE == kMasses ? kMassBits : 5 + job.bits)), y = kLn2 / kPerUnit;
     const float whole = (MODE == kMasses ? unit : unit / 64.0f) + 0x1p23f;
-    const uint64_t m2 = pair(m, m), minus = pair(-1.0f, -1.0f), magic = pair(kMagic, kMagic);
-    const float chf = job.c.h * kPerUnit, clf = job.c.l * kPerUnit;
+    const uint64_t neg_m = pair(-m, -m), minus = pair(-1.0f, -1.0f), magic = pair(kMagic, kMagic);
+    const float chf = -job.c.h * kPerUnit, clf = -job.c.l * kPerUnit;
     const uint64_t ch = pair(chf, chf), cl = pair(clf, clf);
     const uint64_t q0 = pair(whole, whole), q1 = pair(-unit * y, -unit * y);
     const uint64_t q2 = pair(unit * y * y / 2.0f, unit * y * y / 2.0f);
@@ -618,13 +654,16 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
             float x[VE];
             uint32_t at[VE], v[VE];
             Row<F32>::unpack(w[i], x);
+            const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int j = 0; j < VE; j += 2) {
-                const uint64_t d = fma2(pair(x[j], x[j + 1]), minus, m2), r = fma2(d, ch, magic);
+                float d0 = 0.0f, d1 = 0.0f;
+                if constexpr (!F32) add_bf16x2(words[j / 2], -m, d0, d1);
+                const uint64_t d = F32 ? add2(pair(x[j], x[j + 1]), neg_m) : pair(d0, d1), r = fma2(d, ch, magic);
                 float r0, r1, u0 = 0.0f, u1 = 0.0f;
                 unpair(r, r0, r1);
                 if constexpr (MODE != kCounts) {
-                    // 32 c d - n, of which the product's part is exact but for one rounding; the third power of
+                    // -32 c d - n, of which the product's part is exact but for one rounding; the third power of
                     // f ln 2 / 32 is at most 2^-22, as often up as down
                     const uint64_t f = fma2(d, cl, fma2(d, ch, fma2(r, minus, magic)));
                     unpair(fma2(f, fma2(f, q2, q1), q0), u0, u1);
@@ -779,14 +818,7 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
             uint4 w[NV];
             row.load(b, w);
             if (key > hi) s = block_sum<F32, false>(w, key, job.c, job.reach, most);
-            uint32_t in = 0;  // bit i * VE + j: vector i's element j is in the range
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float x[VE];
-                Row<F32>::unpack(w[i], x);
-#pragma unroll
-                for (int j = 0; j < VE; ++j) in |= x[j] >= least && x[j] <= most ? 1u << (i * VE + j) : 0u;
-            }
+            const uint32_t in = Row<F32>::between(w, least, most);
             n = __popc(in);
             if constexpr (GATHER) {
                 if (__any_sync(0xffffffffu, n > 0)) {
@@ -794,8 +826,9 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
                     int at = 0;
                     if (lane == 31) at = atomicAdd(&sh.listed, upto);
                     at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
-                    for (; in; in &= in - 1, ++at) {
-                        const int k = __ffs(in) - 1, id = b * kBlock + (lane + 32 * (k / VE)) * VE + k % VE;
+                    for (uint32_t left = in; left; left &= left - 1, ++at) {
+                        const int k = Row<F32>::element(__ffs(left) - 1);
+                        const int id = b * kBlock + (lane + 32 * (k / VE)) * VE + k % VE;
                         if (at < kGather) {
                             sh.list_key[at] = Key<F32>::of(row.at(id));
                             sh.list_id[at] = id;
