@@ -22,12 +22,12 @@
 // gathered in shared memory, where histograms over their values end the search.
 // A bin that holds too many is first cut by histograms over its values.
 //
-// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 46 us,
-// 3.4 TB/s; by top-p 174, by top-k 106; 64 rows of mixed settings 39; 256 fp32 rows of
-// 32003 49; one row by top-p 23, by temperature 8.5.  The passes are bound by the
-// instructions they issue, 512 rows also by their count on 152 SMs; what lies between
-// the passes by the latency of steps that a whole CTA or cluster takes together, about
-// 0.7 us for each exchange in a cluster.
+// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 40.5 us,
+// 3.9 TB/s; by top-p 161, by top-k 101; 64 rows of mixed settings 37.3; 256 fp32 rows
+// of 32003 49; one row by top-p 22.3, by temperature 8.3.  The passes are bound by the
+// instructions they issue, 512 rows also by their count on 152 SMs (400 rows 32 us, 600
+// 40.7); what lies between the passes by the latency of steps that a whole CTA or
+// cluster takes together, about 0.7 us for each exchange in a cluster.
 #include "twofloat.cuh"
 
 #include "serving.cuh"
@@ -1078,7 +1078,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     // ---- the blocks' largest logits and their masses relative to those
     uint4 ahead[Row<F32>::NV];
     job.reach = 124.0f / job.c.h;
-    constexpr bool kAhead = !F32;  // the next block's loads in flight beside this one's sums, where registers allow it
+    // The next block's loads in flight beside this one's sums, where registers allow it: 1200 rows of 152064 by
+    // temperature 76 us and not 80, 64 rows 11.5 and not 12.5 (2048 rows of 32003 57.9 and not 56.1).
+    constexpr bool kAhead = !F32;
     if (kAhead && job.b0 + warp < job.b1) row.load(job.b0 + warp, ahead);
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
         uint4 w[Row<F32>::NV];
@@ -1361,14 +1363,14 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     const bool plain = !a.top_k && !a.top_p && !a.min_p;
     // CTAs a row: as many as still give each 8 blocks, and the SMs at most two CTAs, or one without a cut, whose one
     // pass gains less from a second than another exchange costs.  Rows of 152064, us at one CTA and at two an SM:
-    // temperature alone 32 rows 9.8 and 11.4, 64 12.2 and 13.6, 100 15.7 and 18.1; with cuts 64 43.8 and 39.1, 100
-    // 63.1 and 55.2 (four an SM: 51.4 for 64).  Rows of 12000 with cuts, 32 of them: 8 blocks 20.4, 4 blocks 23.5;
-    // rows of 32003: 8 blocks 26.0, 16 blocks 27.5.
+    // temperature alone 32 rows 9.5 and 11.2, 64 11.9 and 13.5, 100 14.4 and 16.9; with cuts 64 41.1 and 37.5, 100
+    // 57.9 and 51.0 (four an SM: 50.6 for 64).  32 rows of 12000 with cuts: 8 blocks 19.7, 4 blocks 22.9; of 32003: 8
+    // blocks 25.2, 16 blocks 26.2.
     int splits = 1;
     while (splits < kMaxSplit && 2 * splits * a.rows <= (plain ? sms : 2 * sms) && blocks / (2 * splits) >= 8) splits *= 2;
     // 512 threads a CTA, two an SM (registers).  Without a cut and with more rows than those, 256, four an SM: a row's
-    // end leaves fewer idle, 2048 rows of 32003 60.4 and not 82 us, 512 of 152064 46.2 and not 47.7.  With cuts CTAs of
-    // 256 are slower: 64 rows 40.0 and not 39.1, 256 fp32 rows of 32003 53.7 and not 49.2.
+    // end leaves fewer idle, 2048 rows of 32003 57.6 and not 79.6 us, 512 of 152064 40.5 and not 43.2.  With cuts CTAs of
+    // 256 are slower: 64 rows 38.4 and not 37.5, 256 fp32 rows of 32003 53.9 and not 49.7.
     if (plain) {
         if (splits == 1 && a.rows > 2 * sms)
             return a.f32 ? launch_rows<true, 256, true>(a, splits, stream) : launch_rows<false, 256, true>(a, splits, stream);
