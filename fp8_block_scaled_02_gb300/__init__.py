@@ -868,6 +868,36 @@ def kv4_rope_append(q, k, v, positions, slots, cos_sin, k_scale, v_scale, k_cach
                         interleaved, out, stream)
 
 
+def token_logprobs(logits, targets, top: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
+                   stream=None):
+    """Log probabilities of the targets [M] under logits [M, V] (bf16 or fp32,
+    rows may be padded, or one row expanded to M), each row's entropy and its
+    `top` best tokens (fp8bs_token_logprobs).  Returns a TokenLogprobs."""
+    m, v = _shape2(logits, "logits")
+    stride = logits.stride(0) if m > 1 else v
+    if 0 < stride < v:
+        raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")
+    top = int(top)
+    f32 = logits.dtype == torch.float32
+    given = [spec for spec in (("logprobs", logprobs, torch.float32, m, False), ("entropy", entropy, torch.float32, m, False),
+                               ("top_ids", top_ids, torch.int32, m * top, False),
+                               ("top_logprobs", top_logprobs, torch.float32, m * top, False)) if spec[1] is not None]
+    device = _checked(("logits", logits, torch.float32 if f32 else torch.bfloat16, None, True),
+                      ("targets", targets, torch.int32, m, False), *given)
+    if logprobs is None:
+        logprobs = _empty(stream, device, (m,), torch.float32)
+    if entropy is None:
+        entropy = _empty(stream, device, (m,), torch.float32)
+    if top_ids is None:
+        top_ids = _empty(stream, device, (m, top), torch.int32)
+    if top_logprobs is None:
+        top_logprobs = _empty(stream, device, (m, top), torch.float32)
+    _call(device, "fp8bs_token_logprobs", lib().fp8bs_token_logprobs,
+          (logits.data_ptr(), int(f32), stride, m, v, targets.data_ptr(), top,
+           logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top_logprobs.data_ptr()), stream)
+    return TokenLogprobs(logprobs, entropy, top_ids, top_logprobs)
+
+
 SampledTokens = collections.namedtuple("SampledTokens", "tokens logprobs")
 
 
