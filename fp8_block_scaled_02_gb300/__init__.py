@@ -623,8 +623,8 @@ def moe_route(logits, topk: int, scoring: str = "softmax", bias=None, groups: in
 def moe_combine(y, weights, ids=None, num_experts: int = 0, residual=None, out=None, stream=None):
     """The weighted sum of the experts' outputs y [M, topk, N] bf16
     (fp8bs_moe_combine): out [M, N] bf16 = residual + sum_j weights[:, j] y[:, j].
-    With ids (int32 [M, topk]) a slot whose id is outside [0, num_experts) adds
-    nothing.  out may be residual."""
+    With ids (int32 [M, topk]) and num_experts a slot whose id is outside
+    [0, num_experts) adds nothing.  out may be residual."""
     if y.dim() != 3:
         raise ValueError("y must be [M, topk, N]")
     m, topk, n = y.shape

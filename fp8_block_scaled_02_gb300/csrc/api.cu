@@ -671,7 +671,7 @@ int fp8bs_moe_combine(const void *y_bf16, const float *weights, const int32_t *e
     if (num_tokens < 0 || num_tokens >= kMaxDim || topk < 1 || topk > 1024 || n < 1 || n >= kMaxDim ||
         num_experts < 0 || num_experts >= kMaxDim || num_tokens * topk >= kMaxDim)
         return FP8BS_ERR_SHAPE;
-    if (num_tokens * ((n + 2047) / 2048) >= kMaxDim) return FP8BS_ERR_SHAPE;  // CTAs of 2048 columns of a token
+    if (num_tokens * ((n + 1023) / 1024) >= kMaxDim) return FP8BS_ERR_SHAPE;  // CTAs of 1024 columns of a token
     if (num_tokens == 0) return FP8BS_OK;
     if (!y_bf16 || !weights || !out_bf16) return FP8BS_ERR_NULL;
     if (!aligned(y_bf16, 2) || !aligned(weights, 4) || !aligned(expert_ids, 4) || !aligned(residual_bf16, 2) ||

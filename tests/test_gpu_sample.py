@@ -114,6 +114,21 @@ def test_far_temperatures(pkg, temperature, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("m", [8, 320])
+def test_ends_of_the_temperatures(pkg, m, dtype):
+    """The smallest is greedy among equals, the largest uniform."""
+    v = 3001
+    x = logits(m, v, 37, dtype)
+    x[:, 2990] = x.max(1).values                                # two largest ones
+    for temperature in (float(np.float32(1.0001e-30)), float(np.float32(0.9999e30))):
+        t = np.full(m, temperature)
+        check(pkg, x, uniform(m, 38), temperature=t)
+        check(pkg, x, uniform(m, 39), temperature=t, top_p=np.linspace(0.05, 0.99, m))
+        check(pkg, x, uniform(m, 40), temperature=t, top_k=np.arange(m) + 1, min_p=np.full(m, 0.5))
+        check(pkg, x, uniform(m, 41), temperature=t, top_k=np.full(m, 1500), top_p=np.full(m, 0.6))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m", [8, 320])
 def test_equals(pkg, m, dtype):
     """Rows of few values: cuts through equals keep the lowest of them."""
     v = 10007

@@ -159,7 +159,7 @@ def test_moe_combine_status(L):
     ok = dict(y=P(0x10000), w=P(0x20000), ids=P(0x30000), e=8, res=P(0x40000), m=3, k=2, n=64, out=P(0x50000))
     call = caller(L.fp8bs_moe_combine, ok)
     for kw in (dict(m=-1), dict(m=2 ** 31), dict(k=0), dict(k=1025), dict(n=0), dict(n=2 ** 31), dict(e=-1), dict(e=2 ** 31),
-               dict(m=2 ** 30, n=8192), dict(m=2 ** 30, k=4)):
+               dict(m=2 ** 30, n=8192), dict(m=2 ** 30, n=1025, k=1), dict(m=2 ** 30, k=4)):
         assert call(**kw) == -2, kw
     assert call(m=0, y=None, out=None) == 0
     for name in ("y", "w", "out"):
