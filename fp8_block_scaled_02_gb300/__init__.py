@@ -606,9 +606,14 @@ def moe_route(logits, topk: int, scoring: str = "softmax", bias=None, groups: in
         raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {e} long")
     i32, f32 = torch.int32, torch.float32
     is_f32 = logits.dtype == f32
-    given = [spec for spec in (("bias", bias, f32, e, False), ("ids", ids, i32, m * topk, False),
-                               ("weights", weights, f32, m * topk, False)) if spec[1] is not None]
-    device = _checked(("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), *given)
+    specs = [("logits", logits, f32 if is_f32 else torch.bfloat16, None, True)]
+    if bias is not None:
+        specs.append(("bias", bias, f32, e, False))
+    if ids is not None:
+        specs.append(("ids", ids, i32, m * topk, False))
+    if weights is not None:
+        specs.append(("weights", weights, f32, m * topk, False))
+    device = _checked(*specs)
     if ids is None:
         ids = _empty(stream, device, (m, topk), i32)
     if weights is None:
@@ -631,9 +636,14 @@ def moe_combine(y, weights, ids=None, num_experts: int = 0, residual=None, out=N
     if ids is not None and num_experts < 1:
         raise ValueError("ids need num_experts: a slot whose id is outside [0, num_experts) adds nothing")
     bf16 = torch.bfloat16
-    given = [spec for spec in (("ids", ids, torch.int32, m * topk, False), ("residual", residual, bf16, m * n, False),
-                               ("out", out, bf16, m * n, False)) if spec[1] is not None]
-    device = _checked(("y", y, bf16, None, False), ("weights", weights, torch.float32, m * topk, False), *given)
+    specs = [("y", y, bf16, None, False), ("weights", weights, torch.float32, m * topk, False)]
+    if ids is not None:
+        specs.append(("ids", ids, torch.int32, m * topk, False))
+    if residual is not None:
+        specs.append(("residual", residual, bf16, m * n, False))
+    if out is not None:
+        specs.append(("out", out, bf16, m * n, False))
+    device = _checked(*specs)
     if out is None:
         out = _empty(stream, device, (m, n), bf16)
     _call(device, "fp8bs_moe_combine", lib().fp8bs_moe_combine,
@@ -826,13 +836,10 @@ def _rope_append(four_bit, q, k, v, positions, slots, cos_sin, k_scale, v_scale,
                   ("k_scale", k_scale, f32, 1, False), ("v_scale", v_scale, f32, 1, False))
         what, fn, places = "fp8kv_rope_append", L.fp8kv_rope_append, (shape[0] * shape[1],)
     given = ()
-    q_ptr = k_ptr = None
     if q_norm is not None:
         given = (("q_norm", q_norm, bf16, d, False),)
-        q_ptr = q_norm.data_ptr()
     if k_norm is not None:
         given += (("k_norm", k_norm, bf16, d, False),)
-        k_ptr = k_norm.data_ptr()
     if out is not None:
         given += (("out", out, bf16, t * hq * d, False),)
     device = _checked(*caches, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
@@ -843,8 +850,9 @@ def _rope_append(four_bit, q, k, v, positions, slots, cos_sin, k_scale, v_scale,
     q_stride, k_stride, v_stride = (q.stride(0), k.stride(0), v.stride(0)) if t > 1 else (hq * d, hkv * d, hkv * d)
     _call(device, what, fn,
           (q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, t, hq, hkv, d, positions.data_ptr(),
-           slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, int(interleaved), q_ptr, k_ptr, float(eps), out.data_ptr(),
-           k_scale.data_ptr(), v_scale.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *places), stream)
+           slots.data_ptr(), cos_sin.data_ptr(), max_pos, rot, int(interleaved),
+           q_norm.data_ptr() if q_norm is not None else None, k_norm.data_ptr() if k_norm is not None else None, float(eps),
+           out.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *places), stream)
     return out
 
 
@@ -916,20 +924,29 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
         raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")
     f32, i32 = torch.float32, torch.int32
     is_f32 = logits.dtype == f32
-    given = [spec for spec in (("temperature", temperature, f32, m, False), ("top_k", top_k, i32, m, False),
-                               ("top_p", top_p, f32, m, False), ("min_p", min_p, f32, m, False),
-                               ("tokens", tokens, i32, m, False), ("logprobs", logprobs, f32, m, False))
-             if spec[1] is not None]
-    device = _checked(("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), ("u", u, f32, 2 * m, False),
-                      *given)
+    specs = [("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), ("u", u, f32, 2 * m, False)]
+    if temperature is not None:
+        specs.append(("temperature", temperature, f32, m, False))
+    if top_k is not None:
+        specs.append(("top_k", top_k, i32, m, False))
+    if top_p is not None:
+        specs.append(("top_p", top_p, f32, m, False))
+    if min_p is not None:
+        specs.append(("min_p", min_p, f32, m, False))
+    if tokens is not None:
+        specs.append(("tokens", tokens, i32, m, False))
+    if logprobs is not None:
+        specs.append(("logprobs", logprobs, f32, m, False))
+    device = _checked(*specs)
     if tokens is None:
         tokens = _empty(stream, device, (m,), i32)
     if logprobs is None:
         logprobs = _empty(stream, device, (m,), f32)
     _call(device, "fp8bs_sample_tokens", lib().fp8bs_sample_tokens,
           (logits.data_ptr(), int(is_f32), stride, m, v, u.data_ptr(),
-           *(t.data_ptr() if t is not None else None for t in (temperature, top_k, top_p, min_p)), tokens.data_ptr(),
-           logprobs.data_ptr()), stream)
+           temperature.data_ptr() if temperature is not None else None, top_k.data_ptr() if top_k is not None else None,
+           top_p.data_ptr() if top_p is not None else None, min_p.data_ptr() if min_p is not None else None,
+           tokens.data_ptr(), logprobs.data_ptr()), stream)
     return SampledTokens(tokens, logprobs)
 
 

@@ -82,7 +82,8 @@ def test_right_sizes_on_the_cpu_are_refused_as_not_cuda(call):
 
 @pytest.mark.parametrize("call", [
     lambda: rope8(q=t((4, 8, 128), F32)), lambda: rope4(positions=t(4, torch.int64)), lambda: rope8(cos_sin=t((50, 64), BF)),
-    lambda: rope8(k_norm=t(128, F32)), lambda: route(logits=t((3, 16), torch.float16)), lambda: route(bias=t(16, BF)),
+    lambda: rope8(k_norm=t(128, F32)), lambda: rope4(q_norm=1.0), lambda: route(bias=0.0), lambda: combine(residual=1),
+    lambda: sample(top_k=40), lambda: sample(min_p=0.1), lambda: sample(tokens=[0, 0, 0]), lambda: route(logits=t((3, 16), torch.float16)), lambda: route(bias=t(16, BF)),
     lambda: combine(weights=t((3, 2), BF)), lambda: combine(ids=t((3, 2), torch.int64), num_experts=4), lambda: sample(temperature=0.7),
     lambda: sample(top_k=t(3, torch.int64)), lambda: sample(top_p=t(3, torch.float64)), lambda: sample(u=t((3, 2), BF)),
     lambda: combine(y=t((3, 4, 64), BF)[:, ::2]), lambda: sample(logits=t((3, 100), BF)[:, ::2]),
