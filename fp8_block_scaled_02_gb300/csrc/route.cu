@@ -203,19 +203,22 @@ template <bool F32, int EPL>
 __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t token, Candidates &sh) {
     constexpr float kLog2e = 1.4426950408889634f;
     const int lane = threadIdx.x & 31, experts = static_cast<int>(a.experts), topk = static_cast<int>(a.topk);
-    const int e0 = lane * EPL, groups = static_cast<int>(a.groups), per = groups > 1 ? experts / groups : experts;
-    const int lanes = per / EPL;  // of a group
-    if (groups > 1 && (lanes * EPL != per || (lanes & (lanes - 1)) != 0)) return false;
+    const int groups = static_cast<int>(a.groups), per = groups > 1 ? experts / groups : experts;
+    const int lanes = groups > 1 ? 32 >> (32 - __clz(groups - 1)) : 32;  // of a group, a power of two
+    if (lanes * EPL < per) return false;
+    // this lane's experts, e0 .. e0 + mine - 1: they rise with the lanes
+    const int group = lane / lanes, begin = (lane % lanes) * EPL, left = group < groups ? per - begin : 0;
+    const int e0 = group * per + begin, mine = left < 0 ? 0 : left < EPL ? left : EPL;
     const char *row = static_cast<const char *>(a.logits) + token * a.row_stride * (F32 ? 4 : 2);
     float x[EPL];
     constexpr int kBytes = EPL * (F32 ? 4 : 2);
     bool vector = false;
-    if constexpr (kBytes >= 16) vector = (reinterpret_cast<uintptr_t>(row) & 15) == 0 && e0 + EPL <= experts;
+    if constexpr (kBytes >= 16) vector = (reinterpret_cast<uintptr_t>(row + e0 * (F32 ? 4 : 2)) & 15) == 0 && mine == EPL;
     if (vector) {
         if constexpr (kBytes >= 16) {
 #pragma unroll
             for (int i = 0; i < kBytes / 16; ++i) {
-                const uint4 v = ld_v4(row + static_cast<int64_t>(lane) * kBytes + 16 * i);
+                const uint4 v = ld_v4(row + e0 * (F32 ? 4 : 2) + 16 * i);
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -226,7 +229,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) x[i] = e0 + i < experts ? load_logit<F32>(row, e0 + i) : -INFINITY;
+        for (int i = 0; i < EPL; ++i) x[i] = i < mine ? load_logit<F32>(row, e0 + i) : -INFINITY;
     }
     float m = 0.0f, z = 1.0f;
     if (a.softmax) {
@@ -268,7 +271,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         slack = a.softmax ? (EPL <= 8 ? 0x1p-19f : 0x1p-18f) * to_score : 0x1p-21f;
         float b[EPL] = {};
         bool wide = false;
-        if constexpr (EPL >= 4) wide = a.bias && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0 && e0 + EPL <= experts;
+        if constexpr (EPL >= 4) wide = a.bias && (reinterpret_cast<uintptr_t>(a.bias + e0) & 15) == 0 && mine == EPL;
         if (wide) {
             if constexpr (EPL >= 4) {
 #pragma unroll
@@ -279,7 +282,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
             }
         } else if (a.bias) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) b[i] = e0 + i < experts ? a.bias[e0 + i] : 0.0f;
+            for (int i = 0; i < EPL; ++i) b[i] = i < mine ? a.bias[e0 + i] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) c[i] = fmaf(c[i], to_score, fminf(fmaxf(b[i], -kMostBias), kMostBias));
@@ -291,7 +294,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         bool nan = false;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const float v = e0 + i < experts ? c[i] : -INFINITY;
+            const float v = i < mine ? c[i] : -INFINITY;
             nan |= v != v;
             b2 = fmaxf(b2, fminf(b1, v));
             b1 = fmaxf(b1, v);
@@ -302,18 +305,17 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
             b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
             b1 = fmaxf(b1, o1);
         }
-        const int mine = lane / lanes;
         const float score = a.group_top == 2 ? b1 + b2 : b1;
         int before = 0;
         for (int g = 0; g < groups; ++g) {
             const float other = __shfl_sync(0xffffffffu, score, g * lanes);
-            before += other > score || (other == score && g < mine) ? 1 : 0;
+            before += other > score || (other == score && g < group) ? 1 : 0;
         }
-        open = mine < groups && before < static_cast<int>(a.topk_groups);
+        open = group < groups && before < static_cast<int>(a.topk_groups);
         if (a.topk_groups < a.groups) {
             // the last that is open and the first that is not
             const uint32_t in = __reduce_min_sync(0xffffffffu, open ? logit_key(score) : 0xFFFFFFFFu);
-            const uint32_t out = __reduce_max_sync(0xffffffffu, mine < groups && !open ? logit_key(score) : 0u);
+            const uint32_t out = __reduce_max_sync(0xffffffffu, group < groups && !open ? logit_key(score) : 0u);
             const float low = __uint_as_float(in & 0x80000000u ? in & 0x7FFFFFFFu : ~in);
             const float high = __uint_as_float(out & 0x80000000u ? out & 0x7FFFFFFFu : ~out);
             if (!(low - high > 4.0f * (slack + 0x1p-22f * (fabsf(low) + fabsf(high))))) return false;
@@ -321,7 +323,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     }
     const bool by_score = a.bias != nullptr;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = open && e0 + i < experts ? logit_key(by_score ? c[i] : x[i]) : 0u;
+    for (int i = 0; i < EPL; ++i) key[i] = open && i < mine ? logit_key(by_score ? c[i] : x[i]) : 0u;
     // ---- candidates: what is not below the topk-th largest of the lanes' largest, which is no larger than the topk-th of
     // all; by scores not below what may yet be before it.  To lane j the j-th of them by key, then expert.
     auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); };
@@ -340,10 +342,10 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         least = logit_key(v - 4.0f * (slack + 0x1p-21f * fabsf(v)));
     }
     if (least == 0) least = 1;
-    int mine = 0;
+    int some = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) mine += key[i] >= least ? 1 : 0;
-    int upto = mine;
+    for (int i = 0; i < EPL; ++i) some += key[i] >= least ? 1 : 0;
+    int upto = some;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -353,7 +355,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     if (n > 32) return false;
     sh.key[lane] = 0;
     __syncwarp();
-    int to = upto - mine;
+    int to = upto - some;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
         if (key[i] >= least) {
@@ -457,13 +459,18 @@ cudaError_t launch_route_t(const MoeScoreArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, route_kernel<F32, EPL>, a);
 }
 
+// Experts a lane: what a group's lanes, or all, have to hold; what they cannot is left to pairs of fp32 alone.
 template <bool F32>
 cudaError_t launch_route_epl(const MoeScoreArgs &a, cudaStream_t stream) {
-    if (a.experts <= 32) return launch_route_t<F32, 1>(a, stream);
-    if (a.experts <= 64) return launch_route_t<F32, 2>(a, stream);
-    if (a.experts <= 128) return launch_route_t<F32, 4>(a, stream);
-    if (a.experts <= 256) return launch_route_t<F32, 8>(a, stream);
-    if (a.experts <= 512) return launch_route_t<F32, 16>(a, stream);
+    int64_t lanes = 32;
+    for (int64_t g = 1; g < a.groups; g *= 2) lanes /= 2;
+    const int64_t all = (a.experts + 31) / 32, group = (a.experts / a.groups + lanes - 1) / lanes;
+    const int64_t need = group > 32 || all > group ? all : group;
+    if (need <= 1) return launch_route_t<F32, 1>(a, stream);
+    if (need <= 2) return launch_route_t<F32, 2>(a, stream);
+    if (need <= 4) return launch_route_t<F32, 4>(a, stream);
+    if (need <= 8) return launch_route_t<F32, 8>(a, stream);
+    if (need <= 16) return launch_route_t<F32, 16>(a, stream);
     return launch_route_t<F32, 32>(a, stream);
 }
 

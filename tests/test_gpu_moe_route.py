@@ -63,7 +63,8 @@ def test_matches_float64(pkg, m, e, topk, scoring, dtype):
 @pytest.mark.parametrize("scoring,with_bias", [("sigmoid", True), ("softmax", False), ("softmax", True)])
 @pytest.mark.parametrize("m,e,topk,groups,topk_groups,group_top", [
     (50, 256, 8, 8, 4, 2), (9, 160, 6, 8, 3, 1), (5, 60, 4, 4, 2, 2), (3, 1024, 32, 32, 7, 2), (7, 12, 2, 12, 3, 1),
-    (4, 33, 11, 3, 1, 2), (6, 64, 16, 2, 2, 1), (3, 100, 3, 20, 1, 2)])
+    (4, 33, 11, 3, 1, 2), (6, 64, 16, 2, 2, 1), (3, 100, 3, 20, 1, 2), (70, 160, 6, 8, 3, 2), (5, 384, 8, 8, 4, 2),
+    (7, 93, 5, 3, 2, 1), (3, 1023, 8, 31, 4, 2), (4, 70, 4, 7, 3, 2), (5, 333, 9, 9, 2, 2)])
 def test_groups(pkg, m, e, topk, groups, topk_groups, group_top, scoring, with_bias):
     x = logits(m, e, e + topk)
     bias = torch.randn(e, generator=torch.Generator().manual_seed(1)) * 0.05 if with_bias else None
