@@ -9,8 +9,8 @@
 // of fp32.  Without a bias or groups it goes by the logits themselves.
 //
 // Floor: the logits read once (8192 tokens of 256 experts in fp32: 8.9 MB, 1.3 us).
-// Measured 16.9 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 9.8 (softmax,
-// 12 of 256, no bias), and 3.4 for 32 tokens, most of it the launch and the chain of
+// Measured 16.6 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 9.7 (softmax,
+// 12 of 256, no bias), 14.3 (softmax, 3 of 8 groups, 6 of 160) and 3.4 for 32 tokens, most of it the launch and the chain of
 // dependent steps.  What bounds the prompt is instructions, 1110 and 860 a token, ALU
 // first: the scores, the groups, the order keys.  With pairs of fp32 for every token it
 // took 36.5 us; with the largest left taken topk times in place of a rank among the few
@@ -429,9 +429,10 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
     return true;
 }
 
-// 64 registers to 256 experts: 32 warps an SM, in CTAs of 4
+// CTAs an SM: 32 warps to 8 experts a lane (64 registers); 28 for 16 (8192 x 512, softmax top 10: 12.8 us, 16 warps
+// 15.4), 16 for 32 (1024 experts: 24.7 us, 8 warps 36.7).
 template <bool F32, int EPL>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 8 : 1) route_kernel(const __grid_constant__ MoeScoreArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 8 : EPL == 16 ? 7 : 4) route_kernel(const __grid_constant__ MoeScoreArgs a) {
     extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
     __shared__ Candidates candidates[kRouteWarps];
