@@ -22,11 +22,11 @@
 // gathered in shared memory, where histograms over their values end the search.
 // A bin that holds too many is first cut by histograms over its values.
 //
-// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 40.5 us,
-// 3.9 TB/s; by top-p 161, by top-k 101; 64 rows of mixed settings 37.3; 256 fp32 rows
-// of 32003 49; one row by top-p 22.3, by temperature 8.3.  The passes are bound by the
-// instructions they issue, 512 rows also by their count on 152 SMs (400 rows 32 us, 600
-// 40.7); what lies between the passes by the latency of steps that a whole CTA or
+// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 39.2 us,
+// 4.0 TB/s; by top-p 163, by top-k 103; 64 rows of mixed settings 37; 256 fp32 rows
+// of 32003 44.4; one row by top-p 22, by temperature 8.4.  The passes are bound by the
+// instructions they issue, 512 rows also by their count on 152 SMs (400 rows 33 us, 600
+// 40.1); what lies between the passes by the latency of steps that a whole CTA or
 // cluster takes together, about 0.7 us for each exchange in a cluster.
 #include "twofloat.cuh"
 
@@ -152,7 +152,11 @@ __device__ __forceinline__ uint4 ld_v4_cached(const void *p) {
 }
 
 // A row of logits by blocks: lane l of the warp that has block b holds NV vectors
-// of VE elements, of element b * 1024 + (l + 32 i) * VE on; -inf past the row.
+// of VE elements, of element b * 1024 + (l + 32 i) * VE on, or turned; -inf past the
+// row.  Turned rows read as many vectors as others: 2048 bf16 rows of 32003 by
+// temperature 50.7 us, 57.8 with each vector put together from two; 256 fp32 rows of
+// 32003 with cuts 44.4 and 48.8.  With the next block's loads ahead in registers (bf16)
+// the first took 54.0, 512 rows of 152064 42.6 and not 39.2, 64 of them 11.6 and not 12.1.
 template <bool F32>
 struct Row {
     static constexpr int VE = F32 ? 4 : 8, NV = kBlock / (32 * VE), ES = F32 ? 4 : 2;
@@ -190,11 +194,10 @@ struct Row {
                           __funnelshift_r(u[Q + 2], u[Q + 3], bits),
                           __funnelshift_r(u[Q + 3], Q < 3 ? u[Q < 3 ? Q + 4 : 0] : b.w, bits));
     }
-    template <int Q>
-    __device__ __forceinline__ void load_shifted(int first, uint4 (&w)[NV]) const {
-        const char *p = base + static_cast<int64_t>(first) * ES - off;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) w[i] = shifted<Q>(p + i * 512, (off & 3) * 8);
+    // Elements by which a lane's vectors of block b are turned: where the row is off a boundary they are taken as they
+    // lie in memory, and the first one's elements before the block are those after its last vector instead.
+    __device__ __forceinline__ int turn(int b) const {
+        return off != 0 && b > 0 && (b + 1) * kBlock + VE <= vocab ? off / ES : 0;
     }
     __device__ __forceinline__ void load(int b, uint4 (&w)[NV]) const {
         const int first = b * kBlock + (threadIdx.x & 31) * VE;
@@ -204,13 +207,17 @@ struct Row {
             for (int i = 0; i < NV; ++i) w[i] = ld_v4(p + i * 512);
             return;
         }
-        if (off != 0 && b > 0 && (b + 1) * kBlock + VE <= vocab) {  // with the vectors before and behind it in the row
-            switch (off >> 2) {
-                case 0: load_shifted<0>(first, w); break;
-                case 1: load_shifted<1>(first, w); break;
-                case 2: load_shifted<2>(first, w); break;
-                default: load_shifted<3>(first, w); break;
-            }
+        if (turn(b) != 0) {
+            const char *p = base + static_cast<int64_t>(first) * ES - off;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) w[i] = ld_v4(p + i * 512);
+            const uint4 e = ld_v4(base + static_cast<int64_t>(b + 1) * kBlock * ES - off);
+            const int from = (threadIdx.x & 31) == 0 ? off : 0;  // bytes that are those of e
+            auto join = [&](uint32_t mine, uint32_t behind, int at) {
+                const uint32_t mask = (from > at ? 0xFFFFu : 0u) | (from > at + 2 ? 0xFFFF0000u : 0u);
+                return (behind & mask) | (mine & ~mask);
+            };
+            w[0] = make_uint4(join(w[0].x, e.x, 0), join(w[0].y, e.y, 4), join(w[0].z, e.z, 8), join(w[0].w, e.w, 12));
             return;
         }
 #pragma unroll
@@ -822,13 +829,13 @@ __device__ void sum_blocks(const Row<F32> &row, const Job &job, Shared<TH> &sh, 
             n = __popc(in);
             if constexpr (GATHER) {
                 if (__any_sync(0xffffffffu, n > 0)) {
-                    const int upto = warp_inclusive(n);
+                    const int upto = warp_inclusive(n), turn = row.turn(b);
                     int at = 0;
                     if (lane == 31) at = atomicAdd(&sh.listed, upto);
                     at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
                     for (uint32_t left = in; left; left &= left - 1, ++at) {
                         const int k = Row<F32>::element(__ffs(left) - 1);
-                        const int id = b * kBlock + (lane + 32 * (k / VE)) * VE + k % VE;
+                        const int id = b * kBlock + (((lane + 32 * (k / VE)) * VE + k % VE - turn) & (kBlock - 1));
                         if (at < kGather) {
                             sh.list_key[at] = Key<F32>::of(row.at(id));
                             sh.list_id[at] = id;
@@ -1076,21 +1083,10 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         __syncthreads();
     }
     // ---- the blocks' largest logits and their masses relative to those
-    uint4 ahead[Row<F32>::NV];
     job.reach = 124.0f / job.c.h;
-    // The next block's loads in flight beside this one's sums, where registers allow it: 1200 rows of 152064 by
-    // temperature 76 us and not 80, 64 rows 11.5 and not 12.5 (2048 rows of 32003 57.9 and not 56.1).
-    constexpr bool kAhead = !F32;
-    if (kAhead && job.b0 + warp < job.b1) row.load(job.b0 + warp, ahead);
     for (int b = job.b0 + warp; b < job.b1; b += kWarps) {
         uint4 w[Row<F32>::NV];
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int i = 0; i < Row<F32>::NV; ++i) w[i] = ahead[i];
-            if (b + kWarps < job.b1) row.load(b + kWarps, ahead);
-        } else {
-            row.load(b, w);
-        }
+        row.load(b, w);
         const uint32_t lane_key = K::of(Row<F32>::most(w)), key = __reduce_max_sync(0xffffffffu, lane_key);
         if (!PLAIN && by_k) atomicAdd(&sh.n[lane_key >> kBoundShift], 1u);
         float s = 0.0f;
@@ -1369,7 +1365,7 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     int splits = 1;
     while (splits < kMaxSplit && 2 * splits * a.rows <= (plain ? sms : 2 * sms) && blocks / (2 * splits) >= 8) splits *= 2;
     // 512 threads a CTA, two an SM (registers).  Without a cut and with more rows than those, 256, four an SM: a row's
-    // end leaves fewer idle, 2048 rows of 32003 57.6 and not 79.6 us, 512 of 152064 40.5 and not 43.2.  With cuts CTAs of
+    // end leaves fewer idle, 2048 rows of 32003 57.6 and not 79.6 us, 512 of 152064 40.5 and not 43.2 (with loads ahead).  With cuts CTAs of
     // 256 are slower: 64 rows 38.4 and not 37.5, 256 fp32 rows of 32003 53.9 and not 49.7.
     if (plain) {
         if (splits == 1 && a.rows > 2 * sms)
