@@ -385,7 +385,7 @@ __device__ __forceinline__ void rope_cached(const KvRopeArgs &a, int64_t token, 
 // its last warp is done; at 64 tokens 64 takes 2.3 us, 128 2.15.  A lane with 8
 // elements (a third more instructions a byte, 48 warps an SM) took 51.6 us, a warp
 // with several tokens one after the other, the next one's heads loaded ahead into
-// registers 52 to 106, into shared memory 59 to 86.
+// registers 44 to 106, into shared memory 59 to 86.
 template <int D, bool F4, bool NEXT>
 __global__ void __launch_bounds__(kRopeThreads, 8) kv_rope_kernel(const __grid_constant__ KvRopeArgs a, uint32_t kv_blocks,
                                                                   uint64_t kv_inverse, uint64_t q_inverse) {

@@ -12,7 +12,7 @@
 // Measured 16.6 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 9.7 (softmax,
 // 12 of 256, no bias), 14.3 (softmax, 3 of 8 groups, 6 of 160) and 3.4 for 32 tokens,
 // most of it the launch and the chain of dependent steps.  What bounds the prompt is
-// instructions, 1110 and 860 a token, ALU first: the scores, the groups, the order
+// instructions, 1090 and 860 a token, ALU first: the scores, the groups, the order
 // keys.  With pairs of fp32 for every token it took 36.5 us; with the largest left
 // taken topk times in place of a rank among the few that can be chosen 18.9, 13.8 and
 // 4.2.  Warps an SM: 16 20.0 us (with those rounds), 32 16.9 and 9.8, 40 17.1 and 9.7,
