@@ -9,6 +9,8 @@ weight, below 2^-19 to E = 256.
 Combine: topk fused multiply-adds round by 2^-24 of the running sum, below
 the sum of the magnitudes; one bf16 rounding, 2^-8 of the result at most.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -137,6 +139,33 @@ def test_nan_comes_last_and_ids_stay_distinct(pkg, with_bias):
     ids, _ = pkg.moe_route(x.to(DEV), 10, bias=None if bias is None else bias.to(DEV))
     for row in ids.tolist():
         assert len(set(row)) == 10 and min(row) >= 0 and max(row) < 96
+
+
+@pytest.mark.parametrize("scoring,with_bias", [("sigmoid", True), ("sigmoid", False), ("softmax", False), ("softmax", True)])
+@pytest.mark.parametrize("e,topk,groups,topk_groups", [(256, 8, 8, 4), (256, 12, 1, 1), (40, 32, 1, 1), (7, 7, 1, 1),
+                                                       (160, 20, 8, 1), (96, 5, 3, 2), (600, 31, 1, 1)])
+def test_any_logits_give_distinct_ids(pkg, e, topk, groups, topk_groups, scoring, with_bias):
+    """Rows of equals, of few values, of zeros of both signs, of infinities, the largest numbers and NaN: ids in range and
+    distinct; and the definition's where nothing is NaN or +inf."""
+    g = torch.Generator().manual_seed(e + topk)
+    big = torch.finfo(torch.float32).max
+    values = torch.tensor([0.0, -0.0, 1.0, 1.0 + 2.0 ** -23, -1.0, big, -big, 1e-40, -math.inf, 90.0, -90.0, math.inf, math.nan])
+    x = torch.randn((60, e), generator=g)
+    for r in range(60):
+        pick = values[torch.randint(0, 9 + 4 * (r % 4 == 3), (e,), generator=g)]
+        x[r] = torch.where(torch.rand(e, generator=g) < (r % 10) / 9, pick, x[r])
+    x[0], x[1], x[2] = 0.25, -math.inf, math.nan
+    bias = torch.randn(e, generator=g) * 0.05 if with_bias else None
+    kw = dict(scoring=scoring, groups=groups, topk_groups=topk_groups, group_top=1)
+    ids, w = pkg.moe_route(x.to(DEV), topk, bias=None if bias is None else bias.to(DEV), **kw)
+    ids = ids.cpu().numpy()
+    assert ids.min() >= 0 and ids.max() < e and all(len(set(row)) == topk for row in ids)
+    fine = [r for r in range(60) if not bool((torch.isnan(x[r]) | (x[r] == math.inf)).any())]
+    want, weights = ref.route(x[fine].double().numpy(), topk, bias=None if bias is None else bias.numpy(), **kw)
+    assert np.array_equal(ids[fine], want)
+    # within 2^-18 of itself; of e^-|x| below 2^-126 nothing is left
+    assert np.all(np.abs(w.cpu().double().numpy()[fine] - weights) <= 2.0 ** -18 * weights + 2.0 ** -120)
+    assert pkg.check_device_error() == 0
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

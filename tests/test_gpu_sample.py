@@ -128,6 +128,18 @@ def test_ends_of_the_temperatures(pkg, m, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale,temperature", [(1e31, 0.9e30), (5e37, 0.9e30), (5e37, 1.0), (1e-35, 1e-30), (1e-38, 1.0)])
+def test_huge_and_tiny_logits(pkg, scale, temperature, dtype):
+    """Logits near the type's largest, and subnormal ones."""
+    m, v = 12, 5003
+    x = (logits(m, v, 42, torch.float32, tall=False).clamp(-6, 6).double() * scale).to(dtype)
+    t = np.full(m, np.float64(np.float32(temperature)))
+    check(pkg, x, uniform(m, 43), temperature=t)
+    check(pkg, x, uniform(m, 44), temperature=t, top_p=np.linspace(0.05, 0.99, m))
+    check(pkg, x, uniform(m, 45), temperature=t, top_k=np.arange(m) * 9 + 1, min_p=np.full(m, 0.01))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("m", [8, 320])
 def test_equals(pkg, m, dtype):
     """Rows of few values: cuts through equals keep the lowest of them."""
