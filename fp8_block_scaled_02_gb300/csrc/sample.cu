@@ -145,10 +145,23 @@ __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-__device__ __forceinline__ uint4 ld_v4_cached(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+// Elements e0 .. of a row, 16 bytes of them, -inf past it: what the ends of a row that is off a boundary need.  One copy
+// of its code, which every pass would have for each of a lane's vectors.
+template <bool F32>
+__device__ __noinline__ uint4 one_by_one(const char *base, int vocab, int e0) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (F32) {
+            w[j] = e0 + j < vocab ? reinterpret_cast<const uint32_t *>(base)[e0 + j] : 0xFF800000u;
+        } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(base);
+            const uint32_t lo = e0 + 2 * j < vocab ? p[e0 + 2 * j] : 0xFF80u;
+            const uint32_t hi = e0 + 2 * j + 1 < vocab ? p[e0 + 2 * j + 1] : 0xFF80u;
+            w[j] = lo | hi << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A row of logits by blocks: lane l of the warp that has block b holds NV vectors
@@ -168,31 +181,6 @@ struct Row {
     __device__ __forceinline__ float at(int e) const {
         if constexpr (F32) return reinterpret_cast<const float *>(base)[e];
         else return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[e]);
-    }
-    __device__ __forceinline__ uint4 slow(int e0) const {  // at the row's ends
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (F32) {
-                w[j] = e0 + j < vocab ? reinterpret_cast<const uint32_t *>(base)[e0 + j] : 0xFF800000u;
-            } else {
-                const uint16_t *p = reinterpret_cast<const uint16_t *>(base);
-                const uint32_t lo = e0 + 2 * j < vocab ? p[e0 + 2 * j] : 0xFF80u;
-                const uint32_t hi = e0 + 2 * j + 1 < vocab ? p[e0 + 2 * j + 1] : 0xFF80u;
-                w[j] = lo | hi << 16;
-            }
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    // Elements e0 .. e0 + VE - 1 of a row that is 4 Q bytes and `bits` off a boundary, from the two vectors that hold them.
-    template <int Q>
-    __device__ __forceinline__ uint4 shifted(const char *p, int bits) const {
-        const uint4 a = ld_v4_cached(p), b = ld_v4_cached(p + 16);
-        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        if constexpr (F32) return make_uint4(u[Q], u[Q + 1], u[Q + 2], u[Q + 3]);
-        return make_uint4(__funnelshift_r(u[Q], u[Q + 1], bits), __funnelshift_r(u[Q + 1], u[Q + 2], bits),
-                          __funnelshift_r(u[Q + 2], u[Q + 3], bits),
-                          __funnelshift_r(u[Q + 3], Q < 3 ? u[Q < 3 ? Q + 4 : 0] : b.w, bits));
     }
     // Elements by which a lane's vectors of block b are turned: where the row is off a boundary they are taken as they
     // lie in memory, and the first one's elements before the block are those after its last vector instead.
@@ -227,11 +215,7 @@ struct Row {
             if (e0 >= vocab) w[i] = F32 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
                                         : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
             else if (off == 0 && e0 + VE <= vocab) w[i] = ld_v4(p);
-            else if (off == 0 || e0 * ES < off || e0 + 2 * VE > vocab) w[i] = slow(e0);
-            else if (off < 4) w[i] = shifted<0>(p - off, (off & 3) * 8);
-            else if (off < 8) w[i] = shifted<1>(p - off, (off & 3) * 8);
-            else if (off < 12) w[i] = shifted<2>(p - off, (off & 3) * 8);
-            else w[i] = shifted<3>(p - off, (off & 3) * 8);
+            else w[i] = one_by_one<F32>(base, vocab, e0);
         }
     }
     static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[VE]) {
