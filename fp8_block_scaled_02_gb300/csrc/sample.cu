@@ -22,9 +22,9 @@
 // gathered in shared memory, where histograms over their values end the search.
 // A bin that holds too many is first cut by histograms over its values.
 //
-// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 39.2 us,
+// Floor: the logits once.  512 rows of 152064 (bf16, 156 MB) by temperature 38.6 us,
 // 4.0 TB/s; by top-p 163, by top-k 103; 64 rows of mixed settings 37; 256 fp32 rows
-// of 32003 44.4; one row by top-p 22, by temperature 8.4.  The passes are bound by the
+// of 32003 44.1; one row by top-p 21.8, by temperature 8.4.  The passes are bound by the
 // instructions they issue, 512 rows also by their count on 152 SMs (400 rows 33 us, 600
 // 40.1); what lies between the passes by the latency of steps that a whole CTA or
 // cluster takes together, about 0.7 us for each exchange in a cluster.
