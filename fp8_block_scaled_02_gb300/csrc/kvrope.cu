@@ -85,7 +85,9 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
     unpair(v, a, b);
     return f32x2_to_bf16x2(a, b);
 }
-__device__ __forceinline__ uint4 pack8(const uint64_t *x) { return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3])); }
+__device__ __forceinline__ uint4 pack8(const uint64_t *x) {
+    return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+}
 // (x0, y0), (x1, y1) of the pairs (x0, x1), (y0, y1)
 __device__ __forceinline__ void pack_together(uint64_t x, uint64_t y, uint32_t &a, uint32_t &b) {
     float x0, x1, y0, y1;

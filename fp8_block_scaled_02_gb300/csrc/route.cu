@@ -452,7 +452,8 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
 // CTAs an SM: 32 warps to 8 experts a lane (64 registers); 28 for 16 (8192 x 512, softmax top 10: 12.8 us, 16 warps
 // 15.4), 16 for 32 (1024 experts: 24.7 us, 8 warps 36.7).
 template <bool F32, int EPL>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 8 : EPL == 16 ? 7 : 4) route_kernel(const __grid_constant__ MoeScoreArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 8 : EPL == 16 ? 7 : 4)
+    route_kernel(const __grid_constant__ MoeScoreArgs a) {
     extern __shared__ uint64_t sh_scores[];  // [warps][experts], with groups
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
     __shared__ Candidates candidates[kRouteWarps];

@@ -1183,7 +1183,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             }
             if (!sh.range.none) {
                 find_cut<F32, TH>(row, job, sh, target, list, true);
-                if (sh.range.lo > cut || (sh.range.lo == cut && sh.range.equals < ties)) cut = sh.range.lo, ties = sh.range.equals;
+                if (sh.range.lo > cut || (sh.range.lo == cut && sh.range.equals < ties))
+                    cut = sh.range.lo, ties = sh.range.equals;
                 __syncthreads();
             }
         }
@@ -1349,8 +1350,9 @@ cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
     int splits = 1;
     while (splits < kMaxSplit && 2 * splits * a.rows <= (plain ? sms : 2 * sms) && blocks / (2 * splits) >= 8) splits *= 2;
     // 512 threads a CTA, two an SM (registers).  Without a cut and with more rows than those, 256, four an SM: a row's
-    // end leaves fewer idle, 2048 rows of 32003 57.6 and not 79.6 us, 512 of 152064 40.5 and not 43.2 (with loads ahead).  With cuts CTAs of
-    // 256 are slower: 64 rows 38.4 and not 37.5, 256 fp32 rows of 32003 53.9 and not 49.7.
+    // end leaves fewer idle, 2048 rows of 32003 57.6 and not 79.6 us, 512 of 152064 40.5 and not 43.2 (with the loads
+    // ahead of then).  With cuts CTAs of 256 are slower: 64 rows 38.4 and not 37.5, 256 fp32 rows of 32003 53.9 and not
+    // 49.7.
     if (plain) {
         if (splits == 1 && a.rows > 2 * sms)
             return a.f32 ? launch_rows<true, 256, true>(a, splits, stream) : launch_rows<false, 256, true>(a, splits, stream);
