@@ -306,6 +306,7 @@ struct Shared {
     uint64_t warp_sum[kWarps], part_mass[kMaxSplit], part_in[kMaxSplit];
     double log_min_p;
     int warp_int[kWarps];
+    uint64_t went_in[kWarps];         // of count_exponents, which no barrier parts from the sums before it
     uint32_t warp_key[kWarps], part_key[kMaxSplit], part_bound[kMaxSplit], bound, min_key;
     uint64_t bin_weight[32];          // kBinWeight: lanes ask for different ones
     int listed, collected, last, block, allowed;
@@ -342,7 +343,8 @@ __device__ __forceinline__ uint32_t dsmem_next(int *local, int rank, uint32_t n)
     return r;
 }
 
-// The sum of the values of the threads before this one, and of all.
+// The sum of the values of the threads before this one, and of all.  It ends with every thread reading `warps`, and no
+// barrier after that: whoever writes one of the arrays that are given here, warp_int and warp_sum, has a barrier before.
 template <class T, int TH>
 __device__ __forceinline__ T cta_exclusive(T v, T *warps, T &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -682,13 +684,13 @@ __device__ void count_exponents(const Row<F32> &row, const Job &job, Shared<TH> 
     if constexpr (MODE == kMasses) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) went_in += __shfl_xor_sync(0xffffffffu, went_in, o);
-        if (lane == 0) sh.warp_sum[warp] = went_in;
+        if (lane == 0) sh.went_in[warp] = went_in;
     }
     __syncthreads();
     if constexpr (MODE == kMasses) {
         if (tid == 0) {
             went_in = 0;
-            for (int i = 0; i < TH / 32; ++i) went_in += sh.warp_sum[i];
+            for (int i = 0; i < TH / 32; ++i) went_in += sh.went_in[i];
             if (job.splits > 1) dsmem_put(&sh.part_in[job.part], 0, went_in);
             else sh.part_in[0] = went_in;
         }
