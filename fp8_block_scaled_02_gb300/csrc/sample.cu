@@ -29,6 +29,7 @@
 // 40.1); what lies between the passes by the latency of steps that a whole CTA or
 // cluster takes together, about 0.7 us for each exchange in a cluster.
 #include "twofloat.cuh"
+#include "samplebins.cuh"
 
 #include "serving.cuh"
 #include "internal.h"
@@ -46,11 +47,8 @@ __device__ uint32_t g_sample_err;
 constexpr int kBlock = 1024;                    // tokens of a block
 constexpr int kMaxBlocks = kSampleMaxVocab / kBlock;
 constexpr int kMaxSplit = 8;                    // CTAs a row
-constexpr int kBins = 2048;                     // of the exponents
 constexpr int kFine = 512;                      // of the values in a range
 constexpr int kGather = 2048;                   // tokens that the last histograms can take
-constexpr float kPerUnit = 32.0f;               // bins in a factor 2 of the weight
-constexpr float kWindow = kBins / kPerUnit - 1; // in log2: lighter tokens do not count
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMagic = 12582912.0f;           // 1.5 * 2^23: adding it rounds to whole numbers
 constexpr uint32_t kMagicBits = 0x4B400000u;
@@ -1137,7 +1135,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
         }
         return;
     }
-    job.lowest = max(max(K::from(job.m - kWindow / job.c.h), K::kNegInf + 1), bound);
+    job.lowest = max(max(K::from(window_end(job.m, job.c.h)), K::kNegInf + 1), bound);
     job.bits = min(32 - (vocab > 1 ? 32 - __clz(vocab - 1) : 0), 18);  // 2^bits residuals of `vocab` tokens fit 32 bits
 
     // ---- the cut: tokens above its value are kept, and `ties` equal to it
