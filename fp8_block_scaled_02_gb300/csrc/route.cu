@@ -36,11 +36,18 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
     return x != x ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// c in multiples of 2^-44, above 0, for |c| < 2^17; NaN below everything.
-__device__ __forceinline__ uint64_t score_key(Two c) {
-    if (c.h != c.h) return 1;
-    const float h = c.h * 0x1p44f, l = c.l * 0x1p44f;
-    const long long v = fabsf(h) < 0x1p23f ? __float2ll_rn(h + l) : __float2ll_rn(h) + __float2ll_rn(l);
+// To the nearest whole number, for a number below 2^62.
+__device__ __forceinline__ long long to_whole(float h, float l) {
+    return fabsf(h) < 0x1p23f ? __float2ll_rn(h + l) : __float2ll_rn(h) + __float2ll_rn(l);
+}
+// c = s + bias in multiples of 2^-44, above 0, for s in [0, 1] and a bias of at most 2^16; NaN below everything.  A
+// bias of 2^-20 and more is a whole number of them and added as one: a pair of fp32 near 65536 resolves 2^-32 only.
+__device__ __forceinline__ uint64_t score_key(Two s, float bias) {
+    long long v = 0;
+    if (fabsf(bias) < 0x1p-20f) s = add(s, bias);
+    else v = __float2ll_rn(bias * 0x1p44f);
+    if (s.h != s.h || bias != bias) return 1;
+    v += to_whole(s.h * 0x1p44f, s.l * 0x1p44f);
     return static_cast<uint64_t>(v + (1ll << 62));
 }
 
@@ -106,7 +113,7 @@ __device__ __noinline__ void route_exactly(const MoeScoreArgs &a, int64_t token,
         for (int i = 0; i < EPL; ++i) {
             float b = 0.0f;
             if (a.bias && e0 + i < experts) b = fminf(fmaxf(a.bias[e0 + i], -kMostBias), kMostBias);
-            key[i] = score_key(add(s[i], b));
+            key[i] = score_key(s[i], b);
         }
     }
 #pragma unroll
@@ -413,7 +420,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         if (lane < n) {
             const float v = load_logit<F32>(row, id), d = -fabsf(v);
             const Two u = d > kNoScore ? two_exp2(times_log2e(Two{d, 0.0f})) : Two{0.0f, 0.0f}, one{1.0f, 0.0f};
-            exact = score_key(add(div(v < 0.0f ? u : one, add(u, 1.0f)), fminf(fmaxf(a.bias[id], -kMostBias), kMostBias)));
+            exact = score_key(div(v < 0.0f ? u : one, add(u, 1.0f)), fminf(fmaxf(a.bias[id], -kMostBias), kMostBias));
         }
         place = 0;
         for (int j = 0; j < n; ++j) {

@@ -419,9 +419,9 @@ int fp8bs_moe_gemv_ws(const void *x_bf16, int64_t m, const int32_t *expert_ids,
  *   expert_ids[t, j],  weights[t, j] = scale * s_e,  divided by the sum of the
  *   chosen s where renormalize is not 0 (0 where that sum is 0).
  * Equals go to the lowest index.  c and groups' scores are compared in multiples
- * of 2^-44 (c held within 2^-43 of its value, biases taken as at most 65536 in
- * magnitude); without a bias experts are compared by x itself, which is the same
- * order.  Weights within 2^-18 of themselves; e^-|x| below 2^-126 counts as 0.
+ * of 2^-44 (each c within two of them, whatever its bias; biases taken as at most
+ * 65536 in magnitude); without a bias experts are compared by x itself, which is
+ * the same order.  Weights within 2^-18 of themselves; e^-|x| below 2^-126 counts as 0.
  *
  * Defined by: no passage of the source pages has a counterpart (Atlas
  * spark_model/weight_map/quantize_fp8_bs.rs: decode reads the top-12 of 256
