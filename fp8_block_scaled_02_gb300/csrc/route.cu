@@ -313,7 +313,8 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
             b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
             b1 = fmaxf(b1, o1);
         }
-        const float score = a.group_top == 2 ? b1 + b2 : b1;
+        const bool two = a.group_top == 2;
+        const float score = two ? b1 + b2 : b1;
         int before = 0;
         for (int g = 0; g < groups; ++g) {
             const float other = __shfl_sync(0xffffffffu, score, g * lanes);
@@ -321,12 +322,12 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         }
         open = group < groups && before < static_cast<int>(a.topk_groups);
         if (a.topk_groups < a.groups) {
-            // the last that is open and the first that is not
-            const uint32_t in = __reduce_min_sync(0xffffffffu, open ? logit_key(score) : 0xFFFFFFFFu);
-            const uint32_t out = __reduce_max_sync(0xffffffffu, group < groups && !open ? logit_key(score) : 0u);
-            const float low = __uint_as_float(in & 0x80000000u ? in & 0x7FFFFFFFu : ~in);
-            const float high = __uint_as_float(out & 0x80000000u ? out & 0x7FFFFFFFu : ~out);
-            if (!(low - high > 4.0f * (slack + 0x1p-22f * (fabsf(low) + fabsf(high))))) return false;
+            // A score is off by what its parts are, which the sum does not tell: a large c and its opposite may cancel.
+            // The last that is open, at its least, and the first that is not, at its most.
+            const float off = 2.0f * (slack + 0x1p-22f * (fabsf(b1) + (two ? fabsf(b2) : 0.0f)));
+            const uint32_t in = __reduce_min_sync(0xffffffffu, open ? logit_key(score - off) : 0xFFFFFFFFu);
+            const uint32_t out = __reduce_max_sync(0xffffffffu, group < groups && !open ? logit_key(score + off) : 0u);
+            if (in <= out) return false;
         }
     }
     const bool by_score = a.bias != nullptr;
