@@ -51,6 +51,14 @@ __device__ __forceinline__ uint64_t score_key(Two s, float bias) {
     return static_cast<uint64_t>(v + (1ll << 62));
 }
 
+// A bias as it counts: in [-kMostBias, kMostBias]; NaN stays NaN, as its c then is.
+__device__ __forceinline__ float bias_of(float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(b), "f"(-kMostBias));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(kMostBias));
+    return r;
+}
+
 __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     const uint32_t hi = static_cast<uint32_t>(v >> 32), top = __reduce_max_sync(0xffffffffu, hi);
     const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == top ? static_cast<uint32_t>(v) : 0u);
@@ -112,7 +120,7 @@ __device__ __noinline__ void route_exactly(const MoeScoreArgs &a, int64_t token,
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             float b = 0.0f;
-            if (a.bias && e0 + i < experts) b = fminf(fmaxf(a.bias[e0 + i], -kMostBias), kMostBias);
+            if (a.bias && e0 + i < experts) b = bias_of(a.bias[e0 + i]);
             key[i] = score_key(s[i], b);
         }
     }
@@ -293,7 +301,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
             for (int i = 0; i < EPL; ++i) b[i] = i < mine ? a.bias[e0 + i] : 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) c[i] = fmaf(c[i], to_score, fminf(fmaxf(b[i], -kMostBias), kMostBias));
+        for (int i = 0; i < EPL; ++i) c[i] = fmaf(c[i], to_score, bias_of(b[i]));
     }
     bool open = true;
     if (groups > 1) {
@@ -421,7 +429,7 @@ __device__ __forceinline__ bool route_quickly(const MoeScoreArgs &a, int64_t tok
         if (lane < n) {
             const float v = load_logit<F32>(row, id), d = -fabsf(v);
             const Two u = d > kNoScore ? two_exp2(times_log2e(Two{d, 0.0f})) : Two{0.0f, 0.0f}, one{1.0f, 0.0f};
-            exact = score_key(div(v < 0.0f ? u : one, add(u, 1.0f)), fminf(fmaxf(a.bias[id], -kMostBias), kMostBias));
+            exact = score_key(div(v < 0.0f ? u : one, add(u, 1.0f)), bias_of(a.bias[id]));
         }
         place = 0;
         for (int j = 0; j < n; ++j) {

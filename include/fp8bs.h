@@ -431,8 +431,10 @@ int fp8bs_moe_gemv_ws(const void *x_bf16, int64_t m, const int32_t *expert_ids,
  *                non-zero, rows row_stride elements apart (>= num_experts, or 0:
  *                one row for every token); aligned to its element size.  -inf
  *                shuts an expert out of the softmax (all of them: s = 0).  An
- *                expert whose c is NaN comes after every other; the ids are
- *                distinct and in range whatever the logits
+ *                expert whose c is NaN, by its logit or its bias, comes after
+ *                every other, a group with one among its group_top best after
+ *                every group without; the ids are distinct and in range
+ *                whatever the logits and the biases
  *   num_experts  1..1024;  topk 1..32, <= topk_groups * num_experts / groups
  *   bias         device, [num_experts] fp32, or NULL
  *   groups       1..32, a divisor of num_experts;  topk_groups 1..groups;
