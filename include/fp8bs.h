@@ -870,11 +870,12 @@ int fp8bs_token_logprobs(const void *logits, int logits_f32,
  * Two numbers a row, because one fp32 number in steps of 2^-24 cannot give
  * 152064 tokens their probabilities, and the borders of as many tokens on
  * one line would be moved by every rounding of a sum.  T = 0 is greedy (the
- * first token, log probability 0).  A weight is within 2^-22 of itself, and masses
- * are whole multiples of 2^-41 of the largest weight: what is below half of that
- * may count as nothing.  Errors of single weights mostly cancel in a mass; a
- * draw, or a top_p, nearer to a border than what is left of them (some 2^-27 of
- * the mass) may fall to either side.
+ * first token, log probability 0).  Masses are whole multiples of 2^-41 of the
+ * largest weight: what is below half of that may count as nothing.  What rounds is
+ * a weight (2^-22 of itself, or half a step of the histogram that finds a cut) and
+ * a block's sum in fp32: a first number or a top_p nearer than 2^-17 of itself
+ * (a top_p over more than 2^18 tokens 2^-16) to a border may fall to either side;
+ * as a rule what is further than 2^-21 does not.
  *
  * Defined by: no passage of the source pages has a counterpart (FreeToken PR
  * #636 serves the lm_head whose logits these are).
