@@ -264,14 +264,15 @@ def _rows_contiguous(t):
 
 
 def _checked(*specs):
-    """_Args' checks of (name, tensor, dtype, numel or None, rows) in one
-    quick pass; raises what _Args raises.  Returns the call's device."""
+    """_Args' checks of (name, tensor, dtype, numel or shape or None, rows) in
+    one quick pass; raises what _Args raises.  Returns the call's device."""
     try:
         first = specs[0][1]
         index = first.get_device()  # -1: not a GPU
         if index >= 0:
             for _, t, dtype, numel, rows in specs:
-                if (t.dtype is not dtype or t.get_device() != index or (numel is not None and t.numel() != numel)
+                if (t.dtype is not dtype or t.get_device() != index
+                        or (numel is not None and (t.shape if numel.__class__ is tuple else t.numel()) != numel)
                         or not (t.is_contiguous() or (rows and _rows_contiguous(t)))):
                     break
             else:
@@ -280,7 +281,7 @@ def _checked(*specs):
         pass
     a = _Args()
     for name, t, dtype, numel, rows in specs:
-        a.need(name, t, dtype, numel=numel, rows=rows)
+        a.need(name, t, dtype, **{"shape" if isinstance(numel, tuple) else "numel": numel}, rows=rows)
     return a.check().device
 
 
@@ -610,9 +611,9 @@ def moe_route(logits, topk: int, scoring: str = "softmax", bias=None, groups: in
     if bias is not None:
         specs.append(("bias", bias, f32, e, False))
     if ids is not None:
-        specs.append(("ids", ids, i32, m * topk, False))
+        specs.append(("ids", ids, i32, (m, topk), False))
     if weights is not None:
-        specs.append(("weights", weights, f32, m * topk, False))
+        specs.append(("weights", weights, f32, (m, topk), False))
     device = _checked(*specs)
     if ids is None:
         ids = _empty(stream, device, (m, topk), i32)
@@ -636,13 +637,13 @@ def moe_combine(y, weights, ids=None, num_experts: int = 0, residual=None, out=N
     if ids is not None and num_experts < 1:
         raise ValueError("ids need num_experts: a slot whose id is outside [0, num_experts) adds nothing")
     bf16 = torch.bfloat16
-    specs = [("y", y, bf16, None, False), ("weights", weights, torch.float32, m * topk, False)]
+    specs = [("y", y, bf16, None, False), ("weights", weights, torch.float32, (m, topk), False)]
     if ids is not None:
-        specs.append(("ids", ids, torch.int32, m * topk, False))
+        specs.append(("ids", ids, torch.int32, (m, topk), False))
     if residual is not None:
-        specs.append(("residual", residual, bf16, m * n, False))
+        specs.append(("residual", residual, bf16, (m, n), False))
     if out is not None:
-        specs.append(("out", out, bf16, m * n, False))
+        specs.append(("out", out, bf16, (m, n), False))
     device = _checked(*specs)
     if out is None:
         out = _empty(stream, device, (m, n), bf16)
@@ -841,7 +842,7 @@ def _rope_append(four_bit, q, k, v, positions, slots, cos_sin, k_scale, v_scale,
     if k_norm is not None:
         given += (("k_norm", k_norm, bf16, d, False),)
     if out is not None:
-        given += (("out", out, bf16, t * hq * d, False),)
+        given += (("out", out, bf16, (t, hq, d), False),)
     device = _checked(*caches, ("positions", positions, i32, t, False), ("slots", slots, i32, t, False),
                       ("cos_sin", cos_sin, f32, None, False), ("q", q, bf16, None, True), ("k", k, bf16, None, True),
                       ("v", v, bf16, None, True), *given)
@@ -924,7 +925,7 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
         raise ValueError(f"the rows of logits overlap: they are {stride} elements apart and {v} long")
     f32, i32 = torch.float32, torch.int32
     is_f32 = logits.dtype == f32
-    specs = [("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), ("u", u, f32, 2 * m, False)]
+    specs = [("logits", logits, f32 if is_f32 else torch.bfloat16, None, True), ("u", u, f32, (m, 2), False)]
     if temperature is not None:
         specs.append(("temperature", temperature, f32, m, False))
     if top_k is not None:
