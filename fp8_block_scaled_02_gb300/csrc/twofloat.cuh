@@ -102,7 +102,8 @@ TWOFLOAT_FN Two times_log2e(Two x) {
     return fast_two_sum(p.h, p.l);
 }
 
-// 2^(t.h + t.l) within 2^-45 of itself, for -126 < t < 126; 0 below.  With n
+// 2^(t.h + t.l) within 2^-45 of itself and 2^-149, for -126 < t < 126; 0 below.
+// (Under t = -100 the low part is subnormal, and what counts is the 2^-149.)  With n
 // the nearest integer and f the rest, the sum of (f ln 2)^k / k! to k = 12; the
 // terms from k = 7 on are below 2^-23 of the sum and need one fp32 each.
 TWOFLOAT_FN Two two_exp2(Two t) {
