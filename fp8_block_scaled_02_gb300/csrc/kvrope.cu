@@ -9,9 +9,10 @@
 // cache are defined exactly.  r is the rounding of the exact value but for one
 // head in about 2^17: a key's sum of squares is carried in two fp32 numbers (a
 // square of a bf16 number is exact in one), and a step of Newton's method with
-// an exact residual corrects the square root's reciprocal.  With a plain fp32
-// sum r is off by a unit in the last place for every third head, and a 4-bit
-// code in some ten million with it.
+// an exact residual corrects the square root's reciprocal; for |a| below 2^50 and
+// mean a^2 + eps from 2^-100 on, beyond which the low parts are subnormal.  With a
+// plain fp32 sum r is off by a unit in the last place for every third head, and a
+// 4-bit code in some ten million with it; queries, which end in bf16, have that.
 #include "twofloat.cuh"
 
 #include "serving.cuh"

@@ -702,12 +702,16 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  * of fp4kv_append).  Of a head vector a with norm weights w, each fl one fp32
  * rounding:
  *   r = fl(1 / sqrt(mean a^2 + eps)),  n_i = fl(fl(a_i * r) * w_i)
- * (n = a where the weights are NULL; |a| below 2^60 where they are not); of a
- * pair (n1, n2) with the cos c and the sin s of the token's position:
+ * (n = a where the weights are NULL; where they are not |a| is below 2^50 and
+ * mean a^2 + eps at least 2^-100: beyond, r may be off by more than its rounding,
+ * and NaN from |a| = 2^60 on or below a sum of 2^-126); of a pair (n1, n2) with the
+ * cos c and the sin s of the token's position:
  *   o1 = fl(fl(n1 * c) - fl(n2 * s)),  o2 = fl(fl(n2 * c) + fl(n1 * s))
- * over the first rot_dim elements, the others o = n.  q_out = bf16(o); k is
- * stored as o is by the cache's own rule (e4m3(fl(o / k_scale)), or the group
- * rule of fp4kv_append with x = o), v as the append stores it.
+ * over the first rot_dim elements, the others o = n.  q_out = bf16(o), where a
+ * query's squares are summed in plain fp32, so that next to a border between two
+ * bf16 numbers it may be either; k is stored as o is by the cache's own rule
+ * (e4m3(fl(o / k_scale)), or the group rule of fp4kv_append with x = o), v as the
+ * append stores it.
  *
  * Defined by: no passage of the source pages has a counterpart for the norm
  * and the rotation; the FP8 cache and its scales are InfiniLM PR #586's.
@@ -726,7 +730,7 @@ int fp4kv_gather(const uint8_t *k_cache, const uint8_t *v_cache,
  *   rot_dim      16..head_dim, a multiple of 16
  *   interleaved  0: pair j is elements j and j + rot_dim / 2; else 2j and 2j + 1
  *   q_weight, k_weight   device, [head_dim] bf16, 16-byte aligned, or NULL
- *   eps          >= 0, finite (a head of zeros with eps = 0 gives NaN)
+ *   eps          >= 0, finite (with eps = 0 a head of zeros gives NaN)
  *   q_out        device, [num_tokens, num_q_heads, head_dim] bf16, 16-byte aligned;
  *                may be q_bf16 itself where q_stride is num_q_heads * head_dim
  *   k_scale, v_scale   device, 1 positive float each
