@@ -308,6 +308,7 @@ struct Shared {
     uint32_t warp_key[kWarps], part_key[kMaxSplit], part_bound[kMaxSplit], bound, min_key;
     uint64_t bin_weight[32];          // kBinWeight: lanes ask for different ones
     int listed, collected, last, block, allowed;
+    uint64_t beside;                  // the mass outside the drawn block
     // from here on for the search of a cut only
     alignas(16) uint32_t n[kBins], q[kBins];  // tokens of a bin, and what they weigh beside its weight
     union {
@@ -1255,6 +1256,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
             if (at <= target && at + v[i] > target) {  // one block
                 sh.block = first + i;
                 sh.allowed = n[i];
+                sh.beside = total - v[i];
             }
             at += v[i];
         }
@@ -1284,17 +1286,22 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_kernel(const SampleArgs 
     uint64_t at = cta_exclusive<uint64_t, TH>(sum, sh.warp_sum, all);
     uint64_t target = part_of(all, u1);
     if (target >= all) target = all - 1;  // u1 = 1: the last token
+    int hit = -1;
+    float x_hit = 0.0f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        if (at <= target && at + w[j] > target) {  // one token
-            a.tokens[r] = e0 + j;
-            if (a.logprobs) {
-                // (x - m) / T - log(mass / 2^41)
-                const Two t = mul(mul(two_sum(x[j], -job.m), job.c), Two{kLn2, -0x1.05c61p-29f});
-                a.logprobs[r] = (t.h - logf(__ull2float_rn(total) * (1.0f / kUnit))) + t.l;
-            }
-        }
+        if (at <= target && at + w[j] > target) hit = j, x_hit = x[j];
         at += w[j];
+    }
+    if (hit >= 0) {  // one token
+        a.tokens[r] = e0 + hit;
+        if (a.logprobs) {
+            // (x - m) / T - log(mass / 2^41).  Of a mass near that of the largest logit, 2^41, the rest counts: if the
+            // block has that logit, its own mass is taken from the weights here (2^-45)
+            const uint64_t mass = block_m == job.m ? sh.beside + ((all + 8) >> 4) : total;
+            const Two t = mul(mul(two_sum(x_hit, -job.m), job.c), Two{kLn2, -0x1.05c61p-29f});
+            a.logprobs[r] = (t.h - log1pf(__ull2float_rn(mass - (1ull << 41)) * (1.0f / kUnit))) + t.l;
+        }
     }
 }
 
