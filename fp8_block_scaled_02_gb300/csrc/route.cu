@@ -9,8 +9,8 @@
 // of fp32.  Without a bias or groups it goes by the logits themselves.
 //
 // Floor: the logits read once (8192 tokens of 256 experts in fp32: 8.9 MB, 1.3 us).
-// Measured 16.6 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 9.7 (softmax,
-// 12 of 256, no bias), 14.3 (softmax, 3 of 8 groups, 6 of 160) and 3.4 for 32 tokens,
+// Measured 14.6 us (sigmoid, bias, the best 4 of 8 groups; 8 of 256), 9.7 (softmax,
+// 12 of 256, no bias), 14.6 (softmax, 3 of 8 groups, 6 of 160) and 3.3 for 32 tokens,
 // most of it the launch and the chain of dependent steps.  What bounds the prompt is
 // instructions, 1090 and 860 a token, ALU first: the scores, the groups, the order
 // keys.  With pairs of fp32 for every token it took 36.5 us; with the largest left
@@ -497,7 +497,9 @@ cudaError_t launch_route_t(const MoeScoreArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, route_kernel<F32, EPL>, a);
 }
 
-// Experts a lane: what a group's lanes, or all, have to hold; what they cannot is left to pairs of fp32 alone.
+// Experts a lane: what a group's lanes, or all, have to hold.  Where 32 a lane are not enough (a group has a power of
+// two of the lanes: 1023 experts in 3 groups are 341 on 8 lanes) every token is left to pairs of fp32: 8192 tokens 244
+// us, 32 tokens 47, against 58 and 7 for 1024 in 4 groups, the best 2 of them open.
 template <bool F32>
 cudaError_t launch_route_epl(const MoeScoreArgs &a, cudaStream_t stream) {
     int64_t lanes = 32;

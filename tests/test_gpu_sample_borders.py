@@ -4,7 +4,7 @@ block's, as near as include/fp8bs.h says that they are told apart.
 
 A block's mass: a lane's two chains of 16 fp32 additions, their sum, the fma that
 takes the exponents' losses back and 5 additions across the warp round by half a step
-each, 23 2^-24, and ex2 is within 2^-22: 2^-19.3, and 2^-18 for the two masses that a first
+each, 23 2^-24, and ex2 is within 2^-22: 2^-19.2, and 2^-18 for the two masses that a first
 number's border compares.  A cut compares the mass of all with that of the
 histogram, whose weights are in steps of 2^-20, or of 2^-(5 + b) where tokens are counted too (with
 top_k, or many equals), b = 18 to 2^14 tokens and one less for each doubling, at least 12: half a
